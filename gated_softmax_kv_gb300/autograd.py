@@ -1,4 +1,5 @@
-"""A thin torch.autograd wrapper over the two C-ABI calls.
+"""Thin torch.autograd wrappers: `compressor` over the Compressor's two C-ABI
+calls, and `rope` over csa_rope and its transpose.
 
 `compressor(...)` returns `out` and, on backward, calls csa_compress_bwd for
 dkv, dscore and dape (cuDNN-frontend "CSA Fused Compressor", sections
@@ -12,6 +13,7 @@ from typing import Optional
 import torch
 
 from .binding import csa_compress_bwd, csa_compress_fwd
+from .rope import csa_rope
 
 
 class CompressorFunction(torch.autograd.Function):
@@ -45,3 +47,35 @@ def compressor(kv: torch.Tensor, score: torch.Tensor, ape: torch.Tensor, cu_seql
         capacity = int(cu_seqlens_comp[-1].item())
     return CompressorFunction.apply(kv, score, ape, cu_seqlens, cu_seqlens_comp, capacity, ratio,
                                     coff, head_dim, exact)
+
+
+class RopeFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, freqs, positions, cu_seqlens_comp, ratio: int, offset: int, layout: str,
+                amplitude: float, transpose: bool):
+        ctx.save_for_backward(freqs, positions, cu_seqlens_comp)
+        ctx.meta = (ratio, offset, layout, amplitude, transpose)
+        return csa_rope(x, freqs, positions, cu_seqlens_comp=cu_seqlens_comp, ratio=ratio,
+                        offset=offset, layout=layout, amplitude=amplitude, transpose=transpose)
+
+    @staticmethod
+    def backward(ctx, grad):
+        # the operator is linear: its gradient is its transpose, itself differentiable
+        freqs, positions, cuc = ctx.saved_tensors
+        ratio, offset, layout, amplitude, transpose = ctx.meta
+        if grad.stride(-1) != 1:
+            grad = grad.contiguous()
+        dx = RopeFunction.apply(grad, freqs, positions, cuc, ratio, offset, layout, amplitude,
+                                not transpose)
+        return dx, None, None, None, None, None, None, None, None
+
+
+def rope(x: torch.Tensor, freqs: torch.Tensor, positions: Optional[torch.Tensor] = None, *,
+         cu_seqlens_comp: Optional[torch.Tensor] = None, ratio: int = 1, offset: int = 0,
+         layout: str = "interleaved", amplitude: float = 1.0,
+         transpose: bool = False) -> torch.Tensor:
+    """Differentiable csa_rope (same arguments, no in-place form): the gradient
+    with respect to x is the transposed turn of grad_out, in one launch.
+    freqs and positions are constants."""
+    return RopeFunction.apply(x, freqs, positions, cu_seqlens_comp, ratio, offset, layout,
+                              amplitude, transpose)

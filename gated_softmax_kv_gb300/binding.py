@@ -1,4 +1,5 @@
-"""Python binding of the C ABI in include/csa_compress.h (argument marshalling only).
+"""Python binding of the C ABI in include/csa_compress.h (argument marshalling only);
+rope.py and cache.py bind csa_rope.h and csa_cache.h over the library loaded here.
 
 Every computation runs in libcsa_compress.so; this module checks tensor
 dtypes/devices/shapes, derives the sizes the C calls want from tensor shapes,
@@ -51,6 +52,24 @@ def load() -> ctypes.CDLL:
     lib.csa_compress_bwd_noalloc.restype = ctypes.c_int
     lib.csa_check_segments.argtypes = [vp, vp, i32, i64, i64, i32, vp, vp]
     lib.csa_check_segments.restype = ctypes.c_int
+    lib.csa_rope.argtypes = ([vp] * 4 + [i32, vp, i32, i32, i64, i32, i32] + [i64] * 4
+                             + [i32] * 4 + [ctypes.c_float, i32, vp])
+    lib.csa_rope.restype = ctypes.c_int
+    lib.csa_cache_append.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, i32, vp, vp, vp]
+    lib.csa_cache_append.restype = ctypes.c_int
+    lib.csa_cache_attend.argtypes = [vp, vp, i32, i64, i32, i64, i64, i32, i32, ctypes.c_float, vp,
+                                     i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.csa_cache_attend.restype = ctypes.c_int
+    lib.csa_cache_copy_pages.argtypes = [vp, vp, vp, i32, vp]
+    lib.csa_cache_copy_pages.restype = ctypes.c_int
+    lib.csa_cache_fork.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp, vp]
+    lib.csa_cache_fork.restype = ctypes.c_int
+    lib.csa_cache_reserve.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, i32, vp, vp]
+    lib.csa_cache_reserve.restype = ctypes.c_int
+    lib.csa_cache_free.argtypes = [vp, vp, vp, i32, i32, i32, vp, i32, vp]
+    lib.csa_cache_free.restype = ctypes.c_int
+    lib.csa_cache_compact.argtypes = [vp, vp, vp, i32, i32, vp, vp]
+    lib.csa_cache_compact.restype = ctypes.c_int
     lib.csa_status_string.argtypes = [ctypes.c_int]
     lib.csa_status_string.restype = ctypes.c_char_p
     lib.csa_last_cuda_error.argtypes = []

@@ -8,6 +8,7 @@
 
 #include <mutex>
 
+#include "csa_cache_internal.h"
 #include "csa_compress.h"
 #include "csa_internal.h"
 
@@ -188,6 +189,15 @@ csa_status_t check_bwd_args(const void* kv, const void* score, const float* ape,
 
 csa_status_t record_cuda_error(cudaError_t e) { return cuda_fail(e); }
 
+// The same stream-ordered pool for the cache's kernels (csa_cache_internal.h).
+cudaError_t workspace_take(void** ptr, size_t bytes, cudaStream_t stream) {
+  cudaMemPool_t pool;
+  const cudaError_t e = workspace_pool(&pool);
+  if (e != cudaSuccess) return e;
+  return cudaMallocFromPoolAsync(ptr, bytes, pool, stream);
+}
+cudaError_t workspace_give(void* ptr, cudaStream_t stream) { return cudaFreeAsync(ptr, stream); }
+
 namespace {
 
 // Driver entry points, looked up once through the runtime (no link against
@@ -284,9 +294,9 @@ const char* csa_status_string(csa_status_t status) {
   switch (status) {
     case CSA_OK: return "ok";
     case CSA_ERR_NULL: return "a required pointer is null";
-    case CSA_ERR_ALIGN: return "a base pointer is misaligned (16 bytes for tensors, 4 for segment arrays)";
-    case CSA_ERR_UNSUPPORTED: return "ratio, coff or head_dim outside the supported envelope";
-    case CSA_ERR_RANGE: return "a size is negative, overflows int32 flat offsets, or capacity > 0 with total_tokens < ratio";
+    case CSA_ERR_ALIGN: return "a base pointer or stride is misaligned (16 bytes for tensors, 4 for index arrays)";
+    case CSA_ERR_UNSUPPORTED: return "ratio, coff, head_dim or another size, type or layout outside the supported envelope";
+    case CSA_ERR_RANGE: return "a size or stride is negative or too large (flat offsets, table limits), or capacity > 0 with total_tokens < ratio";
     case CSA_ERR_CUDA: return "a CUDA runtime call failed";
     case CSA_ERR_SCRATCH: return "the backward needs more dape scratch than the no-allocation buffer holds (CSA_NOALLOC_SCRATCH_FLOATS)";
     default: return "unknown status";

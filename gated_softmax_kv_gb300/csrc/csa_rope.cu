@@ -1,0 +1,370 @@
+// Rotary positions (declared in include/csa_rope.h): turns column pairs of
+// every head by position * frequency, in one pass over the data.
+//
+// Angles. A frequency f (radians a position, fp64) becomes F = f / (2 pi) in
+// 64-bit fixed point, so the phase of position p is p * F modulo 2^64: the
+// reduction to one turn is the integer product's own overflow, exact for any
+// position, with no fp64 arithmetic per element (fp64 runs at 1/64 of the
+// fp32 rate here). The top 32 bits go through sincospif.
+//
+// The kernel is a copy with some arithmetic: it is bound by memory. A thread
+// keeps one column vector of the head for its whole loop, so F is worked out
+// once per thread, and the sine and cosine of a token are shared by the heads
+// that a thread takes.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "csa_device.cuh"
+#include "csa_internal.h"
+#include "csa_rope.h"
+
+namespace csa {
+
+namespace {
+
+struct RopeArgs {
+  const void* x;
+  void* y;
+  const double* freqs;
+  const void* positions;
+  const int32_t* cu;
+  int64_t tokens;
+  int64_t xt, xh, yt, yh;  // strides in elements
+  int32_t position_bits, nseq, ratio;
+  int32_t heads, d, rope, offset;
+  float amplitude;
+  bool transpose, in_place;
+};
+
+struct Bf16 {
+  uint16_t bits;
+};
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<Bf16> {
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return make_float2(bf16_lo(w), bf16_hi(w));
+  }
+  static __device__ __forceinline__ uint32_t pack(float2 v) { return pack_bf16x2(v.x, v.y); }
+  static __device__ __forceinline__ float load(const Bf16* p) {
+    return __uint_as_float((uint32_t)p->bits << 16);
+  }
+  static __device__ __forceinline__ void store(Bf16* p, float v) {
+    p->bits = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+  }
+};
+template <>
+struct Elem<__half> {
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return __half22float2(*reinterpret_cast<__half2*>(&w));
+  }
+  static __device__ __forceinline__ uint32_t pack(float2 v) {
+    __half2 h = __float22half2_rn(v);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float load(const __half* p) { return __half2float(*p); }
+  static __device__ __forceinline__ void store(__half* p, float v) { *p = __float2half_rn(v); }
+};
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ float load(const float* p) { return *p; }
+  static __device__ __forceinline__ void store(float* p, float v) { *p = v; }
+};
+
+// 16 bytes of T as fp32 values and back.
+template <typename T>
+struct Vec {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(uint4 w, float* v) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = Elem<T>::unpack(u[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = Elem<T>::pack(make_float2(v[2 * i], v[2 * i + 1]));
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(uint4 w, float* v) {
+    v[0] = __uint_as_float(w.x);
+    v[1] = __uint_as_float(w.y);
+    v[2] = __uint_as_float(w.z);
+    v[3] = __uint_as_float(w.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  }
+};
+
+// f / (2 pi) modulo 1 as a 64-bit fraction, from the bits of f: with f =
+// m 2^(e-52), m a 53-bit integer, and K = floor(2^66 / (2 pi)), the product's
+// high word (m 2^11) K / 2^64 times 2^(e-1) is 2^64 f / (2 pi), within 2^-61
+// relative before the shift drops what is below 2^-64 turns.
+__device__ __forceinline__ uint64_t turns_of(double f) {
+  const uint64_t b = (uint64_t)__double_as_longlong(f);
+  const int e = (int)((b >> 52) & 0x7FF) - 1023;
+  const uint64_t m = (b & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull;
+  const uint64_t kInv2Pi = 0xA2F9836E4E441529ull;  // floor(2^66 / (2 pi))
+  const uint64_t p = __umul64hi(m << 11, kInv2Pi);
+  const int s = e - 1;
+  const uint64_t r = s <= -64 ? 0ull : s < 0 ? (p >> -s) : s < 64 ? (p << s) : 0ull;
+  return (int64_t)b < 0 ? 0ull - r : r;
+}
+
+__device__ __forceinline__ void turn_of(uint64_t f, int64_t pos, float amplitude, float sign,
+                                        float* c, float* s) {
+  const uint64_t phase = f * (uint64_t)pos + 0x80000000ull;  // nearest of the top 32 bits
+  const float half_turns = (float)(int32_t)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31
+  float sn, cs;
+  sincospif(half_turns, &sn, &cs);
+  *c = cs * amplitude;
+  *s = sn * (amplitude * sign);
+}
+
+__device__ __forceinline__ int64_t position_of(const RopeArgs& a, int64_t t) {
+  if (a.positions)
+    return a.position_bits == 64 ? __ldg(static_cast<const long long*>(a.positions) + t)
+                                 : (int64_t)__ldg(static_cast<const int32_t*>(a.positions) + t);
+  if (t >= __ldg(a.cu + a.nseq)) return 0;
+  int lo = 0, hi = a.nseq;  // last s with cu[s] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.cu + mid) <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return (t - __ldg(a.cu + lo)) * a.ratio;
+}
+
+// Vector kernel: 16-byte aligned rows, part and strides. A chunk is one
+// vector of interleaved pairs, two vectors half a part apart, or (out of
+// place) one vector to copy.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int32_t chunks,
+                                                       int32_t heads_each, int32_t groups) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  constexpr int N = Vec<T>::N;
+  constexpr int PAIRS = HALF ? N : N / 2;
+  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t lanes = (int64_t)gridDim.x * blockDim.x / chunks;  // whole rows of chunks
+  const int32_t c = (int32_t)(id % chunks);
+  const int64_t first = id / chunks;
+  if (first >= lanes) return;
+  const int turned = HALF ? a.rope / (2 * N) : a.rope / N;
+  const int64_t items = a.tokens * groups;
+  const T* x = static_cast<const T*>(a.x);
+  T* y = static_cast<T*>(a.y);
+  if (c < turned) {
+    uint64_t f[PAIRS];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) f[i] = turns_of(__ldg(a.freqs + c * PAIRS + i));
+    const int col = a.offset + c * N;
+    const float sign = a.transpose ? -1.0f : 1.0f;
+    for (int64_t it = first; it < items; it += lanes) {
+      const int64_t t = it / groups;
+      const int h0 = (int)(it - t * groups) * heads_each;
+      const int h1 = min(h0 + heads_each, a.heads);
+      const int64_t pos = position_of(a, t);
+      float cs[PAIRS], sn[PAIRS];
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) turn_of(f[i], pos, a.amplitude, sign, &cs[i], &sn[i]);
+      for (int h = h0; h < h1; ++h) {
+        const T* px = x + t * a.xt + h * a.xh + col;
+        T* py = y + t * a.yt + h * a.yh + col;
+        float v[N];
+        Vec<T>::unpack(*reinterpret_cast<const uint4*>(px), v);
+        if constexpr (HALF) {
+          float w[N];
+          Vec<T>::unpack(*reinterpret_cast<const uint4*>(px + a.rope / 2), w);
+          float va[N], wb[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            va[i] = fmaf(-w[i], sn[i], v[i] * cs[i]);
+            wb[i] = fmaf(v[i], sn[i], w[i] * cs[i]);
+          }
+          *reinterpret_cast<uint4*>(py) = Vec<T>::pack(va);
+          *reinterpret_cast<uint4*>(py + a.rope / 2) = Vec<T>::pack(wb);
+        } else {
+          float o[N];
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) {
+            o[2 * i] = fmaf(-v[2 * i + 1], sn[i], v[2 * i] * cs[i]);
+            o[2 * i + 1] = fmaf(v[2 * i], sn[i], v[2 * i + 1] * cs[i]);
+          }
+          *reinterpret_cast<uint4*>(py) = Vec<T>::pack(o);
+        }
+      }
+    }
+  } else {
+    const int k = (c - turned) * N;
+    const int col = k < a.offset ? k : k + a.rope;
+    for (int64_t it = first; it < items; it += lanes) {
+      const int64_t t = it / groups;
+      const int h0 = (int)(it - t * groups) * heads_each;
+      const int h1 = min(h0 + heads_each, a.heads);
+      for (int h = h0; h < h1; ++h)
+        *reinterpret_cast<uint4*>(y + t * a.yt + h * a.yh + col) =
+            *reinterpret_cast<const uint4*>(x + t * a.xt + h * a.xh + col);
+    }
+  }
+}
+
+// Any alignment, any even part: a thread takes one pair or one column.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(256) rope_any_kernel(const RopeArgs a) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int pairs = a.rope / 2;
+  const int units = pairs + (a.in_place ? 0 : a.d - a.rope);
+  const int64_t items = a.tokens * a.heads * units;
+  const T* x = static_cast<const T*>(a.x);
+  T* y = static_cast<T*>(a.y);
+  for (int64_t it = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; it < items;
+       it += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = it / units;
+    const int u = (int)(it - row * units);
+    const int64_t t = row / a.heads;
+    const int h = (int)(row - t * a.heads);
+    const T* px = x + t * a.xt + h * a.xh;
+    T* py = y + t * a.yt + h * a.yh;
+    if (u < pairs) {
+      float c, s;
+      turn_of(turns_of(__ldg(a.freqs + u)), position_of(a, t), a.amplitude,
+              a.transpose ? -1.0f : 1.0f, &c, &s);
+      const int ia = a.offset + (HALF ? u : 2 * u), ib = HALF ? ia + pairs : ia + 1;
+      const float va = Elem<T>::load(px + ia), vb = Elem<T>::load(px + ib);
+      Elem<T>::store(py + ia, fmaf(-vb, s, va * c));
+      Elem<T>::store(py + ib, fmaf(va, s, vb * c));
+    } else {
+      const int k = u - pairs;
+      const int col = k < a.offset ? k : k + a.rope;
+      py[col] = px[col];
+    }
+  }
+}
+
+template <typename T, bool HALF>
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
+  constexpr int N = Vec<T>::N;
+  const uintptr_t bytes = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y);
+  const int64_t cols = a.xt | a.xh | a.yt | a.yh | a.offset | a.d | (HALF ? a.rope / 2 : a.rope);
+  if (bytes % 16 == 0 && cols % N == 0) {
+    const int chunks = (HALF ? a.rope / (2 * N) : a.rope / N) + (a.in_place ? 0 : (a.d - a.rope) / N);
+    // As many heads a thread as leave every SM a full set of threads: the
+    // sines are shared by them.
+    int heads_each = 1;
+    const int64_t full = (int64_t)152 * 2048;
+    while (heads_each < 8 && heads_each < a.heads &&
+           a.tokens * ((a.heads + 2 * heads_each - 1) / (2 * heads_each)) * chunks >= full)
+      heads_each *= 2;
+    const int groups = (a.heads + heads_each - 1) / heads_each;
+    const int64_t want = a.tokens * groups * chunks;
+    int64_t blocks = (want + 255) / 256;
+    const int64_t most = 152 * 8;
+    if (blocks > most) blocks = most;
+    const int64_t least = (chunks + 255) / 256;  // at least one whole row of chunks
+    if (blocks < least) blocks = least;
+    return launch_dependent(rope_vec_kernel<T, HALF>, dim3((unsigned)blocks), dim3(256), 0, stream,
+                            a, (int32_t)chunks, (int32_t)heads_each, (int32_t)groups);
+  }
+  const int64_t items = a.tokens * a.heads * (a.rope / 2 + (a.in_place ? 0 : a.d - a.rope));
+  int64_t blocks = (items + 255) / 256;
+  if (blocks > 152 * 32) blocks = 152 * 32;
+  return launch_dependent(rope_any_kernel<T, HALF>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+}
+
+template <typename T>
+cudaError_t launch_rope_layout(const RopeArgs& a, int32_t layout, cudaStream_t stream) {
+  return layout == CSA_ROPE_HALF ? launch_rope<T, true>(a, stream) : launch_rope<T, false>(a, stream);
+}
+
+}  // namespace
+
+}  // namespace csa
+
+extern "C" csa_status_t csa_rope(const void* x, void* y, const double* freqs, const void* positions,
+                                 int32_t position_bits, const int32_t* cu_rows, int32_t num_seqs,
+                                 int32_t ratio, int64_t tokens, int32_t heads, int32_t head_dim,
+                                 int64_t x_token_stride, int64_t x_head_stride,
+                                 int64_t y_token_stride, int64_t y_head_stride, int32_t rope_dim,
+                                 int32_t offset, int32_t layout, int32_t dtype, float amplitude,
+                                 int32_t transpose, cudaStream_t stream) {
+  if (dtype != CSA_BF16 && dtype != CSA_FP16 && dtype != CSA_FP32) return CSA_ERR_UNSUPPORTED;
+  if (layout != CSA_ROPE_INTERLEAVED && layout != CSA_ROPE_HALF) return CSA_ERR_UNSUPPORTED;
+  if (rope_dim < 2 || rope_dim % 2 != 0 || offset < 0 || head_dim < 1 ||
+      (int64_t)offset + rope_dim > head_dim)
+    return CSA_ERR_UNSUPPORTED;
+  if (positions && position_bits != 32 && position_bits != 64) return CSA_ERR_UNSUPPORTED;
+  if (tokens < 0 || heads < 1) return CSA_ERR_RANGE;
+  if (x_token_stride < 0 || x_head_stride < 0 || y_token_stride < 0 || y_head_stride < 0)
+    return CSA_ERR_RANGE;
+  // no index may pass 63 bits
+  const int64_t most = (int64_t)1 << 60;
+  if (tokens > most / heads / head_dim) return CSA_ERR_RANGE;
+  const int64_t by_token = tokens > 1 ? most / (tokens - 1) : most;
+  const int64_t by_head = heads > 1 ? most / (heads - 1) : most;
+  if (x_token_stride > by_token || y_token_stride > by_token || x_head_stride > by_head ||
+      y_head_stride > by_head)
+    return CSA_ERR_RANGE;
+  // distinct output elements: heads within a token's stretch, or tokens within a head's
+  const int64_t head_span = (heads - 1) * y_head_stride + head_dim;
+  const int64_t token_span = tokens > 0 ? (tokens - 1) * y_token_stride + head_dim : 0;
+  const bool heads_apart = heads == 1 || y_head_stride >= head_dim;
+  const bool tokens_apart = tokens <= 1 || y_token_stride >= head_dim;
+  if (!heads_apart || !tokens_apart) return CSA_ERR_RANGE;
+  if (heads > 1 && tokens > 1 && y_token_stride < head_span && y_head_stride < token_span)
+    return CSA_ERR_RANGE;
+  if (!freqs || (!positions && !cu_rows)) return CSA_ERR_NULL;
+  if (!positions && (num_seqs < 1 || ratio < 1)) return CSA_ERR_RANGE;
+  if (tokens > 0 && (!x || !y)) return CSA_ERR_NULL;
+  const uintptr_t size = dtype == CSA_FP32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) % size != 0 ||
+      reinterpret_cast<uintptr_t>(freqs) % 8 != 0 || reinterpret_cast<uintptr_t>(cu_rows) % 4 != 0 ||
+      (positions && reinterpret_cast<uintptr_t>(positions) % (position_bits / 8) != 0))
+    return CSA_ERR_ALIGN;
+  const bool same = x == y;
+  if (same && ((tokens > 1 && x_token_stride != y_token_stride) ||
+               (heads > 1 && x_head_stride != y_head_stride)))
+    return CSA_ERR_RANGE;
+  if (tokens == 0) return CSA_OK;
+  csa::RopeArgs a;
+  a.x = x;
+  a.y = y;
+  a.freqs = freqs;
+  a.positions = positions;
+  a.cu = cu_rows;
+  a.tokens = tokens;
+  a.xt = tokens > 1 ? x_token_stride : 0;  // the stride of a single element is never stepped
+  a.xh = heads > 1 ? x_head_stride : 0;
+  a.yt = tokens > 1 ? y_token_stride : 0;
+  a.yh = heads > 1 ? y_head_stride : 0;
+  a.position_bits = position_bits;
+  a.nseq = num_seqs;
+  a.ratio = ratio;
+  a.heads = heads;
+  a.d = head_dim;
+  a.rope = rope_dim;
+  a.offset = offset;
+  a.amplitude = amplitude;
+  a.transpose = transpose != 0;
+  a.in_place = same;
+  const cudaError_t e = dtype == CSA_BF16   ? csa::launch_rope_layout<csa::Bf16>(a, layout, stream)
+                        : dtype == CSA_FP16 ? csa::launch_rope_layout<__half>(a, layout, stream)
+                                            : csa::launch_rope_layout<float>(a, layout, stream);
+  return e == cudaSuccess ? CSA_OK : csa::record_cuda_error(e);
+}
