@@ -76,6 +76,9 @@ def rope(x: torch.Tensor, freqs: torch.Tensor, positions: Optional[torch.Tensor]
          transpose: bool = False) -> torch.Tensor:
     """Differentiable csa_rope (same arguments, no in-place form): the gradient
     with respect to x is the transposed turn of grad_out, in one launch.
-    freqs and positions are constants."""
+    freqs and positions are constants. As with every operator of torch, a
+    backward pass is captured into a CUDA graph only while no eager graph of
+    the same leaf tensors is alive (torch ties a leaf's accumulation node to
+    the stream it was made on and would make the capture wait for it)."""
     return RopeFunction.apply(x, freqs, positions, cu_seqlens_comp, ratio, offset, layout,
                               amplitude, transpose)
