@@ -54,6 +54,9 @@ extern "C" csa_status_t csa_cache_attend(const csa_cache_t* cache, const void* q
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.ws = nullptr;
-  const cudaError_t e = csa::launch_attend_rows(a, dtype == CSA_FP16, shared != 0, stream);
+  // Query rows of a sequence and cache head, on average over the sequences.
+  const bool wide = cache->head_dim >= 128 && num_tokens * a.group >= (int64_t)32 * num_seqs;
+  const cudaError_t e = wide ? csa::launch_attend_wide(a, dtype == CSA_FP16, shared != 0, stream)
+                             : csa::launch_attend_rows(a, dtype == CSA_FP16, shared != 0, stream);
   return e == cudaSuccess ? CSA_OK : csa::record_cuda_error(e);
 }

@@ -1,0 +1,783 @@
+// Attention over the 8-bit cache for many query rows of one cache head (large
+// groups of heads, chunks of a prompt): tcgen05.
+//
+// One CTA an SM works on a tile of R = 64 query rows and runs over the keys 128
+// at a time, transposed so that the accumulator's lanes are keys, then columns:
+//   S^T [128 keys x R] = K [128 x D] Q^T        (TMEM, two buffers)
+//   O^T [D x R] += V^T [D x 128] P^T            (TMEM, D / 128 tiles of 128 x R)
+// TMEM's 512 columns hold 2 R + R D / 128 of them. The rows are the N of both
+// products, so 64 heads fill the tensor core as well as 128 do.
+//
+// Roles: producer warps read the 8-bit rows into registers several panels
+// ahead, widen them to fp16 (exact) and store them to a ring of panels (128 keys
+// x 128 columns) in shared memory in the 128-byte swizzle; a panel is the
+// K-major operand of S^T and, unchanged, the M-major operand of O^T, so a row
+// that is key and value is stored once. One thread issues the matrix
+// instructions. Softmax warps own a key a thread: they read S^T from TMEM, form
+// the weights and store P^T [key][row], the N-major operand.
+//
+// Numerics as in csa_cache_attend_rows.cu: references m and m' that rise only
+// when passed, fp16 weights that carry the value scale. Where scales lie
+// within 2^30 and the references within 2^60 of one another, the weight is the
+// softmax term times two factors; beyond, it takes an exponential of its own.
+//
+// Every wait on an mbarrier is bounded: a wait that runs out marks the CTA,
+// whose later waits then return at once, and its results become NaN.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "csa_cache_attend.h"
+#include "csa_cache_join.cuh"
+#include "csa_cache_plan.cuh"
+#include "csa_device.cuh"
+#include "csa_e4m3.cuh"
+
+namespace csa {
+
+namespace {
+
+constexpr int kPolls = 1 << 20;
+
+__device__ __forceinline__ uint32_t smem_at(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded: after kPolls the CTA is marked dead and no further wait waits.
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int32_t* dead) {
+  if (mbar_try(bar, parity)) return;
+  for (int i = 0; i < kPolls; ++i) {
+    if (mbar_try(bar, parity)) return;
+    if (*dead) return;
+  }
+  *dead = 1;
+}
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void tc_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+#define CSA_R10(b) "%" #b "0, %" #b "1, %" #b "2, %" #b "3, %" #b "4, %" #b "5, %" #b "6, %" #b "7, %" #b "8, %" #b "9"
+__device__ __forceinline__ void tc_load32(uint32_t at, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, " CSA_R10(1) ", " CSA_R10(
+          2) ", %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_store32(uint32_t at, const float* v) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, " CSA_R10(1) ", " CSA_R10(
+          2) ", %30, %31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+      "r"(at)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+#undef CSA_R10
+// Whether any of the `threads` threads of barrier `id` says so.
+__device__ __forceinline__ bool barrier_any(int id, int threads, bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)mine), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void barrier_of(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// Shared-memory operand in the 128-byte swizzle: groups of 8 rows of 128 bytes,
+// 1024 bytes apart; `lead` bytes between 64-wide slabs of an M- or N-major one.
+__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead) {
+  return (uint64_t)((at >> 4) & 0x3FFF) | ((uint64_t)((lead >> 4) & 0x3FFF) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+template <int D, bool SHARED>
+struct Wide {
+  static constexpr int R = 64;                      // query rows of a tile
+  static constexpr int PP = D / 128;                // panels of 128 keys
+  static constexpr int SW = R / 8;                  // softmax warps: 4 for each 32 rows
+  static constexpr int PW = 4;                      // producer warps
+  static constexpr int THREADS = (SW + PW + 1) * 32;
+  static constexpr int NS = 4;                      // panels of the ring
+  static constexpr bool AHEAD = !SHARED || 2 * PP <= NS;  // S^T of the next keys before O^T of these
+  static constexpr int SLAB = 16384;                // 128 keys x 64 columns
+  static constexpr int PANEL = 2 * SLAB;
+  static constexpr int QSLAB = R * 128;
+  static constexpr int Q = R * D * 2;
+  static constexpr int P = R * 256;                 // [128 keys][R rows]: one 128-byte line a key
+  static_assert(R == 64, "a line of P^T holds 64 rows");
+  static constexpr int SMEM = NS * PANEL + Q + P + 1024;
+  static constexpr int KV = 1024 / (PW * 32);       // 16-byte vectors a thread and panel
+  static constexpr int DEPTH = 2;                   // panels in flight in registers
+  static constexpr int SLOT = R * (D + 4);
+  static constexpr uint32_t S0 = 0, O0 = 2 * R;     // TMEM columns
+  // fp32 accumulator, fp16 operands, N = R, M = 128; O^T has both transposed.
+  static constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(R >> 3) << 17) | (8u << 24);
+  static constexpr uint32_t IDESC_O = IDESC_S | (1u << 15) | (1u << 16);
+};
+
+// Largest over the warp of each of 32 values: lane i gets that of v[i].
+__device__ __forceinline__ float column_max(float* v, int lane) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float keep = lane & o ? v[j + o] : v[j], send = lane & o ? v[j] : v[j + o];
+      v[j] = fmaxf(keep, __shfl_xor_sync(0xFFFFFFFFu, send, o));
+    }
+  return v[0];
+}
+
+template <int D, bool SHARED, bool HALF>
+__global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
+    attend_wide_kernel(const AttendArgs a, const PlanShape plan) {
+  using C = Wide<D, SHARED>;
+  constexpr int R = C::R;
+  extern __shared__ uint8_t raw_smem[];
+  __shared__ int64_t sums[C::THREADS / 32 + 1];
+  __shared__ Place found;
+  __shared__ __align__(16) float zf[R], mref[R], mpref[R], rl[R], rf[R];  // see the softmax warps
+  __shared__ __align__(16) int32_t sees[R];
+  __shared__ float lscale[R], oscale[R], factor[R];
+  __shared__ float best[2][R / 32][4][32];
+  __shared__ int64_t row_at[R];
+  __shared__ int32_t sees_least, sees_most, far_refs, nan_rows, dead_flag, first_nan;
+  __shared__ uint32_t tmem_base;
+  __shared__ __align__(8) uint64_t bars[2 * C::NS + 6];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Place place = locate<C::THREADS>(a, plan, blockIdx.x, sums, &found);
+  if (place.pos < 0) return;
+  volatile int32_t* dead = &dead_flag;
+
+  const uint32_t ring = (smem_at(raw_smem) + 1023u) & ~1023u;
+  uint8_t* ring_ptr = raw_smem + (ring - smem_at(raw_smem));
+  const uint32_t q_at = ring + C::NS * C::PANEL, p_at = q_at + C::Q;
+  uint8_t* q_ptr = ring_ptr + C::NS * C::PANEL;
+  uint8_t* p_ptr = q_ptr + C::Q;
+  const uint32_t full = smem_at(bars), empty = full + 8 * C::NS, s_full = empty + 8 * C::NS,
+                 s_empty = s_full + 16, p_full = s_empty + 16, p_empty = p_full + 8;
+  if (threadIdx.x == 0) {
+    dead_flag = 0;
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(full + 8 * i, C::PW);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(s_empty + 8 * i, C::SW);
+    }
+    mbar_init(p_full, C::SW);
+    mbar_init(p_empty, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == C::SW + C::PW) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_at(&tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = tmem_base;
+  const int pb = a.c.page_bits, bb = a.c.block_bits;
+
+  uint32_t panels_done = 0, tiles_done = 0;  // over all items: ring slots and barrier phases
+  int s = place.s;
+  SeqWork work = seq_work(a, plan, s);
+  int64_t within = place.within;
+  for (int64_t pos = place.pos; pos < place.end;) {
+    if (within >= work.tiles * work.chunks * a.kv) {  // the next sequence with queries
+      ++s;
+      work = seq_work(a, plan, s);
+      within = 0;
+      continue;
+    }
+    const int64_t item = within / work.chunks;
+    const int64_t c0 = within - item * work.chunks;
+    const int h = (int)(item / work.tiles);
+    const int64_t tile_of_rows = item - h * work.tiles;
+    const int64_t c1 = min(work.chunks, c0 + (place.end - pos));
+
+    // ---- the rows: what they see, and Q as fp16 --------------------------------
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      sees_least = 0x7FFFFFFF;
+      sees_most = 0;
+      far_refs = 0;
+      nan_rows = 0;
+      first_nan = 0x7FFFFFFF;
+    }
+    __syncthreads();
+    for (int i = warp; i < R; i += C::THREADS / 32) {
+      const Row w = row_of(a, s, tile_of_rows, h, R, i);
+      constexpr int V = D / 256 > 0 ? D / 256 : 1;
+      float amax = 0.0f, v[V][8];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        const int col = (k * 32 + lane) * 8;
+        if (w.there && col < D)
+          x = __ldg(reinterpret_cast<const uint4*>(a.q + w.token * a.qt + w.head * a.qh + col));
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t bits = e & 1 ? u[e >> 1] >> 16 : u[e >> 1] & 0xFFFFu;
+          v[k][e] = HALF ? __half2float(__ushort_as_half((unsigned short)bits))
+                         : __uint_as_float(bits << 16);
+          const float m = fabsf(v[k][e]);
+          if (m < INFINITY) amax = fmaxf(amax, m);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+      const int lift = amax > 0.0f ? min(14 - ilogbf(amax), 126) : 0;
+      const float f = exp2i(max(lift, -126));
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int col = (k * 32 + lane) * 8;
+        if (col < D) {
+          uint4 x;
+          x.x = pack_f16x2(v[k][0] * f, v[k][1] * f);
+          x.y = pack_f16x2(v[k][2] * f, v[k][3] * f);
+          x.z = pack_f16x2(v[k][4] * f, v[k][5] * f);
+          x.w = pack_f16x2(v[k][6] * f, v[k][7] * f);
+          *reinterpret_cast<uint4*>(q_ptr + (col >> 6) * C::QSLAB + i * 128 +
+                                    ((((col >> 3) & 7) ^ (i & 7)) << 4)) = x;
+        }
+      }
+      if (lane == 0) {
+        zf[i] = ldexpf(a.scale, -lift);
+        mref[i] = mpref[i] = kNone;
+        rl[i] = kLift;
+        rf[i] = 128.0f;
+        int64_t n = w.there ? work.keys : 0;
+        if (w.there && a.visible) n = min(n, (int64_t)max(__ldg(a.visible + w.token), 0));
+        sees[i] = w.there ? (int)n : 0x7FFFFFFF;  // rows that are not there are not looked at
+        row_at[i] = w.there ? w.token * a.heads + w.head : -1;
+        if (w.there) {
+          atomicMin(&sees_least, (int)n);
+          atomicMax(&sees_most, (int)n);
+        }
+      }
+    }
+    fence_async();
+    __syncthreads();
+    const int least = sees_least, most = sees_most;
+    const int64_t stop = min(c1, ((int64_t)most + 127) / 128);
+    const int n = stop > c0 ? (int)(stop - c0) : 0;  // tiles of 128 keys
+    const int32_t* row_table = a.table + (int64_t)s * a.max_pages;
+
+    if (warp < C::SW) {
+      // ---- softmax -----------------------------------------------------------------
+      // A thread has key `mine` of each tile and 32 of the rows. For a row:
+      // z = S * (key scale * zf) in log2 units, t = z - mref; the weight is
+      // 2^(t + log2(value scale) + rl), rl = mref - mpref + 7, rf = 2^rl.
+      const int quarter = warp & 3, half = warp >> 2, mine = quarter * 32 + lane;
+      const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+      const int col = half * 32;
+      float l[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) l[c] = 0.0f;
+      auto page_at = [&](int i) -> int32_t {
+        const int64_t key = (c0 + i) * 128 + mine;
+        return i < n && key < most ? __ldg(row_table + (key >> pb)) : -1;
+      };
+      float sk_next = -1.0f, sv_next = 0.0f;
+      auto scales_at = [&](int i, int32_t page) {  // of this thread's key of tile i; -1: no row
+        sk_next = -1.0f;
+        sv_next = 1.0f;
+        if (page >= 0 && page < a.c.num_pages) {
+          const int slot = (int)(((c0 + i) * 128 + mine) & ((1 << pb) - 1));
+          const int64_t at = (int64_t)page * a.c.heads + h;
+          sk_next = __ldg(a.c.scales + (at << (pb - bb)) + (slot >> bb));
+          sv_next = SHARED ? sk_next : __ldg(a.c.scales + ((at + a.v_first) << (pb - bb)) + (slot >> bb));
+        }
+      };
+      scales_at(0, page_at(0));
+      int32_t page_next = page_at(1);
+      for (int i = 0; i < n; ++i) {
+        const uint32_t tc = tiles_done + i, b = tc & 1;
+        const float sk = sk_next;
+        const bool there = !(sk < 0.0f);
+        const float lv = there ? log2f(sv_next) : 0.0f;
+        const float kf = exp2f(lv);
+        scales_at(i + 1, page_next);
+        page_next = page_at(i + 2);
+        const int64_t key = (c0 + i) * 128 + mine;
+        const bool mixed = (c0 + i + 1) * 128 > least;
+        mbar_wait(s_full + 8 * b, (tc >> 1) & 1, dead);
+        tc_after();
+        bool o_free = false;  // O^T of the tile before is complete
+        const bool far_key = !(fabsf(lv) <= 30.0f);
+        {
+          const uint32_t s_at = tmem + lanes + C::S0 + b * R + col;
+          float t[32];
+          auto logits = [&](bool with_value) {  // z, or z + log2(value scale)
+            tc_load32(s_at, t);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float z = __fmul_rn(t[c], __fmul_rn(sk, zf[col + c]));
+              t[c] = with_value ? z + lv : z;
+              if (!there || key >= sees[col + c]) t[c] = -INFINITY;
+            }
+          };
+          for (int attempt = 0;; ++attempt) {
+            float mx = -INFINITY, mw = -INFINITY;
+            tc_load32(s_at, t);
+            const float2 sk2 = make_float2(sk, sk), lv2 = make_float2(lv, lv);
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const float4 z4 = *reinterpret_cast<const float4*>(zf + col + c);
+              const float4 m4 = *reinterpret_cast<const float4*>(mref + col + c);
+              const float4 r4 = *reinterpret_cast<const float4*>(rl + col + c);
+              const float2 ca = mul2_rn(make_float2(z4.x, z4.y), sk2);
+              const float2 cb = mul2_rn(make_float2(z4.z, z4.w), sk2);
+              float2 ta = sub2_rn(make_float2(__fmul_rn(t[c], ca.x), __fmul_rn(t[c + 1], ca.y)),
+                                  make_float2(m4.x, m4.y));
+              float2 tb = sub2_rn(make_float2(__fmul_rn(t[c + 2], cb.x), __fmul_rn(t[c + 3], cb.y)),
+                                  make_float2(m4.z, m4.w));
+              if (mixed) {
+                const int4 s4 = *reinterpret_cast<const int4*>(sees + col + c);
+                if (!there || key >= s4.x) ta.x = -INFINITY;
+                if (!there || key >= s4.y) ta.y = -INFINITY;
+                if (!there || key >= s4.z) tb.x = -INFINITY;
+                if (!there || key >= s4.w) tb.y = -INFINITY;
+              } else if (!there) {
+                ta = tb = make_float2(-INFINITY, -INFINITY);
+              }
+              const float2 wa = add2_rn(ta, add2_rn(make_float2(r4.x, r4.y), lv2));
+              const float2 wb = add2_rn(tb, add2_rn(make_float2(r4.z, r4.w), lv2));
+              mx = fmaxf(fmaxf(mx, ta.x), fmaxf(ta.y, fmaxf(tb.x, tb.y)));
+              mw = fmaxf(fmaxf(mw, wa.x), fmaxf(wa.y, fmaxf(wb.x, wb.y)));
+              t[c] = ta.x;
+              t[c + 1] = ta.y;
+              t[c + 2] = tb.x;
+              t[c + 3] = tb.y;
+            }
+            const bool up = mx > kSlackM || mw > kSlackW + kLift;
+            if (attempt || !barrier_any(1 + half, 128, up)) break;
+            // Some weight passes its reference: raise both to the tile's maxima.
+            logits(false);
+            best[0][half][quarter][lane] = column_max(t, lane);
+            logits(true);
+            best[1][half][quarter][lane] = column_max(t, lane);
+            if (!o_free && tc > 0) mbar_wait(p_empty, (tc - 1) & 1, dead);
+            o_free = true;
+            tc_after();
+            barrier_of(1 + half, 128);
+            if (quarter == 0) {
+              const int c = col + lane;
+              float x = mref[c], y = mpref[c];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                x = fmaxf(x, best[0][half][k][lane]);
+                y = fmaxf(y, best[1][half][k][lane]);
+              }
+              lscale[c] = exp2f(mref[c] - x);
+              oscale[c] = exp2f(mpref[c] - y);
+              mref[c] = x;
+              mpref[c] = y;
+              rl[c] = x - y + kLift;
+              rf[c] = exp2f(x - y + kLift);
+              if (!(fabsf(x - y) <= 60.0f)) far_refs = 1;
+            }
+            barrier_of(1 + half, 128);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) l[c] *= lscale[col + c];
+            if (i > 0) {
+              for (int pp = 0; pp < C::PP; ++pp) {
+                const uint32_t o_at = tmem + lanes + C::O0 + pp * R + col;
+                tc_load32(o_at, t);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) t[c] *= oscale[col + c];
+                tc_store32(o_at, t);
+              }
+            }
+          }
+          {  // S^T is read
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_empty + 8 * b);
+          }
+          const bool far = __any_sync(0xFFFFFFFFu, far_key) || *(volatile int32_t*)&far_refs;
+          uint32_t w[16];
+          if (!far) {
+            const float2 kf2 = make_float2(kf, kf);
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const float4 f4 = *reinterpret_cast<const float4*>(rf + col + c);
+              const float2 pa = make_float2(ex2_approx_ftz(t[c]), ex2_approx_ftz(t[c + 1]));
+              const float2 pb2 = make_float2(ex2_approx_ftz(t[c + 2]), ex2_approx_ftz(t[c + 3]));
+              float2* la = reinterpret_cast<float2*>(l + c);
+              la[0] = add2_rn(la[0], pa);
+              la[1] = add2_rn(la[1], pb2);
+              const float2 wa = mul2_rn(pa, mul2_rn(make_float2(f4.x, f4.y), kf2));
+              const float2 wb = mul2_rn(pb2, mul2_rn(make_float2(f4.z, f4.w), kf2));
+              w[c / 2] = pack_f16x2(wa.x, wa.y);
+              w[c / 2 + 1] = pack_f16x2(wb.x, wb.y);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              l[c] += ex2_approx_ftz(t[c]);
+              l[c + 1] += ex2_approx_ftz(t[c + 1]);
+              // -inf stays: log2 of a zero scale is -inf, of a huge one finite
+              w[c / 2] = pack_f16x2(ex2_approx_ftz(t[c] + (rl[col + c] + lv)),
+                                    ex2_approx_ftz(t[c + 1] + (rl[col + c + 1] + lv)));
+            }
+          }
+          if (!o_free) {  // P^T's old contents have been used
+            if (tc > 0) mbar_wait(p_empty, (tc - 1) & 1, dead);
+            o_free = true;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(p_ptr + mine * 128 + (((half * 4 + k) ^ (mine & 7)) << 4)) =
+                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        }
+        fence_async();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+      }
+      // ---- the item's result -------------------------------------------------------
+      if (n > 0) mbar_wait(p_empty, (tiles_done + n - 1) & 1, dead);
+      tc_after();
+      float* lsum = reinterpret_cast<float*>(ring_ptr);  // every operand has been used
+#pragma unroll
+      for (int c = 0; c < 32; c += 4)
+        *reinterpret_cast<float4*>(lsum + mine * R + col + c) =
+            make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
+      // NaN that the producers took out of rows that only some queries see: the
+      // first such row (for shared rows: of any column) decides who gets it.
+      const int64_t mixed0 = max(c0 * 128, (int64_t)(least / 128) * 128);
+      const int64_t mixed1 = min(stop * 128, (int64_t)most);
+      const bool nans = nan_rows != 0;
+      if (nans && SHARED)
+        for (int64_t key = mixed0 + threadIdx.x; key < mixed1; key += C::SW * 32) {
+          const int32_t page = __ldg(row_table + (key >> pb));
+          if (page < 0 || page >= a.c.num_pages) continue;
+          const uint8_t* p = a.c.data +
+                             ((((int64_t)page * a.c.heads + h) << pb) + (key & ((1 << pb) - 1))) * D;
+          uint32_t any = 0;
+          for (int k = 0; k < D; k += 4) any |= nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(p + k)));
+          if (any) atomicMin(&first_nan, (int)key);
+        }
+      barrier_of(3, C::SW * 32);
+      if (threadIdx.x < R) {
+        float x = 0.0f;
+        for (int k = 0; k < 128; ++k) x += lsum[k * R + threadIdx.x];
+        if ((SHARED && sees[threadIdx.x] > first_nan && row_at[threadIdx.x] >= 0) || *dead) x = NAN;
+        RowStats r = {mref[threadIdx.x], mpref[threadIdx.x], x};
+        factor[threadIdx.x] = out_factor(r);
+        if (c0 == 0 && c1 == work.chunks) {
+          if (a.lse && row_at[threadIdx.x] >= 0) a.lse[row_at[threadIdx.x]] = row_lse(r);
+        } else {
+          *reinterpret_cast<float4*>(a.ws + ((int64_t)blockIdx.x * 2 + (c0 == 0)) * C::SLOT + R * D +
+                                     threadIdx.x * 4) = make_float4(r.m, r.mp, r.l, 0.0f);
+        }
+      }
+      barrier_of(3, C::SW * 32);
+      for (int pp = 0; pp < C::PP; ++pp) {
+        const int d = pp * 128 + mine;
+        int bad = 0x7FFFFFFF;  // first row whose value in column d is NaN
+        if (nans && !SHARED)
+          for (int64_t key = mixed0; key < mixed1; ++key) {
+            const int32_t page = __ldg(row_table + (key >> pb));
+            if (page < 0 || page >= a.c.num_pages) continue;
+            const uint8_t byte = __ldg(
+                a.c.data +
+                ((((int64_t)page * a.c.heads + a.v_first + h) << pb) + (key & ((1 << pb) - 1))) * D + d);
+            if ((byte & 0x7F) == 0x7F) {
+              bad = (int)key;
+              break;
+            }
+          }
+        {
+          float v[32];
+          if (n > 0) {
+            tc_load32(tmem + lanes + C::O0 + pp * R + col, v);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = 0.0f;
+          }
+          if (bad != 0x7FFFFFFF) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (sees[col + c] > bad) v[c] = NAN;
+          }
+          if (c0 == 0 && c1 == work.chunks) {
+            // neighbouring lanes trade rows, so that each stores two columns
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float fa = factor[col + c], fb = factor[col + c + 1];
+              const float x = fa == 0.0f ? 0.0f : v[c] * fa, y = fb == 0.0f ? 0.0f : v[c + 1] * fb;
+              const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? x : y, 1);
+              const uint32_t o = lane & 1 ? (HALF ? pack_f16x2(other, y) : pack_bf16x2(other, y))
+                                          : (HALF ? pack_f16x2(x, other) : pack_bf16x2(x, other));
+              const int64_t at = row_at[col + c + (lane & 1)];
+              if (at >= 0) *reinterpret_cast<uint32_t*>(a.out + at * D + (d & ~1)) = o;
+            }
+          } else {  // slot 0: the item began with another worker, slot 1: it did here
+            float* ws = a.ws + ((int64_t)blockIdx.x * 2 + (c0 == 0)) * C::SLOT + d;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) ws[(col + c) * D] = v[c];
+          }
+        }
+      }
+      tc_before();
+    } else if (warp < C::SW + C::PW) {
+      // ---- producers ---------------------------------------------------------------
+      // A plane is one tile of keys or of values (or, shared, of both): PP panels.
+      // Planes come in the order in which the matrix instructions use them: K0, K1,
+      // V0, K2, V1, ... In a warp's load 4 keys x 8 chunks of 16 bytes; a store's
+      // quarter warp covers 2 keys x 4 chunks, which the swizzle spreads over all
+      // banks.
+      const int pw = warp - C::SW;
+      const int chunk = (lane & 3) | ((lane >> 1) & 4), kb = ((lane >> 2) & 1) | ((lane >> 3) & 2);
+      const int planes = SHARED ? n : 2 * n;
+      auto tile_of = [&](int q) {
+        if (SHARED) return q;
+        if (q == 2 * n - 1) return n - 1;
+        return q == 0 ? 0 : (q & 1) ? (q + 1) / 2 : q / 2 - 1;
+      };
+      auto is_value = [&](int q) { return !SHARED && q > 0 && (q == 2 * n - 1 || (q & 1) == 0); };
+      int32_t pages[C::KV];
+      auto look_up = [&](int q) {
+#pragma unroll
+        for (int k = 0; k < C::KV; ++k) {
+          const int64_t key = (c0 + (q < planes ? tile_of(q) : 0)) * 128 + (k * C::PW + pw) * 4 + kb;
+          pages[k] = q < planes && key < most ? __ldg(row_table + (key >> pb)) : -1;
+        }
+      };
+      uint4 buf[C::DEPTH][C::KV];
+      const uint8_t* src[C::KV];
+      int load_q = 0, load_pp = 0;
+      look_up(0);
+      auto load = [&](uint4* v) {  // the next panel of the sequence
+        if (load_q >= planes) return;
+        if (load_pp == 0) {
+          const int head = (is_value(load_q) ? a.v_first : 0) + h;
+#pragma unroll
+          for (int k = 0; k < C::KV; ++k) {
+            const int64_t key = (c0 + tile_of(load_q)) * 128 + (k * C::PW + pw) * 4 + kb;
+            src[k] = nullptr;
+            if (pages[k] >= 0 && pages[k] < a.c.num_pages)
+              src[k] = a.c.data +
+                       ((((int64_t)pages[k] * a.c.heads + head) << pb) + (key & ((1 << pb) - 1))) * D +
+                       chunk * 16;
+          }
+          look_up(load_q + 1);
+        }
+#pragma unroll
+        for (int k = 0; k < C::KV; ++k)
+          v[k] = src[k] ? ld_stream(reinterpret_cast<const uint16_t*>(src[k] + load_pp * 128))
+                        : make_uint4(0, 0, 0, 0);
+        if (++load_pp == C::PP) {
+          load_pp = 0;
+          ++load_q;
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < C::DEPTH; ++j) load(buf[j]);
+      const int total = planes * C::PP;
+      for (int p0 = 0; p0 < total; p0 += C::DEPTH) {
+#pragma unroll
+        for (int j = 0; j < C::DEPTH; ++j) {
+          const int p = p0 + j;
+          if (p < total) {
+            const uint32_t pc = panels_done + p, slot = pc % C::NS;
+            const int q = p / C::PP;
+            // Rows that only some queries see must not bring NaN into the product.
+            if ((SHARED || is_value(q)) && (c0 + tile_of(q) + 1) * 128 > least) {
+              uint32_t any = 0;
+#pragma unroll
+              for (int k = 0; k < C::KV; ++k) {
+                uint32_t* x = reinterpret_cast<uint32_t*>(&buf[j][k]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t bad = nan_bytes(x[e]);
+                  any |= bad;
+                  x[e] &= ~bad;
+                }
+              }
+              if (any) nan_rows = 1;
+            }
+            mbar_wait(empty + 8 * slot, ((pc / C::NS) & 1) ^ 1, dead);
+            uint8_t* panel = ring_ptr + slot * C::PANEL + (chunk >> 2) * C::SLAB;
+#pragma unroll
+            for (int k = 0; k < C::KV; ++k) {
+              const int key = (k * C::PW + pw) * 4 + kb;
+              const uint4 x = buf[j][k];
+              uint8_t* row = panel + key * 128;
+              const int c16 = (chunk & 3) * 2;
+              *reinterpret_cast<uint4*>(row + ((c16 ^ (key & 7)) << 4)) =
+                  make_uint4(lo_f16x2(x.x), hi_f16x2(x.x), lo_f16x2(x.y), hi_f16x2(x.y));
+              *reinterpret_cast<uint4*>(row + (((c16 + 1) ^ (key & 7)) << 4)) =
+                  make_uint4(lo_f16x2(x.z), hi_f16x2(x.z), lo_f16x2(x.w), hi_f16x2(x.w));
+            }
+            load(buf[j]);
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + 8 * slot);
+          }
+        }
+      }
+    } else {
+      // ---- matrix instructions -----------------------------------------------------
+      auto scores = [&](int i) {
+        const uint32_t tc = tiles_done + i, b = tc & 1;
+        const int q = SHARED ? i : i == 0 ? 0 : 2 * i - 1;
+        mbar_wait(s_empty + 8 * b, ((tc >> 1) & 1) ^ 1, dead);
+        tc_after();
+        for (int pp = 0; pp < C::PP; ++pp) {
+          const uint32_t pc = panels_done + q * C::PP + pp, slot = pc % C::NS;
+          mbar_wait(full + 8 * slot, (pc / C::NS) & 1, dead);
+          tc_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc_mma(tmem + C::S0 + b * R,
+                     operand(ring + slot * C::PANEL + (k >> 2) * C::SLAB + (k & 3) * 32, 16),
+                     operand(q_at + (pp * 2 + (k >> 2)) * C::QSLAB + (k & 3) * 32, 16), C::IDESC_S,
+                     pp > 0 || k > 0);
+            if (!SHARED) tc_commit(empty + 8 * slot);
+          }
+        }
+        if (lane == 0) tc_commit(s_full + 8 * b);
+        __syncwarp();
+      };
+      auto values = [&](int i) {
+        const uint32_t tc = tiles_done + i;
+        const int q = SHARED ? i : i == n - 1 ? 2 * n - 1 : 2 * i + 2;
+        mbar_wait(p_full, tc & 1, dead);
+        tc_after();
+        for (int pp = 0; pp < C::PP; ++pp) {
+          const uint32_t pc = panels_done + q * C::PP + pp, slot = pc % C::NS;
+          if (!SHARED) {
+            mbar_wait(full + 8 * slot, (pc / C::NS) & 1, dead);
+            tc_after();
+          }
+          if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc_mma(tmem + C::O0 + pp * R, operand(ring + slot * C::PANEL + k * 2048, C::SLAB),
+                     operand(p_at + k * 2048, 1024), C::IDESC_O, i > 0 || k > 0);
+            tc_commit(empty + 8 * slot);
+          }
+        }
+        if (lane == 0) tc_commit(p_empty);
+        __syncwarp();
+      };
+      if (C::AHEAD) {
+        if (n > 0) scores(0);
+        for (int i = 0; i < n; ++i) {
+          if (i + 1 < n) scores(i + 1);
+          values(i);
+        }
+      } else {
+        for (int i = 0; i < n; ++i) {
+          scores(i);
+          values(i);
+        }
+      }
+    }
+    panels_done += (SHARED ? 1 : 2) * n * C::PP;
+    tiles_done += n;
+    pos += c1 - c0;
+    within += c1 - c0;
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == C::SW + C::PW)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+template <int D, bool SHARED, bool HALF>
+cudaError_t launch_wide(AttendArgs a, cudaStream_t stream) {
+  using C = Wide<D, SHARED>;
+  PlanShape p;
+  p.rows = C::R;
+  p.keys = 128;
+  p.workers = 152;
+  p.least = 2;
+  auto* kernel = attend_wide_kernel<D, SHARED, HALF>;
+  cudaError_t e = allow_dynamic_smem((const void*)kernel, C::SMEM);
+  if (e != cudaSuccess) return e;
+  void* ws = nullptr;
+  e = workspace_take(&ws, sizeof(float) * (size_t)p.workers * 2 * C::SLOT, stream);
+  if (e != cudaSuccess) return e;
+  a.ws = static_cast<float*>(ws);
+  e = launch_dependent(kernel, dim3((unsigned)p.workers), dim3(C::THREADS), C::SMEM, stream, a, p);
+  if (e == cudaSuccess)
+    e = launch_dependent(attend_join_kernel<D, C::R, HALF>, dim3((unsigned)(p.workers - 1)),
+                         dim3(kThreads), 0, stream, a, p);
+  const cudaError_t ef = workspace_give(ws, stream);
+  return e != cudaSuccess ? e : ef;
+}
+
+template <int D>
+cudaError_t launch_dim(const AttendArgs& a, bool half, bool shared, cudaStream_t stream) {
+  if (shared) return half ? launch_wide<D, true, true>(a, stream) : launch_wide<D, true, false>(a, stream);
+  return half ? launch_wide<D, false, true>(a, stream) : launch_wide<D, false, false>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_wide(const AttendArgs& a, bool half, bool shared, cudaStream_t stream) {
+  switch (a.c.d) {
+    case 128: return launch_dim<128>(a, half, shared, stream);
+    case 256: return launch_dim<256>(a, half, shared, stream);
+    default: return launch_dim<512>(a, half, shared, stream);
+  }
+}
+
+}  // namespace csa
