@@ -118,7 +118,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
   uint8_t* ring = smem + warp * C::RING;
   const uint32_t ring_at = smem_addr(ring);
   const Place place = locate<kThreads>(a, plan, blockIdx.x, sums, &found);
-  if (place.pos < 0) return;
+  Shared* left = shared_items<C::ROWS, D>(a, plan.workers) + blockIdx.x;
+  if (place.pos < 0) {
+    if (threadIdx.x == 0) left->parts = 0;
+    return;
+  }
+  Shared tail = {0, 0, 0, 0};  // an item that begins here and ends with another worker
   const int pb = a.c.page_bits, bb = a.c.block_bits;
 
   int s = place.s;
@@ -136,6 +141,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
     const int h = (int)(item / work.tiles);
     const int64_t tile = item - h * work.tiles;
     const int64_t c1 = min(work.chunks, c0 + (place.end - pos));
+    if (c0 == 0 && c1 < work.chunks)
+      tail = {1 + (int32_t)((work.chunks - c1 + place.per - 1) / place.per), s, (int32_t)tile, h};
 
     // ---- the rows: what they see, and Q as fp16 --------------------------------
     __syncthreads();  // the last item is out of shared memory
@@ -550,27 +557,26 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
     pos += c1 - c0;
     within += c1 - c0;
   }
+  if (threadIdx.x == 0) *left = tail;
 }
 
 template <int D, bool SHARED, int NT, bool HALF>
 cudaError_t launch_tile(AttendArgs a, cudaStream_t stream) {
   using C = Shape<D, SHARED, NT>;
   PlanShape p;
-  p.rows = C::ROWS;
-  p.keys = C::KS;
+  p.row_bits = log2_of(C::ROWS);
+  p.key_bits = log2_of(C::KS);
   p.workers = 152 * C::PER_SM;
   p.least = 2 * C::GROUPS;
   auto* kernel = attend_rows_kernel<D, SHARED, NT, HALF>;
   cudaError_t e = allow_dynamic_smem((const void*)kernel, C::SMEM);
   if (e != cudaSuccess) return e;
   void* ws = nullptr;
-  e = workspace_take(&ws, sizeof(float) * (size_t)p.workers * 2 * C::SLOT, stream);
+  e = workspace_take(&ws, join_bytes<D, C::ROWS>(p.workers), stream);
   if (e != cudaSuccess) return e;
   a.ws = static_cast<float*>(ws);
   e = launch_dependent(kernel, dim3((unsigned)p.workers), dim3(kThreads), C::SMEM, stream, a, p);
-  if (e == cudaSuccess)
-    e = launch_dependent(attend_join_kernel<D, C::ROWS, HALF>, dim3((unsigned)(p.workers - 1)),
-                         dim3(kThreads), 0, stream, a, p);
+  if (e == cudaSuccess) e = launch_join<D, C::ROWS, HALF>(a, p.workers, stream);
   const cudaError_t ef = workspace_give(ws, stream);
   return e != cudaSuccess ? e : ef;
 }

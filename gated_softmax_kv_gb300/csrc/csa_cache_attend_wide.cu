@@ -135,13 +135,54 @@ __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// One item of work, as the roles read it.
+struct WideItem {
+  const uint8_t* data;
+  const float* scales;
+  const int32_t* row_table;  // the sequence's row of the page table
+  float* ws;                 // slot for a partial result
+  uint16_t* out;
+  float* lse;
+  int64_t c0;                // first tile of 128 keys
+  int32_t n;                 // tiles of 128 keys
+  int32_t least, most;       // rows that the queries see: fewest, most
+  int32_t key_head, value_head, heads, num_pages, page_bits, block_bits;
+  uint32_t panels_done, tiles_done;  // of earlier items: ring slots and barrier phases
+  bool whole;                // from the item's first key to its last
+};
+
+// Shared memory in front of the ring. The roles are functions of their own, so
+// that each has the registers to itself; they reach it through wide_smem.
+template <int R, int NS, int WARPS>
+struct WideState {
+  // read four at a time; see wide_softmax
+  alignas(16) float zf[R];
+  alignas(16) float mref[R];
+  alignas(16) float mpref[R];
+  alignas(16) float rl[R];
+  alignas(16) float rf[R];
+  alignas(16) int32_t sees[R];
+  alignas(16) int64_t sums[WARPS + 1];
+  int64_t row_at[R];
+  uint64_t bars[2 * NS + 6];
+  Place found;
+  WideItem item;
+  float lscale[R], oscale[R], factor[R];
+  float best[2][R / 32][4][32];
+  float part[R * 4];
+  int32_t place[4][2][8];                        // in KiB, see wide_produce
+  int32_t sees_least, sees_most, far_refs, nan_rows, dead, first_nan;
+  uint32_t tmem;
+};
+extern __shared__ __align__(1024) uint8_t wide_smem[];
+
 template <int D, bool SHARED>
 struct Wide {
   static constexpr int R = 64;                      // query rows of a tile
   static constexpr int PP = D / 128;                // panels of 128 keys
   static constexpr int SW = R / 8;                  // softmax warps: 4 for each 32 rows
   static constexpr int PW = 4;                      // producer warps
-  static constexpr int THREADS = (SW + PW + 1) * 32;
+  static constexpr int THREADS = (SW + PW) * 32;
   static constexpr int NS = 4;                      // panels of the ring
   static constexpr bool AHEAD = !SHARED || 2 * PP <= NS;  // S^T of the next keys before O^T of these
   static constexpr int SLAB = 16384;                // 128 keys x 64 columns
@@ -150,8 +191,11 @@ struct Wide {
   static constexpr int Q = R * D * 2;
   static constexpr int P = R * 256;                 // [128 keys][R rows]: one 128-byte line a key
   static_assert(R == 64, "a line of P^T holds 64 rows");
-  static constexpr int SMEM = NS * PANEL + Q + P + 1024;
-  static constexpr int KV = 1024 / (PW * 32);       // 16-byte vectors a thread and panel
+  using State = WideState<R, NS, THREADS / 32>;
+  static constexpr int HEAD = (int)(sizeof(State) + 1023) / 1024 * 1024;
+  static constexpr int SMEM = HEAD + NS * PANEL + Q + P + 1024;
+  static constexpr int KV = 8;                      // 16-byte vectors a thread and panel
+  static_assert(KV * PW * 32 == 1024, "a panel is 128 keys of 8 vectors");
   static constexpr int DEPTH = 2;                   // panels in flight in registers
   static constexpr int SLOT = R * (D + 4);
   static constexpr uint32_t S0 = 0, O0 = 2 * R;     // TMEM columns
@@ -159,6 +203,29 @@ struct Wide {
   static constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(R >> 3) << 17) | (8u << 24);
   static constexpr uint32_t IDESC_O = IDESC_S | (1u << 15) | (1u << 16);
 };
+
+// Where everything is, from the role's point of view.
+template <class C>
+struct Places {
+  uint32_t ring, q, p, full, empty, s_full, s_empty, p_full, p_empty;
+  uint8_t* ring_ptr;
+};
+template <class C>
+__device__ __forceinline__ Places<C> places() {
+  Places<C> x;
+  const uint32_t base = smem_at(wide_smem);
+  x.ring = (base + C::HEAD + 1023u) & ~1023u;
+  x.ring_ptr = wide_smem + (x.ring - base);
+  x.q = x.ring + C::NS * C::PANEL;
+  x.p = x.q + C::Q;
+  x.full = smem_at(reinterpret_cast<typename C::State*>(wide_smem)->bars);
+  x.empty = x.full + 8 * C::NS;
+  x.s_full = x.empty + 8 * C::NS;
+  x.s_empty = x.s_full + 16;
+  x.p_full = x.s_empty + 16;
+  x.p_empty = x.p_full + 8;
+  return x;
+}
 
 // Largest over the warp of each of 32 values: lane i gets that of v[i].
 __device__ __forceinline__ float column_max(float* v, int lane) {
@@ -172,63 +239,594 @@ __device__ __forceinline__ float column_max(float* v, int lane) {
   return v[0];
 }
 
+// Q's rows as fp16 in the K-major operand's layout, scaled row by row, and what
+// each row sees.
+template <int D, bool SHARED, bool HALF>
+__device__ __noinline__ void stage_queries(const AttendArgs& a, int s, int64_t tile, int h, int64_t keys) {
+  using C = Wide<D, SHARED>;
+  constexpr int R = C::R, WARPS = C::THREADS / 32, EACH = (R + WARPS - 1) / WARPS;
+  constexpr int V = D / 256 > 0 ? D / 256 : 1;
+  auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
+  uint8_t* q = places<C>().ring_ptr + C::NS * C::PANEL;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint4 x[EACH][V];
+  Row rows[EACH];
+  int32_t limit[EACH];
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {  // all loads first
+    const int i = warp + e * WARPS;
+    rows[e] = row_of(a, s, tile, h, R, i);
+    rows[e].there = rows[e].there && i < R;
+    limit[e] = rows[e].there && a.visible ? __ldg(a.visible + rows[e].token) : 0x7FFFFFFF;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int col = (k * 32 + lane) * 8;
+      x[e][k] = rows[e].there && col < D
+                    ? __ldg(reinterpret_cast<const uint4*>(a.q + rows[e].token * a.qt +
+                                                           rows[e].head * a.qh + col))
+                    : make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    const int i = warp + e * WARPS;
+    if (i >= R) break;
+    float amax = 0.0f, v[V][8];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const uint32_t u[4] = {x[e][k].x, x[e][k].y, x[e][k].z, x[e][k].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t bits = j & 1 ? u[j >> 1] >> 16 : u[j >> 1] & 0xFFFFu;
+        v[k][j] = HALF ? __half2float(__ushort_as_half((unsigned short)bits))
+                       : __uint_as_float(bits << 16);
+        const float m = fabsf(v[k][j]);
+        if (m < INFINITY) amax = fmaxf(amax, m);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    const int lift = amax > 0.0f ? min(14 - ilogbf(amax), 126) : 0;
+    const float f = exp2i(max(lift, -126));
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int col = (k * 32 + lane) * 8;
+      if (col < D) {
+        uint4 y;
+        y.x = pack_f16x2(v[k][0] * f, v[k][1] * f);
+        y.y = pack_f16x2(v[k][2] * f, v[k][3] * f);
+        y.z = pack_f16x2(v[k][4] * f, v[k][5] * f);
+        y.w = pack_f16x2(v[k][6] * f, v[k][7] * f);
+        *reinterpret_cast<uint4*>(q + (col >> 6) * C::QSLAB + i * 128 +
+                                  ((((col >> 3) & 7) ^ (i & 7)) << 4)) = y;
+      }
+    }
+    if (lane == 0) {
+      st.zf[i] = ldexpf(a.scale, -lift);
+      st.mref[i] = st.mpref[i] = kNone;
+      st.rl[i] = kLift;
+      st.rf[i] = 128.0f;
+      const int sees = (int)min(keys, (int64_t)max(limit[e], 0));
+      st.sees[i] = rows[e].there ? sees : 0x7FFFFFFF;  // rows that are not there are not looked at
+      st.row_at[i] = rows[e].there ? rows[e].token * a.heads + rows[e].head : -1;
+      if (rows[e].there) {
+        atomicMin(&st.sees_least, sees);
+        atomicMax(&st.sees_most, sees);
+      }
+    }
+  }
+}
+
+template <int D, bool SHARED>
+__device__ __noinline__ void wide_softmax() {
+  using C = Wide<D, SHARED>;
+  constexpr int R = C::R;
+  auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
+  const Places<C> at = places<C>();
+  const WideItem& item = st.item;
+  volatile int32_t* dead = &st.dead;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c0 = item.c0;
+  const int n = item.n;
+  // ---- softmax -----------------------------------------------------------------
+  // A thread has key `mine` of each tile and 32 of the rows. For a row:
+  // z = S * (key scale * st.zf) in log2 units, t = z - st.mref; the weight is
+  // 2^(t + log2(value scale) + st.rl), st.rl = st.mref - st.mpref + 7, st.rf = 2^st.rl.
+  const int quarter = warp & 3, half = warp >> 2, mine = quarter * 32 + lane;
+  const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+  const int col = half * 32;
+  uint8_t* p_line = at.ring_ptr + C::NS * C::PANEL + C::Q + mine * 128;
+  float l[32];
+#pragma unroll
+  for (int c = 0; c < 32; ++c) l[c] = 0.0f;
+  auto page_at = [&](int i) -> int32_t {
+    const int64_t key = (c0 + i) * 128 + mine;
+    return i < n && key < item.most ? __ldg(item.row_table + (key >> item.page_bits)) : -1;
+  };
+  float sk_next = -1.0f, sv_next = 0.0f;
+  auto scales_at = [&](int i, int32_t page) {  // of this thread's key of tile i; -1: no row
+    sk_next = -1.0f;
+    sv_next = 1.0f;
+    if (page >= 0 && page < item.num_pages) {
+      const int slot = (int)(((c0 + i) * 128 + mine) & ((1 << item.page_bits) - 1));
+      const int64_t first = (int64_t)page * item.heads;
+      const int bits = item.page_bits - item.block_bits;
+      const float* block = item.scales + (slot >> item.block_bits);
+      sk_next = __ldg(block + ((first + item.key_head) << bits));
+      sv_next = SHARED ? sk_next : __ldg(block + ((first + item.value_head) << bits));
+    }
+  };
+  scales_at(0, page_at(0));
+  int32_t page_next = page_at(1);
+  for (int i = 0; i < n; ++i) {
+    const uint32_t tc = item.tiles_done + i, b = tc & 1;
+    const float sk = sk_next;
+    const bool there = !(sk < 0.0f);
+    const float lv = there ? log2f(sv_next) : 0.0f;
+    const float kf = exp2f(lv);
+    scales_at(i + 1, page_next);
+    page_next = page_at(i + 2);
+    const int64_t key = (c0 + i) * 128 + mine;
+    const bool mixed = (c0 + i + 1) * 128 > item.least;
+    mbar_wait(at.s_full + 8 * b, (tc >> 1) & 1, dead);
+    tc_after();
+    bool o_free = false;  // O^T of the tile before is complete
+    const bool far_key = !(fabsf(lv) <= 30.0f);
+    {
+      const uint32_t s_at = st.tmem + lanes + C::S0 + b * R + col;
+      float t[32];
+      auto logits = [&](bool with_value) {  // z, or z + log2(value scale)
+        tc_load32(s_at, t);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float z = __fmul_rn(t[c], __fmul_rn(sk, st.zf[col + c]));
+          t[c] = with_value ? z + lv : z;
+          if (!there || key >= st.sees[col + c]) t[c] = -INFINITY;
+        }
+      };
+      for (int attempt = 0;; ++attempt) {
+        float mx = -INFINITY, mw = -INFINITY;
+        tc_load32(s_at, t);
+        const float2 sk2 = make_float2(sk, sk), lv2 = make_float2(lv, lv);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 z4 = *reinterpret_cast<const float4*>(st.zf + col + c);
+          const float4 m4 = *reinterpret_cast<const float4*>(st.mref + col + c);
+          const float4 r4 = *reinterpret_cast<const float4*>(st.rl + col + c);
+          const float2 ca = mul2_rn(make_float2(z4.x, z4.y), sk2);
+          const float2 cb = mul2_rn(make_float2(z4.z, z4.w), sk2);
+          float2 ta = sub2_rn(make_float2(__fmul_rn(t[c], ca.x), __fmul_rn(t[c + 1], ca.y)),
+                              make_float2(m4.x, m4.y));
+          float2 tb = sub2_rn(make_float2(__fmul_rn(t[c + 2], cb.x), __fmul_rn(t[c + 3], cb.y)),
+                              make_float2(m4.z, m4.w));
+          if (mixed) {
+            const int4 s4 = *reinterpret_cast<const int4*>(st.sees + col + c);
+            if (!there || key >= s4.x) ta.x = -INFINITY;
+            if (!there || key >= s4.y) ta.y = -INFINITY;
+            if (!there || key >= s4.z) tb.x = -INFINITY;
+            if (!there || key >= s4.w) tb.y = -INFINITY;
+          } else if (!there) {
+            ta = tb = make_float2(-INFINITY, -INFINITY);
+          }
+          const float2 wa = add2_rn(ta, add2_rn(make_float2(r4.x, r4.y), lv2));
+          const float2 wb = add2_rn(tb, add2_rn(make_float2(r4.z, r4.w), lv2));
+          mx = fmaxf(fmaxf(mx, ta.x), fmaxf(ta.y, fmaxf(tb.x, tb.y)));
+          mw = fmaxf(fmaxf(mw, wa.x), fmaxf(wa.y, fmaxf(wb.x, wb.y)));
+          t[c] = ta.x;
+          t[c + 1] = ta.y;
+          t[c + 2] = tb.x;
+          t[c + 3] = tb.y;
+        }
+        const bool up = mx > kSlackM || mw > kSlackW + kLift;
+        if (attempt || !barrier_any(1 + half, 128, up)) break;
+        // Some weight passes its reference: raise both to the tile's maxima.
+        logits(false);
+        st.best[0][half][quarter][lane] = column_max(t, lane);
+        logits(true);
+        st.best[1][half][quarter][lane] = column_max(t, lane);
+        if (!o_free && tc > 0) mbar_wait(at.p_empty, (tc - 1) & 1, dead);
+        o_free = true;
+        tc_after();
+        barrier_of(1 + half, 128);
+        if (quarter == 0) {
+          const int c = col + lane;
+          float x = st.mref[c], y = st.mpref[c];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x = fmaxf(x, st.best[0][half][k][lane]);
+            y = fmaxf(y, st.best[1][half][k][lane]);
+          }
+          st.lscale[c] = exp2f(st.mref[c] - x);
+          st.oscale[c] = exp2f(st.mpref[c] - y);
+          st.mref[c] = x;
+          st.mpref[c] = y;
+          st.rl[c] = x - y + kLift;
+          st.rf[c] = exp2f(x - y + kLift);
+          if (!(fabsf(x - y) <= 60.0f)) st.far_refs = 1;
+        }
+        barrier_of(1 + half, 128);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) l[c] *= st.lscale[col + c];
+        if (i > 0) {
+          for (int pp = 0; pp < C::PP; ++pp) {
+            const uint32_t o_at = st.tmem + lanes + C::O0 + pp * R + col;
+            tc_load32(o_at, t);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) t[c] *= st.oscale[col + c];
+            tc_store32(o_at, t);
+          }
+        }
+      }
+      {  // S^T is read
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(at.s_empty + 8 * b);
+      }
+      const bool far = __any_sync(0xFFFFFFFFu, far_key) || *(volatile int32_t*)&st.far_refs;
+      uint32_t w[16];
+      if (!far) {
+        const float2 kf2 = make_float2(kf, kf);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 f4 = *reinterpret_cast<const float4*>(st.rf + col + c);
+          const float2 pa = make_float2(ex2_approx_ftz(t[c]), ex2_approx_ftz(t[c + 1]));
+          const float2 pb2 = make_float2(ex2_approx_ftz(t[c + 2]), ex2_approx_ftz(t[c + 3]));
+          float2* la = reinterpret_cast<float2*>(l + c);
+          la[0] = add2_rn(la[0], pa);
+          la[1] = add2_rn(la[1], pb2);
+          const float2 wa = mul2_rn(pa, mul2_rn(make_float2(f4.x, f4.y), kf2));
+          const float2 wb = mul2_rn(pb2, mul2_rn(make_float2(f4.z, f4.w), kf2));
+          w[c / 2] = pack_f16x2(wa.x, wa.y);
+          w[c / 2 + 1] = pack_f16x2(wb.x, wb.y);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          l[c] += ex2_approx_ftz(t[c]);
+          l[c + 1] += ex2_approx_ftz(t[c + 1]);
+          // -inf stays: log2 of a zero scale is -inf, of a huge one finite
+          w[c / 2] = pack_f16x2(ex2_approx_ftz(t[c] + (st.rl[col + c] + lv)),
+                                ex2_approx_ftz(t[c + 1] + (st.rl[col + c + 1] + lv)));
+        }
+      }
+      if (!o_free) {  // P^T's old contents have been used
+        if (tc > 0) mbar_wait(at.p_empty, (tc - 1) & 1, dead);
+        o_free = true;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(p_line + (((half * 4 + k) ^ (mine & 7)) << 4)) =
+            make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+    fence_async();
+    tc_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(at.p_full);
+  }
+  // ---- the item's result -------------------------------------------------------
+  if (n > 0) mbar_wait(at.p_empty, (item.tiles_done + n - 1) & 1, dead);
+  tc_after();
+  float* lsum = reinterpret_cast<float*>(at.ring_ptr);  // every operand has been used
+#pragma unroll
+  for (int c = 0; c < 32; c += 4)
+    *reinterpret_cast<float4*>(lsum + mine * R + col + c) =
+        make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
+}
+
+// The item's result, by the softmax warps: the rows' sums, then O^T from TMEM.
+template <int D, bool SHARED, bool HALF>
+__device__ __noinline__ void wide_result() {
+  using C = Wide<D, SHARED>;
+  constexpr int R = C::R;
+  auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
+  const WideItem& item = st.item;
+  volatile int32_t* dead = &st.dead;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c0 = item.c0;
+  const int n = item.n;
+  const int quarter = warp & 3, half = warp >> 2, mine = quarter * 32 + lane;
+  const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+  const int col = half * 32;
+  const float* lsum = reinterpret_cast<const float*>(places<C>().ring_ptr);
+  // NaN that the producers took out of rows that only some queries see: the
+  // first such row (for shared rows: of any column) decides who gets it.
+  const int64_t mixed0 = max(c0 * 128, (int64_t)(item.least / 128) * 128);
+  const int64_t mixed1 = min((c0 + n) * 128, (int64_t)item.most);
+  const bool nans = st.nan_rows != 0;
+  if (nans && SHARED)
+    for (int64_t key = mixed0 + threadIdx.x; key < mixed1; key += C::SW * 32) {
+      const int32_t page = __ldg(item.row_table + (key >> item.page_bits));
+      if (page < 0 || page >= item.num_pages) continue;
+      const uint8_t* p = item.data +
+                         ((((int64_t)page * item.heads + item.key_head) << item.page_bits) + (key & ((1 << item.page_bits) - 1))) * D;
+      uint32_t any = 0;
+      for (int k = 0; k < D; k += 4) any |= nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(p + k)));
+      if (any) atomicMin(&st.first_nan, (int)key);
+    }
+  barrier_of(3, C::SW * 32);
+  constexpr int PARTS = C::SW * 32 / R;  // threads of a row's sum
+  float part = 0.0f;
+#pragma unroll 8
+  for (int k = 0; k < 128 / PARTS; ++k)
+    part += lsum[((threadIdx.x / R) * (128 / PARTS) + k) * R + threadIdx.x % R];
+  st.part[threadIdx.x] = part;
+  barrier_of(3, C::SW * 32);
+  if (threadIdx.x < R) {
+    float x = 0.0f;
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) x += st.part[k * R + threadIdx.x];
+    if ((SHARED && st.sees[threadIdx.x] > st.first_nan && st.row_at[threadIdx.x] >= 0) || *dead) x = NAN;
+    RowStats r = {st.mref[threadIdx.x], st.mpref[threadIdx.x], x};
+    st.factor[threadIdx.x] = out_factor(r);
+    if (item.whole) {
+      if (item.lse && st.row_at[threadIdx.x] >= 0) item.lse[st.row_at[threadIdx.x]] = row_lse(r);
+    } else {
+      *reinterpret_cast<float4*>(item.ws + R * D + threadIdx.x * 4) = make_float4(r.m, r.mp, r.l, 0.0f);
+    }
+  }
+  barrier_of(3, C::SW * 32);
+  for (int pp = 0; pp < C::PP; ++pp) {
+    const int d = pp * 128 + mine;
+    int bad = 0x7FFFFFFF;  // first row whose value in column d is NaN
+    if (nans && !SHARED)
+      for (int64_t key = mixed0; key < mixed1; ++key) {
+        const int32_t page = __ldg(item.row_table + (key >> item.page_bits));
+        if (page < 0 || page >= item.num_pages) continue;
+        const uint8_t byte = __ldg(
+            item.data +
+            ((((int64_t)page * item.heads + item.value_head) << item.page_bits) + (key & ((1 << item.page_bits) - 1))) * D + d);
+        if ((byte & 0x7F) == 0x7F) {
+          bad = (int)key;
+          break;
+        }
+      }
+    {
+      float v[32];
+      if (n > 0) {
+        tc_load32(st.tmem + lanes + C::O0 + pp * R + col, v);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = 0.0f;
+      }
+      if (bad != 0x7FFFFFFF) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (st.sees[col + c] > bad) v[c] = NAN;
+      }
+      if (item.whole) {
+        // neighbouring lanes trade rows, so that each stores two columns
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const float fa = st.factor[col + c], fb = st.factor[col + c + 1];
+          const float x = fa == 0.0f ? 0.0f : v[c] * fa, y = fb == 0.0f ? 0.0f : v[c + 1] * fb;
+          const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? x : y, 1);
+          const uint32_t o = lane & 1 ? (HALF ? pack_f16x2(other, y) : pack_bf16x2(other, y))
+                                      : (HALF ? pack_f16x2(x, other) : pack_bf16x2(x, other));
+          const int64_t at = st.row_at[col + c + (lane & 1)];
+          if (at >= 0) *reinterpret_cast<uint32_t*>(item.out + at * D + (d & ~1)) = o;
+        }
+      } else {  // slot 0: the item began with another worker, slot 1: it did here
+        float* ws = item.ws + d;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) ws[(col + c) * D] = v[c];
+      }
+    }
+  }
+  tc_before();
+}
+
+template <int D, bool SHARED>
+__device__ __noinline__ void wide_produce() {
+  using C = Wide<D, SHARED>;
+  constexpr int R = C::R;
+  auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
+  const Places<C> at = places<C>();
+  const WideItem& item = st.item;
+  volatile int32_t* dead = &st.dead;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c0 = item.c0;
+  const int n = item.n;
+  // ---- producers ---------------------------------------------------------------
+  // A plane is one tile of keys or of values (or, shared, of both): PP panels.
+  // Planes come in the order in which the matrix instructions use them: K0, K1,
+  // V0, K2, V1, ... In a warp's load 4 keys x 8 chunks of 16 bytes; a store's
+  // quarter warp covers 2 keys x 4 chunks, which the swizzle spreads over all
+  // banks.
+  const int pw = warp - C::SW;
+  const int chunk = (lane & 3) | ((lane >> 1) & 4), kb = ((lane >> 2) & 1) | ((lane >> 3) & 2);
+  const int planes = SHARED ? n : 2 * n;
+  auto tile_of = [&](int q) {
+    if (SHARED) return q;
+    if (q == 2 * n - 1) return n - 1;
+    return q == 0 ? 0 : (q & 1) ? (q + 1) / 2 : q / 2 - 1;
+  };
+  auto is_value = [&](int q) { return !SHARED && q > 0 && (q == 2 * n - 1 || (q & 1) == 0); };
+  // 16 keys in a row lie on one page: lane g < 8 looks after keys 16 g .. of the
+  // tile, and the warp finds their place in shared memory.
+  auto page_of = [&](int q) -> int32_t {
+    if (q >= planes || lane >= 8) return -1;
+    const int64_t key = (c0 + tile_of(q)) * 128 + lane * 16;
+    return key < item.most ? __ldg(item.row_table + (key >> item.page_bits)) : -1;
+  };
+  const int mine = (pw * 4 + kb) * D + chunk * 16;  // this thread's place among 16 keys
+  int32_t page = page_of(0);
+  uint4 buf[C::DEPTH][C::KV];
+  int load_q = 0, load_pp = 0, left = 0;
+  auto load = [&](uint4 (&v)[C::KV]) {  // the next panel of the sequence
+    if (load_q >= planes) return;
+    if (load_pp == 0) {
+      const int64_t key = (c0 + tile_of(load_q)) * 128;
+      if (lane < 8) {
+        const int head = is_value(load_q) ? item.value_head : item.key_head;
+        const int slot = (int)((key + lane * 16) & ((1 << item.page_bits) - 1));
+        st.place[pw][load_q & 1][lane] =
+            page >= 0 && page < item.num_pages
+                ? (int32_t)((((((int64_t)page * item.heads + head) << item.page_bits) + slot) * D) >> 10)
+                : -1;
+      }
+      page = page_of(load_q + 1);
+      left = (int)min((int64_t)128, (int64_t)item.most - key);  // keys that some row sees
+      __syncwarp();
+    }
+    const uint8_t* data = item.data + mine + load_pp * 128;
+#pragma unroll
+    for (int k = 0; k < C::KV; ++k) {
+      const int32_t kib = st.place[pw][load_q & 1][k];
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (kib >= 0 && k * 16 + pw * 4 + kb < left)
+        v[k] = ld_stream(reinterpret_cast<const uint16_t*>(data + ((int64_t)kib << 10)));
+    }
+    if (++load_pp == C::PP) {
+      load_pp = 0;
+      ++load_q;
+    }
+  };
+  auto value_panel = [&](int tile, int pp, uint32_t slot) {  // O^T's columns of one panel
+    if (lane == 0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        tc_mma(st.tmem + C::O0 + pp * R, operand(at.ring + slot * C::PANEL + k * 2048, C::SLAB),
+               operand(at.p + k * 2048, 1024), C::IDESC_O, tile > 0 || k > 0);
+      tc_commit(at.empty + 8 * slot);
+    }
+  };
+  auto values = [&](int tile) {  // O^T from panels that are there already
+    const uint32_t tc = item.tiles_done + tile;
+    mbar_wait(at.p_full, tc & 1, dead);
+    tc_after();
+    for (int pp = 0; pp < C::PP; ++pp)
+      value_panel(tile, pp, (item.panels_done + tile * C::PP + pp) % C::NS);
+    if (lane == 0) tc_commit(at.p_empty);
+    __syncwarp();
+  };
+#pragma unroll
+  for (int j = 0; j < C::DEPTH; ++j) load(buf[j]);
+  const int total = planes * C::PP;
+  for (int p0 = 0; p0 < total; p0 += C::DEPTH) {
+#pragma unroll
+    for (int j = 0; j < C::DEPTH; ++j) {
+      const int p = p0 + j;
+      if (p >= total) break;
+      const uint32_t pc = item.panels_done + p, slot = pc % C::NS;
+      const int q = p / C::PP;
+      // Rows that only some queries see must not bring NaN into the product.
+      if ((SHARED || is_value(q)) && (c0 + tile_of(q) + 1) * 128 > item.least) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int k = 0; k < C::KV; ++k) {
+          uint32_t bad = nan_bytes(buf[j][k].x);
+          any |= bad;
+          buf[j][k].x &= ~bad;
+          bad = nan_bytes(buf[j][k].y);
+          any |= bad;
+          buf[j][k].y &= ~bad;
+          bad = nan_bytes(buf[j][k].z);
+          any |= bad;
+          buf[j][k].z &= ~bad;
+          bad = nan_bytes(buf[j][k].w);
+          any |= bad;
+          buf[j][k].w &= ~bad;
+        }
+        if (any) st.nan_rows = 1;
+      }
+      mbar_wait(at.empty + 8 * slot, ((pc / C::NS) & 1) ^ 1, dead);
+      uint8_t* panel = at.ring_ptr + slot * C::PANEL + (chunk >> 2) * C::SLAB + (pw * 4 + kb) * 128;
+      const int swap = (pw * 4 + kb) & 7, c16 = (chunk & 3) * 2;
+#pragma unroll
+      for (int k = 0; k < C::KV; ++k) {
+        const uint4 x = buf[j][k];
+        uint8_t* row = panel + k * 2048;
+        *reinterpret_cast<uint4*>(row + ((c16 ^ swap) << 4)) =
+            make_uint4(lo_f16x2(x.x), hi_f16x2(x.x), lo_f16x2(x.y), hi_f16x2(x.y));
+        *reinterpret_cast<uint4*>(row + (((c16 + 1) ^ swap) << 4)) =
+            make_uint4(lo_f16x2(x.z), hi_f16x2(x.z), lo_f16x2(x.w), hi_f16x2(x.w));
+      }
+      load(buf[j]);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(at.full + 8 * slot);
+      if (pw == 0) {  // the matrix instructions that this panel makes possible
+        const int tile = tile_of(q), pp = p % C::PP;
+        if (SHARED || !is_value(q)) {
+          const uint32_t tc = item.tiles_done + tile, b = tc & 1;
+          if (pp == 0) mbar_wait(at.s_empty + 8 * b, ((tc >> 1) & 1) ^ 1, dead);
+          mbar_wait(at.full + 8 * slot, (pc / C::NS) & 1, dead);
+          tc_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc_mma(st.tmem + C::S0 + b * R,
+                     operand(at.ring + slot * C::PANEL + (k >> 2) * C::SLAB + (k & 3) * 32, 16),
+                     operand(at.q + (pp * 2 + (k >> 2)) * C::QSLAB + (k & 3) * 32, 16), C::IDESC_S,
+                     pp > 0 || k > 0);
+            if (!SHARED) tc_commit(at.empty + 8 * slot);
+            if (pp == C::PP - 1) tc_commit(at.s_full + 8 * b);
+          }
+          __syncwarp();
+          if (SHARED && pp == C::PP - 1) {
+            if (!C::AHEAD) {
+              values(tile);
+            } else {
+              if (tile > 0) values(tile - 1);
+              if (tile == n - 1) values(tile);
+            }
+          }
+        } else {
+          const uint32_t tc = item.tiles_done + tile;
+          if (pp == 0) mbar_wait(at.p_full, tc & 1, dead);
+          mbar_wait(at.full + 8 * slot, (pc / C::NS) & 1, dead);
+          tc_after();
+          value_panel(tile, pp, slot);
+          if (lane == 0 && pp == C::PP - 1) tc_commit(at.p_empty);
+          __syncwarp();
+        }
+      }
+    }
+  }
+}
+
+
 template <int D, bool SHARED, bool HALF>
 __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
     attend_wide_kernel(const AttendArgs a, const PlanShape plan) {
   using C = Wide<D, SHARED>;
-  constexpr int R = C::R;
-  extern __shared__ uint8_t raw_smem[];
-  __shared__ int64_t sums[C::THREADS / 32 + 1];
-  __shared__ Place found;
-  __shared__ __align__(16) float zf[R], mref[R], mpref[R], rl[R], rf[R];  // see the softmax warps
-  __shared__ __align__(16) int32_t sees[R];
-  __shared__ float lscale[R], oscale[R], factor[R];
-  __shared__ float best[2][R / 32][4][32];
-  __shared__ int64_t row_at[R];
-  __shared__ int32_t sees_least, sees_most, far_refs, nan_rows, dead_flag, first_nan;
-  __shared__ uint32_t tmem_base;
-  __shared__ __align__(8) uint64_t bars[2 * C::NS + 6];
+  auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
   grid_dependency_wait();
   allow_dependent_launch();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Place place = locate<C::THREADS>(a, plan, blockIdx.x, sums, &found);
-  if (place.pos < 0) return;
-  volatile int32_t* dead = &dead_flag;
-
-  const uint32_t ring = (smem_at(raw_smem) + 1023u) & ~1023u;
-  uint8_t* ring_ptr = raw_smem + (ring - smem_at(raw_smem));
-  const uint32_t q_at = ring + C::NS * C::PANEL, p_at = q_at + C::Q;
-  uint8_t* q_ptr = ring_ptr + C::NS * C::PANEL;
-  uint8_t* p_ptr = q_ptr + C::Q;
-  const uint32_t full = smem_at(bars), empty = full + 8 * C::NS, s_full = empty + 8 * C::NS,
-                 s_empty = s_full + 16, p_full = s_empty + 16, p_empty = p_full + 8;
+  const int warp = threadIdx.x >> 5;
+  const Place place = locate<C::THREADS>(a, plan, blockIdx.x, st.sums, &st.found);
+  Shared* left = shared_items<C::R, D>(a, plan.workers) + blockIdx.x;
+  if (place.pos < 0) {
+    if (threadIdx.x == 0) left->parts = 0;
+    return;
+  }
+  Shared tail = {0, 0, 0, 0};  // an item that begins here and ends with another worker
+  const Places<C> at = places<C>();
   if (threadIdx.x == 0) {
-    dead_flag = 0;
+    st.dead = 0;
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(full + 8 * i, C::PW);
-      mbar_init(empty + 8 * i, 1);
+      mbar_init(at.full + 8 * i, C::PW);
+      mbar_init(at.empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + 8 * i, 1);
-      mbar_init(s_empty + 8 * i, C::SW);
+      mbar_init(at.s_full + 8 * i, 1);
+      mbar_init(at.s_empty + 8 * i, C::SW);
     }
-    mbar_init(p_full, C::SW);
-    mbar_init(p_empty, 1);
+    mbar_init(at.p_full, C::SW);
+    mbar_init(at.p_empty, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == C::SW + C::PW) {
+  if (warp == C::SW) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     smem_at(&tmem_base))
+                     smem_at(&st.tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = tmem_base;
-  const int pb = a.c.page_bits, bb = a.c.block_bits;
 
-  uint32_t panels_done = 0, tiles_done = 0;  // over all items: ring slots and barrier phases
+  uint32_t panels_done = 0, tiles_done = 0;
   int s = place.s;
   SeqWork work = seq_work(a, plan, s);
   int64_t within = place.within;
@@ -244,522 +842,83 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
     const int h = (int)(item / work.tiles);
     const int64_t tile_of_rows = item - h * work.tiles;
     const int64_t c1 = min(work.chunks, c0 + (place.end - pos));
+    if (c0 == 0 && c1 < work.chunks)
+      tail = {1 + (int32_t)((work.chunks - c1 + place.per - 1) / place.per), s, (int32_t)tile_of_rows, h};
 
     // ---- the rows: what they see, and Q as fp16 --------------------------------
-    __syncthreads();
     if (threadIdx.x == 0) {
-      sees_least = 0x7FFFFFFF;
-      sees_most = 0;
-      far_refs = 0;
-      nan_rows = 0;
-      first_nan = 0x7FFFFFFF;
+      st.sees_least = 0x7FFFFFFF;
+      st.sees_most = 0;
+      st.far_refs = 0;
+      st.nan_rows = 0;
+      st.first_nan = 0x7FFFFFFF;
     }
     __syncthreads();
-    for (int i = warp; i < R; i += C::THREADS / 32) {
-      const Row w = row_of(a, s, tile_of_rows, h, R, i);
-      constexpr int V = D / 256 > 0 ? D / 256 : 1;
-      float amax = 0.0f, v[V][8];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        const int col = (k * 32 + lane) * 8;
-        if (w.there && col < D)
-          x = __ldg(reinterpret_cast<const uint4*>(a.q + w.token * a.qt + w.head * a.qh + col));
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t bits = e & 1 ? u[e >> 1] >> 16 : u[e >> 1] & 0xFFFFu;
-          v[k][e] = HALF ? __half2float(__ushort_as_half((unsigned short)bits))
-                         : __uint_as_float(bits << 16);
-          const float m = fabsf(v[k][e]);
-          if (m < INFINITY) amax = fmaxf(amax, m);
-        }
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-      const int lift = amax > 0.0f ? min(14 - ilogbf(amax), 126) : 0;
-      const float f = exp2i(max(lift, -126));
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int col = (k * 32 + lane) * 8;
-        if (col < D) {
-          uint4 x;
-          x.x = pack_f16x2(v[k][0] * f, v[k][1] * f);
-          x.y = pack_f16x2(v[k][2] * f, v[k][3] * f);
-          x.z = pack_f16x2(v[k][4] * f, v[k][5] * f);
-          x.w = pack_f16x2(v[k][6] * f, v[k][7] * f);
-          *reinterpret_cast<uint4*>(q_ptr + (col >> 6) * C::QSLAB + i * 128 +
-                                    ((((col >> 3) & 7) ^ (i & 7)) << 4)) = x;
-        }
-      }
-      if (lane == 0) {
-        zf[i] = ldexpf(a.scale, -lift);
-        mref[i] = mpref[i] = kNone;
-        rl[i] = kLift;
-        rf[i] = 128.0f;
-        int64_t n = w.there ? work.keys : 0;
-        if (w.there && a.visible) n = min(n, (int64_t)max(__ldg(a.visible + w.token), 0));
-        sees[i] = w.there ? (int)n : 0x7FFFFFFF;  // rows that are not there are not looked at
-        row_at[i] = w.there ? w.token * a.heads + w.head : -1;
-        if (w.there) {
-          atomicMin(&sees_least, (int)n);
-          atomicMax(&sees_most, (int)n);
-        }
-      }
-    }
+    stage_queries<D, SHARED, HALF>(a, s, tile_of_rows, h, work.keys);
     fence_async();
     __syncthreads();
-    const int least = sees_least, most = sees_most;
-    const int64_t stop = min(c1, ((int64_t)most + 127) / 128);
+    const int64_t stop = min(c1, ((int64_t)st.sees_most + 127) / 128);
     const int n = stop > c0 ? (int)(stop - c0) : 0;  // tiles of 128 keys
-    const int32_t* row_table = a.table + (int64_t)s * a.max_pages;
-
-    if (warp < C::SW) {
-      // ---- softmax -----------------------------------------------------------------
-      // A thread has key `mine` of each tile and 32 of the rows. For a row:
-      // z = S * (key scale * zf) in log2 units, t = z - mref; the weight is
-      // 2^(t + log2(value scale) + rl), rl = mref - mpref + 7, rf = 2^rl.
-      const int quarter = warp & 3, half = warp >> 2, mine = quarter * 32 + lane;
-      const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-      const int col = half * 32;
-      float l[32];
-#pragma unroll
-      for (int c = 0; c < 32; ++c) l[c] = 0.0f;
-      auto page_at = [&](int i) -> int32_t {
-        const int64_t key = (c0 + i) * 128 + mine;
-        return i < n && key < most ? __ldg(row_table + (key >> pb)) : -1;
-      };
-      float sk_next = -1.0f, sv_next = 0.0f;
-      auto scales_at = [&](int i, int32_t page) {  // of this thread's key of tile i; -1: no row
-        sk_next = -1.0f;
-        sv_next = 1.0f;
-        if (page >= 0 && page < a.c.num_pages) {
-          const int slot = (int)(((c0 + i) * 128 + mine) & ((1 << pb) - 1));
-          const int64_t at = (int64_t)page * a.c.heads + h;
-          sk_next = __ldg(a.c.scales + (at << (pb - bb)) + (slot >> bb));
-          sv_next = SHARED ? sk_next : __ldg(a.c.scales + ((at + a.v_first) << (pb - bb)) + (slot >> bb));
-        }
-      };
-      scales_at(0, page_at(0));
-      int32_t page_next = page_at(1);
-      for (int i = 0; i < n; ++i) {
-        const uint32_t tc = tiles_done + i, b = tc & 1;
-        const float sk = sk_next;
-        const bool there = !(sk < 0.0f);
-        const float lv = there ? log2f(sv_next) : 0.0f;
-        const float kf = exp2f(lv);
-        scales_at(i + 1, page_next);
-        page_next = page_at(i + 2);
-        const int64_t key = (c0 + i) * 128 + mine;
-        const bool mixed = (c0 + i + 1) * 128 > least;
-        mbar_wait(s_full + 8 * b, (tc >> 1) & 1, dead);
-        tc_after();
-        bool o_free = false;  // O^T of the tile before is complete
-        const bool far_key = !(fabsf(lv) <= 30.0f);
-        {
-          const uint32_t s_at = tmem + lanes + C::S0 + b * R + col;
-          float t[32];
-          auto logits = [&](bool with_value) {  // z, or z + log2(value scale)
-            tc_load32(s_at, t);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float z = __fmul_rn(t[c], __fmul_rn(sk, zf[col + c]));
-              t[c] = with_value ? z + lv : z;
-              if (!there || key >= sees[col + c]) t[c] = -INFINITY;
-            }
-          };
-          for (int attempt = 0;; ++attempt) {
-            float mx = -INFINITY, mw = -INFINITY;
-            tc_load32(s_at, t);
-            const float2 sk2 = make_float2(sk, sk), lv2 = make_float2(lv, lv);
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              const float4 z4 = *reinterpret_cast<const float4*>(zf + col + c);
-              const float4 m4 = *reinterpret_cast<const float4*>(mref + col + c);
-              const float4 r4 = *reinterpret_cast<const float4*>(rl + col + c);
-              const float2 ca = mul2_rn(make_float2(z4.x, z4.y), sk2);
-              const float2 cb = mul2_rn(make_float2(z4.z, z4.w), sk2);
-              float2 ta = sub2_rn(make_float2(__fmul_rn(t[c], ca.x), __fmul_rn(t[c + 1], ca.y)),
-                                  make_float2(m4.x, m4.y));
-              float2 tb = sub2_rn(make_float2(__fmul_rn(t[c + 2], cb.x), __fmul_rn(t[c + 3], cb.y)),
-                                  make_float2(m4.z, m4.w));
-              if (mixed) {
-                const int4 s4 = *reinterpret_cast<const int4*>(sees + col + c);
-                if (!there || key >= s4.x) ta.x = -INFINITY;
-                if (!there || key >= s4.y) ta.y = -INFINITY;
-                if (!there || key >= s4.z) tb.x = -INFINITY;
-                if (!there || key >= s4.w) tb.y = -INFINITY;
-              } else if (!there) {
-                ta = tb = make_float2(-INFINITY, -INFINITY);
-              }
-              const float2 wa = add2_rn(ta, add2_rn(make_float2(r4.x, r4.y), lv2));
-              const float2 wb = add2_rn(tb, add2_rn(make_float2(r4.z, r4.w), lv2));
-              mx = fmaxf(fmaxf(mx, ta.x), fmaxf(ta.y, fmaxf(tb.x, tb.y)));
-              mw = fmaxf(fmaxf(mw, wa.x), fmaxf(wa.y, fmaxf(wb.x, wb.y)));
-              t[c] = ta.x;
-              t[c + 1] = ta.y;
-              t[c + 2] = tb.x;
-              t[c + 3] = tb.y;
-            }
-            const bool up = mx > kSlackM || mw > kSlackW + kLift;
-            if (attempt || !barrier_any(1 + half, 128, up)) break;
-            // Some weight passes its reference: raise both to the tile's maxima.
-            logits(false);
-            best[0][half][quarter][lane] = column_max(t, lane);
-            logits(true);
-            best[1][half][quarter][lane] = column_max(t, lane);
-            if (!o_free && tc > 0) mbar_wait(p_empty, (tc - 1) & 1, dead);
-            o_free = true;
-            tc_after();
-            barrier_of(1 + half, 128);
-            if (quarter == 0) {
-              const int c = col + lane;
-              float x = mref[c], y = mpref[c];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                x = fmaxf(x, best[0][half][k][lane]);
-                y = fmaxf(y, best[1][half][k][lane]);
-              }
-              lscale[c] = exp2f(mref[c] - x);
-              oscale[c] = exp2f(mpref[c] - y);
-              mref[c] = x;
-              mpref[c] = y;
-              rl[c] = x - y + kLift;
-              rf[c] = exp2f(x - y + kLift);
-              if (!(fabsf(x - y) <= 60.0f)) far_refs = 1;
-            }
-            barrier_of(1 + half, 128);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) l[c] *= lscale[col + c];
-            if (i > 0) {
-              for (int pp = 0; pp < C::PP; ++pp) {
-                const uint32_t o_at = tmem + lanes + C::O0 + pp * R + col;
-                tc_load32(o_at, t);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) t[c] *= oscale[col + c];
-                tc_store32(o_at, t);
-              }
-            }
-          }
-          {  // S^T is read
-            tc_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s_empty + 8 * b);
-          }
-          const bool far = __any_sync(0xFFFFFFFFu, far_key) || *(volatile int32_t*)&far_refs;
-          uint32_t w[16];
-          if (!far) {
-            const float2 kf2 = make_float2(kf, kf);
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              const float4 f4 = *reinterpret_cast<const float4*>(rf + col + c);
-              const float2 pa = make_float2(ex2_approx_ftz(t[c]), ex2_approx_ftz(t[c + 1]));
-              const float2 pb2 = make_float2(ex2_approx_ftz(t[c + 2]), ex2_approx_ftz(t[c + 3]));
-              float2* la = reinterpret_cast<float2*>(l + c);
-              la[0] = add2_rn(la[0], pa);
-              la[1] = add2_rn(la[1], pb2);
-              const float2 wa = mul2_rn(pa, mul2_rn(make_float2(f4.x, f4.y), kf2));
-              const float2 wb = mul2_rn(pb2, mul2_rn(make_float2(f4.z, f4.w), kf2));
-              w[c / 2] = pack_f16x2(wa.x, wa.y);
-              w[c / 2 + 1] = pack_f16x2(wb.x, wb.y);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              l[c] += ex2_approx_ftz(t[c]);
-              l[c + 1] += ex2_approx_ftz(t[c + 1]);
-              // -inf stays: log2 of a zero scale is -inf, of a huge one finite
-              w[c / 2] = pack_f16x2(ex2_approx_ftz(t[c] + (rl[col + c] + lv)),
-                                    ex2_approx_ftz(t[c + 1] + (rl[col + c + 1] + lv)));
-            }
-          }
-          if (!o_free) {  // P^T's old contents have been used
-            if (tc > 0) mbar_wait(p_empty, (tc - 1) & 1, dead);
-            o_free = true;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(p_ptr + mine * 128 + (((half * 4 + k) ^ (mine & 7)) << 4)) =
-                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-        }
-        fence_async();
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
-      }
-      // ---- the item's result -------------------------------------------------------
-      if (n > 0) mbar_wait(p_empty, (tiles_done + n - 1) & 1, dead);
-      tc_after();
-      float* lsum = reinterpret_cast<float*>(ring_ptr);  // every operand has been used
-#pragma unroll
-      for (int c = 0; c < 32; c += 4)
-        *reinterpret_cast<float4*>(lsum + mine * R + col + c) =
-            make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
-      // NaN that the producers took out of rows that only some queries see: the
-      // first such row (for shared rows: of any column) decides who gets it.
-      const int64_t mixed0 = max(c0 * 128, (int64_t)(least / 128) * 128);
-      const int64_t mixed1 = min(stop * 128, (int64_t)most);
-      const bool nans = nan_rows != 0;
-      if (nans && SHARED)
-        for (int64_t key = mixed0 + threadIdx.x; key < mixed1; key += C::SW * 32) {
-          const int32_t page = __ldg(row_table + (key >> pb));
-          if (page < 0 || page >= a.c.num_pages) continue;
-          const uint8_t* p = a.c.data +
-                             ((((int64_t)page * a.c.heads + h) << pb) + (key & ((1 << pb) - 1))) * D;
-          uint32_t any = 0;
-          for (int k = 0; k < D; k += 4) any |= nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(p + k)));
-          if (any) atomicMin(&first_nan, (int)key);
-        }
-      barrier_of(3, C::SW * 32);
-      if (threadIdx.x < R) {
-        float x = 0.0f;
-        for (int k = 0; k < 128; ++k) x += lsum[k * R + threadIdx.x];
-        if ((SHARED && sees[threadIdx.x] > first_nan && row_at[threadIdx.x] >= 0) || *dead) x = NAN;
-        RowStats r = {mref[threadIdx.x], mpref[threadIdx.x], x};
-        factor[threadIdx.x] = out_factor(r);
-        if (c0 == 0 && c1 == work.chunks) {
-          if (a.lse && row_at[threadIdx.x] >= 0) a.lse[row_at[threadIdx.x]] = row_lse(r);
-        } else {
-          *reinterpret_cast<float4*>(a.ws + ((int64_t)blockIdx.x * 2 + (c0 == 0)) * C::SLOT + R * D +
-                                     threadIdx.x * 4) = make_float4(r.m, r.mp, r.l, 0.0f);
-        }
-      }
-      barrier_of(3, C::SW * 32);
-      for (int pp = 0; pp < C::PP; ++pp) {
-        const int d = pp * 128 + mine;
-        int bad = 0x7FFFFFFF;  // first row whose value in column d is NaN
-        if (nans && !SHARED)
-          for (int64_t key = mixed0; key < mixed1; ++key) {
-            const int32_t page = __ldg(row_table + (key >> pb));
-            if (page < 0 || page >= a.c.num_pages) continue;
-            const uint8_t byte = __ldg(
-                a.c.data +
-                ((((int64_t)page * a.c.heads + a.v_first + h) << pb) + (key & ((1 << pb) - 1))) * D + d);
-            if ((byte & 0x7F) == 0x7F) {
-              bad = (int)key;
-              break;
-            }
-          }
-        {
-          float v[32];
-          if (n > 0) {
-            tc_load32(tmem + lanes + C::O0 + pp * R + col, v);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = 0.0f;
-          }
-          if (bad != 0x7FFFFFFF) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (sees[col + c] > bad) v[c] = NAN;
-          }
-          if (c0 == 0 && c1 == work.chunks) {
-            // neighbouring lanes trade rows, so that each stores two columns
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float fa = factor[col + c], fb = factor[col + c + 1];
-              const float x = fa == 0.0f ? 0.0f : v[c] * fa, y = fb == 0.0f ? 0.0f : v[c + 1] * fb;
-              const float other = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? x : y, 1);
-              const uint32_t o = lane & 1 ? (HALF ? pack_f16x2(other, y) : pack_bf16x2(other, y))
-                                          : (HALF ? pack_f16x2(x, other) : pack_bf16x2(x, other));
-              const int64_t at = row_at[col + c + (lane & 1)];
-              if (at >= 0) *reinterpret_cast<uint32_t*>(a.out + at * D + (d & ~1)) = o;
-            }
-          } else {  // slot 0: the item began with another worker, slot 1: it did here
-            float* ws = a.ws + ((int64_t)blockIdx.x * 2 + (c0 == 0)) * C::SLOT + d;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) ws[(col + c) * D] = v[c];
-          }
-        }
-      }
-      tc_before();
-    } else if (warp < C::SW + C::PW) {
-      // ---- producers ---------------------------------------------------------------
-      // A plane is one tile of keys or of values (or, shared, of both): PP panels.
-      // Planes come in the order in which the matrix instructions use them: K0, K1,
-      // V0, K2, V1, ... In a warp's load 4 keys x 8 chunks of 16 bytes; a store's
-      // quarter warp covers 2 keys x 4 chunks, which the swizzle spreads over all
-      // banks.
-      const int pw = warp - C::SW;
-      const int chunk = (lane & 3) | ((lane >> 1) & 4), kb = ((lane >> 2) & 1) | ((lane >> 3) & 2);
-      const int planes = SHARED ? n : 2 * n;
-      auto tile_of = [&](int q) {
-        if (SHARED) return q;
-        if (q == 2 * n - 1) return n - 1;
-        return q == 0 ? 0 : (q & 1) ? (q + 1) / 2 : q / 2 - 1;
-      };
-      auto is_value = [&](int q) { return !SHARED && q > 0 && (q == 2 * n - 1 || (q & 1) == 0); };
-      int32_t pages[C::KV];
-      auto look_up = [&](int q) {
-#pragma unroll
-        for (int k = 0; k < C::KV; ++k) {
-          const int64_t key = (c0 + (q < planes ? tile_of(q) : 0)) * 128 + (k * C::PW + pw) * 4 + kb;
-          pages[k] = q < planes && key < most ? __ldg(row_table + (key >> pb)) : -1;
-        }
-      };
-      uint4 buf[C::DEPTH][C::KV];
-      const uint8_t* src[C::KV];
-      int load_q = 0, load_pp = 0;
-      look_up(0);
-      auto load = [&](uint4* v) {  // the next panel of the sequence
-        if (load_q >= planes) return;
-        if (load_pp == 0) {
-          const int head = (is_value(load_q) ? a.v_first : 0) + h;
-#pragma unroll
-          for (int k = 0; k < C::KV; ++k) {
-            const int64_t key = (c0 + tile_of(load_q)) * 128 + (k * C::PW + pw) * 4 + kb;
-            src[k] = nullptr;
-            if (pages[k] >= 0 && pages[k] < a.c.num_pages)
-              src[k] = a.c.data +
-                       ((((int64_t)pages[k] * a.c.heads + head) << pb) + (key & ((1 << pb) - 1))) * D +
-                       chunk * 16;
-          }
-          look_up(load_q + 1);
-        }
-#pragma unroll
-        for (int k = 0; k < C::KV; ++k)
-          v[k] = src[k] ? ld_stream(reinterpret_cast<const uint16_t*>(src[k] + load_pp * 128))
-                        : make_uint4(0, 0, 0, 0);
-        if (++load_pp == C::PP) {
-          load_pp = 0;
-          ++load_q;
-        }
-      };
-#pragma unroll
-      for (int j = 0; j < C::DEPTH; ++j) load(buf[j]);
-      const int total = planes * C::PP;
-      for (int p0 = 0; p0 < total; p0 += C::DEPTH) {
-#pragma unroll
-        for (int j = 0; j < C::DEPTH; ++j) {
-          const int p = p0 + j;
-          if (p < total) {
-            const uint32_t pc = panels_done + p, slot = pc % C::NS;
-            const int q = p / C::PP;
-            // Rows that only some queries see must not bring NaN into the product.
-            if ((SHARED || is_value(q)) && (c0 + tile_of(q) + 1) * 128 > least) {
-              uint32_t any = 0;
-#pragma unroll
-              for (int k = 0; k < C::KV; ++k) {
-                uint32_t* x = reinterpret_cast<uint32_t*>(&buf[j][k]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t bad = nan_bytes(x[e]);
-                  any |= bad;
-                  x[e] &= ~bad;
-                }
-              }
-              if (any) nan_rows = 1;
-            }
-            mbar_wait(empty + 8 * slot, ((pc / C::NS) & 1) ^ 1, dead);
-            uint8_t* panel = ring_ptr + slot * C::PANEL + (chunk >> 2) * C::SLAB;
-#pragma unroll
-            for (int k = 0; k < C::KV; ++k) {
-              const int key = (k * C::PW + pw) * 4 + kb;
-              const uint4 x = buf[j][k];
-              uint8_t* row = panel + key * 128;
-              const int c16 = (chunk & 3) * 2;
-              *reinterpret_cast<uint4*>(row + ((c16 ^ (key & 7)) << 4)) =
-                  make_uint4(lo_f16x2(x.x), hi_f16x2(x.x), lo_f16x2(x.y), hi_f16x2(x.y));
-              *reinterpret_cast<uint4*>(row + (((c16 + 1) ^ (key & 7)) << 4)) =
-                  make_uint4(lo_f16x2(x.z), hi_f16x2(x.z), lo_f16x2(x.w), hi_f16x2(x.w));
-            }
-            load(buf[j]);
-            fence_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full + 8 * slot);
-          }
-        }
-      }
-    } else {
-      // ---- matrix instructions -----------------------------------------------------
-      auto scores = [&](int i) {
-        const uint32_t tc = tiles_done + i, b = tc & 1;
-        const int q = SHARED ? i : i == 0 ? 0 : 2 * i - 1;
-        mbar_wait(s_empty + 8 * b, ((tc >> 1) & 1) ^ 1, dead);
-        tc_after();
-        for (int pp = 0; pp < C::PP; ++pp) {
-          const uint32_t pc = panels_done + q * C::PP + pp, slot = pc % C::NS;
-          mbar_wait(full + 8 * slot, (pc / C::NS) & 1, dead);
-          tc_after();
-          if (lane == 0) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma(tmem + C::S0 + b * R,
-                     operand(ring + slot * C::PANEL + (k >> 2) * C::SLAB + (k & 3) * 32, 16),
-                     operand(q_at + (pp * 2 + (k >> 2)) * C::QSLAB + (k & 3) * 32, 16), C::IDESC_S,
-                     pp > 0 || k > 0);
-            if (!SHARED) tc_commit(empty + 8 * slot);
-          }
-        }
-        if (lane == 0) tc_commit(s_full + 8 * b);
-        __syncwarp();
-      };
-      auto values = [&](int i) {
-        const uint32_t tc = tiles_done + i;
-        const int q = SHARED ? i : i == n - 1 ? 2 * n - 1 : 2 * i + 2;
-        mbar_wait(p_full, tc & 1, dead);
-        tc_after();
-        for (int pp = 0; pp < C::PP; ++pp) {
-          const uint32_t pc = panels_done + q * C::PP + pp, slot = pc % C::NS;
-          if (!SHARED) {
-            mbar_wait(full + 8 * slot, (pc / C::NS) & 1, dead);
-            tc_after();
-          }
-          if (lane == 0) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma(tmem + C::O0 + pp * R, operand(ring + slot * C::PANEL + k * 2048, C::SLAB),
-                     operand(p_at + k * 2048, 1024), C::IDESC_O, i > 0 || k > 0);
-            tc_commit(empty + 8 * slot);
-          }
-        }
-        if (lane == 0) tc_commit(p_empty);
-        __syncwarp();
-      };
-      if (C::AHEAD) {
-        if (n > 0) scores(0);
-        for (int i = 0; i < n; ++i) {
-          if (i + 1 < n) scores(i + 1);
-          values(i);
-        }
-      } else {
-        for (int i = 0; i < n; ++i) {
-          scores(i);
-          values(i);
-        }
-      }
+    if (threadIdx.x == 0) {
+      WideItem& it = st.item;
+      it.data = a.c.data;
+      it.scales = a.c.scales;
+      it.row_table = a.table + (int64_t)s * a.max_pages;
+      it.ws = a.ws + ((int64_t)blockIdx.x * 2 + (c0 == 0)) * C::SLOT;
+      it.out = a.out;
+      it.lse = a.lse;
+      it.c0 = c0;
+      it.n = n;
+      it.least = st.sees_least;
+      it.most = st.sees_most;
+      it.key_head = h;
+      it.value_head = a.v_first + h;
+      it.heads = a.c.heads;
+      it.num_pages = a.c.num_pages;
+      it.page_bits = a.c.page_bits;
+      it.block_bits = a.c.block_bits;
+      it.panels_done = panels_done;
+      it.tiles_done = tiles_done;
+      it.whole = c0 == 0 && c1 == work.chunks;
     }
+    __syncthreads();
+    if (warp < C::SW) {
+      wide_softmax<D, SHARED>();
+      wide_result<D, SHARED, HALF>();
+    } else {
+      wide_produce<D, SHARED>();
+    }
+    __syncthreads();
     panels_done += (SHARED ? 1 : 2) * n * C::PP;
     tiles_done += n;
     pos += c1 - c0;
     within += c1 - c0;
   }
+  if (threadIdx.x == 0) *left = tail;
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == C::SW + C::PW)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (warp == C::SW)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(st.tmem) : "memory");
 }
 
 template <int D, bool SHARED, bool HALF>
 cudaError_t launch_wide(AttendArgs a, cudaStream_t stream) {
   using C = Wide<D, SHARED>;
   PlanShape p;
-  p.rows = C::R;
-  p.keys = 128;
+  p.row_bits = log2_of(C::R);
+  p.key_bits = 7;
   p.workers = 152;
   p.least = 2;
   auto* kernel = attend_wide_kernel<D, SHARED, HALF>;
   cudaError_t e = allow_dynamic_smem((const void*)kernel, C::SMEM);
   if (e != cudaSuccess) return e;
   void* ws = nullptr;
-  e = workspace_take(&ws, sizeof(float) * (size_t)p.workers * 2 * C::SLOT, stream);
+  e = workspace_take(&ws, join_bytes<D, C::R>(p.workers), stream);
   if (e != cudaSuccess) return e;
   a.ws = static_cast<float*>(ws);
   e = launch_dependent(kernel, dim3((unsigned)p.workers), dim3(C::THREADS), C::SMEM, stream, a, p);
-  if (e == cudaSuccess)
-    e = launch_dependent(attend_join_kernel<D, C::R, HALF>, dim3((unsigned)(p.workers - 1)),
-                         dim3(kThreads), 0, stream, a, p);
+  if (e == cudaSuccess) e = launch_join<D, C::R, HALF>(a, p.workers, stream);
   const cudaError_t ef = workspace_give(ws, stream);
   return e != cudaSuccess ? e : ef;
 }

@@ -117,30 +117,118 @@ __device__ __forceinline__ void write_row(const AttendArgs& a, const Row& w, int
   if (c == 0 && a.lse) a.lse[at] = row_lse(r);
 }
 
-// One CTA for each stretch's end: the first one inside an item joins it.
+// Items that several workers share are listed in the workspace behind the
+// workers' slots (two each): the worker that an item begins with leaves the
+// number of workers (0: its last item was finished) and where the item lies.
+struct Shared {
+  int32_t parts, s, tile, h;
+};
+template <int ROWS, int D>
+__device__ __forceinline__ Shared* shared_items(const AttendArgs& a, int workers) {
+  return reinterpret_cast<Shared*>(a.ws + (int64_t)workers * 2 * ROWS * (D + 4));
+}
+
+// Joins the shared items, 64 vectors of four columns a CTA at a time: every
+// CTA reads the list, and all pieces of all items are spread over the grid.
+// Four threads take a quarter of the parts each (a long sequence alone on the
+// GPU has 152 parts), in the parts' order, and are added up in order.
 template <int D, int ROWS, bool HALF>
-__global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a, const PlanShape plan) {
-  __shared__ int64_t sums[kThreads / 32 + 1];
-  __shared__ Place found;
+__global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a, int workers) {
+  constexpr int SLOT = ROWS * (D + 4), PIECES = ROWS * D / 256;
+  __shared__ int32_t list[512], count;
+  __shared__ float4 sum[4][64];
+  __shared__ float4 stat[4][64];
   grid_dependency_wait();
   allow_dependent_launch();
-  const int64_t w = (int64_t)blockIdx.x + 1;
-  const Place place = locate<kThreads>(a, plan, w, sums, &found);
-  if (place.pos < 0) return;
-  const SeqWork work = seq_work(a, plan, place.s);
-  const int64_t item = place.within / work.chunks;
-  const int64_t c0 = place.within - item * work.chunks;
-  if (c0 == 0 || c0 > place.per) return;  // between items, or an earlier end is inside this one
-  const int h = (int)(item / work.tiles);
-  const int64_t tile = item - h * work.tiles;
-  const int n = 1 + (int)((work.chunks - c0 + place.per - 1) / place.per);
-  constexpr int SLOT = ROWS * (D + 4);
-  const float* ws = a.ws;
-  join<D, ROWS, HALF>(
-      n, [&](int i) { return ws + ((w - 1 + i) * 2 + (i == 0)) * SLOT; },
-      [&](int row, int c, const RowStats& r, float4 v) {
-        write_row<D, HALF>(a, row_of(a, place.s, tile, h, ROWS, row), c, r, v);
-      });
+  const Shared* items = shared_items<ROWS, D>(a, workers);
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) {  // the list in the workers' order
+    int n = 0;
+    for (int w = lane; w < ((workers + 31) & ~31); w += 32) {
+      const bool some = w < workers && items[w].parts > 0;
+      const unsigned who = __ballot_sync(0xFFFFFFFFu, some);
+      if (some) list[n + __popc(who & ((1u << lane) - 1))] = w;
+      n += __popc(who);
+    }
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  const int v = threadIdx.x & 63, quarter = threadIdx.x >> 6;
+  for (int u = blockIdx.x; u < count * PIECES; u += gridDim.x) {
+    const int w = list[u / PIECES];
+    const Shared item = items[w];
+    const int at = (u % PIECES) * 256 + v * 4, row = at / D, c = at % D;
+    const int each = (item.parts + 3) / 4, i0 = quarter * each, i1 = min(i0 + each, item.parts);
+    const float* ws = a.ws;
+    auto part = [&](int i) { return ws + ((int64_t)(w + i) * 2 + (i == 0)) * SLOT; };
+    RowStats r = {kNone, kNone, 0.0f};
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = i0; i < i1; i += 8) {  // eight parts' loads at a time
+      float4 st[8], x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float* p = part(min(i + k, i1 - 1));
+        st[k] = __ldg(reinterpret_cast<const float4*>(p + ROWS * D + row * 4));
+        x[k] = __ldg(reinterpret_cast<const float4*>(p + at));
+      }
+      float m = r.m, mp = r.mp;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (i + k >= i1) {
+          st[k] = make_float4(kNone, kNone, 0.0f, 0.0f);
+          x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        m = fmaxf(m, st[k].x);
+        mp = fmaxf(mp, st[k].y);
+      }
+      r.l *= exp2f(r.m - m);
+      float f = exp2f(r.mp - mp);
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        r.l += st[k].z * exp2f(st[k].x - m);
+        f = exp2f(st[k].y - mp);
+        o.x = fmaf(x[k].x, f, o.x);
+        o.y = fmaf(x[k].y, f, o.y);
+        o.z = fmaf(x[k].z, f, o.z);
+        o.w = fmaf(x[k].w, f, o.w);
+      }
+      r.m = m;
+      r.mp = mp;
+    }
+    __syncthreads();
+    sum[quarter][v] = o;
+    stat[quarter][v] = make_float4(r.m, r.mp, r.l, 0.0f);
+    __syncthreads();
+    if (quarter == 0) {
+      for (int k = 1; k < 4; ++k) {
+        const float4 st = stat[k][v], x = sum[k][v];
+        const float m = fmaxf(r.m, st.x), mp = fmaxf(r.mp, st.y);
+        r.l = r.l * exp2f(r.m - m) + st.z * exp2f(st.x - m);
+        const float f0 = exp2f(r.mp - mp), f1 = exp2f(st.y - mp);
+        o.x = o.x * f0 + x.x * f1;
+        o.y = o.y * f0 + x.y * f1;
+        o.z = o.z * f0 + x.z * f1;
+        o.w = o.w * f0 + x.w * f1;
+        r.m = m;
+        r.mp = mp;
+      }
+      write_row<D, HALF>(a, row_of(a, item.s, item.tile, item.h, ROWS, row), c, r, o);
+    }
+  }
+}
+
+// The joining kernel behind a main kernel of `workers` CTAs.
+template <int D, int ROWS, bool HALF>
+cudaError_t launch_join(const AttendArgs& a, int workers, cudaStream_t stream) {
+  return launch_dependent(attend_join_kernel<D, ROWS, HALF>, dim3(152 * 4), dim3(kThreads), 0, stream, a,
+                          workers);
+}
+
+// Workspace of a main kernel of `workers` CTAs.
+template <int D, int ROWS>
+size_t join_bytes(int workers) {
+  return (size_t)workers * (2 * ROWS * (D + 4) * sizeof(float) + sizeof(Shared));
 }
 
 }  // namespace

@@ -14,10 +14,10 @@
 namespace csa {
 
 struct PlanShape {
-  int32_t rows;    // query rows of a tile
-  int32_t keys;    // keys of a chunk
+  int32_t row_bits;  // log2 of the query rows of a tile
+  int32_t key_bits;  // log2 of the keys of a chunk
   int32_t workers;
-  int32_t least;   // fewest chunks a worker takes
+  int32_t least;     // fewest chunks a worker takes
 };
 
 struct SeqWork {
@@ -32,8 +32,8 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, const PlanShape
   const int64_t most = (int64_t)a.max_pages << a.c.page_bits;
   if (w.keys > most) w.keys = most;
   if (w.keys < 0) w.keys = 0;
-  w.tiles = nq > 0 ? (nq * a.group + p.rows - 1) / p.rows : 0;
-  w.chunks = w.keys > p.keys ? (w.keys + p.keys - 1) / p.keys : 1;
+  w.tiles = nq > 0 ? (nq * a.group + (1 << p.row_bits) - 1) >> p.row_bits : 0;
+  w.chunks = w.keys > 0 ? (w.keys + (1 << p.key_bits) - 1) >> p.key_bits : 1;
   return w;
 }
 
