@@ -163,14 +163,13 @@ struct WideState {
   alignas(16) float rf[R];
   alignas(16) int32_t sees[R];
   alignas(16) int64_t sums[WARPS + 1];
-  int64_t row_at[R];
+  int64_t row_at[R], q_at[R];
   uint64_t bars[2 * NS + 6];
   Place found;
   WideItem item;
   float lscale[R], oscale[R], factor[R];
   float best[2][R / 32][4][32];
   float part[R * 4];
-  int32_t place[4][2][8];                        // in KiB, see wide_produce
   int32_t sees_least, sees_most, far_refs, nan_rows, dead, first_nan;
   uint32_t tmem;
 };
@@ -239,38 +238,55 @@ __device__ __forceinline__ float column_max(float* v, int lane) {
   return v[0];
 }
 
-// Q's rows as fp16 in the K-major operand's layout, scaled row by row, and what
-// each row sees.
-template <int D, bool SHARED, bool HALF>
-__device__ __noinline__ void stage_queries(const AttendArgs& a, int s, int64_t tile, int h, int64_t keys) {
+// Which rows the tile has, what each sees, where it is written: a thread a row.
+template <int D, bool SHARED>
+__device__ __forceinline__ void stage_rows(const AttendArgs& a, int s, int64_t tile, int h, int64_t keys) {
   using C = Wide<D, SHARED>;
-  constexpr int R = C::R, WARPS = C::THREADS / 32, EACH = (R + WARPS - 1) / WARPS;
+  auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
+  const int i = threadIdx.x;
+  if (i >= C::R) return;
+  const Row w = row_of(a, s, tile, h, C::R, i);
+  int32_t limit = 0x7FFFFFFF;
+  if (w.there && a.visible) limit = __ldg(a.visible + w.token);
+  const int sees = (int)min(keys, (int64_t)max(limit, 0));
+  st.sees[i] = w.there ? sees : 0x7FFFFFFF;  // rows that are not there are not looked at
+  st.row_at[i] = w.there ? w.token * a.heads + w.head : -1;
+  st.q_at[i] = w.there ? w.token * a.qt + w.head * a.qh : -1;
+  st.mref[i] = st.mpref[i] = kNone;
+  st.rl[i] = kLift;
+  st.rf[i] = 128.0f;
+  const int lo = __reduce_min_sync(0xFFFFFFFFu, w.there ? sees : 0x7FFFFFFF);
+  const int hi = __reduce_max_sync(0xFFFFFFFFu, w.there ? sees : 0);
+  if ((i & 31) == 0) {
+    atomicMin(&st.sees_least, lo);
+    atomicMax(&st.sees_most, hi);
+  }
+}
+
+// Q's rows as fp16 in the K-major operand's layout, scaled row by row, by the
+// softmax warps.
+template <int D, bool SHARED, bool HALF>
+__device__ __forceinline__ void stage_queries(const uint16_t* q, float scale) {
+  using C = Wide<D, SHARED>;
+  constexpr int R = C::R, EACH = R / C::SW;
   constexpr int V = D / 256 > 0 ? D / 256 : 1;
   auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
-  uint8_t* q = places<C>().ring_ptr + C::NS * C::PANEL;
+  uint8_t* to = places<C>().ring_ptr + C::NS * C::PANEL;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint4 x[EACH][V];
-  Row rows[EACH];
-  int32_t limit[EACH];
 #pragma unroll
   for (int e = 0; e < EACH; ++e) {  // all loads first
-    const int i = warp + e * WARPS;
-    rows[e] = row_of(a, s, tile, h, R, i);
-    rows[e].there = rows[e].there && i < R;
-    limit[e] = rows[e].there && a.visible ? __ldg(a.visible + rows[e].token) : 0x7FFFFFFF;
+    const int64_t at = st.q_at[warp + e * C::SW];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int col = (k * 32 + lane) * 8;
-      x[e][k] = rows[e].there && col < D
-                    ? __ldg(reinterpret_cast<const uint4*>(a.q + rows[e].token * a.qt +
-                                                           rows[e].head * a.qh + col))
-                    : make_uint4(0, 0, 0, 0);
+      x[e][k] = at >= 0 && col < D ? __ldg(reinterpret_cast<const uint4*>(q + at + col))
+                                   : make_uint4(0, 0, 0, 0);
     }
   }
 #pragma unroll
   for (int e = 0; e < EACH; ++e) {
-    const int i = warp + e * WARPS;
-    if (i >= R) break;
+    const int i = warp + e * C::SW;
     float amax = 0.0f, v[V][8];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -297,26 +313,104 @@ __device__ __noinline__ void stage_queries(const AttendArgs& a, int s, int64_t t
         y.y = pack_f16x2(v[k][2] * f, v[k][3] * f);
         y.z = pack_f16x2(v[k][4] * f, v[k][5] * f);
         y.w = pack_f16x2(v[k][6] * f, v[k][7] * f);
-        *reinterpret_cast<uint4*>(q + (col >> 6) * C::QSLAB + i * 128 +
+        *reinterpret_cast<uint4*>(to + (col >> 6) * C::QSLAB + i * 128 +
                                   ((((col >> 3) & 7) ^ (i & 7)) << 4)) = y;
       }
     }
-    if (lane == 0) {
-      st.zf[i] = ldexpf(a.scale, -lift);
-      st.mref[i] = st.mpref[i] = kNone;
-      st.rl[i] = kLift;
-      st.rf[i] = 128.0f;
-      const int sees = (int)min(keys, (int64_t)max(limit[e], 0));
-      st.sees[i] = rows[e].there ? sees : 0x7FFFFFFF;  // rows that are not there are not looked at
-      st.row_at[i] = rows[e].there ? rows[e].token * a.heads + rows[e].head : -1;
-      if (rows[e].there) {
-        atomicMin(&st.sees_least, sees);
-        atomicMax(&st.sees_most, sees);
-      }
-    }
+    if (lane == 0) st.zf[i] = ldexpf(scale, -lift);
   }
 }
 
+// The order of the planes. A plane is one tile of keys or of values (or,
+// shared, of both): PP panels. They are loaded, and used by the matrix
+// instructions, as K0, K1, V0, K2, V1, ...
+template <bool SHARED>
+struct Planes {
+  int n;  // tiles
+  __device__ __forceinline__ int count() const { return SHARED ? n : 2 * n; }
+  __device__ __forceinline__ int tile(int q) const {
+    if (SHARED) return q;
+    if (q == 2 * n - 1) return n - 1;
+    return q == 0 ? 0 : (q & 1) ? (q + 1) / 2 : q / 2 - 1;
+  }
+  __device__ __forceinline__ bool value(int q) const {
+    return !SHARED && q > 0 && (q == 2 * n - 1 || (q & 1) == 0);
+  }
+  __device__ __forceinline__ int keys_of(int i) const { return SHARED ? i : i == 0 ? 0 : 2 * i - 1; }
+  __device__ __forceinline__ int values_of(int i) const {
+    return SHARED ? i : i == n - 1 ? 2 * n - 1 : 2 * i + 2;
+  }
+};
+
+// The matrix instructions, issued by one thread of the first softmax warp (all
+// of its lanes call these). The operands' descriptors differ by constants, which
+// keeps the issue ahead of the tensor core: 48 cycles an instruction of 128 x
+// 64 x 16, set by the 6 KB of operands that it reads from shared memory.
+template <int D, bool SHARED>
+struct Issue {
+  using C = Wide<D, SHARED>;
+  const Places<C>& at;
+  Planes<SHARED> planes;
+  volatile int32_t* dead;
+  uint32_t tmem, panels_done, tiles_done;
+  bool leader;
+
+  // Whether every panel of tile i's keys is there.
+  __device__ __forceinline__ bool ready(int i) const {
+    bool all = true;
+    for (int pp = 0; pp < C::PP; ++pp) {
+      const uint32_t pc = panels_done + planes.keys_of(i) * C::PP + pp;
+      all = all && mbar_try(at.full + 8 * (pc % C::NS), (pc / C::NS) & 1);
+    }
+    return __all_sync(0xFFFFFFFFu, all);
+  }
+  __device__ __forceinline__ void scores(int i) const {  // S^T of tile i
+    const uint32_t tc = tiles_done + i, b = tc & 1;
+    mbar_wait(at.s_empty + 8 * b, ((tc >> 1) & 1) ^ 1, dead);
+    for (int pp = 0; pp < C::PP; ++pp) {
+      const uint32_t pc = panels_done + planes.keys_of(i) * C::PP + pp, slot = pc % C::NS;
+      mbar_wait(at.full + 8 * slot, (pc / C::NS) & 1, dead);
+      tc_after();
+      if (leader) {
+        const uint64_t k = operand(at.ring + slot * C::PANEL, 16);
+        const uint64_t q = operand(at.q + pp * 2 * C::QSLAB, 16);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          tc_mma(tmem + C::S0 + b * C::R, k + ((j >> 2) * C::SLAB + (j & 3) * 32) / 16,
+                 q + ((j >> 2) * C::QSLAB + (j & 3) * 32) / 16, C::IDESC_S, pp > 0 || j > 0);
+        if (!SHARED) tc_commit(at.empty + 8 * slot);
+      }
+    }
+    if (leader) tc_commit(at.s_full + 8 * b);
+    __syncwarp();
+  }
+  __device__ __forceinline__ void values(int i) const {  // O^T += V^T P^T of tile i
+    const uint32_t tc = tiles_done + i;
+    mbar_wait(at.p_full, tc & 1, dead);
+    tc_after();
+    const uint64_t p = operand(at.p, 1024);
+    for (int pp = 0; pp < C::PP; ++pp) {
+      const uint32_t pc = panels_done + planes.values_of(i) * C::PP + pp, slot = pc % C::NS;
+      if (!SHARED) {
+        mbar_wait(at.full + 8 * slot, (pc / C::NS) & 1, dead);
+        tc_after();
+      }
+      if (leader) {
+        const uint64_t v = operand(at.ring + slot * C::PANEL, C::SLAB);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          tc_mma(tmem + C::O0 + pp * C::R, v + j * 128, p + j * 128, C::IDESC_O, i > 0 || j > 0);
+        tc_commit(at.empty + 8 * slot);
+      }
+    }
+    if (leader) tc_commit(at.p_empty);
+    __syncwarp();
+  }
+};
+
+// The softmax warps. A thread has key `mine` of each tile and 32 of the rows.
+// For a row: z = S * (key scale * zf) in log2 units, t = z - mref; the weight is
+// 2^(t + log2(value scale) + rl), rl = mref - mpref + 7, rf = 2^rl.
 template <int D, bool SHARED>
 __device__ __noinline__ void wide_softmax() {
   using C = Wide<D, SHARED>;
@@ -327,23 +421,21 @@ __device__ __noinline__ void wide_softmax() {
   volatile int32_t* dead = &st.dead;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c0 = item.c0;
-  const int n = item.n;
-  // ---- softmax -----------------------------------------------------------------
-  // A thread has key `mine` of each tile and 32 of the rows. For a row:
-  // z = S * (key scale * st.zf) in log2 units, t = z - st.mref; the weight is
-  // 2^(t + log2(value scale) + st.rl), st.rl = st.mref - st.mpref + 7, st.rf = 2^st.rl.
+  const int n = item.n, least = item.least, most = item.most;
+  const uint32_t tmem = st.tmem, tiles_done = item.tiles_done;
   const int quarter = warp & 3, half = warp >> 2, mine = quarter * 32 + lane;
   const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
   const int col = half * 32;
+  const Issue<D, SHARED> issue = {at, {n}, dead, tmem, item.panels_done, tiles_done, lane == 0};
   uint8_t* p_line = at.ring_ptr + C::NS * C::PANEL + C::Q + mine * 128;
   float l[32];
 #pragma unroll
   for (int c = 0; c < 32; ++c) l[c] = 0.0f;
   auto page_at = [&](int i) -> int32_t {
     const int64_t key = (c0 + i) * 128 + mine;
-    return i < n && key < item.most ? __ldg(item.row_table + (key >> item.page_bits)) : -1;
+    return i < n && key < most ? __ldg(item.row_table + (key >> item.page_bits)) : -1;
   };
-  float sk_next = -1.0f, sv_next = 0.0f;
+  float sk_next, sv_next;
   auto scales_at = [&](int i, int32_t page) {  // of this thread's key of tile i; -1: no row
     sk_next = -1.0f;
     sv_next = 1.0f;
@@ -358,159 +450,173 @@ __device__ __noinline__ void wide_softmax() {
   };
   scales_at(0, page_at(0));
   int32_t page_next = page_at(1);
+  if (warp == 0 && n > 0) issue.scores(0);
   for (int i = 0; i < n; ++i) {
-    const uint32_t tc = item.tiles_done + i, b = tc & 1;
+    const uint32_t tc = tiles_done + i, b = tc & 1;
     const float sk = sk_next;
     const bool there = !(sk < 0.0f);
-    const float lv = there ? log2f(sv_next) : 0.0f;
-    const float kf = exp2f(lv);
+    const float lv = there ? __log2f(sv_next) : 0.0f;
+    const float kf = ex2_approx_ftz(lv);
     scales_at(i + 1, page_next);
     page_next = page_at(i + 2);
     const int64_t key = (c0 + i) * 128 + mine;
-    const bool mixed = (c0 + i + 1) * 128 > item.least;
+    // some row does not see some key of the tile, or a page is missing
+    const bool mixed = (c0 + i + 1) * 128 > least || !there;
+    const bool far_key = !(fabsf(lv) <= 30.0f);
+    bool ahead = false;  // the next tile's S^T is under way
+    if (C::AHEAD && warp == 0 && i + 1 < n && issue.ready(i + 1)) {
+      issue.scores(i + 1);
+      ahead = true;
+    }
     mbar_wait(at.s_full + 8 * b, (tc >> 1) & 1, dead);
     tc_after();
-    bool o_free = false;  // O^T of the tile before is complete
-    const bool far_key = !(fabsf(lv) <= 30.0f);
-    {
-      const uint32_t s_at = st.tmem + lanes + C::S0 + b * R + col;
-      float t[32];
-      auto logits = [&](bool with_value) {  // z, or z + log2(value scale)
-        tc_load32(s_at, t);
+    const uint32_t s_at = tmem + lanes + C::S0 + b * R + col;
+    const float2 sk2 = make_float2(sk, sk), lv2 = make_float2(lv, lv);
+    float t[32];
+    auto hide = [&]() {  // rows that do not see this key
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float z = __fmul_rn(t[c], __fmul_rn(sk, st.zf[col + c]));
-          t[c] = with_value ? z + lv : z;
-          if (!there || key >= st.sees[col + c]) t[c] = -INFINITY;
-        }
-      };
-      for (int attempt = 0;; ++attempt) {
-        float mx = -INFINITY, mw = -INFINITY;
-        tc_load32(s_at, t);
-        const float2 sk2 = make_float2(sk, sk), lv2 = make_float2(lv, lv);
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 z4 = *reinterpret_cast<const float4*>(st.zf + col + c);
-          const float4 m4 = *reinterpret_cast<const float4*>(st.mref + col + c);
-          const float4 r4 = *reinterpret_cast<const float4*>(st.rl + col + c);
-          const float2 ca = mul2_rn(make_float2(z4.x, z4.y), sk2);
-          const float2 cb = mul2_rn(make_float2(z4.z, z4.w), sk2);
-          float2 ta = sub2_rn(make_float2(__fmul_rn(t[c], ca.x), __fmul_rn(t[c + 1], ca.y)),
-                              make_float2(m4.x, m4.y));
-          float2 tb = sub2_rn(make_float2(__fmul_rn(t[c + 2], cb.x), __fmul_rn(t[c + 3], cb.y)),
-                              make_float2(m4.z, m4.w));
-          if (mixed) {
-            const int4 s4 = *reinterpret_cast<const int4*>(st.sees + col + c);
-            if (!there || key >= s4.x) ta.x = -INFINITY;
-            if (!there || key >= s4.y) ta.y = -INFINITY;
-            if (!there || key >= s4.z) tb.x = -INFINITY;
-            if (!there || key >= s4.w) tb.y = -INFINITY;
-          } else if (!there) {
-            ta = tb = make_float2(-INFINITY, -INFINITY);
-          }
-          const float2 wa = add2_rn(ta, add2_rn(make_float2(r4.x, r4.y), lv2));
-          const float2 wb = add2_rn(tb, add2_rn(make_float2(r4.z, r4.w), lv2));
-          mx = fmaxf(fmaxf(mx, ta.x), fmaxf(ta.y, fmaxf(tb.x, tb.y)));
-          mw = fmaxf(fmaxf(mw, wa.x), fmaxf(wa.y, fmaxf(wb.x, wb.y)));
-          t[c] = ta.x;
-          t[c + 1] = ta.y;
-          t[c + 2] = tb.x;
-          t[c + 3] = tb.y;
-        }
-        const bool up = mx > kSlackM || mw > kSlackW + kLift;
-        if (attempt || !barrier_any(1 + half, 128, up)) break;
-        // Some weight passes its reference: raise both to the tile's maxima.
-        logits(false);
-        st.best[0][half][quarter][lane] = column_max(t, lane);
-        logits(true);
-        st.best[1][half][quarter][lane] = column_max(t, lane);
-        if (!o_free && tc > 0) mbar_wait(at.p_empty, (tc - 1) & 1, dead);
-        o_free = true;
-        tc_after();
-        barrier_of(1 + half, 128);
-        if (quarter == 0) {
-          const int c = col + lane;
-          float x = st.mref[c], y = st.mpref[c];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x = fmaxf(x, st.best[0][half][k][lane]);
-            y = fmaxf(y, st.best[1][half][k][lane]);
-          }
-          st.lscale[c] = exp2f(st.mref[c] - x);
-          st.oscale[c] = exp2f(st.mpref[c] - y);
-          st.mref[c] = x;
-          st.mpref[c] = y;
-          st.rl[c] = x - y + kLift;
-          st.rf[c] = exp2f(x - y + kLift);
-          if (!(fabsf(x - y) <= 60.0f)) st.far_refs = 1;
-        }
-        barrier_of(1 + half, 128);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) l[c] *= st.lscale[col + c];
-        if (i > 0) {
-          for (int pp = 0; pp < C::PP; ++pp) {
-            const uint32_t o_at = st.tmem + lanes + C::O0 + pp * R + col;
-            tc_load32(o_at, t);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) t[c] *= st.oscale[col + c];
-            tc_store32(o_at, t);
-          }
-        }
+      for (int c = 0; c < 32; c += 4) {
+        const int4 s4 = *reinterpret_cast<const int4*>(st.sees + col + c);
+        t[c] = there && key < s4.x ? t[c] : -INFINITY;
+        t[c + 1] = there && key < s4.y ? t[c + 1] : -INFINITY;
+        t[c + 2] = there && key < s4.z ? t[c + 2] : -INFINITY;
+        t[c + 3] = there && key < s4.w ? t[c + 3] : -INFINITY;
       }
-      {  // S^T is read
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(at.s_empty + 8 * b);
-      }
-      const bool far = __any_sync(0xFFFFFFFFu, far_key) || *(volatile int32_t*)&st.far_refs;
-      uint32_t w[16];
-      if (!far) {
-        const float2 kf2 = make_float2(kf, kf);
+    };
+    auto offsets = [&]() {  // t of all rows
+      tc_load32(s_at, t);
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 f4 = *reinterpret_cast<const float4*>(st.rf + col + c);
-          const float2 pa = make_float2(ex2_approx_ftz(t[c]), ex2_approx_ftz(t[c + 1]));
-          const float2 pb2 = make_float2(ex2_approx_ftz(t[c + 2]), ex2_approx_ftz(t[c + 3]));
-          float2* la = reinterpret_cast<float2*>(l + c);
-          la[0] = add2_rn(la[0], pa);
-          la[1] = add2_rn(la[1], pb2);
-          const float2 wa = mul2_rn(pa, mul2_rn(make_float2(f4.x, f4.y), kf2));
-          const float2 wb = mul2_rn(pb2, mul2_rn(make_float2(f4.z, f4.w), kf2));
-          w[c / 2] = pack_f16x2(wa.x, wa.y);
-          w[c / 2 + 1] = pack_f16x2(wb.x, wb.y);
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          l[c] += ex2_approx_ftz(t[c]);
-          l[c + 1] += ex2_approx_ftz(t[c + 1]);
-          // -inf stays: log2 of a zero scale is -inf, of a huge one finite
-          w[c / 2] = pack_f16x2(ex2_approx_ftz(t[c] + (st.rl[col + c] + lv)),
-                                ex2_approx_ftz(t[c + 1] + (st.rl[col + c + 1] + lv)));
-        }
+      for (int c = 0; c < 32; c += 4) {
+        const float4 z4 = *reinterpret_cast<const float4*>(st.zf + col + c);
+        const float4 m4 = *reinterpret_cast<const float4*>(st.mref + col + c);
+        const float2 ca = mul2_rn(make_float2(z4.x, z4.y), sk2);
+        const float2 cb = mul2_rn(make_float2(z4.z, z4.w), sk2);
+        const float2 ta = sub2_rn(make_float2(__fmul_rn(t[c], ca.x), __fmul_rn(t[c + 1], ca.y)),
+                                  make_float2(m4.x, m4.y));
+        const float2 tb = sub2_rn(make_float2(__fmul_rn(t[c + 2], cb.x), __fmul_rn(t[c + 3], cb.y)),
+                                  make_float2(m4.z, m4.w));
+        t[c] = ta.x;
+        t[c + 1] = ta.y;
+        t[c + 2] = tb.x;
+        t[c + 3] = tb.y;
       }
-      if (!o_free) {  // P^T's old contents have been used
-        if (tc > 0) mbar_wait(at.p_empty, (tc - 1) & 1, dead);
-        o_free = true;
-      }
+      if (mixed) hide();
+    };
+    offsets();
+    float mx = -INFINITY, mw = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint4*>(p_line + (((half * 4 + k) ^ (mine & 7)) << 4)) =
-            make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    for (int c = 0; c < 32; c += 4) {
+      const float4 r4 = *reinterpret_cast<const float4*>(st.rl + col + c);
+      const float2 wa = add2_rn(make_float2(t[c], t[c + 1]), add2_rn(make_float2(r4.x, r4.y), lv2));
+      const float2 wb = add2_rn(make_float2(t[c + 2], t[c + 3]), add2_rn(make_float2(r4.z, r4.w), lv2));
+      mx = fmaxf(fmaxf(mx, t[c]), fmaxf(t[c + 1], fmaxf(t[c + 2], t[c + 3])));
+      mw = fmaxf(fmaxf(mw, wa.x), fmaxf(wa.y, fmaxf(wb.x, wb.y)));
     }
+    bool o_free = false;  // O^T of the tile before is complete
+    if (barrier_any(1 + half, 128, mx > kSlackM || mw > kSlackW + kLift)) {
+      // Some weight passes its reference: raise both to the tile's maxima.
+      auto logits = [&](float add) {  // z, or z + log2(value scale)
+        tc_load32(s_at, t);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) t[c] = __fmul_rn(t[c], __fmul_rn(sk, st.zf[col + c])) + add;
+        if (mixed) hide();
+      };
+      logits(0.0f);
+      st.best[0][half][quarter][lane] = column_max(t, lane);
+      logits(lv);
+      st.best[1][half][quarter][lane] = column_max(t, lane);
+      if (tc > 0) mbar_wait(at.p_empty, (tc - 1) & 1, dead);
+      o_free = true;
+      tc_after();
+      barrier_of(1 + half, 128);
+      if (quarter == 0) {
+        const int c = col + lane;
+        float x = st.mref[c], y = st.mpref[c];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x = fmaxf(x, st.best[0][half][k][lane]);
+          y = fmaxf(y, st.best[1][half][k][lane]);
+        }
+        st.lscale[c] = exp2f(st.mref[c] - x);
+        st.oscale[c] = exp2f(st.mpref[c] - y);
+        st.mref[c] = x;
+        st.mpref[c] = y;
+        st.rl[c] = x - y + kLift;
+        st.rf[c] = exp2f(x - y + kLift);
+        if (!(fabsf(x - y) <= 60.0f)) st.far_refs = 1;
+      }
+      barrier_of(1 + half, 128);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) l[c] *= st.lscale[col + c];
+      if (i > 0) {
+        for (int pp = 0; pp < C::PP; ++pp) {
+          const uint32_t o_at = tmem + lanes + C::O0 + pp * R + col;
+          tc_load32(o_at, t);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) t[c] *= st.oscale[col + c];
+          tc_store32(o_at, t);
+        }
+      }
+      offsets();
+    }
+    tc_before();  // S^T is read
+    __syncwarp();
+    if (lane == 0) mbar_arrive(at.s_empty + 8 * b);
+    const bool far = __any_sync(0xFFFFFFFFu, far_key) || *(volatile int32_t*)&st.far_refs;
+    uint32_t w[16];
+    if (!far) {
+      const float2 kf2 = make_float2(kf, kf);
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 f4 = *reinterpret_cast<const float4*>(st.rf + col + c);
+        const float2 pa = make_float2(ex2_approx_ftz(t[c]), ex2_approx_ftz(t[c + 1]));
+        const float2 pb = make_float2(ex2_approx_ftz(t[c + 2]), ex2_approx_ftz(t[c + 3]));
+        const float2 la = add2_rn(make_float2(l[c], l[c + 1]), pa);
+        const float2 lb = add2_rn(make_float2(l[c + 2], l[c + 3]), pb);
+        l[c] = la.x;
+        l[c + 1] = la.y;
+        l[c + 2] = lb.x;
+        l[c + 3] = lb.y;
+        const float2 wa = mul2_rn(pa, mul2_rn(make_float2(f4.x, f4.y), kf2));
+        const float2 wb = mul2_rn(pb, mul2_rn(make_float2(f4.z, f4.w), kf2));
+        w[c / 2] = pack_f16x2(wa.x, wa.y);
+        w[c / 2 + 1] = pack_f16x2(wb.x, wb.y);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        l[c] += ex2_approx_ftz(t[c]);
+        l[c + 1] += ex2_approx_ftz(t[c + 1]);
+        // a zero scale's log2 is -inf: weight 0
+        w[c / 2] = pack_f16x2(ex2_approx_ftz(t[c] + (st.rl[col + c] + lv)),
+                              ex2_approx_ftz(t[c + 1] + (st.rl[col + c + 1] + lv)));
+      }
+    }
+    if (!o_free && tc > 0) mbar_wait(at.p_empty, (tc - 1) & 1, dead);  // P^T's old contents are used
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<uint4*>(p_line + (((half * 4 + k) ^ (mine & 7)) << 4)) =
+          make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
     fence_async();
     tc_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(at.p_full);
+    if (warp == 0) {
+      if (C::AHEAD) {
+        if (i + 1 < n && !ahead) issue.scores(i + 1);
+        issue.values(i);
+      } else {
+        issue.values(i);
+        if (i + 1 < n) issue.scores(i + 1);
+      }
+    }
   }
-  // ---- the item's result -------------------------------------------------------
-  if (n > 0) mbar_wait(at.p_empty, (item.tiles_done + n - 1) & 1, dead);
+  if (n > 0) mbar_wait(at.p_empty, (tiles_done + n - 1) & 1, dead);
   tc_after();
   float* lsum = reinterpret_cast<float*>(at.ring_ptr);  // every operand has been used
 #pragma unroll
   for (int c = 0; c < 32; c += 4)
-    *reinterpret_cast<float4*>(lsum + mine * R + col + c) =
-        make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
+    *reinterpret_cast<float4*>(lsum + mine * R + col + c) = make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
 }
 
 // The item's result, by the softmax warps: the rows' sums, then O^T from TMEM.
@@ -615,176 +721,142 @@ __device__ __noinline__ void wide_result() {
   tc_before();
 }
 
+// The producers. In a warp's load 4 keys x 8 chunks of 16 bytes; a store's
+// quarter warp covers 2 keys x 4 chunks, which the swizzle spreads over all
+// banks. Pages are looked up four planes at a time, one set ahead, and the
+// plane after next is on its way into L2 while the panels before it are
+// loaded into registers.
 template <int D, bool SHARED>
 __device__ __noinline__ void wide_produce() {
   using C = Wide<D, SHARED>;
-  constexpr int R = C::R;
   auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
   const Places<C> at = places<C>();
   const WideItem& item = st.item;
   volatile int32_t* dead = &st.dead;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, pw = (threadIdx.x >> 5) - C::SW;
   const int64_t c0 = item.c0;
-  const int n = item.n;
-  // ---- producers ---------------------------------------------------------------
-  // A plane is one tile of keys or of values (or, shared, of both): PP panels.
-  // Planes come in the order in which the matrix instructions use them: K0, K1,
-  // V0, K2, V1, ... In a warp's load 4 keys x 8 chunks of 16 bytes; a store's
-  // quarter warp covers 2 keys x 4 chunks, which the swizzle spreads over all
-  // banks.
-  const int pw = warp - C::SW;
-  const int chunk = (lane & 3) | ((lane >> 1) & 4), kb = ((lane >> 2) & 1) | ((lane >> 3) & 2);
-  const int planes = SHARED ? n : 2 * n;
-  auto tile_of = [&](int q) {
-    if (SHARED) return q;
-    if (q == 2 * n - 1) return n - 1;
-    return q == 0 ? 0 : (q & 1) ? (q + 1) / 2 : q / 2 - 1;
+  const int n = item.n, most = item.most, least = item.least;
+  const Planes<SHARED> planes = {n};
+  const int chunk = (lane & 3) | ((lane >> 1) & 4);
+  const int own = pw * 4 + (((lane >> 2) & 1) | ((lane >> 3) & 2));  // this thread's of 16 keys
+  // 16 keys in a row lie on one page. Lane 8 p + g holds the page of keys 16 g ..
+  // of plane 4 m + p.
+  auto pages_of = [&](int m) -> int32_t {
+    const int q = 4 * m + (lane >> 3);
+    if (q >= planes.count()) return -1;
+    const int64_t key = (c0 + planes.tile(q)) * 128 + (lane & 7) * 16;
+    return key < most ? __ldg(item.row_table + (key >> item.page_bits)) : -1;
   };
-  auto is_value = [&](int q) { return !SHARED && q > 0 && (q == 2 * n - 1 || (q & 1) == 0); };
-  // 16 keys in a row lie on one page: lane g < 8 looks after keys 16 g .. of the
-  // tile, and the warp finds their place in shared memory.
-  auto page_of = [&](int q) -> int32_t {
-    if (q >= planes || lane >= 8) return -1;
-    const int64_t key = (c0 + tile_of(q)) * 128 + lane * 16;
-    return key < item.most ? __ldg(item.row_table + (key >> item.page_bits)) : -1;
+  int32_t pages = pages_of(0), pages_next = pages_of(1);
+  // Lanes 8 p + g: where the 16 keys begin, in KiB from the pool's start, or -1.
+  auto locate16 = [&](int m, int32_t page) -> int32_t {
+    const int q = 4 * m + (lane >> 3);
+    if (page < 0 || page >= item.num_pages) return -1;
+    const int64_t key = (c0 + planes.tile(q)) * 128 + (lane & 7) * 16;
+    const int head = planes.value(q) ? item.value_head : item.key_head;
+    const int slot = (int)(key & ((1 << item.page_bits) - 1));
+    return (int32_t)((((((int64_t)page * item.heads + head) << item.page_bits) + slot) * D) >> 10);
   };
-  const int mine = (pw * 4 + kb) * D + chunk * 16;  // this thread's place among 16 keys
-  int32_t page = page_of(0);
+  auto prefetch = [&](int32_t kib) {  // 16 whole rows into L2
+    if (pw == 0 && kib >= 0)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(item.data + ((int64_t)kib << 10)),
+                   "r"(16 * D)
+                   : "memory");
+  };
+  int32_t kib = locate16(0, pages), kib_next = -1;
+  prefetch(kib);
   uint4 buf[C::DEPTH][C::KV];
-  int load_q = 0, load_pp = 0, left = 0;
+  int load_q = 0, load_pp = 0;
+  int32_t at16[C::KV];
+  bool whole = true;  // every key of the plane is there
   auto load = [&](uint4 (&v)[C::KV]) {  // the next panel of the sequence
-    if (load_q >= planes) return;
+    if (load_q >= planes.count()) return;
     if (load_pp == 0) {
-      const int64_t key = (c0 + tile_of(load_q)) * 128;
-      if (lane < 8) {
-        const int head = is_value(load_q) ? item.value_head : item.key_head;
-        const int slot = (int)((key + lane * 16) & ((1 << item.page_bits) - 1));
-        st.place[pw][load_q & 1][lane] =
-            page >= 0 && page < item.num_pages
-                ? (int32_t)((((((int64_t)page * item.heads + head) << item.page_bits) + slot) * D) >> 10)
-                : -1;
+      const int m = load_q >> 2, p = load_q & 3;
+      if (p == 0) {
+        if (load_q > 0) {
+          kib = kib_next;
+          pages_next = pages_of(m + 1);
+        }
+      } else if (p == 1) {  // the lookup of the next four has had a plane's time
+        kib_next = locate16(m + 1, pages_next);
+        prefetch(kib_next);
       }
-      page = page_of(load_q + 1);
-      left = (int)min((int64_t)128, (int64_t)item.most - key);  // keys that some row sees
-      __syncwarp();
-    }
-    const uint8_t* data = item.data + mine + load_pp * 128;
+      const int left = (int)min((int64_t)128, (int64_t)most - (c0 + planes.tile(load_q)) * 128);
 #pragma unroll
-    for (int k = 0; k < C::KV; ++k) {
-      const int32_t kib = st.place[pw][load_q & 1][k];
-      v[k] = make_uint4(0, 0, 0, 0);
-      if (kib >= 0 && k * 16 + pw * 4 + kb < left)
-        v[k] = ld_stream(reinterpret_cast<const uint16_t*>(data + ((int64_t)kib << 10)));
+      for (int k = 0; k < C::KV; ++k) {
+        at16[k] = __shfl_sync(0xFFFFFFFFu, kib, p * 8 + k);
+        if (k * 16 + own >= left) at16[k] = -1;
+      }
+      bool all = true;
+#pragma unroll
+      for (int k = 0; k < C::KV; ++k) all = all && at16[k] >= 0;
+      whole = __all_sync(0xFFFFFFFFu, all);
+    }
+    const uint8_t* data = item.data + own * D + chunk * 16 + load_pp * 128;
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < C::KV; ++k)
+        v[k] = ld_stream(reinterpret_cast<const uint16_t*>(data + ((int64_t)at16[k] << 10)));
+    } else {
+#pragma unroll
+      for (int k = 0; k < C::KV; ++k) {
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (at16[k] >= 0) v[k] = ld_stream(reinterpret_cast<const uint16_t*>(data + ((int64_t)at16[k] << 10)));
+      }
     }
     if (++load_pp == C::PP) {
       load_pp = 0;
       ++load_q;
     }
   };
-  auto value_panel = [&](int tile, int pp, uint32_t slot) {  // O^T's columns of one panel
-    if (lane == 0) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        tc_mma(st.tmem + C::O0 + pp * R, operand(at.ring + slot * C::PANEL + k * 2048, C::SLAB),
-               operand(at.p + k * 2048, 1024), C::IDESC_O, tile > 0 || k > 0);
-      tc_commit(at.empty + 8 * slot);
-    }
-  };
-  auto values = [&](int tile) {  // O^T from panels that are there already
-    const uint32_t tc = item.tiles_done + tile;
-    mbar_wait(at.p_full, tc & 1, dead);
-    tc_after();
-    for (int pp = 0; pp < C::PP; ++pp)
-      value_panel(tile, pp, (item.panels_done + tile * C::PP + pp) % C::NS);
-    if (lane == 0) tc_commit(at.p_empty);
-    __syncwarp();
-  };
 #pragma unroll
   for (int j = 0; j < C::DEPTH; ++j) load(buf[j]);
-  const int total = planes * C::PP;
+  const int total = planes.count() * C::PP;
+  const uint32_t panels_done = item.panels_done;
+  uint8_t* const ring = at.ring_ptr + (chunk >> 2) * C::SLAB + own * 128;
+  const int lo16 = (((chunk & 3) * 2) ^ (own & 7)) << 4, hi16 = lo16 ^ 16;
   for (int p0 = 0; p0 < total; p0 += C::DEPTH) {
 #pragma unroll
     for (int j = 0; j < C::DEPTH; ++j) {
       const int p = p0 + j;
       if (p >= total) break;
-      const uint32_t pc = item.panels_done + p, slot = pc % C::NS;
+      const uint32_t pc = panels_done + p, slot = pc % C::NS;
       const int q = p / C::PP;
       // Rows that only some queries see must not bring NaN into the product.
-      if ((SHARED || is_value(q)) && (c0 + tile_of(q) + 1) * 128 > item.least) {
+      if ((SHARED || planes.value(q)) && (c0 + planes.tile(q) + 1) * 128 > least) {
         uint32_t any = 0;
+        auto clean = [&](uint32_t& x) {
+          const uint32_t bad = nan_bytes(x);
+          any |= bad;
+          x &= ~bad;
+        };
 #pragma unroll
         for (int k = 0; k < C::KV; ++k) {
-          uint32_t bad = nan_bytes(buf[j][k].x);
-          any |= bad;
-          buf[j][k].x &= ~bad;
-          bad = nan_bytes(buf[j][k].y);
-          any |= bad;
-          buf[j][k].y &= ~bad;
-          bad = nan_bytes(buf[j][k].z);
-          any |= bad;
-          buf[j][k].z &= ~bad;
-          bad = nan_bytes(buf[j][k].w);
-          any |= bad;
-          buf[j][k].w &= ~bad;
+          clean(buf[j][k].x);
+          clean(buf[j][k].y);
+          clean(buf[j][k].z);
+          clean(buf[j][k].w);
         }
         if (any) st.nan_rows = 1;
       }
       mbar_wait(at.empty + 8 * slot, ((pc / C::NS) & 1) ^ 1, dead);
-      uint8_t* panel = at.ring_ptr + slot * C::PANEL + (chunk >> 2) * C::SLAB + (pw * 4 + kb) * 128;
-      const int swap = (pw * 4 + kb) & 7, c16 = (chunk & 3) * 2;
+      uint8_t* panel = ring + slot * C::PANEL;
 #pragma unroll
       for (int k = 0; k < C::KV; ++k) {
         const uint4 x = buf[j][k];
-        uint8_t* row = panel + k * 2048;
-        *reinterpret_cast<uint4*>(row + ((c16 ^ swap) << 4)) =
+        *reinterpret_cast<uint4*>(panel + k * 2048 + lo16) =
             make_uint4(lo_f16x2(x.x), hi_f16x2(x.x), lo_f16x2(x.y), hi_f16x2(x.y));
-        *reinterpret_cast<uint4*>(row + (((c16 + 1) ^ swap) << 4)) =
+        *reinterpret_cast<uint4*>(panel + k * 2048 + hi16) =
             make_uint4(lo_f16x2(x.z), hi_f16x2(x.z), lo_f16x2(x.w), hi_f16x2(x.w));
       }
-      load(buf[j]);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(at.full + 8 * slot);
-      if (pw == 0) {  // the matrix instructions that this panel makes possible
-        const int tile = tile_of(q), pp = p % C::PP;
-        if (SHARED || !is_value(q)) {
-          const uint32_t tc = item.tiles_done + tile, b = tc & 1;
-          if (pp == 0) mbar_wait(at.s_empty + 8 * b, ((tc >> 1) & 1) ^ 1, dead);
-          mbar_wait(at.full + 8 * slot, (pc / C::NS) & 1, dead);
-          tc_after();
-          if (lane == 0) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma(st.tmem + C::S0 + b * R,
-                     operand(at.ring + slot * C::PANEL + (k >> 2) * C::SLAB + (k & 3) * 32, 16),
-                     operand(at.q + (pp * 2 + (k >> 2)) * C::QSLAB + (k & 3) * 32, 16), C::IDESC_S,
-                     pp > 0 || k > 0);
-            if (!SHARED) tc_commit(at.empty + 8 * slot);
-            if (pp == C::PP - 1) tc_commit(at.s_full + 8 * b);
-          }
-          __syncwarp();
-          if (SHARED && pp == C::PP - 1) {
-            if (!C::AHEAD) {
-              values(tile);
-            } else {
-              if (tile > 0) values(tile - 1);
-              if (tile == n - 1) values(tile);
-            }
-          }
-        } else {
-          const uint32_t tc = item.tiles_done + tile;
-          if (pp == 0) mbar_wait(at.p_full, tc & 1, dead);
-          mbar_wait(at.full + 8 * slot, (pc / C::NS) & 1, dead);
-          tc_after();
-          value_panel(tile, pp, slot);
-          if (lane == 0 && pp == C::PP - 1) tc_commit(at.p_empty);
-          __syncwarp();
-        }
-      }
+      load(buf[j]);
     }
   }
 }
-
 
 template <int D, bool SHARED, bool HALF>
 __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
@@ -854,8 +926,7 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
       st.first_nan = 0x7FFFFFFF;
     }
     __syncthreads();
-    stage_queries<D, SHARED, HALF>(a, s, tile_of_rows, h, work.keys);
-    fence_async();
+    stage_rows<D, SHARED>(a, s, tile_of_rows, h, work.keys);
     __syncthreads();
     const int64_t stop = min(c1, ((int64_t)st.sees_most + 127) / 128);
     const int n = stop > c0 ? (int)(stop - c0) : 0;  // tiles of 128 keys
@@ -883,6 +954,9 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
     }
     __syncthreads();
     if (warp < C::SW) {
+      stage_queries<D, SHARED, HALF>(a.q, a.scale);
+      fence_async();
+      barrier_of(3, C::SW * 32);
       wide_softmax<D, SHARED>();
       wide_result<D, SHARED, HALF>();
     } else {

@@ -100,10 +100,10 @@ struct Row {
 };
 __device__ __forceinline__ Row row_of(const AttendArgs& a, int s, int64_t tile, int h, int rows, int i) {
   const int64_t c0 = __ldg(a.cu + s), c1 = __ldg(a.cu + s + 1);
-  const int64_t r = tile * rows + i, t = r / a.group;
+  const uint32_t r = (uint32_t)(tile * rows + i), t = r / (uint32_t)a.group;  // below tokens * heads < 2^31
   Row w;
   w.token = c0 + t;
-  w.head = h * a.group + (int)(r - t * a.group);
+  w.head = h * a.group + (int)(r - t * (uint32_t)a.group);
   w.there = w.token < c1 && w.token >= 0 && w.token < a.tokens;
   return w;
 }
