@@ -76,17 +76,24 @@ __device__ __forceinline__ void tc_before() {
 __device__ __forceinline__ void tc_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
+// One matrix instruction, and the arrival on a barrier when all before it are
+// done: called by a converged warp, executed by its elected lane.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
+// The same value in every lane, which the compiler then keeps in uniform
+// registers, where the matrix instructions take their operands from.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 #define CSA_R10(b) "%" #b "0, %" #b "1, %" #b "2, %" #b "3, %" #b "4, %" #b "5, %" #b "6, %" #b "7, %" #b "8, %" #b "9"
 __device__ __forceinline__ void tc_load32(uint32_t at, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -180,8 +187,8 @@ struct Wide {
   static constexpr int R = 64;                      // query rows of a tile
   static constexpr int PP = D / 128;                // panels of 128 keys
   static constexpr int SW = R / 8;                  // softmax warps: 4 for each 32 rows
-  static constexpr int PW = 4;                      // producer warps
-  static constexpr int THREADS = (SW + PW) * 32;
+  static constexpr int PW = 3;                      // producer warps
+  static constexpr int THREADS = (SW + PW + 1) * 32;  // 12 warps: 168 registers a thread
   static constexpr int NS = 4;                      // panels of the ring
   static constexpr bool AHEAD = !SHARED || 2 * PP <= NS;  // S^T of the next keys before O^T of these
   static constexpr int SLAB = 16384;                // 128 keys x 64 columns
@@ -193,8 +200,7 @@ struct Wide {
   using State = WideState<R, NS, THREADS / 32>;
   static constexpr int HEAD = (int)(sizeof(State) + 1023) / 1024 * 1024;
   static constexpr int SMEM = HEAD + NS * PANEL + Q + P + 1024;
-  static constexpr int KV = 8;                      // 16-byte vectors a thread and panel
-  static_assert(KV * PW * 32 == 1024, "a panel is 128 keys of 8 vectors");
+  static constexpr int KV = (32 + PW - 1) / PW;     // steps of 4 keys a warp and panel
   static constexpr int DEPTH = 2;                   // panels in flight in registers
   static constexpr int SLOT = R * (D + 4);
   static constexpr uint32_t S0 = 0, O0 = 2 * R;     // TMEM columns
@@ -342,8 +348,8 @@ struct Planes {
   }
 };
 
-// The matrix instructions, issued by one thread of the first softmax warp (all
-// of its lanes call these). The operands' descriptors differ by constants, which
+// The matrix instructions, issued by a warp of their own (all of its lanes call
+// these, one is elected). The operands' descriptors differ by constants, which
 // keeps the issue ahead of the tensor core: 48 cycles an instruction of 128 x
 // 64 x 16, set by the 6 KB of operands that it reads from shared memory.
 template <int D, bool SHARED>
@@ -353,17 +359,7 @@ struct Issue {
   Planes<SHARED> planes;
   volatile int32_t* dead;
   uint32_t tmem, panels_done, tiles_done;
-  bool leader;
 
-  // Whether every panel of tile i's keys is there.
-  __device__ __forceinline__ bool ready(int i) const {
-    bool all = true;
-    for (int pp = 0; pp < C::PP; ++pp) {
-      const uint32_t pc = panels_done + planes.keys_of(i) * C::PP + pp;
-      all = all && mbar_try(at.full + 8 * (pc % C::NS), (pc / C::NS) & 1);
-    }
-    return __all_sync(0xFFFFFFFFu, all);
-  }
   __device__ __forceinline__ void scores(int i) const {  // S^T of tile i
     const uint32_t tc = tiles_done + i, b = tc & 1;
     mbar_wait(at.s_empty + 8 * b, ((tc >> 1) & 1) ^ 1, dead);
@@ -371,18 +367,16 @@ struct Issue {
       const uint32_t pc = panels_done + planes.keys_of(i) * C::PP + pp, slot = pc % C::NS;
       mbar_wait(at.full + 8 * slot, (pc / C::NS) & 1, dead);
       tc_after();
-      if (leader) {
-        const uint64_t k = operand(at.ring + slot * C::PANEL, 16);
-        const uint64_t q = operand(at.q + pp * 2 * C::QSLAB, 16);
+      __syncwarp();
+      const uint64_t k = operand(at.ring + slot * C::PANEL, 16);
+      const uint64_t q = operand(at.q + pp * 2 * C::QSLAB, 16);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          tc_mma(tmem + C::S0 + b * C::R, k + ((j >> 2) * C::SLAB + (j & 3) * 32) / 16,
-                 q + ((j >> 2) * C::QSLAB + (j & 3) * 32) / 16, C::IDESC_S, pp > 0 || j > 0);
-        if (!SHARED) tc_commit(at.empty + 8 * slot);
-      }
+      for (int j = 0; j < 8; ++j)
+        tc_mma(tmem + C::S0 + b * C::R, k + ((j >> 2) * C::SLAB + (j & 3) * 32) / 16,
+               q + ((j >> 2) * C::QSLAB + (j & 3) * 32) / 16, C::IDESC_S, pp > 0 || j > 0);
+      if (!SHARED) tc_commit(at.empty + 8 * slot);
     }
-    if (leader) tc_commit(at.s_full + 8 * b);
-    __syncwarp();
+    tc_commit(at.s_full + 8 * b);
   }
   __device__ __forceinline__ void values(int i) const {  // O^T += V^T P^T of tile i
     const uint32_t tc = tiles_done + i;
@@ -395,18 +389,34 @@ struct Issue {
         mbar_wait(at.full + 8 * slot, (pc / C::NS) & 1, dead);
         tc_after();
       }
-      if (leader) {
-        const uint64_t v = operand(at.ring + slot * C::PANEL, C::SLAB);
+      __syncwarp();
+      const uint64_t v = operand(at.ring + slot * C::PANEL, C::SLAB);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          tc_mma(tmem + C::O0 + pp * C::R, v + j * 128, p + j * 128, C::IDESC_O, i > 0 || j > 0);
-        tc_commit(at.empty + 8 * slot);
-      }
+      for (int j = 0; j < 8; ++j)
+        tc_mma(tmem + C::O0 + pp * C::R, v + j * 128, p + j * 128, C::IDESC_O, i > 0 || j > 0);
+      tc_commit(at.empty + 8 * slot);
     }
-    if (leader) tc_commit(at.p_empty);
-    __syncwarp();
+    tc_commit(at.p_empty);
   }
 };
+
+template <int D, bool SHARED>
+__device__ __noinline__ void wide_products() {
+  using C = Wide<D, SHARED>;
+  auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
+  const Places<C> at = places<C>();
+  const int n = (int)uniform((uint32_t)st.item.n);
+  const Issue<D, SHARED> issue = {at, {n}, &st.dead, uniform(st.tmem), uniform(st.item.panels_done),
+                                  uniform(st.item.tiles_done)};
+  if (C::AHEAD && n > 0) issue.scores(0);
+  for (int i = 0; i < n; ++i) {
+    if (!C::AHEAD)
+      issue.scores(i);
+    else if (i + 1 < n)
+      issue.scores(i + 1);
+    issue.values(i);
+  }
+}
 
 // The softmax warps. A thread has key `mine` of each tile and 32 of the rows.
 // For a row: z = S * (key scale * zf) in log2 units, t = z - mref; the weight is
@@ -426,7 +436,6 @@ __device__ __noinline__ void wide_softmax() {
   const int quarter = warp & 3, half = warp >> 2, mine = quarter * 32 + lane;
   const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
   const int col = half * 32;
-  const Issue<D, SHARED> issue = {at, {n}, dead, tmem, item.panels_done, tiles_done, lane == 0};
   uint8_t* p_line = at.ring_ptr + C::NS * C::PANEL + C::Q + mine * 128;
   float l[32];
 #pragma unroll
@@ -450,7 +459,6 @@ __device__ __noinline__ void wide_softmax() {
   };
   scales_at(0, page_at(0));
   int32_t page_next = page_at(1);
-  if (warp == 0 && n > 0) issue.scores(0);
   for (int i = 0; i < n; ++i) {
     const uint32_t tc = tiles_done + i, b = tc & 1;
     const float sk = sk_next;
@@ -463,11 +471,6 @@ __device__ __noinline__ void wide_softmax() {
     // some row does not see some key of the tile, or a page is missing
     const bool mixed = (c0 + i + 1) * 128 > least || !there;
     const bool far_key = !(fabsf(lv) <= 30.0f);
-    bool ahead = false;  // the next tile's S^T is under way
-    if (C::AHEAD && warp == 0 && i + 1 < n && issue.ready(i + 1)) {
-      issue.scores(i + 1);
-      ahead = true;
-    }
     mbar_wait(at.s_full + 8 * b, (tc >> 1) & 1, dead);
     tc_after();
     const uint32_t s_at = tmem + lanes + C::S0 + b * R + col;
@@ -601,15 +604,6 @@ __device__ __noinline__ void wide_softmax() {
     tc_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(at.p_full);
-    if (warp == 0) {
-      if (C::AHEAD) {
-        if (i + 1 < n && !ahead) issue.scores(i + 1);
-        issue.values(i);
-      } else {
-        issue.values(i);
-        if (i + 1 < n) issue.scores(i + 1);
-      }
-    }
   }
   if (n > 0) mbar_wait(at.p_empty, (tiles_done + n - 1) & 1, dead);
   tc_after();
@@ -738,7 +732,7 @@ __device__ __noinline__ void wide_produce() {
   const int n = item.n, most = item.most, least = item.least;
   const Planes<SHARED> planes = {n};
   const int chunk = (lane & 3) | ((lane >> 1) & 4);
-  const int own = pw * 4 + (((lane >> 2) & 1) | ((lane >> 3) & 2));  // this thread's of 16 keys
+  const int kb = ((lane >> 2) & 1) | ((lane >> 3) & 2);  // this thread's of a step's 4 keys
   // 16 keys in a row lie on one page. Lane 8 p + g holds the page of keys 16 g ..
   // of plane 4 m + p.
   auto pages_of = [&](int m) -> int32_t {
@@ -765,57 +759,53 @@ __device__ __noinline__ void wide_produce() {
   };
   int32_t kib = locate16(0, pages), kib_next = -1;
   prefetch(kib);
+  // Step k of this warp is keys 4 e .. 4 e + 3 of the tile, e = k PW + pw (the
+  // last step of some warps is one too many and repeats the one before).
+  auto step = [&](int k) { return min(k * C::PW + pw, 31); };
   uint4 buf[C::DEPTH][C::KV];
+  uint32_t here[C::DEPTH];  // bit k: the key of step k is there; the others are loaded from
+                            // the pool's start and stored as zeros
   int load_q = 0, load_pp = 0;
   int32_t at16[C::KV];
-  bool whole = true;  // every key of the plane is there
-  auto load = [&](uint4 (&v)[C::KV]) {  // the next panel of the sequence
-    if (load_q >= planes.count()) return;
+  uint32_t there = 0;
+  auto load = [&](uint4 (&v)[C::KV], uint32_t& mask) {  // the next panel of the sequence
     if (load_pp == 0) {
       const int m = load_q >> 2, p = load_q & 3;
-      if (p == 0) {
-        if (load_q > 0) {
-          kib = kib_next;
-          pages_next = pages_of(m + 1);
-        }
+      if (p == 0 && load_q > 0) {
+        kib = kib_next;
+        pages_next = pages_of(m + 1);
       } else if (p == 1) {  // the lookup of the next four has had a plane's time
         kib_next = locate16(m + 1, pages_next);
         prefetch(kib_next);
       }
-      const int left = (int)min((int64_t)128, (int64_t)most - (c0 + planes.tile(load_q)) * 128);
+      const int left = load_q < planes.count()
+                           ? (int)min((int64_t)128, (int64_t)most - (c0 + planes.tile(load_q)) * 128)
+                           : 0;
+      there = 0;
 #pragma unroll
       for (int k = 0; k < C::KV; ++k) {
-        at16[k] = __shfl_sync(0xFFFFFFFFu, kib, p * 8 + k);
-        if (k * 16 + own >= left) at16[k] = -1;
-      }
-      bool all = true;
-#pragma unroll
-      for (int k = 0; k < C::KV; ++k) all = all && at16[k] >= 0;
-      whole = __all_sync(0xFFFFFFFFu, all);
-    }
-    const uint8_t* data = item.data + own * D + chunk * 16 + load_pp * 128;
-    if (whole) {
-#pragma unroll
-      for (int k = 0; k < C::KV; ++k)
-        v[k] = ld_stream(reinterpret_cast<const uint16_t*>(data + ((int64_t)at16[k] << 10)));
-    } else {
-#pragma unroll
-      for (int k = 0; k < C::KV; ++k) {
-        v[k] = make_uint4(0, 0, 0, 0);
-        if (at16[k] >= 0) v[k] = ld_stream(reinterpret_cast<const uint16_t*>(data + ((int64_t)at16[k] << 10)));
+        const int e = step(k);
+        at16[k] = __shfl_sync(0xFFFFFFFFu, kib, p * 8 + (e >> 2));
+        if (at16[k] >= 0 && e * 4 + kb < left) there |= 1u << k;
+        at16[k] = (there >> k) & 1 ? at16[k] : 0;
       }
     }
+    mask = there;
+    const uint8_t* data = item.data + kb * D + chunk * 16 + load_pp * 128;
+#pragma unroll
+    for (int k = 0; k < C::KV; ++k)
+      v[k] = ld_stream(reinterpret_cast<const uint16_t*>(data + ((int64_t)at16[k] << 10) +
+                                                         (step(k) & 3) * 4 * D));
     if (++load_pp == C::PP) {
       load_pp = 0;
       ++load_q;
     }
   };
 #pragma unroll
-  for (int j = 0; j < C::DEPTH; ++j) load(buf[j]);
+  for (int j = 0; j < C::DEPTH; ++j) load(buf[j], here[j]);
   const int total = planes.count() * C::PP;
   const uint32_t panels_done = item.panels_done;
-  uint8_t* const ring = at.ring_ptr + (chunk >> 2) * C::SLAB + own * 128;
-  const int lo16 = (((chunk & 3) * 2) ^ (own & 7)) << 4, hi16 = lo16 ^ 16;
+  uint8_t* const ring = at.ring_ptr + (chunk >> 2) * C::SLAB + kb * 128;
   for (int p0 = 0; p0 < total; p0 += C::DEPTH) {
 #pragma unroll
     for (int j = 0; j < C::DEPTH; ++j) {
@@ -823,6 +813,11 @@ __device__ __noinline__ void wide_produce() {
       if (p >= total) break;
       const uint32_t pc = panels_done + p, slot = pc % C::NS;
       const int q = p / C::PP;
+      if (here[j] != (1u << C::KV) - 1) {
+#pragma unroll
+        for (int k = 0; k < C::KV; ++k)
+          if (!((here[j] >> k) & 1)) buf[j][k] = make_uint4(0, 0, 0, 0);
+      }
       // Rows that only some queries see must not bring NaN into the product.
       if ((SHARED || planes.value(q)) && (c0 + planes.tile(q) + 1) * 128 > least) {
         uint32_t any = 0;
@@ -845,15 +840,17 @@ __device__ __noinline__ void wide_produce() {
 #pragma unroll
       for (int k = 0; k < C::KV; ++k) {
         const uint4 x = buf[j][k];
-        *reinterpret_cast<uint4*>(panel + k * 2048 + lo16) =
+        const int key = step(k) * 4 + kb, c16 = ((chunk & 3) * 2) ^ (key & 7);
+        uint8_t* line = panel + step(k) * 512;
+        *reinterpret_cast<uint4*>(line + (c16 << 4)) =
             make_uint4(lo_f16x2(x.x), hi_f16x2(x.x), lo_f16x2(x.y), hi_f16x2(x.y));
-        *reinterpret_cast<uint4*>(panel + k * 2048 + hi16) =
+        *reinterpret_cast<uint4*>(line + ((c16 ^ 1) << 4)) =
             make_uint4(lo_f16x2(x.z), hi_f16x2(x.z), lo_f16x2(x.w), hi_f16x2(x.w));
       }
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(at.full + 8 * slot);
-      load(buf[j]);
+      load(buf[j], here[j]);
     }
   }
 }
@@ -959,8 +956,10 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
       barrier_of(3, C::SW * 32);
       wide_softmax<D, SHARED>();
       wide_result<D, SHARED, HALF>();
-    } else {
+    } else if (warp < C::SW + C::PW) {
       wide_produce<D, SHARED>();
+    } else {
+      wide_products<D, SHARED>();
     }
     __syncthreads();
     panels_done += (SHARED ? 1 : 2) * n * C::PP;
