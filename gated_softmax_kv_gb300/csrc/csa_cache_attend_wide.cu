@@ -953,12 +953,13 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
     if (warp < C::SW) {
       stage_queries<D, SHARED, HALF>(a.q, a.scale);
       fence_async();
-      barrier_of(3, C::SW * 32);
+      barrier_of(4, C::SW * 32 + 32);  // Q is there, for the warp of the matrix instructions
       wide_softmax<D, SHARED>();
       wide_result<D, SHARED, HALF>();
     } else if (warp < C::SW + C::PW) {
       wide_produce<D, SHARED>();
     } else {
+      barrier_of(4, C::SW * 32 + 32);
       wide_products<D, SHARED>();
     }
     __syncthreads();
