@@ -187,8 +187,8 @@ struct Wide {
   static constexpr int R = 64;                      // query rows of a tile
   static constexpr int PP = D / 128;                // panels of 128 keys
   static constexpr int SW = R / 8;                  // softmax warps: 4 for each 32 rows
-  static constexpr int PW = 3;                      // producer warps
-  static constexpr int THREADS = (SW + PW + 1) * 32;  // 12 warps: 168 registers a thread
+  static constexpr int PW = 7;                      // producer warps
+  static constexpr int THREADS = (SW + PW + 1) * 32;  // 16 warps: 128 registers a thread
   static constexpr int NS = 4;                      // panels of the ring
   static constexpr bool AHEAD = !SHARED || 2 * PP <= NS;  // S^T of the next keys before O^T of these
   static constexpr int SLAB = 16384;                // 128 keys x 64 columns
@@ -201,7 +201,7 @@ struct Wide {
   static constexpr int HEAD = (int)(sizeof(State) + 1023) / 1024 * 1024;
   static constexpr int SMEM = HEAD + NS * PANEL + Q + P + 1024;
   static constexpr int KV = (32 + PW - 1) / PW;     // steps of 4 keys a warp and panel
-  static constexpr int DEPTH = 2;                   // panels in flight in registers
+  static constexpr int DEPTH = 3;                   // panels in flight in registers
   static constexpr int SLOT = R * (D + 4);
   static constexpr uint32_t S0 = 0, O0 = 2 * R;     // TMEM columns
   // fp32 accumulator, fp16 operands, N = R, M = 128; O^T has both transposed.
@@ -773,9 +773,9 @@ __device__ __noinline__ void wide_produce() {
       const int m = load_q >> 2, p = load_q & 3;
       if (p == 0 && load_q > 0) {
         kib = kib_next;
-        pages_next = pages_of(m + 1);
-      } else if (p == 1) {  // the lookup of the next four has had a plane's time
+      } else if (p == 1) {  // the lookup of the next four has had four planes' time
         kib_next = locate16(m + 1, pages_next);
+        pages_next = pages_of(m + 2);
         prefetch(kib_next);
       }
       const int left = load_q < planes.count()
