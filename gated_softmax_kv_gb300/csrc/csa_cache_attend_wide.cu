@@ -201,7 +201,7 @@ struct Wide {
   static constexpr int HEAD = (int)(sizeof(State) + 1023) / 1024 * 1024;
   static constexpr int SMEM = HEAD + NS * PANEL + Q + P + 1024;
   static constexpr int KV = (32 + PW - 1) / PW;     // steps of 4 keys a warp and panel
-  static constexpr int DEPTH = 3;                   // panels in flight in registers
+  static constexpr int DEPTH = 4;                   // panels in flight in registers
   static constexpr int SLOT = R * (D + 4);
   static constexpr uint32_t S0 = 0, O0 = 2 * R;     // TMEM columns
   // fp32 accumulator, fp16 operands, N = R, M = 128; O^T has both transposed.
@@ -717,9 +717,7 @@ __device__ __noinline__ void wide_result() {
 
 // The producers. In a warp's load 4 keys x 8 chunks of 16 bytes; a store's
 // quarter warp covers 2 keys x 4 chunks, which the swizzle spreads over all
-// banks. Pages are looked up four planes at a time, one set ahead, and the
-// plane after next is on its way into L2 while the panels before it are
-// loaded into registers.
+// banks. Pages are looked up four planes at a time, a set ahead.
 template <int D, bool SHARED>
 __device__ __noinline__ void wide_produce() {
   using C = Wide<D, SHARED>;
@@ -751,14 +749,7 @@ __device__ __noinline__ void wide_produce() {
     const int slot = (int)(key & ((1 << item.page_bits) - 1));
     return (int32_t)((((((int64_t)page * item.heads + head) << item.page_bits) + slot) * D) >> 10);
   };
-  auto prefetch = [&](int32_t kib) {  // 16 whole rows into L2
-    if (pw == 0 && kib >= 0)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(item.data + ((int64_t)kib << 10)),
-                   "r"(16 * D)
-                   : "memory");
-  };
   int32_t kib = locate16(0, pages), kib_next = -1;
-  prefetch(kib);
   // Step k of this warp is keys 4 e .. 4 e + 3 of the tile, e = k PW + pw (the
   // last step of some warps is one too many and repeats the one before).
   auto step = [&](int k) { return min(k * C::PW + pw, 31); };
@@ -776,7 +767,6 @@ __device__ __noinline__ void wide_produce() {
       } else if (p == 1) {  // the lookup of the next four has had four planes' time
         kib_next = locate16(m + 1, pages_next);
         pages_next = pages_of(m + 2);
-        prefetch(kib_next);
       }
       const int left = load_q < planes.count()
                            ? (int)min((int64_t)128, (int64_t)most - (c0 + planes.tile(load_q)) * 128)
