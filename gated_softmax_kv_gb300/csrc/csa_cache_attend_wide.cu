@@ -201,7 +201,7 @@ struct Wide {
   static constexpr int HEAD = (int)(sizeof(State) + 1023) / 1024 * 1024;
   static constexpr int SMEM = HEAD + NS * PANEL + Q + P + 1024;
   static constexpr int KV = (32 + PW - 1) / PW;     // steps of 4 keys a warp and panel
-  static constexpr int DEPTH = 4;                   // panels in flight in registers
+  static constexpr int DEPTH = 2;                   // panels in flight in registers
   static constexpr int SLOT = R * (D + 4);
   static constexpr uint32_t S0 = 0, O0 = 2 * R;     // TMEM columns
   // fp32 accumulator, fp16 operands, N = R, M = 128; O^T has both transposed.
@@ -418,6 +418,60 @@ __device__ __noinline__ void wide_products() {
   }
 }
 
+// Some weight passes its reference: both references rise to the tile's maxima,
+// and what O^T has so far is scaled down. By the four warps of 32 rows; each
+// thread has a key, as in wide_softmax, which scales its sums by lscale.
+template <int D, bool SHARED>
+__device__ __noinline__ void wide_raise(uint32_t s_at, float sk, float lv, bool there, int64_t key, uint32_t tc,
+                                        int i) {
+  using C = Wide<D, SHARED>;
+  constexpr int R = C::R;
+  auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int quarter = warp & 3, half = warp >> 2, col = half * 32;
+  float t[32];
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {  // z, then z + log2(value scale)
+    tc_load32(s_at, t);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      t[c] = __fmul_rn(t[c], __fmul_rn(sk, st.zf[col + c])) + (k ? lv : 0.0f);
+      t[c] = there && key < st.sees[col + c] ? t[c] : -INFINITY;
+    }
+    st.best[k][half][quarter][lane] = column_max(t, lane);
+  }
+  if (tc > 0) mbar_wait(places<C>().p_empty, (tc - 1) & 1, &st.dead);
+  tc_after();
+  barrier_of(1 + half, 128);
+  if (quarter == 0) {
+    const int c = col + lane;
+    float x = st.mref[c], y = st.mpref[c];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x = fmaxf(x, st.best[0][half][k][lane]);
+      y = fmaxf(y, st.best[1][half][k][lane]);
+    }
+    st.lscale[c] = exp2f(st.mref[c] - x);
+    st.oscale[c] = exp2f(st.mpref[c] - y);
+    st.mref[c] = x;
+    st.mpref[c] = y;
+    st.rl[c] = x - y + kLift;
+    st.rf[c] = exp2f(x - y + kLift);
+    if (!(fabsf(x - y) <= 60.0f)) st.far_refs = 1;
+  }
+  barrier_of(1 + half, 128);
+  if (i > 0) {
+#pragma unroll 1
+    for (int pp = 0; pp < C::PP; ++pp) {
+      const uint32_t o_at = st.tmem + ((uint32_t)(quarter * 32) << 16) + C::O0 + pp * R + col;
+      tc_load32(o_at, t);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) t[c] *= st.oscale[col + c];
+      tc_store32(o_at, t);
+    }
+  }
+}
+
 // The softmax warps. A thread has key `mine` of each tile and 32 of the rows.
 // For a row: z = S * (key scale * zf) in log2 units, t = z - mref; the weight is
 // 2^(t + log2(value scale) + rl), rl = mref - mpref + 7, rf = 2^rl.
@@ -476,17 +530,8 @@ __device__ __noinline__ void wide_softmax() {
     const uint32_t s_at = tmem + lanes + C::S0 + b * R + col;
     const float2 sk2 = make_float2(sk, sk), lv2 = make_float2(lv, lv);
     float t[32];
-    auto hide = [&]() {  // rows that do not see this key
-#pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const int4 s4 = *reinterpret_cast<const int4*>(st.sees + col + c);
-        t[c] = there && key < s4.x ? t[c] : -INFINITY;
-        t[c + 1] = there && key < s4.y ? t[c + 1] : -INFINITY;
-        t[c + 2] = there && key < s4.z ? t[c + 2] : -INFINITY;
-        t[c + 3] = there && key < s4.w ? t[c + 3] : -INFINITY;
-      }
-    };
-    auto offsets = [&]() {  // t of all rows
+    bool o_free = false;  // O^T of the tile before is complete
+    for (int attempt = 0;; ++attempt) {
       tc_load32(s_at, t);
 #pragma unroll
       for (int c = 0; c < 32; c += 4) {
@@ -503,64 +548,24 @@ __device__ __noinline__ void wide_softmax() {
         t[c + 2] = tb.x;
         t[c + 3] = tb.y;
       }
-      if (mixed) hide();
-    };
-    offsets();
-    float mx = -INFINITY, mw = -INFINITY;
+      if (mixed) {  // rows that do not see this key
 #pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-      const float4 r4 = *reinterpret_cast<const float4*>(st.rl + col + c);
-      const float2 wa = add2_rn(make_float2(t[c], t[c + 1]), add2_rn(make_float2(r4.x, r4.y), lv2));
-      const float2 wb = add2_rn(make_float2(t[c + 2], t[c + 3]), add2_rn(make_float2(r4.z, r4.w), lv2));
-      mx = fmaxf(fmaxf(mx, t[c]), fmaxf(t[c + 1], fmaxf(t[c + 2], t[c + 3])));
-      mw = fmaxf(fmaxf(mw, wa.x), fmaxf(wa.y, fmaxf(wb.x, wb.y)));
-    }
-    bool o_free = false;  // O^T of the tile before is complete
-    if (barrier_any(1 + half, 128, mx > kSlackM || mw > kSlackW + kLift)) {
-      // Some weight passes its reference: raise both to the tile's maxima.
-      auto logits = [&](float add) {  // z, or z + log2(value scale)
-        tc_load32(s_at, t);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) t[c] = __fmul_rn(t[c], __fmul_rn(sk, st.zf[col + c])) + add;
-        if (mixed) hide();
-      };
-      logits(0.0f);
-      st.best[0][half][quarter][lane] = column_max(t, lane);
-      logits(lv);
-      st.best[1][half][quarter][lane] = column_max(t, lane);
-      if (tc > 0) mbar_wait(at.p_empty, (tc - 1) & 1, dead);
-      o_free = true;
-      tc_after();
-      barrier_of(1 + half, 128);
-      if (quarter == 0) {
-        const int c = col + lane;
-        float x = st.mref[c], y = st.mpref[c];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x = fmaxf(x, st.best[0][half][k][lane]);
-          y = fmaxf(y, st.best[1][half][k][lane]);
-        }
-        st.lscale[c] = exp2f(st.mref[c] - x);
-        st.oscale[c] = exp2f(st.mpref[c] - y);
-        st.mref[c] = x;
-        st.mpref[c] = y;
-        st.rl[c] = x - y + kLift;
-        st.rf[c] = exp2f(x - y + kLift);
-        if (!(fabsf(x - y) <= 60.0f)) st.far_refs = 1;
+        for (int c = 0; c < 32; ++c) t[c] = there && key < st.sees[col + c] ? t[c] : -INFINITY;
       }
-      barrier_of(1 + half, 128);
+      float mx = -INFINITY, mw = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 r4 = *reinterpret_cast<const float4*>(st.rl + col + c);
+        const float2 wa = add2_rn(make_float2(t[c], t[c + 1]), add2_rn(make_float2(r4.x, r4.y), lv2));
+        const float2 wb = add2_rn(make_float2(t[c + 2], t[c + 3]), add2_rn(make_float2(r4.z, r4.w), lv2));
+        mx = fmaxf(fmaxf(mx, t[c]), fmaxf(t[c + 1], fmaxf(t[c + 2], t[c + 3])));
+        mw = fmaxf(fmaxf(mw, wa.x), fmaxf(wa.y, fmaxf(wb.x, wb.y)));
+      }
+      if (attempt > 0 || !barrier_any(1 + half, 128, mx > kSlackM || mw > kSlackW + kLift)) break;
+      wide_raise<D, SHARED>(s_at, sk, lv, there, key, tc, i);
+      o_free = true;
 #pragma unroll
       for (int c = 0; c < 32; ++c) l[c] *= st.lscale[col + c];
-      if (i > 0) {
-        for (int pp = 0; pp < C::PP; ++pp) {
-          const uint32_t o_at = tmem + lanes + C::O0 + pp * R + col;
-          tc_load32(o_at, t);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) t[c] *= st.oscale[col + c];
-          tc_store32(o_at, t);
-        }
-      }
-      offsets();
     }
     tc_before();  // S^T is read
     __syncwarp();
@@ -715,6 +720,35 @@ __device__ __noinline__ void wide_result() {
   tc_before();
 }
 
+// What a producer's thread has stored of a panel: zeros where its mask says that
+// the key is not there, and (`nans`) zeros for NaN, which it takes note of.
+template <int D, bool SHARED>
+__device__ __noinline__ void wide_clean(uint8_t* panel, int chunk, int kb, int pw, uint32_t here, bool nans) {
+  using C = Wide<D, SHARED>;
+  auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
+#pragma unroll 1
+  for (int k = 0; k < C::KV; ++k) {
+    const int e = min(k * C::PW + pw, 31), c16 = ((chunk & 3) * 2) ^ ((e * 4 + kb) & 7);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      uint4* v = reinterpret_cast<uint4*>(panel + e * 512 + ((c16 ^ i) << 4));
+      uint4 x = *v;
+      auto clean = [&](uint32_t w) -> uint32_t {  // fp16: an e4m3 NaN is all ones but the sign
+        uint32_t keep = 0;
+        if ((w & 0x7C00u) != 0x7C00u) keep |= 0xFFFFu;
+        if ((w & 0x7C000000u) != 0x7C000000u) keep |= 0xFFFF0000u;
+        if (keep != 0xFFFFFFFFu) st.nan_rows = 1;
+        return w & keep;
+      };
+      if (!((here >> k) & 1))
+        x = make_uint4(0, 0, 0, 0);
+      else if (nans)
+        x = make_uint4(clean(x.x), clean(x.y), clean(x.z), clean(x.w));
+      *v = x;
+    }
+  }
+}
+
 // The producers. In a warp's load 4 keys x 8 chunks of 16 bytes; a store's
 // quarter warp covers 2 keys x 4 chunks, which the swizzle spreads over all
 // banks. Pages are looked up four planes at a time, a set ahead.
@@ -803,28 +837,6 @@ __device__ __noinline__ void wide_produce() {
       if (p >= total) break;
       const uint32_t pc = panels_done + p, slot = pc % C::NS;
       const int q = p / C::PP;
-      if (here[j] != (1u << C::KV) - 1) {
-#pragma unroll
-        for (int k = 0; k < C::KV; ++k)
-          if (!((here[j] >> k) & 1)) buf[j][k] = make_uint4(0, 0, 0, 0);
-      }
-      // Rows that only some queries see must not bring NaN into the product.
-      if ((SHARED || planes.value(q)) && (c0 + planes.tile(q) + 1) * 128 > least) {
-        uint32_t any = 0;
-        auto clean = [&](uint32_t& x) {
-          const uint32_t bad = nan_bytes(x);
-          any |= bad;
-          x &= ~bad;
-        };
-#pragma unroll
-        for (int k = 0; k < C::KV; ++k) {
-          clean(buf[j][k].x);
-          clean(buf[j][k].y);
-          clean(buf[j][k].z);
-          clean(buf[j][k].w);
-        }
-        if (any) st.nan_rows = 1;
-      }
       mbar_wait(at.empty + 8 * slot, ((pc / C::NS) & 1) ^ 1, dead);
       uint8_t* panel = ring + slot * C::PANEL;
 #pragma unroll
@@ -837,6 +849,10 @@ __device__ __noinline__ void wide_produce() {
         *reinterpret_cast<uint4*>(line + ((c16 ^ 1) << 4)) =
             make_uint4(lo_f16x2(x.z), hi_f16x2(x.z), lo_f16x2(x.w), hi_f16x2(x.w));
       }
+      // Missing rows become zeros, and rows that only some queries see must not
+      // bring NaN into the product: both rare.
+      const bool mixed = (SHARED || planes.value(q)) && (c0 + planes.tile(q) + 1) * 128 > least;
+      if (mixed || here[j] != (1u << C::KV) - 1) wide_clean<D, SHARED>(panel, chunk, kb, pw, here[j], mixed);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(at.full + 8 * slot);
