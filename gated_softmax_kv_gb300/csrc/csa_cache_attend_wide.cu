@@ -786,12 +786,18 @@ __device__ __noinline__ void wide_produce() {
   int32_t kib = locate16(0, pages), kib_next = -1;
   // Step k of this warp is keys 4 e .. 4 e + 3 of the tile, e = k PW + pw (the
   // last step of some warps is one too many and repeats the one before).
-  auto step = [&](int k) { return min(k * C::PW + pw, 31); };
+  int line[C::KV];  // where the step's first 8 values go in a panel
+#pragma unroll
+  for (int k = 0; k < C::KV; ++k) {
+    const int e = min(k * C::PW + pw, 31);
+    line[k] = (chunk >> 2) * C::SLAB + (e * 4 + kb) * 128 + ((((chunk & 3) * 2) ^ ((e * 4 + kb) & 7)) << 4);
+  }
+  const uint8_t* const pool = item.data;
+  const uint8_t* src[C::KV];
   uint4 buf[C::DEPTH][C::KV];
   uint32_t here[C::DEPTH];  // bit k: the key of step k is there; the others are loaded from
                             // the pool's start and stored as zeros
   int load_q = 0, load_pp = 0;
-  int32_t at16[C::KV];
   uint32_t there = 0;
   auto load = [&](uint4 (&v)[C::KV], uint32_t& mask) {  // the next panel of the sequence
     if (load_pp == 0) {
@@ -808,18 +814,17 @@ __device__ __noinline__ void wide_produce() {
       there = 0;
 #pragma unroll
       for (int k = 0; k < C::KV; ++k) {
-        const int e = step(k);
-        at16[k] = __shfl_sync(0xFFFFFFFFu, kib, p * 8 + (e >> 2));
-        if (at16[k] >= 0 && e * 4 + kb < left) there |= 1u << k;
-        at16[k] = (there >> k) & 1 ? at16[k] : 0;
+        const int e = min(k * C::PW + pw, 31);
+        const int32_t first = __shfl_sync(0xFFFFFFFFu, kib, p * 8 + (e >> 2));
+        const bool ok = first >= 0 && e * 4 + kb < left;
+        there |= (uint32_t)ok << k;
+        src[k] = pool + (ok ? (int64_t)first << 10 : 0) + ((e & 3) * 4 + kb) * D + chunk * 16;
       }
     }
     mask = there;
-    const uint8_t* data = item.data + kb * D + chunk * 16 + load_pp * 128;
 #pragma unroll
     for (int k = 0; k < C::KV; ++k)
-      v[k] = ld_stream(reinterpret_cast<const uint16_t*>(data + ((int64_t)at16[k] << 10) +
-                                                         (step(k) & 3) * 4 * D));
+      v[k] = ld_stream(reinterpret_cast<const uint16_t*>(src[k] + load_pp * 128));
     if (++load_pp == C::PP) {
       load_pp = 0;
       ++load_q;
@@ -829,7 +834,7 @@ __device__ __noinline__ void wide_produce() {
   for (int j = 0; j < C::DEPTH; ++j) load(buf[j], here[j]);
   const int total = planes.count() * C::PP;
   const uint32_t panels_done = item.panels_done;
-  uint8_t* const ring = at.ring_ptr + (chunk >> 2) * C::SLAB + kb * 128;
+  uint8_t* const ring = at.ring_ptr;
   for (int p0 = 0; p0 < total; p0 += C::DEPTH) {
 #pragma unroll
     for (int j = 0; j < C::DEPTH; ++j) {
@@ -842,17 +847,15 @@ __device__ __noinline__ void wide_produce() {
 #pragma unroll
       for (int k = 0; k < C::KV; ++k) {
         const uint4 x = buf[j][k];
-        const int key = step(k) * 4 + kb, c16 = ((chunk & 3) * 2) ^ (key & 7);
-        uint8_t* line = panel + step(k) * 512;
-        *reinterpret_cast<uint4*>(line + (c16 << 4)) =
+        *reinterpret_cast<uint4*>(panel + line[k]) =
             make_uint4(lo_f16x2(x.x), hi_f16x2(x.x), lo_f16x2(x.y), hi_f16x2(x.y));
-        *reinterpret_cast<uint4*>(line + ((c16 ^ 1) << 4)) =
+        *reinterpret_cast<uint4*>(panel + (line[k] ^ 16)) =
             make_uint4(lo_f16x2(x.z), hi_f16x2(x.z), lo_f16x2(x.w), hi_f16x2(x.w));
       }
       // Missing rows become zeros, and rows that only some queries see must not
       // bring NaN into the product: both rare.
       const bool mixed = (SHARED || planes.value(q)) && (c0 + planes.tile(q) + 1) * 128 > least;
-      if (mixed || here[j] != (1u << C::KV) - 1) wide_clean<D, SHARED>(panel, chunk, kb, pw, here[j], mixed);
+      if (mixed || here[j] != (1u << C::KV) - 1) wide_clean<D, SHARED>(panel + (chunk >> 2) * C::SLAB + kb * 128, chunk, kb, pw, here[j], mixed);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(at.full + 8 * slot);
