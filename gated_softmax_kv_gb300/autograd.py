@@ -65,8 +65,12 @@ class RopeFunction(torch.autograd.Function):
         ratio, offset, layout, amplitude, transpose = ctx.meta
         if grad.stride(-1) != 1:
             grad = grad.contiguous()
-        dx = RopeFunction.apply(grad, freqs, positions, cuc, ratio, offset, layout, amplitude,
-                                not transpose)
+        if grad.requires_grad and torch.is_grad_enabled():  # a graph of the gradient is wanted
+            dx = RopeFunction.apply(grad, freqs, positions, cuc, ratio, offset, layout, amplitude,
+                                    not transpose)
+        else:
+            dx = csa_rope(grad, freqs, positions, cu_seqlens_comp=cuc, ratio=ratio, offset=offset,
+                          layout=layout, amplitude=amplitude, transpose=not transpose)
         return dx, None, None, None, None, None, None, None, None
 
 

@@ -128,74 +128,114 @@ __device__ __forceinline__ Shared* shared_items(const AttendArgs& a, int workers
   return reinterpret_cast<Shared*>(a.ws + (int64_t)workers * 2 * ROWS * (D + 4));
 }
 
-// Joins the shared items, 64 vectors of four columns a CTA at a time: every
-// CTA reads the list, and all pieces of all items are spread over the grid.
-// Four threads take a quarter of the parts each (a long sequence alone on the
-// GPU has 152 parts), in the parts' order, and are added up in order.
+// Adds parts [i0, i1) of a shared item to (r, o), BATCH parts' loads at a time.
+template <int BATCH, int ROWS, int D>
+__device__ __forceinline__ void add_parts(const float* first, const float* rest, int i0, int i1, int at, int row,
+                                          RowStats& r, float4& o) {
+  constexpr int SLOT = ROWS * (D + 4);
+  for (int i = i0; i < i1; i += BATCH) {
+    float4 st[BATCH], x[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      st[k] = make_float4(kNone, kNone, 0.0f, 0.0f);
+      x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i + k < i1) {
+        const float* p = i + k == 0 ? first : rest + (int64_t)(i + k) * 2 * SLOT;
+        st[k] = __ldg(reinterpret_cast<const float4*>(p + ROWS * D + row * 4));
+        x[k] = __ldg(reinterpret_cast<const float4*>(p + at));
+      }
+    }
+    float m = r.m, mp = r.mp;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      m = fmaxf(m, st[k].x);
+      mp = fmaxf(mp, st[k].y);
+    }
+    r.l *= exp2f(r.m - m);
+    float f = exp2f(r.mp - mp);
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      r.l += st[k].z * exp2f(st[k].x - m);
+      f = exp2f(st[k].y - mp);
+      o.x = fmaf(x[k].x, f, o.x);
+      o.y = fmaf(x[k].y, f, o.y);
+      o.z = fmaf(x[k].z, f, o.z);
+      o.w = fmaf(x[k].w, f, o.w);
+    }
+    r.m = m;
+    r.mp = mp;
+  }
+}
+
+// Joins the shared items: every CTA reads the list, and all pieces of all items
+// are spread over the grid. An item of few parts (a batch: two or three) is
+// streamed, four columns a thread. Of a long one (a sequence alone on the GPU
+// has up to 152 parts) four threads take a quarter of the parts each, and are
+// added up in order.
 template <int D, int ROWS, bool HALF>
 __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a, int workers) {
-  constexpr int SLOT = ROWS * (D + 4), PIECES = ROWS * D / 256;
-  __shared__ int32_t list[512], count;
+  constexpr int SLOT = ROWS * (D + 4), QUADS = ROWS * D / 4, FEW = 12;
+  __shared__ int32_t list[512], start[513];
   __shared__ float4 sum[4][64];
   __shared__ float4 stat[4][64];
   grid_dependency_wait();
   allow_dependent_launch();
   const Shared* items = shared_items<ROWS, D>(a, workers);
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) {  // the list in the workers' order
-    int n = 0;
+  __shared__ int count;
+  if (threadIdx.x < 32) {  // the list in the workers' order, and each item's first piece
+    int n = 0, pieces = 0;
     for (int w = lane; w < ((workers + 31) & ~31); w += 32) {
-      const bool some = w < workers && items[w].parts > 0;
-      const unsigned who = __ballot_sync(0xFFFFFFFFu, some);
-      if (some) list[n + __popc(who & ((1u << lane) - 1))] = w;
+      const int parts = w < workers ? items[w].parts : 0;
+      const unsigned who = __ballot_sync(0xFFFFFFFFu, parts > 0);
+      int mine = parts > FEW ? QUADS / 64 : parts > 0 ? (QUADS + 255) / 256 : 0, before = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        if (lane >= o) before += y;
+      }
+      if (parts > 0) {
+        const int k = n + __popc(who & ((1u << lane) - 1));
+        list[k] = w;
+        start[k] = pieces + before - mine;
+      }
       n += __popc(who);
+      pieces += __shfl_sync(0xFFFFFFFFu, before, 31);
     }
-    if (lane == 0) count = n;
+    if (lane == 0) {
+      count = n;
+      start[n] = pieces;
+    }
   }
   __syncthreads();
-  const int v = threadIdx.x & 63, quarter = threadIdx.x >> 6;
-  for (int u = blockIdx.x; u < count * PIECES; u += gridDim.x) {
-    const int w = list[u / PIECES];
+  const int n = count, total = start[n];
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    int lo = 0, hi = n;  // the item that piece u belongs to
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= u)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int w = list[lo], piece = u - start[lo];
     const Shared item = items[w];
-    const int at = (u % PIECES) * 256 + v * 4, row = at / D, c = at % D;
-    const int each = (item.parts + 3) / 4, i0 = quarter * each, i1 = min(i0 + each, item.parts);
-    const float* ws = a.ws;
-    auto part = [&](int i) { return ws + ((int64_t)(w + i) * 2 + (i == 0)) * SLOT; };
+    const float* first = a.ws + ((int64_t)w * 2 + 1) * SLOT;  // the worker's slot 1, then slots 0
+    const float* rest = a.ws + (int64_t)w * 2 * SLOT;
     RowStats r = {kNone, kNone, 0.0f};
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = i0; i < i1; i += 8) {  // eight parts' loads at a time
-      float4 st[8], x[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float* p = part(min(i + k, i1 - 1));
-        st[k] = __ldg(reinterpret_cast<const float4*>(p + ROWS * D + row * 4));
-        x[k] = __ldg(reinterpret_cast<const float4*>(p + at));
-      }
-      float m = r.m, mp = r.mp;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (i + k >= i1) {
-          st[k] = make_float4(kNone, kNone, 0.0f, 0.0f);
-          x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-        m = fmaxf(m, st[k].x);
-        mp = fmaxf(mp, st[k].y);
-      }
-      r.l *= exp2f(r.m - m);
-      float f = exp2f(r.mp - mp);
-      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        r.l += st[k].z * exp2f(st[k].x - m);
-        f = exp2f(st[k].y - mp);
-        o.x = fmaf(x[k].x, f, o.x);
-        o.y = fmaf(x[k].y, f, o.y);
-        o.z = fmaf(x[k].z, f, o.z);
-        o.w = fmaf(x[k].w, f, o.w);
-      }
-      r.m = m;
-      r.mp = mp;
+    if (item.parts <= FEW) {
+      const int at = (piece * 256 + threadIdx.x) * 4, row = at / D;
+      if (at >= ROWS * D) continue;
+      add_parts<4, ROWS, D>(first, rest, 0, item.parts, at, row, r, o);
+      write_row<D, HALF>(a, row_of(a, item.s, item.tile, item.h, ROWS, row), at % D, r, o);
+      continue;
     }
+    const int v = threadIdx.x & 63, quarter = threadIdx.x >> 6;
+    const int at = (piece * 64 + v) * 4, row = at / D;
+    const int each = (item.parts + 3) / 4, i0 = quarter * each, i1 = min(i0 + each, item.parts);
+    add_parts<8, ROWS, D>(first, rest, i0, i1, at, row, r, o);
     __syncthreads();
     sum[quarter][v] = o;
     stat[quarter][v] = make_float4(r.m, r.mp, r.l, 0.0f);
@@ -213,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
         r.m = m;
         r.mp = mp;
       }
-      write_row<D, HALF>(a, row_of(a, item.s, item.tile, item.h, ROWS, row), c, r, o);
+      write_row<D, HALF>(a, row_of(a, item.s, item.tile, item.h, ROWS, row), at % D, r, o);
     }
   }
 }
@@ -221,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
 // The joining kernel behind a main kernel of `workers` CTAs.
 template <int D, int ROWS, bool HALF>
 cudaError_t launch_join(const AttendArgs& a, int workers, cudaStream_t stream) {
-  return launch_dependent(attend_join_kernel<D, ROWS, HALF>, dim3(152 * 4), dim3(kThreads), 0, stream, a,
+  return launch_dependent(attend_join_kernel<D, ROWS, HALF>, dim3(152 * 6), dim3(kThreads), 0, stream, a,
                           workers);
 }
 

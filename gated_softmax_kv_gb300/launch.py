@@ -2,29 +2,46 @@
 device, the stream, the life of the tensors and the overlap of an output."""
 from __future__ import annotations
 
-from .binding import _stream_handle
+from . import binding
 
 
-class on_device:
-    """Makes `dev` the current device for a call and `stream` (None: the
-    device's current stream) the one that outputs are allocated on. The common
-    case, everything current already, switches nothing."""
+class _Launch:
+    """A launch on the device's current stream, which is where everything lives already."""
 
-    def __init__(self, dev: int, stream=None):
+    __slots__ = ("handle",)
+
+    def __init__(self, handle: int):
+        self.handle = handle
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+    def used(self, *tensors):
+        pass
+
+
+class _GuardedLaunch(_Launch):
+    """A launch on another device than the current one, or on a stream of the
+    caller's choosing: both are current for the call, so that outputs are
+    allocated there, and the caching allocator is told which tensors the
+    stream uses before it may hand their memory on."""
+
+    __slots__ = ("_stream", "_guards", "_dev")
+
+    def __init__(self, dev: int, stream):
         import torch
-        self._stream = stream
-        self._guards = []
-        if torch.cuda.current_device() != dev:
-            self._guards.append(torch.cuda.device(dev))
+        self._stream, self._dev = stream, dev
+        self._guards = [torch.cuda.device(dev)]
         if stream is not None:
             self._guards.append(torch.cuda.stream(stream))
-        self._dev = dev
-        self.handle = 0
 
     def __enter__(self):
         for g in self._guards:
             g.__enter__()
-        self.handle = _stream_handle(self._stream, self._dev)
+        self.handle = binding._stream_handle(self._stream, self._dev)
         return self
 
     def __exit__(self, *exc):
@@ -33,12 +50,25 @@ class on_device:
         return False
 
     def used(self, *tensors):
-        """With a stream of the caller's choosing: the caching allocator must
-        not hand a tensor's memory on before that stream is done with it."""
         if self._stream is not None:
             for t in tensors:
                 if t is not None:
                     t.record_stream(self._stream)
+
+
+_current_device = None
+
+
+def on_device(dev: int, stream=None) -> _Launch:
+    """The launch of a call on device `dev` and `stream` (None: the device's
+    current stream), to be used as a context."""
+    global _current_device
+    if _current_device is None:
+        import torch
+        _current_device = torch.cuda.current_device
+    if stream is None and _current_device() == dev:
+        return _Launch(binding._stream_handle(None, dev))
+    return _GuardedLaunch(dev, stream)
 
 
 def _span(t):
@@ -52,7 +82,7 @@ def _span(t):
 
 def output_overlaps(out, x) -> bool:
     """Whether out and x share memory without being the same elements."""
-    if out.data_ptr() == x.data_ptr() and out.stride() == x.stride():
+    if out is x or out.data_ptr() == x.data_ptr() and out.stride() == x.stride():
         return False
     a, b = _span(out)
     c, d = _span(x)

@@ -9,11 +9,15 @@ from .binding import _check, _check_detail, _raise, load
 from .launch import on_device, output_overlaps
 
 LAYOUTS = {"interleaved": 0, "half": 1}
+_codes = {}
 
 
 def _dtype_code(dtype) -> Optional[int]:
-    import torch
-    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    """CSA_BF16, CSA_FP16, CSA_FP32; None for other types."""
+    if not _codes:
+        import torch
+        _codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    return _codes.get(dtype)
 
 
 def csa_rope(x, freqs, positions=None, *, cu_seqlens_comp=None, ratio: int = 1, offset: int = 0,
@@ -34,18 +38,24 @@ def csa_rope(x, freqs, positions=None, *, cu_seqlens_comp=None, ratio: int = 1, 
     import torch
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    code = _dtype_code(x.dtype)
+    dtype, shape, strides = x.dtype, x.shape, x.stride()
+    code = _dtype_code(dtype)
     if code is None:
-        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
-    if x.dim() not in (2, 3):
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {dtype}")
+    if len(shape) == 3:
+        T, heads, D = shape
+        xt, xh, last = strides
+    elif len(shape) == 2:
+        (T, D), heads = shape, 1
+        (xt, last), xh = strides, 0
+    else:
         raise ValueError("x must be [tokens, heads, head_dim] or [tokens, head_dim]")
     dev = x.get_device()
     if dev < 0:
-        _check_detail(x, "x", x.dtype, 0, None)
+        _check_detail(x, "x", dtype, 0, None)
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
     _check(freqs, "freqs", torch.float64, dev, 1)
-    T = x.shape[0]
     pos_ptr, bits, cu_ptr, nseq = None, 0, None, 0
     if positions is not None:
         if cu_seqlens_comp is not None:
@@ -55,37 +65,36 @@ def csa_rope(x, freqs, positions=None, *, cu_seqlens_comp=None, ratio: int = 1, 
         _check(positions, "positions", positions.dtype, dev, 1)
         if positions.shape[0] != T:
             raise ValueError("positions must be [tokens]")
-        pos_ptr, bits = positions.data_ptr(), 64 if positions.dtype == torch.int64 else 32
-        if T == 0:
-            pos_ptr = freqs.data_ptr()  # an empty tensor has no address; nothing is read
+        # an empty tensor has no address, and nothing of it is read
+        pos_ptr, bits = positions.data_ptr() if T else freqs.data_ptr(), 8 * positions.element_size()
     elif cu_seqlens_comp is not None:
         _check(cu_seqlens_comp, "cu_seqlens_comp", torch.int32, dev, 1)
-        if cu_seqlens_comp.shape[0] < 2:
+        nseq = cu_seqlens_comp.shape[0] - 1
+        if nseq < 1:
             raise ValueError("cu_seqlens_comp must be [num_seqs + 1]")
-        cu_ptr, nseq = cu_seqlens_comp.data_ptr(), cu_seqlens_comp.shape[0] - 1
+        cu_ptr = cu_seqlens_comp.data_ptr()
     else:
         raise ValueError("positions or cu_seqlens_comp must be given")
-    heads = x.shape[1] if x.dim() == 3 else 1
-    D = x.shape[-1]
     if heads < 1 or D < 1:
         raise ValueError("x has no heads or no columns")
-    if x.stride(-1) != 1 and D > 1:
+    if last != 1 and D > 1:
         raise ValueError("the last dimension of x must be contiguous")
     with on_device(dev, stream) as launch:
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = torch.empty(shape, dtype=dtype, device=x.device)
+            yt, yh = heads * D, D
         else:
-            if not isinstance(out, torch.Tensor) or out.dtype != x.dtype or out.get_device() != dev:
+            if not isinstance(out, torch.Tensor) or out.dtype != dtype or out.get_device() != dev:
                 raise TypeError("out must be a tensor of x's type and device")
-            if out.shape != x.shape or (out.stride(-1) != 1 and D > 1):
+            ys = out.stride()
+            if out.shape != shape or (ys[-1] != 1 and D > 1):
                 raise ValueError("out must have x's shape and a contiguous last dimension")
             if output_overlaps(out, x):
                 raise ValueError("out overlaps x: it must be x itself, with the same strides, or apart")
-        xs = (x.stride(0), x.stride(1)) if x.dim() == 3 else (x.stride(0), 0)
-        ys = (out.stride(0), out.stride(1)) if out.dim() == 3 else (out.stride(0), 0)
+            yt, yh = ys[0], ys[1] if len(ys) == 3 else 0
         st = load().csa_rope(x.data_ptr(), out.data_ptr(), freqs.data_ptr(), pos_ptr, bits, cu_ptr,
-                             nseq, ratio, T, heads, D, *xs, *ys, 2 * freqs.shape[0], offset,
-                             LAYOUTS[layout], code, amplitude, int(transpose), launch.handle)
+                             nseq, ratio, T, heads, D, xt, xh, yt, yh, 2 * freqs.shape[0], offset,
+                             LAYOUTS[layout], code, amplitude, transpose, launch.handle)
         if st != 0:
             _raise(st)
         launch.used(x, out, freqs, positions, cu_seqlens_comp)
