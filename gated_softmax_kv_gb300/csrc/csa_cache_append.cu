@@ -5,7 +5,7 @@
 // maximum of |x| over the new rows of the block, settles the block's scale,
 // requantises the rows that were there if the scale grew, and writes the new
 // ones, so nothing is shared between groups and no order matters. The rows
-// stay in registers between the two passes (16 vectors a thread; what is
+// stay in registers between the two passes (8 or 16 vectors a thread; what is
 // beyond is read again). Bound by memory: 2 bytes read and 1 written a value
 // for 16-bit rows.
 #include <cuda_fp16.h>
@@ -89,16 +89,16 @@ __device__ __forceinline__ void store_quantised(uint8_t* p, const uint4& w, floa
   }
 }
 
-// THREADS 256: a CTA owns a task; THREADS 32: each warp does.
+// THREADS 512: a CTA owns a task; THREADS 32: each of a CTA's 8 warps does.
 template <int DTYPE, int THREADS>
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(THREADS == 512 ? 512 : 256, 2) append_kernel(const AppendArgs a) {
   grid_dependency_wait();
   allow_dependent_launch();
   constexpr int N = Row16<DTYPE>::N;
-  constexpr int KEEP = 16;
-  __shared__ float warp_max[8];
-  const int lane = THREADS == 256 ? threadIdx.x : threadIdx.x & 31;
-  const int64_t unit = THREADS == 256 ? (int64_t)blockIdx.x
+  constexpr int KEEP = THREADS == 512 ? 8 : 16;
+  __shared__ float warp_max[THREADS / 32];
+  const int lane = THREADS == 512 ? threadIdx.x : threadIdx.x & 31;
+  const int64_t unit = THREADS == 512 ? (int64_t)blockIdx.x
                                       : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t task = unit / a.c.heads;
   const int head = (int)(unit - task * a.c.heads);
@@ -162,11 +162,11 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   float old = 0.0f;
   const bool begun = first > begin;
   if (begun) old = *scale;
-  if constexpr (THREADS == 256) {
+  if constexpr (THREADS == 512) {
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
     __syncthreads();  // also: every thread has read the old scale
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, warp_max[w]);
+    for (int w = 0; w < THREADS / 32; ++w) m = fmaxf(m, warp_max[w]);
   } else {
     __syncwarp();
   }
@@ -200,11 +200,11 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
 
 template <int DTYPE>
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
-  // A block of 8192 values and more keeps 256 threads busy; smaller ones
+  // A block of 8192 values and more keeps a CTA's threads busy; smaller ones
   // would leave most of them idle and take a warp.
   const int64_t units = a.tasks * a.c.heads;
   if (((int64_t)a.c.d << a.c.block_bits) >= 8192)
-    return launch_dependent(append_kernel<DTYPE, 256>, dim3((unsigned)units), dim3(256), 0, stream,
+    return launch_dependent(append_kernel<DTYPE, 512>, dim3((unsigned)units), dim3(512), 0, stream,
                             a);
   return launch_dependent(append_kernel<DTYPE, 32>, dim3((unsigned)((units + 7) / 8)), dim3(256), 0,
                           stream, a);

@@ -182,34 +182,48 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
   grid_dependency_wait();
   allow_dependent_launch();
   const Shared* items = shared_items<ROWS, D>(a, workers);
-  const int lane = threadIdx.x & 31;
-  __shared__ int count;
-  if (threadIdx.x < 32) {  // the list in the workers' order, and each item's first piece
-    int n = 0, pieces = 0;
-    for (int w = lane; w < ((workers + 31) & ~31); w += 32) {
-      const int parts = w < workers ? items[w].parts : 0;
-      const unsigned who = __ballot_sync(0xFFFFFFFFu, parts > 0);
-      int mine = parts > FEW ? QUADS / 64 : parts > 0 ? (QUADS + 255) / 256 : 0, before = mine;
+  __shared__ int2 sums[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // The list in the workers' order, and each item's first piece: two workers a thread.
+  int parts[2];
+  int2 before = make_int2(0, 0);  // items and pieces up to this thread's last
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, before, o);
-        if (lane >= o) before += y;
-      }
-      if (parts > 0) {
-        const int k = n + __popc(who & ((1u << lane) - 1));
-        list[k] = w;
-        start[k] = pieces + before - mine;
-      }
-      n += __popc(who);
-      pieces += __shfl_sync(0xFFFFFFFFu, before, 31);
-    }
-    if (lane == 0) {
-      count = n;
-      start[n] = pieces;
+  for (int k = 0; k < 2; ++k) {
+    const int w = threadIdx.x * 2 + k;
+    parts[k] = w < workers ? __ldg(&items[w].parts) : 0;
+    before.x += parts[k] > 0;
+    before.y += parts[k] > FEW ? QUADS / 64 : parts[k] > 0 ? (QUADS + 255) / 256 : 0;
+  }
+  const int2 mine = before;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xFFFFFFFFu, before.x, o), y = __shfl_up_sync(0xFFFFFFFFu, before.y, o);
+    if (lane >= o) {
+      before.x += x;
+      before.y += y;
     }
   }
+  if (lane == 31) sums[warp] = before;
   __syncthreads();
-  const int n = count, total = start[n];
+  int n = 0, total = 0;
+#pragma unroll
+  for (int k = 0; k < kThreads / 32; ++k) {
+    if (k < warp) {
+      before.x += sums[k].x;
+      before.y += sums[k].y;
+    }
+    n += sums[k].x;
+    total += sums[k].y;
+  }
+  int at_item = before.x - mine.x, at_piece = before.y - mine.y;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (parts[k] > 0) {
+      list[at_item] = threadIdx.x * 2 + k;
+      start[at_item++] = at_piece;
+      at_piece += parts[k] > FEW ? QUADS / 64 : (QUADS + 255) / 256;
+    }
+  __syncthreads();
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     int lo = 0, hi = n;  // the item that piece u belongs to
     while (hi - lo > 1) {

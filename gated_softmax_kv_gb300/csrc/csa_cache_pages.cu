@@ -190,13 +190,42 @@ struct ReserveArgs {
   int32_t* count;
 };
 
-// Entries [lo, hi) of its table row that request i will write to.
-__device__ __forceinline__ void write_range(const ReserveArgs& a, int i, int* s, int64_t* lo,
-                                            int64_t* hi) {
-  *s = a.seqs[i];
-  const int64_t len = max(a.lens[*s], 0), rows = a.rows[i];
-  *lo = len >> a.c.page_bits;
-  *hi = rows > 0 ? (len + rows + (1 << a.c.page_bits) - 1) >> a.c.page_bits : *lo;
+// Entries [lo, hi) of its table row that a request will write to.
+struct Reach {
+  int32_t s;
+  int64_t lo, hi, len;
+};
+__device__ __forceinline__ Reach reach_of(const ReserveArgs& a, int i) {
+  Reach r;
+  r.s = a.seqs[i];
+  const int64_t rows = a.rows[i];
+  r.len = max(a.lens[r.s], 0);
+  r.lo = r.len >> a.c.page_bits;
+  r.hi = rows > 0 ? (r.len + rows + (1 << a.c.page_bits) - 1) >> a.c.page_bits : r.lo;
+  return r;
+}
+constexpr int kShort = 4;  // entries that a thread goes through by itself
+
+// Calls f(request, reach, first entry, stride, group) for every request: a
+// thread by itself for a short one (a decoding step's: all of them at once), a
+// warp for a long one. `group` is 1 or 32, the threads that share the request.
+template <class F>
+__device__ __forceinline__ void for_requests(const ReserveArgs& a, F f) {
+  const int lane = threadIdx.x & 31;
+  for (int i0 = (threadIdx.x >> 5) * 32; i0 < a.n; i0 += kPlanThreads) {
+    const int i = i0 + lane;
+    Reach r = {0, 0, 0, 0};
+    if (i < a.n) r = reach_of(a, i);
+    const bool longer = r.hi - r.lo > kShort;
+    if (i < a.n && !longer) f(i, r, r.lo, 1, 1);
+    __syncwarp();
+    for (unsigned left = __ballot_sync(0xFFFFFFFFu, longer); left; left &= left - 1) {
+      const int j = i0 + __ffs(left) - 1;
+      const Reach q = reach_of(a, j);
+      f(j, q, q.lo + lane, 32, 32);
+      __syncwarp();
+    }
+  }
 }
 
 __device__ __forceinline__ bool in_pool(const ReserveArgs& a, int page) {
@@ -216,8 +245,6 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const ReserveArgs
   allow_dependent_launch();
   extern __shared__ uint32_t seen[];
   __shared__ int found, copies;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kWarps = kPlanThreads / 32;
   for (int i = threadIdx.x; i < (a.nseq + 31) / 32; i += kPlanThreads) seen[i] = 0;
   if (threadIdx.x == 0) {
     found = 0;
@@ -244,12 +271,9 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const ReserveArgs
   }
   // requests that write each shared page: cleared, then counted
   for (int pass = 0; pass < 2; ++pass) {
-    for (int i = warp; i < a.n; i += kWarps) {
-      int s;
-      int64_t lo, hi;
-      write_range(a, i, &s, &lo, &hi);
-      for (int64_t e = lo + lane; e < hi; e += 32) {
-        const int page = a.table[(int64_t)s * a.max_pages + e];
+    for_requests(a, [&](int i, const Reach& r, int64_t e, int step, int) {
+      for (; e < r.hi; e += step) {
+        const int page = a.table[(int64_t)r.s * a.max_pages + e];
         if (!in_pool(a, page) || a.refs[page] <= 1) continue;
         if (pass == 0) {
           a.asked[page] = 0;
@@ -259,16 +283,14 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const ReserveArgs
           atomicMax(a.last + page, i + 1);
         }
       }
-    }
+    });
     __syncthreads();
   }
   // pages that each request takes
-  for (int i = warp; i < a.n; i += kWarps) {
-    int s, take = 0;
-    int64_t lo, hi;
-    write_range(a, i, &s, &lo, &hi);
-    for (int64_t e = lo + lane; e < hi; e += 32) {
-      const int page = a.table[(int64_t)s * a.max_pages + e];
+  for_requests(a, [&](int i, const Reach& r, int64_t e, int step, int group) {
+    int take = 0;
+    for (; e < r.hi; e += step) {
+      const int page = a.table[(int64_t)r.s * a.max_pages + e];
       if (page < 0)
         ++take;
       else if (!in_pool(a, page))
@@ -276,9 +298,9 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const ReserveArgs
       else
         take += replaces(a, i, page, a.refs[page]);
     }
-    take = __reduce_add_sync(0xFFFFFFFFu, take);
-    if (lane == 0) a.need[i] = take;
-  }
+    if (group == 32) take = __reduce_add_sync(0xFFFFFFFFu, take);
+    if (group == 1 || (threadIdx.x & 31) == 0) a.need[i] = take;
+  });
   if (bits) atomicOr(a.status, bits);
   __syncthreads();
   int64_t wanted = 0;
@@ -317,35 +339,31 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const ReserveArgs
   }
   // Every request has to see the counts from before the call: the new table
   // entries and copies first, the counts after the barrier.
-  for (int i = warp; i < a.n; i += kWarps) {
-    int s;
-    int64_t lo, hi;
-    write_range(a, i, &s, &lo, &hi);
-    const int64_t len = max(a.lens[s], 0);
+  for_requests(a, [&](int i, const Reach& r, int64_t e, int step, int group) {
     int at = a.need[i];
-    for (int64_t e0 = lo; e0 < hi; e0 += 32) {
-      const int64_t e = e0 + lane;
+    const unsigned below = group == 32 ? (1u << (threadIdx.x & 31)) - 1 : 0;
+    for (int64_t e0 = r.lo; e0 < r.hi; e0 += step, e += step) {
       int page = -1;
       bool take = false, shared = false;
-      if (e < hi) {
-        page = a.table[(int64_t)s * a.max_pages + e];
+      if (e < r.hi) {
+        page = a.table[(int64_t)r.s * a.max_pages + e];
         shared = in_pool(a, page) && replaces(a, i, page, a.refs[page]);
         take = page < 0 || shared;
       }
-      const unsigned takers = __ballot_sync(0xFFFFFFFFu, take);
+      const unsigned takers = group == 32 ? __ballot_sync(0xFFFFFFFFu, take) : take;
       if (take) {
-        const int got_page = a.fresh[at + __popc(takers & ((1u << lane) - 1))];
-        a.table[(int64_t)s * a.max_pages + e] = got_page;
+        const int got_page = a.fresh[at + __popc(takers & below)];
+        a.table[(int64_t)r.s * a.max_pages + e] = got_page;
         if (shared) {
           // a page without rows is only replaced
           const int k = atomicAdd(&copies, 1);
           a.src[k] = page;
-          a.dst[k] = (e << a.c.page_bits) < len ? got_page : page;
+          a.dst[k] = (e << a.c.page_bits) < r.len ? got_page : page;
         }
       }
       at += __popc(takers);
     }
-  }
+  });
   __syncthreads();
   for (int k = threadIdx.x; k < copies; k += kPlanThreads) atomicSub(a.refs + a.src[k], 1);
   for (int64_t k = threadIdx.x; k < wanted; k += kPlanThreads) a.refs[a.fresh[k]] = 1;

@@ -32,6 +32,7 @@ struct RopeArgs {
   int64_t tokens;
   int64_t xt, xh, yt, yh;  // strides in elements
   int32_t position_bits, nseq, ratio;
+  int32_t search;  // the largest power of two below nseq (0: one segment)
   int32_t heads, d, rope, offset;
   float amplitude;
   bool transpose, in_place;
@@ -109,6 +110,45 @@ struct Vec<float> {
   }
 };
 
+// One pair of a head, as it lies in memory: next to one another or half a part
+// apart.
+template <typename E, bool HALF>
+__device__ __forceinline__ void load_pair(const E* p, int half, uint32_t& a, uint32_t& b) {
+  if constexpr (sizeof(E) == 4) {
+    if constexpr (HALF) {
+      a = __float_as_uint(p[0]);
+      b = __float_as_uint(p[half]);
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      a = v.x;
+      b = v.y;
+    }
+  } else if constexpr (HALF) {
+    a = reinterpret_cast<const uint16_t*>(p)[0];
+    b = reinterpret_cast<const uint16_t*>(p)[half];
+  } else {
+    a = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+template <typename E, bool HALF>
+__device__ __forceinline__ float2 pair_value(uint32_t a, uint32_t b) {
+  if constexpr (sizeof(E) == 4)
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
+  else
+    return Elem<E>::unpack(HALF ? a | (b << 16) : a);
+}
+template <typename E, bool HALF>
+__device__ __forceinline__ void store_pair(E* p, int half, float2 v) {
+  if constexpr (HALF) {
+    Elem<E>::store(p, v.x);
+    Elem<E>::store(p + half, v.y);
+  } else if constexpr (sizeof(E) == 4) {
+    *reinterpret_cast<float2*>(p) = v;
+  } else {
+    *reinterpret_cast<uint32_t*>(p) = Elem<E>::pack(v);
+  }
+}
+
 // f / (2 pi) modulo 1 as a 64-bit fraction, from the bits of f: with f =
 // m 2^(e-52), m a 53-bit integer, and K = floor(2^66 / (2 pi)), the product's
 // high word (m 2^11) K / 2^64 times 2^(e-1) is 2^64 f / (2 pi), within 2^-61
@@ -138,39 +178,46 @@ __device__ __forceinline__ int64_t position_of(const RopeArgs& a, int64_t t) {
   if (a.positions)
     return a.position_bits == 64 ? __ldg(static_cast<const long long*>(a.positions) + t)
                                  : (int64_t)__ldg(static_cast<const int32_t*>(a.positions) + t);
-  if (t >= __ldg(a.cu + a.nseq)) return 0;
-  int lo = 0, hi = a.nseq;  // last s with cu[s] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.cu + mid) <= t)
-      lo = mid;
-    else
-      hi = mid;
+  // the last s with cu[s] <= t, by halving steps of the same number for every
+  // row, so that several rows' searches run side by side
+  int lo = 0;
+  int64_t base = __ldg(a.cu);
+  for (int step = a.search; step; step >>= 1) {
+    const int mid = lo + step;
+    if (mid < a.nseq) {
+      const int64_t at = __ldg(a.cu + mid);
+      if (at <= t) {
+        lo = mid;
+        base = at;
+      }
+    }
   }
-  return (t - __ldg(a.cu + lo)) * a.ratio;
+  return t >= __ldg(a.cu + a.nseq) ? 0 : (t - base) * a.ratio;
 }
 
-// Vector kernel: 16-byte aligned rows, part and strides. A chunk is one
-// vector of interleaved pairs, two vectors half a part apart, or (out of
-// place) one vector to copy; a thread has the same chunk in every row that it
-// visits. It takes T tokens x H heads at a time and issues all their loads
-// before it works out the angles: with one load a thread in flight a pack of
-// 66533 rows of 512 bf16 columns took 58 us, as much as two copies.
-template <typename E, bool HALF, int T, int H>
+// Vector kernel: 16-byte aligned rows, part and strides. A chunk is PAIRS pairs
+// of the turned part (16 bytes of interleaved pairs, or twice 16 bytes half a
+// part apart, where heads share the sines; else one pair, so that a warp's
+// lanes share out the sines of a row) or, out of place, one vector to copy; a
+// thread has the same chunk in every row that it visits. It takes T tokens x H
+// heads at a time and issues all their loads before it works out the angles.
+// A pack of 66533 rows of 512 bf16 columns, 64 of them turned: 58 us with one
+// load a thread in flight and 16 bytes a turning thread, 44 us with four.
+template <typename E, bool HALF, int T, int H, int PAIRS>
 __global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int32_t chunks, int32_t groups) {
   grid_dependency_wait();
   allow_dependent_launch();
   constexpr int N = Vec<E>::N;
-  constexpr int PAIRS = HALF ? N : N / 2;
+  constexpr bool WIDE = PAIRS > 1;
   const uint32_t id = blockIdx.x * blockDim.x + threadIdx.x;
   const uint32_t lanes = gridDim.x * blockDim.x / chunks;  // whole rows of chunks
   const uint32_t first = id / chunks;
   const int c = (int)(id - first * chunks);
   if (first >= lanes) return;
-  const int turned = HALF ? a.rope / (2 * N) : a.rope / N;
+  const int turned = a.rope / (2 * PAIRS);
   const bool turns = c < turned;
   const int k = (c - turned) * N;
-  const int col = turns ? a.offset + c * N : k < a.offset ? k : k + a.rope;
+  const int col = turns ? a.offset + c * (HALF ? PAIRS : 2 * PAIRS) : k < a.offset ? k : k + a.rope;
   const int64_t items = a.tokens * groups;
   const E* x = static_cast<const E*>(a.x) + col;
   E* y = static_cast<E*>(a.y) + col;
@@ -193,8 +240,12 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int32_t
       for (int h = 0; h < H; ++h) {
         if (u < items && head[j] + h < a.heads) {
           const E* p = x + token[j] * a.xt + (head[j] + h) * a.xh;
-          v[j][h] = *reinterpret_cast<const uint4*>(p);
-          if (HALF && turns) w[j][h] = *reinterpret_cast<const uint4*>(p + a.rope / 2);
+          if (!WIDE && turns) {
+            load_pair<E, HALF>(p, a.rope / 2, v[j][h].x, v[j][h].y);
+          } else {
+            v[j][h] = *reinterpret_cast<const uint4*>(p);
+            if (HALF && turns) w[j][h] = *reinterpret_cast<const uint4*>(p + a.rope / 2);
+          }
         }
       }
     }
@@ -208,9 +259,15 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int32_t
         for (int i = 0; i < PAIRS; ++i) turn_of(f[i], pos, a.amplitude, sign, &cs[i], &sn[i]);
 #pragma unroll
         for (int h = 0; h < H; ++h) {
+          if constexpr (!WIDE) {
+            const float2 p = pair_value<E, HALF>(v[j][h].x, v[j][h].y);
+            v[j][h].x = __float_as_uint(fmaf(-p.y, sn[0], p.x * cs[0]));
+            v[j][h].y = __float_as_uint(fmaf(p.x, sn[0], p.y * cs[0]));
+            continue;
+          }
           float p[N];
           Vec<E>::unpack(v[j][h], p);
-          if constexpr (HALF) {
+          if constexpr (HALF && WIDE) {
             float q[N], va[N], wb[N];
             Vec<E>::unpack(w[j][h], q);
 #pragma unroll
@@ -220,7 +277,7 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int32_t
             }
             v[j][h] = Vec<E>::pack(va);
             w[j][h] = Vec<E>::pack(wb);
-          } else {
+          } else if constexpr (WIDE) {
             float o[N];
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) {
@@ -238,8 +295,13 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int32_t
       for (int h = 0; h < H; ++h)
         if (it + (int64_t)j * lanes < items && head[j] + h < a.heads) {
           E* p = y + token[j] * a.yt + (head[j] + h) * a.yh;
-          *reinterpret_cast<uint4*>(p) = v[j][h];
-          if (HALF && turns) *reinterpret_cast<uint4*>(p + a.rope / 2) = w[j][h];
+          if (!WIDE && turns) {
+            store_pair<E, HALF>(p, a.rope / 2,
+                                make_float2(__uint_as_float(v[j][h].x), __uint_as_float(v[j][h].y)));
+          } else {
+            *reinterpret_cast<uint4*>(p) = v[j][h];
+            if (HALF && turns) *reinterpret_cast<uint4*>(p + a.rope / 2) = w[j][h];
+          }
         }
   }
 }
@@ -284,21 +346,23 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
   const uintptr_t bytes = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y);
   const int64_t cols = a.xt | a.xh | a.yt | a.yh | a.offset | a.d | (HALF ? a.rope / 2 : a.rope);
   if (bytes % 16 == 0 && cols % N == 0) {
-    const int chunks = (HALF ? a.rope / (2 * N) : a.rope / N) + (a.in_place ? 0 : (a.d - a.rope) / N);
+    constexpr int WIDE = HALF ? N : N / 2;
+    const int copied = a.in_place ? 0 : (a.d - a.rope) / N;
     // Heads share a token's sines: four at a time where that still leaves every
     // SM its threads, else (few heads, or a decoding step) one.
     const int64_t full = (int64_t)152 * 1024;
-    const bool four = a.heads >= 4 && a.tokens * ((a.heads + 3) / 4) * chunks >= full;
+    const bool four = a.heads >= 4 && a.tokens * ((a.heads + 3) / 4) * (a.rope / (2 * WIDE) + copied) >= full;
     const int groups = four ? (a.heads + 3) / 4 : a.heads;
+    const int chunks = a.rope / (four ? 2 * WIDE : 2) + copied;
     const bool some = !four && a.tokens * groups * chunks >= 4 * full;  // four tokens a thread
     int64_t blocks = (a.tokens * groups * chunks + 255) / 256;
     const int64_t most = 152 * (HALF ? 4 : 6);  // as many as are resident
     if (blocks > most) blocks = most;
     const int64_t least = (chunks + 255) / 256;  // at least one whole row of chunks
     if (blocks < least) blocks = least;
-    auto* kernel = four ? rope_vec_kernel<T, HALF, 1, 4>
-                   : some ? rope_vec_kernel<T, HALF, HALF ? 2 : 4, 1>
-                          : rope_vec_kernel<T, HALF, 1, 1>;
+    auto* kernel = four ? rope_vec_kernel<T, HALF, 1, 4, WIDE>
+                   : some ? rope_vec_kernel<T, HALF, 4, 1, 1>
+                          : rope_vec_kernel<T, HALF, 1, 1, 1>;
     return launch_dependent(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a, (int32_t)chunks,
                             (int32_t)groups);
   }
@@ -376,6 +440,8 @@ extern "C" csa_status_t csa_rope(const void* x, void* y, const double* freqs, co
   a.position_bits = position_bits;
   a.nseq = num_seqs;
   a.ratio = ratio;
+  a.search = 0;
+  for (int64_t step = 1; !positions && step < num_seqs; step *= 2) a.search = (int32_t)step;
   a.heads = heads;
   a.d = head_dim;
   a.rope = rope_dim;
