@@ -7,10 +7,8 @@
 // position, with no fp64 arithmetic per element (fp64 runs at 1/64 of the
 // fp32 rate here). The top 32 bits go through sincospif.
 //
-// The kernel is a copy with some arithmetic: it is bound by memory. A thread
-// keeps one column vector of the head for its whole loop, so F is worked out
-// once per thread, and the sine and cosine of a token are shared by the heads
-// that a thread takes.
+// The kernels are copies with some arithmetic, bound by memory. A thread keeps
+// its columns for its whole loop, so F is worked out once per thread.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -195,20 +193,17 @@ __device__ __forceinline__ int64_t position_of(const RopeArgs& a, int64_t t) {
   return t >= __ldg(a.cu + a.nseq) ? 0 : (t - base) * a.ratio;
 }
 
-// Vector kernel: 16-byte aligned rows, part and strides. A chunk is PAIRS pairs
-// of the turned part (16 bytes of interleaved pairs, or twice 16 bytes half a
-// part apart, where heads share the sines; else one pair, so that a warp's
-// lanes share out the sines of a row) or, out of place, one vector to copy; a
-// thread has the same chunk in every row that it visits. It takes T tokens x H
-// heads at a time and issues all their loads before it works out the angles.
-// A pack of 66533 rows of 512 bf16 columns, 64 of them turned: 58 us with one
-// load a thread in flight and 16 bytes a turning thread, 44 us with four.
-template <typename E, bool HALF, int T, int H, int PAIRS>
-__global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int32_t chunks, int32_t groups) {
+// Vector kernel where heads share sines: 16-byte aligned rows, part and
+// strides. A chunk is 16 bytes of interleaved pairs, twice 16 bytes half a part
+// apart, or (out of place) one vector to copy; a thread has the same chunk of
+// four heads of every token that it visits, and issues their loads before it
+// works out the angles.
+template <typename E, bool HALF>
+__global__ void __launch_bounds__(256) rope_heads_kernel(const RopeArgs a, int32_t chunks, int32_t groups) {
   grid_dependency_wait();
   allow_dependent_launch();
-  constexpr int N = Vec<E>::N;
-  constexpr bool WIDE = PAIRS > 1;
+  constexpr int N = Vec<E>::N, H = 4;
+  constexpr int PAIRS = HALF ? N : N / 2;
   const uint32_t id = blockIdx.x * blockDim.x + threadIdx.x;
   const uint32_t lanes = gridDim.x * blockDim.x / chunks;  // whole rows of chunks
   const uint32_t first = id / chunks;
@@ -217,7 +212,7 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int32_t
   const int turned = a.rope / (2 * PAIRS);
   const bool turns = c < turned;
   const int k = (c - turned) * N;
-  const int col = turns ? a.offset + c * (HALF ? PAIRS : 2 * PAIRS) : k < a.offset ? k : k + a.rope;
+  const int col = turns ? a.offset + c * N : k < a.offset ? k : k + a.rope;
   const int64_t items = a.tokens * groups;
   const E* x = static_cast<const E*>(a.x) + col;
   E* y = static_cast<E*>(a.y) + col;
@@ -227,82 +222,145 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int32_t
     for (int i = 0; i < PAIRS; ++i) f[i] = turns_of(__ldg(a.freqs + c * PAIRS + i));
   }
   const float sign = a.transpose ? -1.0f : 1.0f;
-  for (int64_t it = first; it < items; it += (int64_t)lanes * T) {
-    uint4 v[T][H], w[T][H];
-    int64_t token[T];
-    int head[T];
+  for (int64_t it = first; it < items; it += lanes) {
+    const int64_t token = it / groups;
+    const int head = (int)(it - token * groups) * H;
+    uint4 v[H], w[H];
 #pragma unroll
-    for (int j = 0; j < T; ++j) {
-      const int64_t u = it + (int64_t)j * lanes;
-      token[j] = groups == 1 ? u : u / groups;
-      head[j] = (int)(u - token[j] * groups) * H;
+    for (int h = 0; h < H; ++h)
+      if (head + h < a.heads) {
+        const E* p = x + token * a.xt + (head + h) * a.xh;
+        v[h] = *reinterpret_cast<const uint4*>(p);
+        if (HALF && turns) w[h] = *reinterpret_cast<const uint4*>(p + a.rope / 2);
+      }
+    if (turns) {
+      const int64_t pos = position_of(a, token);
+      float cs[PAIRS], sn[PAIRS];
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) turn_of(f[i], pos, a.amplitude, sign, &cs[i], &sn[i]);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        if (u < items && head[j] + h < a.heads) {
-          const E* p = x + token[j] * a.xt + (head[j] + h) * a.xh;
-          if (!WIDE && turns) {
-            load_pair<E, HALF>(p, a.rope / 2, v[j][h].x, v[j][h].y);
-          } else {
-            v[j][h] = *reinterpret_cast<const uint4*>(p);
-            if (HALF && turns) w[j][h] = *reinterpret_cast<const uint4*>(p + a.rope / 2);
+        float p[N];
+        Vec<E>::unpack(v[h], p);
+        if constexpr (HALF) {
+          float q[N], va[N], wb[N];
+          Vec<E>::unpack(w[h], q);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            va[i] = fmaf(-q[i], sn[i], p[i] * cs[i]);
+            wb[i] = fmaf(p[i], sn[i], q[i] * cs[i]);
           }
+          v[h] = Vec<E>::pack(va);
+          w[h] = Vec<E>::pack(wb);
+        } else {
+          float o[N];
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) {
+            o[2 * i] = fmaf(-p[2 * i + 1], sn[i], p[2 * i] * cs[i]);
+            o[2 * i + 1] = fmaf(p[2 * i], sn[i], p[2 * i + 1] * cs[i]);
+          }
+          v[h] = Vec<E>::pack(o);
         }
       }
     }
-    if (turns) {
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (head + h < a.heads) {
+        E* p = y + token * a.yt + (head + h) * a.yh;
+        *reinterpret_cast<uint4*>(p) = v[h];
+        if (HALF && turns) *reinterpret_cast<uint4*>(p + a.rope / 2) = w[h];
+      }
+  }
+}
+
+// The position of a token, worked out by a warp: segments are searched 32 at a
+// time.
+__device__ __forceinline__ int64_t warp_position(const RopeArgs& a, int64_t t, int lane) {
+  if (a.positions) return position_of(a, t);
+  int lo = 0, span = a.nseq;  // the segment is in [lo, lo + span)
+  while (span > 1) {
+    const int step = (span + 31) / 32, at = lo + lane * step;
+    const bool before = lane * step < span && __ldg(a.cu + at) <= t;
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, before);
+    const int k = who ? 31 - __clz(who) : 0;
+    span = min(step, span - k * step);
+    lo += k * step;
+  }
+  return t >= __ldg(a.cu + a.nseq) ? 0 : (t - __ldg(a.cu + lo)) * a.ratio;
+}
+
+// Rows that share nothing (one head, or a decoding step): whole warps turn 32
+// pairs of T rows at a time, a lane a pair, so that a row's sines cost one pass
+// of a warp; the other half of the CTA's warps copy what is not turned, 16 bytes
+// a thread and T of them in flight. One kernel whose lanes did either cost 455
+// instructions a warp and row of 512 bf16 columns, 64 of them turned (58 us for
+// 66533 rows); this one about a third of that.
+template <typename E, bool HALF, int T>
+__global__ void __launch_bounds__(256) rope_rows_kernel(const RopeArgs a, int32_t blocks_of_pairs, int32_t copied) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  constexpr int N = Vec<E>::N;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t rows = a.tokens * a.heads;
+  const int turners = copied ? 4 : 8;  // warps of the CTA
+  if (warp < turners) {
+    const int64_t id = (int64_t)blockIdx.x * turners + warp, warps = (int64_t)gridDim.x * turners;
+    // each warp keeps one block of pairs
+    const int64_t each = warps / blocks_of_pairs;
+    const int block = (int)(id / (each > 0 ? each : 1));
+    if (each == 0 || block >= blocks_of_pairs) return;
+    const int pair = block * 32 + lane, pairs = a.rope / 2;
+    const bool on = pair < pairs;
+    const uint64_t f = on ? turns_of(__ldg(a.freqs + pair)) : 0;
+    const int col = a.offset + (HALF ? pair : 2 * pair);
+    const E* x = static_cast<const E*>(a.x) + col;
+    E* y = static_cast<E*>(a.y) + col;
+    const float sign = a.transpose ? -1.0f : 1.0f;
+    for (int64_t r = (id - block * each) * T; r < rows; r += each * T) {
+      uint32_t va[T], vb[T];
+      int64_t token[T];
+      int head[T];
 #pragma unroll
       for (int j = 0; j < T; ++j) {
-        if (it + (int64_t)j * lanes >= items) break;
-        const int64_t pos = position_of(a, token[j]);
-        float cs[PAIRS], sn[PAIRS];
+        const int64_t row = min(r + j, rows - 1);
+        token[j] = a.heads == 1 ? row : row / a.heads;
+        head[j] = (int)(row - token[j] * a.heads);
+        if (on) load_pair<E, HALF>(x + token[j] * a.xt + head[j] * a.xh, pairs, va[j], vb[j]);
+      }
 #pragma unroll
-        for (int i = 0; i < PAIRS; ++i) turn_of(f[i], pos, a.amplitude, sign, &cs[i], &sn[i]);
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          if constexpr (!WIDE) {
-            const float2 p = pair_value<E, HALF>(v[j][h].x, v[j][h].y);
-            v[j][h].x = __float_as_uint(fmaf(-p.y, sn[0], p.x * cs[0]));
-            v[j][h].y = __float_as_uint(fmaf(p.x, sn[0], p.y * cs[0]));
-            continue;
-          }
-          float p[N];
-          Vec<E>::unpack(v[j][h], p);
-          if constexpr (HALF && WIDE) {
-            float q[N], va[N], wb[N];
-            Vec<E>::unpack(w[j][h], q);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-              va[i] = fmaf(-q[i], sn[i], p[i] * cs[i]);
-              wb[i] = fmaf(p[i], sn[i], q[i] * cs[i]);
-            }
-            v[j][h] = Vec<E>::pack(va);
-            w[j][h] = Vec<E>::pack(wb);
-          } else if constexpr (WIDE) {
-            float o[N];
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-              o[2 * i] = fmaf(-p[2 * i + 1], sn[i], p[2 * i] * cs[i]);
-              o[2 * i + 1] = fmaf(p[2 * i], sn[i], p[2 * i + 1] * cs[i]);
-            }
-            v[j][h] = Vec<E>::pack(o);
-          }
-        }
+      for (int j = 0; j < T; ++j) {
+        const int64_t pos = warp_position(a, token[j], lane);
+        float c, s;
+        turn_of(f, pos, a.amplitude, sign, &c, &s);
+        const float2 p = pair_value<E, HALF>(va[j], vb[j]);
+        if (on && r + j < rows)
+          store_pair<E, HALF>(y + token[j] * a.yt + head[j] * a.yh, pairs,
+                              make_float2(fmaf(-p.y, s, p.x * c), fmaf(p.x, s, p.y * c)));
       }
     }
+  } else {
+    const uint32_t id = blockIdx.x * 128 + threadIdx.x - 128, lanes = gridDim.x * 128 / copied;
+    const uint32_t first = id / copied;
+    const int c = (int)(id - first * copied) * N;
+    if (first >= lanes) return;
+    const int col = c < a.offset ? c : c + a.rope;
+    const E* x = static_cast<const E*>(a.x) + col;
+    E* y = static_cast<E*>(a.y) + col;
+    for (int64_t r = first; r < rows; r += (int64_t)lanes * T) {
+      uint4 v[T];
+      E* to[T];
 #pragma unroll
-    for (int j = 0; j < T; ++j)
+      for (int j = 0; j < T; ++j) {
+        const int64_t row = r + (int64_t)j * lanes;
+        const int64_t token = a.heads == 1 ? row : row / a.heads;
+        const int head = (int)(row - token * a.heads);
+        to[j] = y + token * a.yt + head * a.yh;
+        if (row < rows) v[j] = ld_stream(reinterpret_cast<const uint16_t*>(x + token * a.xt + head * a.xh));
+      }
 #pragma unroll
-      for (int h = 0; h < H; ++h)
-        if (it + (int64_t)j * lanes < items && head[j] + h < a.heads) {
-          E* p = y + token[j] * a.yt + (head[j] + h) * a.yh;
-          if (!WIDE && turns) {
-            store_pair<E, HALF>(p, a.rope / 2,
-                                make_float2(__uint_as_float(v[j][h].x), __uint_as_float(v[j][h].y)));
-          } else {
-            *reinterpret_cast<uint4*>(p) = v[j][h];
-            if (HALF && turns) *reinterpret_cast<uint4*>(p + a.rope / 2) = w[j][h];
-          }
-        }
+      for (int j = 0; j < T; ++j)
+        if (r + (int64_t)j * lanes < rows) *reinterpret_cast<uint4*>(to[j]) = v[j];
+    }
   }
 }
 
@@ -348,23 +406,32 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
   if (bytes % 16 == 0 && cols % N == 0) {
     constexpr int WIDE = HALF ? N : N / 2;
     const int copied = a.in_place ? 0 : (a.d - a.rope) / N;
-    // Heads share a token's sines: four at a time where that still leaves every
-    // SM its threads, else (few heads, or a decoding step) one.
-    const int64_t full = (int64_t)152 * 1024;
-    const bool four = a.heads >= 4 && a.tokens * ((a.heads + 3) / 4) * (a.rope / (2 * WIDE) + copied) >= full;
-    const int groups = four ? (a.heads + 3) / 4 : a.heads;
-    const int chunks = a.rope / (four ? 2 * WIDE : 2) + copied;
-    const bool some = !four && a.tokens * groups * chunks >= 4 * full;  // four tokens a thread
-    int64_t blocks = (a.tokens * groups * chunks + 255) / 256;
-    const int64_t most = 152 * (HALF ? 4 : 6);  // as many as are resident
-    if (blocks > most) blocks = most;
-    const int64_t least = (chunks + 255) / 256;  // at least one whole row of chunks
+    // Heads share a token's sines, four at a time, where that still leaves every
+    // SM its threads.
+    const int chunks = a.rope / (2 * WIDE) + copied, groups = (a.heads + 3) / 4;
+    const int64_t most = 152 * 4;
+    if (a.heads >= 4 && a.tokens * groups * chunks >= (int64_t)152 * 1024) {
+      int64_t blocks = (a.tokens * groups * chunks + 255) / 256;
+      if (blocks > most) blocks = most;
+      const int64_t least = (chunks + 255) / 256;  // at least one whole row of chunks
+      if (blocks < least) blocks = least;
+      return launch_dependent(rope_heads_kernel<T, HALF>, dim3((unsigned)blocks), dim3(256), 0, stream, a,
+                              (int32_t)chunks, (int32_t)groups);
+    }
+    // Four rows a warp where there are enough of them to fill the GPU.
+    const int64_t rows = a.tokens * a.heads;
+    const int pairs32 = (a.rope / 2 + 31) / 32, turners = copied ? 4 : 8;
+    const bool four = rows * pairs32 >= (int64_t)152 * 64;
+    int64_t blocks = (rows * pairs32 + turners * (four ? 4 : 1) - 1) / (turners * (four ? 4 : 1));
+    const int64_t copies = (rows * copied + (four ? 511 : 127)) / (four ? 512 : 128);
+    if (blocks < copies) blocks = copies;
+    if (blocks > 2 * most) blocks = 2 * most;
+    const int64_t least = (pairs32 + turners - 1) / turners > (copied + 127) / 128
+                              ? (pairs32 + turners - 1) / turners
+                              : (copied + 127) / 128;  // every block of pairs, a whole row of copies
     if (blocks < least) blocks = least;
-    auto* kernel = four ? rope_vec_kernel<T, HALF, 1, 4, WIDE>
-                   : some ? rope_vec_kernel<T, HALF, 4, 1, 1>
-                          : rope_vec_kernel<T, HALF, 1, 1, 1>;
-    return launch_dependent(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, a, (int32_t)chunks,
-                            (int32_t)groups);
+    return launch_dependent(four ? rope_rows_kernel<T, HALF, 4> : rope_rows_kernel<T, HALF, 1>,
+                            dim3((unsigned)blocks), dim3(256), 0, stream, a, (int32_t)pairs32, (int32_t)copied);
   }
   const int64_t items = a.tokens * a.heads * (a.rope / 2 + (a.in_place ? 0 : a.d - a.rope));
   int64_t blocks = (items + 255) / 256;
