@@ -4,10 +4,11 @@
 // One group of threads owns one (sequence, block of rows, head): it takes the
 // maximum of |x| over the new rows of the block, settles the block's scale,
 // requantises the rows that were there if the scale grew, and writes the new
-// ones, so nothing is shared between groups and no order matters. The rows
-// stay in registers between the two passes (8 or 16 vectors a thread; what is
-// beyond is read again). Bound by memory: 2 bytes read and 1 written a value
-// for 16-bit rows.
+// ones, so nothing is shared between groups and no order matters. The second
+// pass finds the rows in L1 (a task is 64 KB at most for 64 rows of 512 bf16
+// columns); keeping them in registers instead left two CTAs an SM and took 33 us
+// for 79144 such rows. Bound by memory: 2 bytes read and 1 written a value for
+// 16-bit rows.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -57,27 +58,50 @@ struct Row16<CSA_FP32> {
   }
 };
 
+// Magnitudes are compared as integers: without the sign, the bits of each type
+// grow with the value, infinities and NaN above every finite one. 16-bit types
+// go two to an instruction.
 template <int DTYPE>
-__device__ __forceinline__ float finite_amax(const uint4& w) {
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < Row16<DTYPE>::N; ++i) {
-    const float v = fabsf(Row16<DTYPE>::at(w, i));
-    if (v < INFINITY) m = fmaxf(m, v);
+struct Magnitude {
+  static constexpr uint32_t INF = DTYPE == CSA_BF16 ? 0x7F80u : DTYPE == CSA_FP16 ? 0x7C00u : 0x7F800000u;
+  static constexpr bool PACKED = DTYPE != CSA_FP32;
+  // the larger of m and the vector's magnitudes (a pair of maxima for 16-bit types)
+  static __device__ __forceinline__ uint32_t max_of(uint32_t m, const uint4& w) {
+    if constexpr (PACKED) {
+      m = __vmaxu2(m, __vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu));
+      return __vmaxu2(m, __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+    } else {
+      m = max(m, max(w.x & 0x7FFFFFFFu, w.y & 0x7FFFFFFFu));
+      return max(m, max(w.z & 0x7FFFFFFFu, w.w & 0x7FFFFFFFu));
+    }
   }
-  return m;
-}
+  // the same over the finite ones
+  static __device__ __forceinline__ uint32_t finite_max_of(uint32_t m, const uint4& w) {
+#pragma unroll
+    for (int i = 0; i < Row16<DTYPE>::N; ++i) {
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t b = PACKED ? (u[i / 2] >> (16 * (i & 1))) & 0x7FFFu : u[i] & 0x7FFFFFFFu;
+      if (b < INF) m = max(m, b);
+    }
+    return m;
+  }
+  static __device__ __forceinline__ float value(uint32_t bits) {
+    return DTYPE == CSA_BF16   ? __uint_as_float(bits << 16)
+           : DTYPE == CSA_FP16 ? __half2float(__ushort_as_half((unsigned short)bits))
+                               : __uint_as_float(bits);
+  }
+};
 
 // One vector times the inverse scale, as e4m3. The product is exact (a power
 // of two) wherever it matters: below 2^-126 it rounds to an e4m3 zero anyway.
-template <int DTYPE>
+template <int DTYPE, bool FINITE>
 __device__ __forceinline__ void store_quantised(uint8_t* p, const uint4& w, float inv) {
   constexpr int N = Row16<DTYPE>::N;
   float v[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float x = Row16<DTYPE>::at(w, i);
-    v[i] = fabsf(x) < INFINITY ? x * inv : NAN;  // infinities have no e4m3 value
+    v[i] = FINITE || fabsf(x) < INFINITY ? x * inv : NAN;  // infinities have no e4m3 value
   }
   if constexpr (N == 8) {
     uint2 o;
@@ -89,16 +113,15 @@ __device__ __forceinline__ void store_quantised(uint8_t* p, const uint4& w, floa
   }
 }
 
-// THREADS 512: a CTA owns a task; THREADS 32: each of a CTA's 8 warps does.
+// THREADS 256: a CTA owns a task; THREADS 32: each of a CTA's 8 warps does.
 template <int DTYPE, int THREADS>
-__global__ void __launch_bounds__(THREADS == 512 ? 512 : 256, 2) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   grid_dependency_wait();
   allow_dependent_launch();
   constexpr int N = Row16<DTYPE>::N;
-  constexpr int KEEP = THREADS == 512 ? 8 : 16;
-  __shared__ float warp_max[THREADS / 32];
-  const int lane = THREADS == 512 ? threadIdx.x : threadIdx.x & 31;
-  const int64_t unit = THREADS == 512 ? (int64_t)blockIdx.x
+  __shared__ uint32_t warp_max[8];
+  const int lane = THREADS == 256 ? threadIdx.x : threadIdx.x & 31;
+  const int64_t unit = THREADS == 256 ? (int64_t)blockIdx.x
                                       : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t task = unit / a.c.heads;
   const int head = (int)(unit - task * a.c.heads);
@@ -141,35 +164,42 @@ __global__ void __launch_bounds__(THREADS == 512 ? 512 : 256, 2) append_kernel(c
   const int row_bits = 31 - __clz(per_row);
   const int vecs = (int)(last - first) << row_bits;
 
-  uint4 keep[KEEP];
-  float m = 0.0f;
+  auto vec = [&](int v) {
+    return reinterpret_cast<const uint4*>(src + (v >> row_bits) * src_row) + (v & (per_row - 1));
+  };
+  using Mag = Magnitude<DTYPE>;
+  // the group's maximum of a thread's
+  auto group_max = [&](uint32_t m) {
+    if (Mag::PACKED) m = max(m >> 16, m & 0xFFFFu);
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if constexpr (THREADS == 256) {
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+      __syncthreads();
 #pragma unroll
-  for (int k = 0; k < KEEP; ++k) {
-    const int v = lane + k * THREADS;
-    if (v < vecs)
-      keep[k] = __ldg(reinterpret_cast<const uint4*>(src + (v >> row_bits) * src_row) +
-                      (v & (per_row - 1)));
-  }
-#pragma unroll
-  for (int k = 0; k < KEEP; ++k)
-    if (lane + k * THREADS < vecs) m = fmaxf(m, finite_amax<DTYPE>(keep[k]));
-  for (int v = lane + KEEP * THREADS; v < vecs; v += THREADS)
-    m = fmaxf(m, finite_amax<DTYPE>(__ldg(
-                     reinterpret_cast<const uint4*>(src + (v >> row_bits) * src_row) +
-                     (v & (per_row - 1)))));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  float old = 0.0f;
+      for (int w = 0; w < THREADS / 32; ++w) m = max(m, warp_max[w]);
+    }
+    return m;
+  };
   const bool begun = first > begin;
-  if (begun) old = *scale;
-  if constexpr (THREADS == 512) {
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
-    __syncthreads();  // also: every thread has read the old scale
+  const float old = begun ? *scale : 0.0f;
+  uint32_t top = 0;
+  for (int v = lane; v < vecs; v += 4 * THREADS) {
+    uint4 x[4];
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) m = fmaxf(m, warp_max[w]);
-  } else {
-    __syncwarp();
+    for (int k = 0; k < 4; ++k) x[k] = v + k * THREADS < vecs ? __ldg(vec(v + k * THREADS)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = Mag::max_of(top, x[k]);
   }
+  top = group_max(top);  // for a CTA, also: every thread has read the old scale
+  const bool finite = top < Mag::INF;
+  if (!finite) {
+    top = 0;
+    for (int v = lane; v < vecs; v += THREADS) top = Mag::finite_max_of(top, __ldg(vec(v)));
+    top = group_max(top);
+  }
+  __syncwarp();
+  const float m = Mag::value(top);
   const float need = exp2i(scale_exp(m));
   const bool grew = !begun || need > old;
   const float now = grew ? need : old;
@@ -186,16 +216,21 @@ __global__ void __launch_bounds__(THREADS == 512 ? 512 : 256, 2) append_kernel(c
   }
   const float inv = 1.0f / now;
   uint8_t* dst = data + (int64_t)(first - begin) * a.c.d;
+  for (int v = lane; v < vecs; v += 4 * THREADS) {
+    uint4 x[4];
 #pragma unroll
-  for (int k = 0; k < KEEP; ++k) {
-    const int v = lane + k * THREADS;
-    if (v < vecs) store_quantised<DTYPE>(dst + (int64_t)v * N, keep[k], inv);
+    for (int k = 0; k < 4; ++k)
+      if (v + k * THREADS < vecs) x[k] = __ldg(vec(v + k * THREADS));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (v + k * THREADS < vecs) {
+        uint8_t* p = dst + (int64_t)(v + k * THREADS) * N;
+        if (finite)
+          store_quantised<DTYPE, true>(p, x[k], inv);
+        else
+          store_quantised<DTYPE, false>(p, x[k], inv);
+      }
   }
-  for (int v = lane + KEEP * THREADS; v < vecs; v += THREADS)
-    store_quantised<DTYPE>(
-        dst + (int64_t)v * N,
-        __ldg(reinterpret_cast<const uint4*>(src + (v >> row_bits) * src_row) + (v & (per_row - 1))),
-        inv);
 }
 
 template <int DTYPE>
@@ -204,7 +239,7 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   // would leave most of them idle and take a warp.
   const int64_t units = a.tasks * a.c.heads;
   if (((int64_t)a.c.d << a.c.block_bits) >= 8192)
-    return launch_dependent(append_kernel<DTYPE, 512>, dim3((unsigned)units), dim3(512), 0, stream,
+    return launch_dependent(append_kernel<DTYPE, 256>, dim3((unsigned)units), dim3(256), 0, stream,
                             a);
   return launch_dependent(append_kernel<DTYPE, 32>, dim3((unsigned)((units + 7) / 8)), dim3(256), 0,
                           stream, a);
