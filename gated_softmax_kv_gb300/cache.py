@@ -132,7 +132,7 @@ def csa_cache_attend(q, cache, scales, page_table, seq_lens, cu_q, kv_heads: int
     qh = q.stride(1) if H > 1 else 0
     with on_device(dev, stream) as launch:
         if out is None:
-            out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
             _check(out, "out", q.dtype, dev, 3)
             if out.shape != q.shape:

@@ -118,9 +118,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
   uint8_t* ring = smem + warp * C::RING;
   const uint32_t ring_at = smem_addr(ring);
   const Place place = locate<kThreads>(a, plan, blockIdx.x, sums, &found);
-  Shared* left = shared_items<C::ROWS, D>(a, plan.workers) + blockIdx.x;
+  Shared* left = shared_items<C::ROWS, D>(a, plan.workers) + blockIdx.x;  // unless items are whole
   if (place.pos < 0) {
-    if (threadIdx.x == 0) left->parts = 0;
+    if (threadIdx.x == 0 && !plan.whole) left->parts = 0;
     return;
   }
   Shared tail = {0, 0, 0, 0};  // an item that begins here and ends with another worker
@@ -140,8 +140,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
     const int64_t c0 = within - item * work.chunks;
     const int h = (int)(item / work.tiles);
     const int64_t tile = item - h * work.tiles;
-    const int64_t c1 = min(work.chunks, c0 + (place.end - pos));
-    if (c0 == 0 && c1 < work.chunks)
+    const int64_t units = plan.whole ? 1 : min(work.chunks - c0, place.end - pos);
+    const int64_t c1 = plan.whole ? (int64_t)1 << 40 : c0 + units;
+    const bool whole = plan.whole || units == work.chunks;
+    if (c0 == 0 && !whole)
       tail = {1 + (int32_t)((work.chunks - c1 + place.per - 1) / place.per), s, (int32_t)tile, h};
 
     // ---- the rows: what they see, and Q as fp16 --------------------------------
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
     __syncthreads();
     const float* parts = reinterpret_cast<const float*>(smem);
     auto part = [&](int i) { return parts + i * C::SLOT; };
-    if (c0 == 0 && c1 == work.chunks) {
+    if (whole) {
       join<D, C::ROWS, HALF>(C::GROUPS, part, [&](int row, int c, const RowStats& r, float4 v) {
         write_row<D, HALF>(a, row_of(a, s, tile, h, C::ROWS, row), c, r, v);
       });
@@ -554,23 +556,21 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
           *reinterpret_cast<float4*>(ws + C::ROWS * D + row * 4) = make_float4(r.m, r.mp, r.l, 0.0f);
       });
     }
-    pos += c1 - c0;
-    within += c1 - c0;
+    pos += units;
+    within += units;
   }
-  if (threadIdx.x == 0) *left = tail;
+  if (threadIdx.x == 0 && !plan.whole) *left = tail;
 }
 
 template <int D, bool SHARED, int NT, bool HALF>
 cudaError_t launch_tile(AttendArgs a, cudaStream_t stream) {
   using C = Shape<D, SHARED, NT>;
-  PlanShape p;
-  p.row_bits = log2_of(C::ROWS);
-  p.key_bits = log2_of(C::KS);
-  p.workers = 152 * C::PER_SM;
-  p.least = 2 * C::GROUPS;
+  const PlanShape p = plan_of(a, C::ROWS, C::KS, 152 * C::PER_SM, 2 * C::GROUPS, 8 * C::GROUPS);
   auto* kernel = attend_rows_kernel<D, SHARED, NT, HALF>;
   cudaError_t e = allow_dynamic_smem((const void*)kernel, C::SMEM);
   if (e != cudaSuccess) return e;
+  if (p.whole)
+    return launch_dependent(kernel, dim3((unsigned)p.workers), dim3(kThreads), C::SMEM, stream, a, p);
   void* ws = nullptr;
   e = workspace_take(&ws, join_bytes<D, C::ROWS>(p.workers), stream);
   if (e != cudaSuccess) return e;

@@ -873,9 +873,9 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
   allow_dependent_launch();
   const int warp = threadIdx.x >> 5;
   const Place place = locate<C::THREADS>(a, plan, blockIdx.x, st.sums, &st.found);
-  Shared* left = shared_items<C::R, D>(a, plan.workers) + blockIdx.x;
+  Shared* left = shared_items<C::R, D>(a, plan.workers) + blockIdx.x;  // unless items are whole
   if (place.pos < 0) {
-    if (threadIdx.x == 0) left->parts = 0;
+    if (threadIdx.x == 0 && !plan.whole) left->parts = 0;
     return;
   }
   Shared tail = {0, 0, 0, 0};  // an item that begins here and ends with another worker
@@ -919,8 +919,10 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
     const int64_t c0 = within - item * work.chunks;
     const int h = (int)(item / work.tiles);
     const int64_t tile_of_rows = item - h * work.tiles;
-    const int64_t c1 = min(work.chunks, c0 + (place.end - pos));
-    if (c0 == 0 && c1 < work.chunks)
+    const int64_t units = plan.whole ? 1 : min(work.chunks - c0, place.end - pos);
+    const int64_t c1 = plan.whole ? (int64_t)1 << 40 : c0 + units;
+    const bool whole = plan.whole || units == work.chunks;
+    if (c0 == 0 && !whole)
       tail = {1 + (int32_t)((work.chunks - c1 + place.per - 1) / place.per), s, (int32_t)tile_of_rows, h};
 
     // ---- the rows: what they see, and Q as fp16 --------------------------------
@@ -956,7 +958,7 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
       it.block_bits = a.c.block_bits;
       it.panels_done = panels_done;
       it.tiles_done = tiles_done;
-      it.whole = c0 == 0 && c1 == work.chunks;
+      it.whole = whole;
     }
     __syncthreads();
     if (warp < C::SW) {
@@ -974,10 +976,10 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
     __syncthreads();
     panels_done += (SHARED ? 1 : 2) * n * C::PP;
     tiles_done += n;
-    pos += c1 - c0;
-    within += c1 - c0;
+    pos += units;
+    within += units;
   }
-  if (threadIdx.x == 0) *left = tail;
+  if (threadIdx.x == 0 && !plan.whole) *left = tail;
   tc_before();
   __syncthreads();
   tc_after();
@@ -988,14 +990,12 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
 template <int D, bool SHARED, bool HALF>
 cudaError_t launch_wide(AttendArgs a, cudaStream_t stream) {
   using C = Wide<D, SHARED>;
-  PlanShape p;
-  p.row_bits = log2_of(C::R);
-  p.key_bits = 7;
-  p.workers = 152;
-  p.least = 2;
+  const PlanShape p = plan_of(a, C::R, 128, 152, 2, 8);
   auto* kernel = attend_wide_kernel<D, SHARED, HALF>;
   cudaError_t e = allow_dynamic_smem((const void*)kernel, C::SMEM);
   if (e != cudaSuccess) return e;
+  if (p.whole)
+    return launch_dependent(kernel, dim3((unsigned)p.workers), dim3(C::THREADS), C::SMEM, stream, a, p);
   void* ws = nullptr;
   e = workspace_take(&ws, join_bytes<D, C::R>(p.workers), stream);
   if (e != cudaSuccess) return e;

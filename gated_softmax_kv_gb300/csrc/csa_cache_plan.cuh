@@ -18,6 +18,7 @@ struct PlanShape {
   int32_t key_bits;  // log2 of the keys of a chunk
   int32_t workers;
   int32_t least;     // fewest chunks a worker takes
+  bool whole;        // items are not cut: one unit each
 };
 
 struct SeqWork {
@@ -33,7 +34,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, const PlanShape
   if (w.keys > most) w.keys = most;
   if (w.keys < 0) w.keys = 0;
   w.tiles = nq > 0 ? (nq * a.group + (1 << p.row_bits) - 1) >> p.row_bits : 0;
-  w.chunks = w.keys > 0 ? (w.keys + (1 << p.key_bits) - 1) >> p.key_bits : 1;
+  w.chunks = w.keys > 0 && !p.whole ? (w.keys + (1 << p.key_bits) - 1) >> p.key_bits : 1;
   return w;
 }
 
@@ -94,6 +95,25 @@ __device__ __forceinline__ Place locate(const AttendArgs& a, const PlanShape& p,
   }
   __syncthreads();
   return *found;
+}
+
+// The plan of a call, on the host. Items of at most `few` chunks, as the table's
+// width shows, are not worth cutting: no workspace, no joining kernel, and as
+// many workers as there can be items, up to four for each that is resident.
+inline PlanShape plan_of(const AttendArgs& a, int rows, int keys, int resident, int least, int few) {
+  PlanShape p;
+  p.row_bits = log2_of(rows);
+  p.key_bits = log2_of(keys);
+  p.least = least;
+  p.workers = resident;
+  const int64_t chunks = (((int64_t)a.max_pages << a.c.page_bits) + keys - 1) / keys;
+  p.whole = chunks <= few;
+  if (p.whole) {
+    const int64_t items = ((a.tokens * a.group) / rows + a.nseq) * a.kv;
+    p.workers = (int32_t)(items < 4 * resident ? items : 4 * resident);
+    p.least = 1;
+  }
+  return p;
 }
 
 }  // namespace csa

@@ -81,7 +81,7 @@ def csa_rope(x, freqs, positions=None, *, cu_seqlens_comp=None, ratio: int = 1, 
         raise ValueError("the last dimension of x must be contiguous")
     with on_device(dev, stream) as launch:
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=x.device)
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
             yt, yh = heads * D, D
         else:
             if not isinstance(out, torch.Tensor) or out.dtype != dtype or out.get_device() != dev:
