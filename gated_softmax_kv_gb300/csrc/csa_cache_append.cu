@@ -257,7 +257,7 @@ extern "C" csa_status_t csa_cache_append(const csa_cache_t* cache, const void* r
   const csa_status_t st = csa::check_cache(cache);
   if (st != CSA_OK) return st;
   if (dtype != CSA_BF16 && dtype != CSA_FP16 && dtype != CSA_FP32) return CSA_ERR_UNSUPPORTED;
-  if (num_seqs < 1 || num_seqs > csa::kMaxSeqs || max_pages < 1 || num_rows < 0 ||
+  if (num_seqs < 1 || num_seqs > csa::kMaxSeqs || max_pages < 1 || max_pages > csa::kMaxPages || num_rows < 0 ||
       num_rows >= ((int64_t)1 << 31) || row_stride < 0 || head_stride < 0)
     return CSA_ERR_RANGE;
   const int64_t most = (int64_t)1 << 56;

@@ -19,7 +19,7 @@ extern "C" csa_status_t csa_cache_attend(const csa_cache_t* cache, const void* q
   if (kv_heads < 1 || num_q_heads < 1 || num_q_heads > 65536 || num_q_heads % kv_heads != 0 ||
       (int64_t)kv_heads * (shared ? 1 : 2) > cache->num_heads)
     return CSA_ERR_UNSUPPORTED;
-  if (num_seqs < 1 || num_seqs > csa::kMaxSeqs || max_pages < 1 || num_tokens < 0 ||
+  if (num_seqs < 1 || num_seqs > csa::kMaxSeqs || max_pages < 1 || max_pages > csa::kMaxPages || num_tokens < 0 ||
       q_token_stride < 0 || q_head_stride < 0)
     return CSA_ERR_RANGE;
   if (num_tokens >= ((int64_t)1 << 31) || num_tokens * num_q_heads >= ((int64_t)1 << 31))

@@ -12,6 +12,7 @@
 namespace csa {
 
 constexpr int32_t kMaxSeqs = 262144;
+constexpr int32_t kMaxPages = 1 << 27;  // of a table row: 2^31 rows of the smallest pages
 
 // Envelope, alignment and pointers of a cache description.
 inline csa_status_t check_cache(const csa_cache_t* c) {

@@ -19,23 +19,24 @@ namespace {
 constexpr int kPlanThreads = 1024;
 
 // Sum of v over the CTA's threads before this one; *total gets the whole sum.
-__device__ __forceinline__ int block_prefix(int v, int* total) {
-  __shared__ int sums[kPlanThreads / 32];
+template <typename T>
+__device__ __forceinline__ T block_prefix(T v, T* total) {
+  __shared__ T sums[kPlanThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    const T y = __shfl_up_sync(0xFFFFFFFFu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();  // sums may still be read by an earlier call
   if (lane == 31) sums[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int w = sums[lane];
+    T w = sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+      const T y = __shfl_up_sync(0xFFFFFFFFu, w, o);
       if (lane >= o) w += y;
     }
     sums[lane] = w;
@@ -306,8 +307,8 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const ReserveArgs
   int64_t wanted = 0;
   for (int b = 0; b < a.n; b += kPlanThreads) {
     const int i = b + threadIdx.x;
-    int total;
-    const int before = block_prefix(i < a.n ? min(a.need[i], 1 << 20) : 0, &total);
+    int64_t total;
+    const int64_t before = block_prefix(i < a.n ? (int64_t)a.need[i] : (int64_t)0, &total);
     // the prefix is used only if the whole sum fits the pool, hence 32 bits
     if (i < a.n) a.need[i] = (int)min(wanted + before, (int64_t)INT32_MAX);
     wanted += total;
@@ -463,16 +464,16 @@ csa_status_t done(cudaError_t e) { return e == cudaSuccess ? CSA_OK : record_cud
 // The table, lengths and counts that every call here takes.
 csa_status_t check_tables(const void* table, const void* lens, const void* refs, int32_t num_seqs,
                           int32_t max_pages, int32_t num_pages) {
-  if (num_seqs < 1 || num_seqs > kMaxSeqs || max_pages < 1 || num_pages < 1 ||
-      num_pages > (1 << 24))
+  if (num_seqs < 1 || num_seqs > kMaxSeqs || max_pages < 1 || max_pages > kMaxPages ||
+      num_pages < 1 || num_pages > (1 << 24))
     return CSA_ERR_RANGE;
   if (!table || !lens || !refs) return CSA_ERR_NULL;
   if (misaligned4(table) || misaligned4(lens) || misaligned4(refs)) return CSA_ERR_ALIGN;
   return CSA_OK;
 }
 
-csa_status_t check_list(const void* a, const void* b, int32_t n) {
-  if (n < 0) return CSA_ERR_RANGE;
+csa_status_t check_list(const void* a, const void* b, int32_t n, int32_t most) {
+  if (n < 0 || n > most) return CSA_ERR_RANGE;
   if (n > 0 && (!a || !b)) return CSA_ERR_NULL;
   if (misaligned4(a) || misaligned4(b)) return CSA_ERR_ALIGN;
   return CSA_OK;
@@ -487,7 +488,7 @@ extern "C" {
 csa_status_t csa_cache_copy_pages(const csa_cache_t* cache, const int32_t* src, const int32_t* dst,
                                   int32_t n, cudaStream_t stream) {
   csa_status_t st = csa::check_cache(cache);
-  if (st == CSA_OK) st = csa::check_list(src, dst, n);
+  if (st == CSA_OK) st = csa::check_list(src, dst, n, INT32_MAX);
   if (st != CSA_OK || n == 0) return st;
   csa::CopyArgs a;
   a.c = csa::view_of(cache);
@@ -509,7 +510,7 @@ csa_status_t csa_cache_fork(int32_t* page_table, int32_t* seq_lens, int32_t* pag
     return CSA_ERR_UNSUPPORTED;
   csa_status_t st =
       csa::check_tables(page_table, seq_lens, page_refs, num_seqs, max_pages, num_pages);
-  if (st == CSA_OK) st = csa::check_list(parents, children, n);
+  if (st == CSA_OK) st = csa::check_list(parents, children, n, csa::kMaxSeqs);
   if (st != CSA_OK) return st;
   if (!status) return CSA_ERR_NULL;
   if (csa::misaligned4(status)) return CSA_ERR_ALIGN;
@@ -538,7 +539,7 @@ csa_status_t csa_cache_reserve(const csa_cache_t* cache, int32_t* page_table,
   csa_status_t st = csa::check_cache(cache);
   if (st == CSA_OK)
     st = csa::check_tables(page_table, seq_lens, page_refs, num_seqs, max_pages, cache->num_pages);
-  if (st == CSA_OK) st = csa::check_list(seqs, rows, n);
+  if (st == CSA_OK) st = csa::check_list(seqs, rows, n, csa::kMaxSeqs);
   if (st != CSA_OK) return st;
   if (!status) return CSA_ERR_NULL;
   if (csa::misaligned4(status)) return CSA_ERR_ALIGN;
@@ -589,7 +590,7 @@ csa_status_t csa_cache_free(int32_t* page_table, int32_t* seq_lens, int32_t* pag
                             const int32_t* seqs, int32_t n, cudaStream_t stream) {
   csa_status_t st =
       csa::check_tables(page_table, seq_lens, page_refs, num_seqs, max_pages, num_pages);
-  if (st == CSA_OK) st = csa::check_list(seqs, seqs, n);
+  if (st == CSA_OK) st = csa::check_list(seqs, seqs, n, csa::kMaxSeqs);
   if (st != CSA_OK || n == 0) return st;
   return csa::done(csa::launch_dependent(
       csa::free_kernel, dim3((unsigned)(n < 1216 ? n : 1216)), dim3(256), 0, stream, page_table,

@@ -27,7 +27,8 @@ struct SeqWork {
 };
 
 __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, const PlanShape& p, int s) {
-  const int64_t nq = (int64_t)__ldg(a.cu + s + 1) - __ldg(a.cu + s);
+  // no more queries than the call has, whatever cu holds: the line stays finite
+  const int64_t nq = min((int64_t)__ldg(a.cu + s + 1), a.tokens) - max((int64_t)__ldg(a.cu + s), (int64_t)0);
   SeqWork w;
   w.keys = __ldg(a.lens + s);
   const int64_t most = (int64_t)a.max_pages << a.c.page_bits;

@@ -28,7 +28,8 @@
  * null pointers on the host before any launch (CSA_ERR_*). Tables, lengths and
  * index lists are read on the device only. Kernels stay inside the buffers
  * whatever those hold: a page outside [0, num_pages) or a row outside the
- * table is treated as not there (not read, not written, not seen).
+ * table is treated as not there (not read, not written, not seen). max_pages
+ * is at most 2^27, num_seqs and the lists of sequences at most 262144 long.
  */
 #ifndef CSA_CACHE_H
 #define CSA_CACHE_H
@@ -76,7 +77,8 @@ typedef struct csa_cache {
  * the block behind the last row keep what they hold. Appending row by row
  * gives the bits of appending at once, except for values that fall below 2^-6
  * of the final scale, which may have been rounded twice.
- * One launch; num_rows == 0 launches nothing. num_seqs <= 262144.
+ * One launch; num_rows == 0 launches nothing. (num_rows / block + 2 num_seqs) *
+ * num_heads < 2^31.
  */
 csa_status_t csa_cache_append(const csa_cache_t* cache, const void* rows, int32_t dtype,
                               int64_t num_rows, int64_t row_stride, int64_t head_stride,
@@ -99,8 +101,8 @@ csa_status_t csa_cache_append(const csa_cache_t* cache, const void* rows, int32_
  * seen. A compressed row that ends at token (j + 1) * ratio - 1 is in the
  * past of the query at position p when j < (p + 1) / ratio. Rows that a query
  * does not see have no influence on it, whatever they hold (NaN included).
- * A query that sees no row, or whose logits are all -inf, gets out 0 and lse
- * -inf. out [num_tokens, num_q_heads, head_dim] in q's type, contiguous, and
+ * A query that sees no row, or whose logits are all -inf (those below -6e37
+ * count as -inf), gets out 0 and lse -inf. out [num_tokens, num_q_heads, head_dim] in q's type, contiguous, and
  * lse fp32 [num_tokens, num_q_heads] (may be null) are written in full for
  * tokens below cu_q[num_seqs]; tokens behind it are left as they were.
  * Logits, softmax statistics and sums are fp32; the weights enter the second
@@ -108,7 +110,8 @@ csa_status_t csa_cache_append(const csa_cache_t* cache, const void* rows, int32_
  *
  * Results are the same from call to call; the order of sums depends on the
  * sizes and lengths of the call alone. Workspace comes from the library's
- * stream-ordered pool. num_tokens == 0 launches nothing. num_seqs <= 262144.
+ * stream-ordered pool. num_tokens == 0 launches nothing. num_tokens * num_q_heads
+ * < 2^31.
  */
 csa_status_t csa_cache_attend(const csa_cache_t* cache, const void* q, int32_t dtype,
                               int64_t num_tokens, int32_t num_q_heads, int64_t q_token_stride,

@@ -24,7 +24,8 @@
  * Angles: frequencies are radians a position in fp64. The kernel holds them
  * in turns as 64-bit fixed-point numbers and multiplies modulo 2^64, so the
  * reduction to one turn is exact whatever the position; the angle used is
- * within 2^-32 turns of p * freqs[i] as long as |p| < 2^31. Frequencies must
+ * within 2^-32 turns of p * freqs[i] as long as |p| < 2^31 (and then rounded to
+ * fp32 in half turns, |angle| <= 1: 2^-25). Frequencies must
  * be finite and below 2^62 in magnitude. Products and sums are fp32, rounded
  * once to the tensor's type.
  *

@@ -346,3 +346,65 @@ def test_a_pool_past_32_bits(gsk):
         got = gsk.csa_cache_attend(s.q[:, :h].contiguous(), cache, scales, i32([t]), i32([300]), i32([0, 1]), 1, s.scale, shared=True)
         small = gsk.csa_cache_attend(s.q[:, :h].contiguous(), *s.args(), shared=True)
         assert torch.equal(got[0], small[0])
+
+
+@pytest.mark.parametrize("D,shared,kv,group,queries", [(64, True, 1, 2, 1), (64, False, 2, 3, 5), (128, False, 2, 8, 1),
+                                                       (256, True, 1, 4, 3), (512, False, 1, 5, 1), (512, True, 1, 64, 1),
+                                                       (128, False, 1, 8, 20), (256, False, 1, 64, 1)])
+def test_short_and_wide_tables(gsk, D, shared, kv, group, queries):
+    """Items are cut or not by the width of the table: the same sequences under a
+    table just wide enough, and under ones that have room for far more rows."""
+    lens = [250, 1, 0, 97, 256, 16, 130]
+    s = Setup(lens, [queries] * len(lens), kv * group, kv, D, shared, 64, 16, seed=D + group)
+    narrow, table = s.check(gsk), s.table
+    for width in (16, 17, 40, 4000):
+        s.table = np.full((len(lens), width), -1)
+        s.table[:, :table.shape[1]] = table
+        out, lse = s.check(gsk)
+        seen = np.repeat(np.array(lens) > 0, queries)
+        # each is within its tolerance of the same value; fewer than two rows need no sum
+        one = np.repeat(np.array(lens) < 2, queries)
+        assert torch.equal(out[one], narrow[0][one]) and torch.equal(lse[one], narrow[1][one])
+        assert (out[~seen] == 0).all()
+
+
+@pytest.mark.parametrize("D,group,tokens", [(64, 2, 8), (512, 4, 6), (128, 16, 40), (512, 64, 7)])
+def test_queries_that_are_not_there(gsk, D, group, tokens):
+    """Offsets that promise more queries than the call has give those of the call;
+    decreasing and negative ones give none, and the other sequences theirs."""
+    s = Setup([200], [tokens], group, 1, D, True, seed=D)
+    want = s.check(gsk)
+    a = list(s.args())
+    for cu in ([0, 2 ** 30], [0, 2 ** 31 - 1]):
+        a[4] = i32(cu)
+        out, lse = gsk.csa_cache_attend(s.q, *a, shared=True)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    a[2], a[3] = i32(np.repeat(s.table, 3, 0)), i32([200] * 3)
+    for cu, first in (([9, 2, 0, tokens], 0), ([-2 ** 31, -5, 2, tokens], 2), ([2 ** 31 - 1, -2 ** 31, 2, 1], None)):
+        a[4] = i32(cu)
+        out, lse = torch.full_like(want[0], 3.0), torch.full_like(want[1], 3.0)
+        gsk.csa_cache_attend(s.q, *a, shared=True, out=out, lse=lse)
+        if first is not None:
+            # the same logits, summed from another split: 200 2^-24 for the sum, 2^-22 a
+            # term and 128 2^-24 for its exponent, |lse| 2^-23 < 2^-16: below 2^-14 together
+            assert ((lse[first:] - want[1][first:]).abs() <= 2.0 ** -14).all(), cu
+            assert (lse[:first] == 3).all() and (out[:first] == 3).all()
+        else:
+            assert (out == 3).all() and (lse == 3).all()
+
+
+def test_two_streams_at_once(gsk):
+    """Calls of both kernels on two streams, each with its own workspace."""
+    sets = []
+    for D, group in ((128, 8), (512, 64)):
+        s = Setup([3000, 900, 7], [1, 1, 1], group, 1, D, True, seed=D)
+        sets.append((s, s.args(), s.check(gsk), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for k, (s, args, want, stream) in enumerate(sets):
+            got[k].append(gsk.csa_cache_attend(s.q, *args, shared=True, stream=stream))
+    torch.cuda.synchronize()
+    for k, (s, args, want, stream) in enumerate(sets):
+        for out, lse in got[k]:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])

@@ -241,3 +241,21 @@ def test_refusals(gsk):
     with pytest.raises(ValueError):
         gsk.csa_cache_compact(w.cache, w.scales, w.table[:, ::2], w.refs)
     w.check()
+
+
+def test_a_request_of_more_than_a_million_pages(gsk):
+    n = (1 << 20) + 50
+    pages = n + 3
+    cache = torch.zeros((pages, 1, 16, 64), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    scales = torch.zeros((pages, 1, 1), device="cuda")
+    table, lens, refs, status = i32(np.full((2, n), -1)), i32([0, 0]), i32(np.zeros(pages)), i32([0])
+    refs[5] = 1                                             # held by nobody in the table
+    gsk.csa_cache_reserve(cache, scales, table, lens, refs, i32([1, 0]), i32([16 * n, 16 * 3]), status)
+    assert status.item() == 8 and (table == -1).all() and refs.sum().item() == 1
+    status.zero_()
+    gsk.csa_cache_reserve(cache, scales, table, lens, refs, i32([1, 0]), i32([16 * n, 16 * 2]), status)
+    free = torch.tensor([p for p in range(pages) if p != 5], dtype=torch.int32, device="cuda")
+    assert status.item() == 0 and torch.equal(table[1], free[:n])
+    assert torch.equal(table[0, :2], free[n:]) and (table[0, 2:] == -1).all() and (refs == 1).all()
+    gsk.csa_cache_free(table, lens, refs, i32([1, 0]))
+    assert (table == -1).all() and refs.sum().item() == 1

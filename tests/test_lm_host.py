@@ -187,6 +187,18 @@ def test_page_call_refusals(lib):
         assert reserve(lib, **bad) == ALIGN, bad
 
 
+def test_sizes_past_the_limits(lib):
+    """Table rows wider than 2^31 rows need and lists longer than there can be sequences."""
+    c, wide, long = ctypes.byref(cache_of()), (1 << 27) + 1, 262145
+    assert append(lib, width=1 << 27) == 0 and append(lib, width=wide) == RANGE
+    assert attend(lib, width=1 << 27) == 0 and attend(lib, width=wide) == RANGE
+    assert reserve(lib, width=wide) == RANGE and reserve(lib, n=long) == RANGE
+    for width, n in ((wide, 0), (4, long), ((1 << 31) - 1, 1)):
+        assert lib.csa_cache_fork(A, A, A, 4, width, 8, 64, A, A, n, A, None) == RANGE
+        assert lib.csa_cache_free(A, A, A, 4, width, 8, A, n, None) == RANGE
+    assert lib.csa_cache_compact(c, A, A, 4, wide, None, None) == RANGE
+
+
 def test_headers_compile_as_c(tmp_path):
     gcc = shutil.which("gcc")
     if gcc is None:
