@@ -100,6 +100,14 @@ __device__ __forceinline__ int swizzled(int k, int ch) {
     return ch ^ ((k >> 1) & 3);
 }
 
+// Where column c (a multiple of 4) of a row lies in a group's sums: the four
+// rows that a quarter warp stores to are kept on different banks.
+template <int DW>
+__device__ __forceinline__ int merged_at(int row, int c) {
+  const int t = (row >> 1) & 3;
+  return c ^ ((DW == 128 ? t : (t & 1) | ((t & 2) << 1)) << 2);
+}
+
 template <int D, bool SHARED, int NT, bool HALF>
 __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
     attend_rows_kernel(const AttendArgs a, const PlanShape plan) {
@@ -109,6 +117,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
   __shared__ Place found;
   __shared__ int32_t row_sees[C::ROWS];
   __shared__ float row_factor[C::ROWS];
+  __shared__ int64_t row_at[C::ROWS];                  // where its output row is, or -1
+  __shared__ float merged[C::ROWS], part_factor[C::GROUPS][C::ROWS];
   __shared__ int32_t sees_least, sees_most;
   grid_dependency_wait();
   allow_dependent_launch();
@@ -154,17 +164,38 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
     }
     __syncthreads();
     uint16_t* qs = reinterpret_cast<uint16_t*>(smem);
-    for (int i = warp; i < C::ROWS; i += 8) {
-      const Row w = row_of(a, s, tile, h, C::ROWS, i);
-      constexpr int V = D / 256 > 0 ? D / 256 : 1;  // 16-byte vectors a lane
+    constexpr int V = D / 256 > 0 ? D / 256 : 1;  // 16-byte vectors a lane
+    Row rows[NT];
+    uint4 x[NT][V];
+#pragma unroll
+    for (int r = 0; r < NT; ++r) {  // all loads first
+      rows[r] = row_of(a, s, tile, h, C::ROWS, warp + 8 * r);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int col = (k * 32 + lane) * 8;
+        x[r][k] = rows[r].there && col < D ? __ldg(reinterpret_cast<const uint4*>(
+                                                 a.q + rows[r].token * a.qt + rows[r].head * a.qh + col))
+                                           : make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < NT; ++r) {
+      const int i = warp + 8 * r;
+      const Row& w = rows[r];
+      if (lane == 0) {
+        int64_t n = w.there ? work.keys : 0;
+        if (w.there && a.visible) n = min(n, (int64_t)max(__ldg(a.visible + w.token), 0));
+        row_sees[i] = w.there ? (int)n : -1;
+        row_at[i] = w.there ? w.token * a.heads + w.head : -1;
+        if (w.there) {
+          atomicMin(&sees_least, (int)n);
+          atomicMax(&sees_most, (int)n);
+        }
+      }
       float amax = 0.0f, v[V][8];
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        const int col = (k * 32 + lane) * 8;
-        if (w.there && col < D)
-          x = __ldg(reinterpret_cast<const uint4*>(a.q + w.token * a.qt + w.head * a.qh + col));
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t u[4] = {x[r][k].x, x[r][k].y, x[r][k].z, x[r][k].w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const uint32_t bits = e & 1 ? u[e >> 1] >> 16 : u[e >> 1] & 0xFFFFu;
@@ -183,24 +214,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
       for (int k = 0; k < V; ++k) {
         const int col = (k * 32 + lane) * 8;
         if (col < D) {
-          uint4 x;
-          x.x = pack_f16x2(v[k][0] * f, v[k][1] * f);
-          x.y = pack_f16x2(v[k][2] * f, v[k][3] * f);
-          x.z = pack_f16x2(v[k][4] * f, v[k][5] * f);
-          x.w = pack_f16x2(v[k][6] * f, v[k][7] * f);
-          *reinterpret_cast<uint4*>(qs + i * D + col) = x;
+          uint4 y;
+          y.x = pack_f16x2(v[k][0] * f, v[k][1] * f);
+          y.y = pack_f16x2(v[k][2] * f, v[k][3] * f);
+          y.z = pack_f16x2(v[k][4] * f, v[k][5] * f);
+          y.w = pack_f16x2(v[k][6] * f, v[k][7] * f);
+          *reinterpret_cast<uint4*>(qs + i * D + col) = y;
         }
       }
-      if (lane == 0) {
-        row_factor[i] = ldexpf(a.scale, -lift);
-        int64_t n = w.there ? work.keys : 0;
-        if (w.there && a.visible) n = min(n, (int64_t)max(__ldg(a.visible + w.token), 0));
-        row_sees[i] = w.there ? (int)n : -1;
-        if (w.there) {
-          atomicMin(&sees_least, (int)n);
-          atomicMax(&sees_most, (int)n);
-        }
-      }
+      if (lane == 0) row_factor[i] = ldexpf(a.scale, -lift);
     }
     __syncthreads();
     uint32_t qf[NT][C::DW / 16][2];
@@ -285,15 +307,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
         m[n][j] = mp[n][j] = kNone;
         l[n][j] = 0.0f;
       }
+    // the first steps' lookups at once, a lane each
+    const int32_t lookup = lane < C::STAGES * C::SUB ? page_at(lane / C::SUB, lane % C::SUB) : -1;
     int32_t pages[C::SUB];
+#pragma unroll 1
+    for (int i = 0; i < C::STAGES; ++i) {
 #pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) {
-#pragma unroll
-      for (int u = 0; u < C::SUB; ++u) pages[u] = page_at(i, u);
-      fetch(i, pages);
+      for (int u = 0; u < C::SUB; ++u) pages[u] = __shfl_sync(0xFFFFFFFFu, lookup, i * C::SUB + u);
+      if (i < C::STAGES - 1) fetch(i, pages);
     }
-#pragma unroll
-    for (int u = 0; u < C::SUB; ++u) pages[u] = page_at(C::STAGES - 1, u);
 
     for (int i = 0; i < steps; ++i) {
       cp_wait<C::STAGES - 2>();
@@ -537,24 +559,53 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
           mg[C::ROWS * D + row * 4 + 2] = x;
         }
 #pragma unroll
-        for (int k = 0; k < C::DW / 16; ++k)
-          *reinterpret_cast<float2*>(mg + row * D + wd * C::DW + g * (C::DW / 8) + 2 * k) =
-              make_float2(o[k][n][j], o[k][n][j + 2]);
+        for (int k = 0; k < C::DW / 16; k += 2)
+          *reinterpret_cast<float4*>(mg + row * D + merged_at<C::DW>(row, wd * C::DW + g * (C::DW / 8) + 2 * k)) =
+              make_float4(o[k][n][j], o[k][n][j + 2], o[k + 1][n][j], o[k + 1][n][j + 2]);
       }
     __syncthreads();
-    const float* parts = reinterpret_cast<const float*>(smem);
-    auto part = [&](int i) { return parts + i * C::SLOT; };
-    if (whole) {
-      join<D, C::ROWS, HALF>(C::GROUPS, part, [&](int row, int c, const RowStats& r, float4 v) {
-        write_row<D, HALF>(a, row_of(a, s, tile, h, C::ROWS, row), c, r, v);
-      });
-    } else {  // slot 0: the item began with another worker, slot 1: it did here
-      float* ws = a.ws + ((int64_t)blockIdx.x * 2 + (c0 == 0)) * C::SLOT;
-      join<D, C::ROWS, HALF>(C::GROUPS, part, [&](int row, int c, const RowStats& r, float4 v) {
+    // A thread a row: its statistics over the groups, and the factor of each
+    // group's sums, with which they are finished or (split items) joined.
+    float* const parts = reinterpret_cast<float*>(smem);
+    // slot 0: the item began with another worker, slot 1: it did here
+    float* const ws = a.ws + ((int64_t)blockIdx.x * 2 + (c0 == 0)) * C::SLOT;
+    if (threadIdx.x < C::ROWS) {
+      const float* st = parts + C::ROWS * D + threadIdx.x * 4;
+      RowStats r = {kNone, kNone, 0.0f};
+#pragma unroll
+      for (int k = 0; k < C::GROUPS; ++k) {
+        r.m = fmaxf(r.m, st[k * C::SLOT]);
+        r.mp = fmaxf(r.mp, st[k * C::SLOT + 1]);
+      }
+#pragma unroll
+      for (int k = 0; k < C::GROUPS; ++k) r.l += st[k * C::SLOT + 2] * exp2f(st[k * C::SLOT] - r.m);
+      const float up = whole ? r.m + kLift + log2f(r.l) : r.mp;
+#pragma unroll
+      for (int k = 0; k < C::GROUPS; ++k) part_factor[k][threadIdx.x] = exp2f(st[k * C::SLOT + 1] - up);
+      merged[threadIdx.x] = r.l;
+      if (!whole)
+        *reinterpret_cast<float4*>(ws + C::ROWS * D + threadIdx.x * 4) = make_float4(r.m, r.mp, r.l, 0.0f);
+      else if (a.lse && row_at[threadIdx.x] >= 0)
+        a.lse[row_at[threadIdx.x]] = row_lse(r);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int u = threadIdx.x; u < C::ROWS * (D / 4); u += kThreads) {
+      const int row = u / (D / 4), c = (u % (D / 4)) * 4;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < C::GROUPS; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(parts + k * C::SLOT + row * D + merged_at<C::DW>(row, c));
+        const float f = part_factor[k][row];
+        v.x = fmaf(x.x, f, v.x);
+        v.y = fmaf(x.y, f, v.y);
+        v.z = fmaf(x.z, f, v.z);
+        v.w = fmaf(x.w, f, v.w);
+      }
+      if (!whole)
         *reinterpret_cast<float4*>(ws + row * D + c) = v;
-        if (c == 0)
-          *reinterpret_cast<float4*>(ws + C::ROWS * D + row * 4) = make_float4(r.m, r.mp, r.l, 0.0f);
-      });
+      else if (row_at[row] >= 0)
+        store4<HALF>(a.out + row_at[row] * D + c, v, merged[row] == 0.0f ? 0.0f : 1.0f);
     }
     pos += units;
     within += units;

@@ -63,35 +63,6 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v, float f) {
   *reinterpret_cast<uint2*>(p) = o;
 }
 
-// Joins n partial results of one tile, each `ROWS` x D sums and the rows'
-// statistics, in their order: part(i) gives the sums, stats(i) the statistics
-// of part i.
-template <int D, int ROWS, bool HALF, class Part, class Out>
-__device__ __forceinline__ void join(int n, Part part, Out out) {
-  for (int u = threadIdx.x; u < ROWS * (D / 4); u += kThreads) {
-    const int row = u / (D / 4), c = (u % (D / 4)) * 4;
-    RowStats r = {kNone, kNone, 0.0f};
-    for (int i = 0; i < n; ++i) {
-      const float* st = part(i) + ROWS * D + row * 4;
-      r.m = fmaxf(r.m, st[0]);
-      r.mp = fmaxf(r.mp, st[1]);
-    }
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = 0; i < n; ++i) {
-      const float* p = part(i);
-      const float* st = p + ROWS * D + row * 4;
-      const float4 v = *reinterpret_cast<const float4*>(p + row * D + c);
-      r.l += st[2] * exp2f(st[0] - r.m);
-      const float f = exp2f(st[1] - r.mp);
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
-    }
-    out(row, c, r, o);
-  }
-}
-
 // Where row `i` of tile `tile` (of cache head h) of sequence s reads and writes.
 struct Row {
   int64_t token;
