@@ -13,7 +13,6 @@ import ctypes
 
 from .binding import _check, _check_detail, _raise, load
 from .launch import on_device, output_overlaps
-from .rope import _dtype_code
 
 CACHE_STATUS = {1: "a sequence index outside the table", 2: "an index twice, or both child and parent",
                 4: "a child that holds rows or pages", 8: "fewer free pages than needed",
@@ -25,6 +24,35 @@ class _Cache(ctypes.Structure):
                 ("num_pages", ctypes.c_int32), ("num_heads", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("block", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32)]
+
+
+class _Types:
+    """torch's types, looked up once."""
+
+    def __getattr__(self, name):
+        import torch
+        self.e4m3, self.f32, self.i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+        self.queries = {torch.bfloat16: 0, torch.float16: 1}
+        self.rows = {**self.queries, torch.float32: 2}
+        self.contiguous = {"memory_format": torch.contiguous_format}
+        self.empty, self.empty_like = torch.empty, torch.empty_like
+        return self.__dict__[name]
+
+
+_types = _Types()
+
+
+def _fine(cache, scales, rows, codes, dev, *ints) -> bool:
+    """Whether a cache, packed rows and int32 tensors are of the right types and
+    layouts and on the device. The checks that name the fault run where not:
+    reading attributes is most of the host's time of a call."""
+    i32 = _types.i32
+    for t in ints:
+        if t.dtype is not i32 or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return (dev >= 0 and cache.dtype is _types.e4m3 and cache.is_contiguous()
+            and scales.dtype is _types.f32 and scales.get_device() == dev and scales.is_contiguous()
+            and rows.dtype in codes and rows.get_device() == dev)
 
 
 def _cache(cache, scales):
@@ -85,21 +113,36 @@ def csa_cache_append(rows, cache, scales, page_table, seq_lens, cu_rows, stream=
     """Quantises rows [num_rows, num_heads, head_dim] (bf16, fp16 or fp32) into
     the cache: sequence s gets rows cu_rows[s] .. cu_rows[s + 1] - 1 behind its
     seq_lens[s] rows. seq_lens is not changed: add the lengths afterwards."""
-    import torch
-    c, dev = _cache(cache, scales)
-    n, width = _tables(page_table, seq_lens, dev)
-    _check(cu_rows, "cu_rows", torch.int32, dev, 1)
-    _rows(rows, "rows", (torch.bfloat16, torch.float16, torch.float32), dev)
-    if cu_rows.shape[0] != n + 1:
-        raise ValueError("cu_rows must be [num_seqs + 1]")
-    if rows.shape[1] != c.num_heads or rows.shape[2] != c.head_dim:
-        raise ValueError("rows must be [num_rows, num_heads, head_dim] of the cache")
+    try:
+        dev = cache.get_device()
+        (pages, heads, page, D), (sp, sh, blocks) = cache.shape, scales.shape
+        (n, width), (lens,), (cu,) = page_table.shape, seq_lens.shape, cu_rows.shape
+        (T, H, cols), (rs, hs, last) = rows.shape, rows.stride()
+        fine = (sp == pages and sh == heads == H and cols == D and blocks >= 1 and page % blocks == 0
+                and n == lens == cu - 1 and n >= 1 and width >= 1 and heads >= 1 and last == 1
+                and _fine(cache, scales, rows, _types.rows, dev, page_table, seq_lens, cu_rows))
+    except (AttributeError, ValueError):
+        fine = False
+    if fine:
+        c = _Cache(cache.data_ptr(), scales.data_ptr(), pages, heads, page, page // blocks, D)
+    else:
+        c, dev = _cache(cache, scales)
+        n, width = _tables(page_table, seq_lens, dev)
+        _check(cu_rows, "cu_rows", _types.i32, dev, 1)
+        _rows(rows, "rows", tuple(_types.rows), dev)
+        if cu_rows.shape[0] != n + 1:
+            raise ValueError("cu_rows must be [num_seqs + 1]")
+        if rows.shape[1] != c.num_heads or rows.shape[2] != c.head_dim:
+            raise ValueError("rows must be [num_rows, num_heads, head_dim] of the cache")
+        (T, H, _), (rs, hs, _) = rows.shape, rows.stride()
     # the stride of a dimension of one element is never stepped: 0
-    rs = rows.stride(0) if rows.shape[0] > 1 else 0
-    hs = rows.stride(1) if rows.shape[1] > 1 else 0
+    if T <= 1:
+        rs = 0
+    if H <= 1:
+        hs = 0
     with on_device(dev, stream) as launch:
-        st = load().csa_cache_append(ctypes.byref(c), rows.data_ptr(), _dtype_code(rows.dtype),
-                                     rows.shape[0], rs, hs, page_table.data_ptr(), n, width,
+        st = load().csa_cache_append(ctypes.byref(c), rows.data_ptr(), _types.rows[rows.dtype],
+                                     T, rs, hs, page_table.data_ptr(), n, width,
                                      seq_lens.data_ptr(), cu_rows.data_ptr(), launch.handle)
         if st != 0:
             _raise(st)
@@ -114,25 +157,40 @@ def csa_cache_attend(q, cache, scales, page_table, seq_lens, cu_q, kv_heads: int
     visible (int32 [tokens]): rows that each query sees, all where None. lse
     (natural logarithm, fp32 [tokens, heads]) lets the result be merged with
     attention over other rows. Tokens at or behind cu_q[-1] are not written."""
-    import torch
-    c, dev = _cache(cache, scales)
-    n, width = _tables(page_table, seq_lens, dev)
-    _check(cu_q, "cu_q", torch.int32, dev, 1)
-    _rows(q, "q", (torch.bfloat16, torch.float16), dev)
-    if cu_q.shape[0] != n + 1:
-        raise ValueError("cu_q must be [num_seqs + 1]")
-    T, H, D = q.shape
-    if D != c.head_dim:
-        raise ValueError("q must be [tokens, heads, head_dim] with the cache's head_dim")
+    try:
+        dev = cache.get_device()
+        (pages, heads, page, D), (sp, sh, blocks) = cache.shape, scales.shape
+        (n, width), (lens,), (cu,) = page_table.shape, seq_lens.shape, cu_q.shape
+        (T, H, cols), (qt, qh, last) = q.shape, q.stride()
+        fine = (sp == pages and sh == heads and cols == D and blocks >= 1 and page % blocks == 0
+                and n == lens == cu - 1 and n >= 1 and width >= 1 and H >= 1 and last == 1
+                and _fine(cache, scales, q, _types.queries, dev, page_table, seq_lens, cu_q))
+    except (AttributeError, ValueError):
+        fine = False
+    if fine:
+        c = _Cache(cache.data_ptr(), scales.data_ptr(), pages, heads, page, page // blocks, D)
+    else:
+        c, dev = _cache(cache, scales)
+        n, width = _tables(page_table, seq_lens, dev)
+        _check(cu_q, "cu_q", _types.i32, dev, 1)
+        _rows(q, "q", tuple(_types.queries), dev)
+        if cu_q.shape[0] != n + 1:
+            raise ValueError("cu_q must be [num_seqs + 1]")
+        (T, H, D), (qt, qh, _) = q.shape, q.stride()
+        if D != c.head_dim:
+            raise ValueError("q must be [tokens, heads, head_dim] with the cache's head_dim")
     if visible is not None:
-        _check(visible, "visible", torch.int32, dev, 1)
+        _check(visible, "visible", _types.i32, dev, 1)
         if visible.shape[0] != T:
             raise ValueError("visible must be [tokens]")
-    qt = q.stride(0) if T > 1 else 0
-    qh = q.stride(1) if H > 1 else 0
+    # the stride of a dimension of one element is never stepped: 0
+    if T <= 1:
+        qt = 0
+    if H <= 1:
+        qh = 0
     with on_device(dev, stream) as launch:
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out = _types.empty_like(q, **_types.contiguous)
         else:
             _check(out, "out", q.dtype, dev, 3)
             if out.shape != q.shape:
@@ -140,13 +198,13 @@ def csa_cache_attend(q, cache, scales, page_table, seq_lens, cu_q, kv_heads: int
             if out.data_ptr() == q.data_ptr() and T > 0 or output_overlaps(out, q):
                 raise ValueError("out overlaps q")
         if lse is None:
-            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+            lse = _types.empty((T, H), dtype=_types.f32, device=dev)
         else:
-            _check(lse, "lse", torch.float32, dev, 2)
+            _check(lse, "lse", _types.f32, dev, 2)
             if tuple(lse.shape) != (T, H):
                 raise ValueError("lse must be [tokens, heads]")
         st = load().csa_cache_attend(
-            ctypes.byref(c), q.data_ptr(), _dtype_code(q.dtype), T, H, qt, qh, kv_heads,
+            ctypes.byref(c), q.data_ptr(), _types.queries[q.dtype], T, H, qt, qh, kv_heads,
             int(shared), sm_scale, page_table.data_ptr(), n, width, seq_lens.data_ptr(),
             cu_q.data_ptr(), None if visible is None or T == 0 else visible.data_ptr(),
             out.data_ptr(), lse.data_ptr() if T else None, launch.handle)

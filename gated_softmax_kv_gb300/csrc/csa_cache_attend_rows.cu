@@ -67,6 +67,26 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 __device__ __forceinline__ void group_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// The same place in the shared memory of block `rank` of the cluster.
+__device__ __forceinline__ uint32_t smem_of(uint32_t at, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+template <bool CLUSTER>
+__device__ __forceinline__ float4 load_shared(uint32_t at) {
+  float4 v;
+  if (CLUSTER)
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  else
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+constexpr int kMostSplit = 8;  // blocks of a cluster
+
 template <int D, bool SHARED, int NT>
 struct Shape {
   static constexpr int DW = D < 128 ? D : 128;  // columns of a warp
@@ -108,8 +128,8 @@ __device__ __forceinline__ int merged_at(int row, int c) {
   return c ^ ((DW == 128 ? t : (t & 1) | ((t & 2) << 1)) << 2);
 }
 
-template <int D, bool SHARED, int NT, bool HALF>
-__global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
+template <int D, bool SHARED, int NT, bool HALF, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, CLUSTER ? 1 : Shape<D, SHARED, NT>::PER_SM)
     attend_rows_kernel(const AttendArgs a, const PlanShape plan) {
   using C = Shape<D, SHARED, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -118,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
   __shared__ int32_t row_sees[C::ROWS];
   __shared__ float row_factor[C::ROWS];
   __shared__ int64_t row_at[C::ROWS];                  // where its output row is, or -1
-  __shared__ float merged[C::ROWS], part_factor[C::GROUPS][C::ROWS];
+  __shared__ float merged[C::ROWS], part_factor[(CLUSTER ? kMostSplit : 1) * C::GROUPS][C::ROWS];
   __shared__ int32_t sees_least, sees_most;
   grid_dependency_wait();
   allow_dependent_launch();
@@ -127,7 +147,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
   const int grp = warp / C::WD, wd = warp % C::WD;
   uint8_t* ring = smem + warp * C::RING;
   const uint32_t ring_at = smem_addr(ring);
-  const Place place = locate<kThreads>(a, plan, blockIdx.x, sums, &found);
+  const int split = CLUSTER ? plan.split : 1, rank = CLUSTER ? blockIdx.x & (split - 1) : 0;
+  const int stride = C::GROUPS * split;  // chunks of a step of the worker
+  const Place place = locate<kThreads>(a, plan, CLUSTER ? blockIdx.x / split : blockIdx.x, sums, &found);
   Shared* left = shared_items<C::ROWS, D>(a, plan.workers) + blockIdx.x;  // unless items are whole
   if (place.pos < 0) {
     if (threadIdx.x == 0 && !plan.whole) left->parts = 0;
@@ -192,37 +214,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
           atomicMax(&sees_most, (int)n);
         }
       }
-      float amax = 0.0f, v[V][8];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const uint32_t u[4] = {x[r][k].x, x[r][k].y, x[r][k].z, x[r][k].w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t bits = e & 1 ? u[e >> 1] >> 16 : u[e >> 1] & 0xFFFFu;
-          v[k][e] = HALF ? __half2float(__ushort_as_half((unsigned short)bits))
-                         : __uint_as_float(bits << 16);
-          const float m = fabsf(v[k][e]);
-          if (m < INFINITY) amax = fmaxf(amax, m);
-        }
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-      // 2^lift puts the largest finite value into [2^14, 2^15) (as far as 2^126 reaches)
-      const int lift = amax > 0.0f ? min(14 - ilogbf(amax), 126) : 0;
-      const float f = exp2i(max(lift, -126));
+      const int lift = query_lift<HALF>(finite_max<HALF, V>(x[r]));
+      const float f = exp2i(lift);
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int col = (k * 32 + lane) * 8;
-        if (col < D) {
-          uint4 y;
-          y.x = pack_f16x2(v[k][0] * f, v[k][1] * f);
-          y.y = pack_f16x2(v[k][2] * f, v[k][3] * f);
-          y.z = pack_f16x2(v[k][4] * f, v[k][5] * f);
-          y.w = pack_f16x2(v[k][6] * f, v[k][7] * f);
-          *reinterpret_cast<uint4*>(qs + i * D + col) = y;
-        }
+        if (col < D) *reinterpret_cast<uint4*>(qs + i * D + col) = lifted<HALF>(x[r][k], f);
       }
-      if (lane == 0) row_factor[i] = ldexpf(a.scale, -lift);
+      if (lane == 0) row_factor[i] = a.scale * exp2i(-lift);
     }
     __syncthreads();
     uint32_t qf[NT][C::DW / 16][2];
@@ -249,12 +248,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
 
     // ---- the keys --------------------------------------------------------------
     const int64_t stop = min(c1, ((int64_t)most + C::KS - 1) / C::KS);
-    const int64_t begin = c0 + grp;
-    const int steps = stop > begin ? (int)((stop - begin + C::GROUPS - 1) / C::GROUPS) : 0;
+    const int64_t begin = c0 + rank * C::GROUPS + grp;
+    const int steps = stop > begin ? (int)((stop - begin + stride - 1) / stride) : 0;
     const int32_t* row_table = a.table + (int64_t)s * a.max_pages;
     auto page_at = [&](int i, int u) -> int32_t {  // page of part u of step i
       if (i >= steps) return -1;
-      const int64_t key = (begin + (int64_t)i * C::GROUPS) * C::KS + u * 16;
+      const int64_t key = (begin + (int64_t)i * stride) * C::KS + u * 16;
       return key < most ? __ldg(row_table + (key >> pb)) : -1;
     };
     auto fetch = [&](int i, const int32_t* pages) {
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
         const uint32_t at = ring_at + (i % C::STAGES) * C::STAGE;
 #pragma unroll
         for (int u = 0; u < C::SUB; ++u) {
-          const int64_t key0 = (begin + (int64_t)i * C::GROUPS) * C::KS + u * 16;
+          const int64_t key0 = (begin + (int64_t)i * stride) * C::KS + u * 16;
           const bool in = pages[u] >= 0 && pages[u] < a.c.num_pages && key0 < most;
           const int slot = (int)(key0 & ((1 << pb) - 1));
           const int left = (int)min((int64_t)16, most - key0);  // rows that some query sees
@@ -325,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
       for (int u = 0; u < C::SUB; ++u) pages[u] = page_at(i + C::STAGES, u);
       const uint8_t* stage = ring + (i % C::STAGES) * C::STAGE;
       const float* scales = reinterpret_cast<const float*>(stage + C::SUB * C::PLANES * C::TILE);
-      const int64_t key0 = (begin + (int64_t)i * C::GROUPS) * C::KS;
+      const int64_t key0 = (begin + (int64_t)i * stride) * C::KS;
 
       // S^T
       float sc[C::SUB][NT][4];
@@ -563,50 +562,77 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
           *reinterpret_cast<float4*>(mg + row * D + merged_at<C::DW>(row, wd * C::DW + g * (C::DW / 8) + 2 * k)) =
               make_float4(o[k][n][j], o[k][n][j + 2], o[k + 1][n][j], o[k + 1][n][j + 2]);
       }
-    __syncthreads();
-    // A thread a row: its statistics over the groups, and the factor of each
-    // group's sums, with which they are finished or (split items) joined.
-    float* const parts = reinterpret_cast<float*>(smem);
+    if constexpr (CLUSTER)
+      cluster_barrier();
+    else
+      __syncthreads();
+    // A warp a row: its statistics over the groups (a lane each), and the factor
+    // of each group's sums, with which they are finished or (split items) joined.
+    // The blocks of a cluster share the rows out.
+    const uint32_t parts = smem_addr(smem);
+    const int n = stride, own = C::ROWS / split, row0 = rank * own;
+    auto part_at = [&](int k) -> uint32_t {  // of group k of the worker
+      if (!CLUSTER) return parts + k * (C::SLOT * 4);
+      return smem_of(parts + (k % C::GROUPS) * (C::SLOT * 4), k / C::GROUPS);
+    };
     // slot 0: the item began with another worker, slot 1: it did here
     float* const ws = a.ws + ((int64_t)blockIdx.x * 2 + (c0 == 0)) * C::SLOT;
-    if (threadIdx.x < C::ROWS) {
-      const float* st = parts + C::ROWS * D + threadIdx.x * 4;
+    for (int row = row0 + warp; row < row0 + own; row += 8) {
+      constexpr int LANES = CLUSTER ? kMostSplit * C::GROUPS / 32 + (kMostSplit * C::GROUPS < 32) : 1;
+      float4 st[LANES];
       RowStats r = {kNone, kNone, 0.0f};
 #pragma unroll
-      for (int k = 0; k < C::GROUPS; ++k) {
-        r.m = fmaxf(r.m, st[k * C::SLOT]);
-        r.mp = fmaxf(r.mp, st[k * C::SLOT + 1]);
+      for (int k = 0; k < LANES; ++k) {
+        st[k] = make_float4(kNone, kNone, 0.0f, 0.0f);
+        if (lane + 32 * k < n) st[k] = load_shared<CLUSTER>(part_at(lane + 32 * k) + (C::ROWS * D + row * 4) * 4);
+        r.m = fmaxf(r.m, st[k].x);
+        r.mp = fmaxf(r.mp, st[k].y);
       }
 #pragma unroll
-      for (int k = 0; k < C::GROUPS; ++k) r.l += st[k * C::SLOT + 2] * exp2f(st[k * C::SLOT] - r.m);
+      for (int w = 16; w; w >>= 1) {
+        r.m = fmaxf(r.m, __shfl_xor_sync(0xFFFFFFFFu, r.m, w));
+        r.mp = fmaxf(r.mp, __shfl_xor_sync(0xFFFFFFFFu, r.mp, w));
+      }
+#pragma unroll
+      for (int k = 0; k < LANES; ++k) r.l += st[k].z * exp2f(st[k].x - r.m);
+#pragma unroll
+      for (int w = 16; w; w >>= 1) r.l += __shfl_xor_sync(0xFFFFFFFFu, r.l, w);
       const float up = whole ? r.m + kLift + log2f(r.l) : r.mp;
 #pragma unroll
-      for (int k = 0; k < C::GROUPS; ++k) part_factor[k][threadIdx.x] = exp2f(st[k * C::SLOT + 1] - up);
-      merged[threadIdx.x] = r.l;
-      if (!whole)
-        *reinterpret_cast<float4*>(ws + C::ROWS * D + threadIdx.x * 4) = make_float4(r.m, r.mp, r.l, 0.0f);
-      else if (a.lse && row_at[threadIdx.x] >= 0)
-        a.lse[row_at[threadIdx.x]] = row_lse(r);
+      for (int k = 0; k < LANES; ++k)
+        if (lane + 32 * k < n) part_factor[lane + 32 * k][row] = exp2f(st[k].y - up);
+      if (lane == 0) {
+        merged[row] = r.l;
+        if (!whole)
+          *reinterpret_cast<float4*>(ws + C::ROWS * D + row * 4) = make_float4(r.m, r.mp, r.l, 0.0f);
+        else if (a.lse && row_at[row] >= 0)
+          a.lse[row_at[row]] = row_lse(r);
+      }
     }
     __syncthreads();
-#pragma unroll 4
-    for (int u = threadIdx.x; u < C::ROWS * (D / 4); u += kThreads) {
-      const int row = u / (D / 4), c = (u % (D / 4)) * 4;
+#pragma unroll 2
+    for (int u = threadIdx.x; u < own * (D / 4); u += kThreads) {
+      const int row = row0 + u / (D / 4), c = (u % (D / 4)) * 4;
+      const uint32_t at = (row * D + merged_at<C::DW>(row, c)) * 4;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int b = 0; b < split; ++b) {
+        const uint32_t from = part_at(b * C::GROUPS) + at;
 #pragma unroll
-      for (int k = 0; k < C::GROUPS; ++k) {
-        const float4 x = *reinterpret_cast<const float4*>(parts + k * C::SLOT + row * D + merged_at<C::DW>(row, c));
-        const float f = part_factor[k][row];
-        v.x = fmaf(x.x, f, v.x);
-        v.y = fmaf(x.y, f, v.y);
-        v.z = fmaf(x.z, f, v.z);
-        v.w = fmaf(x.w, f, v.w);
+        for (int k = 0; k < C::GROUPS; ++k) {
+          const float4 x = load_shared<CLUSTER>(from + k * (C::SLOT * 4));
+          const float f = part_factor[b * C::GROUPS + k][row];
+          v.x = fmaf(x.x, f, v.x);
+          v.y = fmaf(x.y, f, v.y);
+          v.z = fmaf(x.z, f, v.z);
+          v.w = fmaf(x.w, f, v.w);
+        }
       }
       if (!whole)
         *reinterpret_cast<float4*>(ws + row * D + c) = v;
       else if (row_at[row] >= 0)
         store4<HALF>(a.out + row_at[row] * D + c, v, merged[row] == 0.0f ? 0.0f : 1.0f);
     }
+    if (CLUSTER) cluster_barrier();  // the other blocks have read this one's sums
     pos += units;
     within += units;
   }
@@ -616,8 +642,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, SHARED, NT>::PER_SM)
 template <int D, bool SHARED, int NT, bool HALF>
 cudaError_t launch_tile(AttendArgs a, cudaStream_t stream) {
   using C = Shape<D, SHARED, NT>;
-  const PlanShape p = plan_of(a, C::ROWS, C::KS, 152 * C::PER_SM, 2 * C::GROUPS, 8 * C::GROUPS);
-  auto* kernel = attend_rows_kernel<D, SHARED, NT, HALF>;
+  const PlanShape p = plan_of(a, C::ROWS, C::KS, 152 * C::PER_SM, 2 * C::GROUPS, 8 * C::GROUPS, C::GROUPS);
+  if (p.split > 1) {
+    auto* kernel = attend_rows_kernel<D, SHARED, NT, HALF, true>;
+    const cudaError_t e = allow_dynamic_smem((const void*)kernel, C::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(kernel, dim3((unsigned)(p.workers * p.split)), dim3(kThreads), C::SMEM, (unsigned)p.split,
+                           stream, a, p);
+  }
+  auto* kernel = attend_rows_kernel<D, SHARED, NT, HALF, false>;
   cudaError_t e = allow_dynamic_smem((const void*)kernel, C::SMEM);
   if (e != cudaSuccess) return e;
   if (p.whole)

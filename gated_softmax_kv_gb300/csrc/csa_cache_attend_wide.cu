@@ -293,37 +293,16 @@ __device__ __forceinline__ void stage_queries(const uint16_t* q, float scale) {
 #pragma unroll
   for (int e = 0; e < EACH; ++e) {
     const int i = warp + e * C::SW;
-    float amax = 0.0f, v[V][8];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const uint32_t u[4] = {x[e][k].x, x[e][k].y, x[e][k].z, x[e][k].w};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t bits = j & 1 ? u[j >> 1] >> 16 : u[j >> 1] & 0xFFFFu;
-        v[k][j] = HALF ? __half2float(__ushort_as_half((unsigned short)bits))
-                       : __uint_as_float(bits << 16);
-        const float m = fabsf(v[k][j]);
-        if (m < INFINITY) amax = fmaxf(amax, m);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    const int lift = amax > 0.0f ? min(14 - ilogbf(amax), 126) : 0;
-    const float f = exp2i(max(lift, -126));
+    const int lift = query_lift<HALF>(finite_max<HALF, V>(x[e]));
+    const float f = exp2i(lift);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int col = (k * 32 + lane) * 8;
-      if (col < D) {
-        uint4 y;
-        y.x = pack_f16x2(v[k][0] * f, v[k][1] * f);
-        y.y = pack_f16x2(v[k][2] * f, v[k][3] * f);
-        y.z = pack_f16x2(v[k][4] * f, v[k][5] * f);
-        y.w = pack_f16x2(v[k][6] * f, v[k][7] * f);
-        *reinterpret_cast<uint4*>(to + (col >> 6) * C::QSLAB + i * 128 +
-                                  ((((col >> 3) & 7) ^ (i & 7)) << 4)) = y;
-      }
+      if (col < D)
+        *reinterpret_cast<uint4*>(to + (col >> 6) * C::QSLAB + i * 128 + ((((col >> 3) & 7) ^ (i & 7)) << 4)) =
+            lifted<HALF>(x[e][k], f);
     }
-    if (lane == 0) st.zf[i] = ldexpf(scale, -lift);
+    if (lane == 0) st.zf[i] = scale * exp2i(-lift);
   }
 }
 
@@ -433,10 +412,15 @@ __device__ __noinline__ void wide_raise(uint32_t s_at, float sk, float lv, bool 
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {  // z, then z + log2(value scale)
     tc_load32(s_at, t);
+    const float add = k ? lv : 0.0f;
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      t[c] = __fmul_rn(t[c], __fmul_rn(sk, st.zf[col + c])) + (k ? lv : 0.0f);
-      t[c] = there && key < st.sees[col + c] ? t[c] : -INFINITY;
+    for (int c = 0; c < 32; c += 4) {
+      const float4 z4 = *reinterpret_cast<const float4*>(st.zf + col + c);
+      const int4 n4 = *reinterpret_cast<const int4*>(st.sees + col + c);
+      t[c] = there && key < n4.x ? __fmul_rn(t[c], __fmul_rn(sk, z4.x)) + add : -INFINITY;
+      t[c + 1] = there && key < n4.y ? __fmul_rn(t[c + 1], __fmul_rn(sk, z4.y)) + add : -INFINITY;
+      t[c + 2] = there && key < n4.z ? __fmul_rn(t[c + 2], __fmul_rn(sk, z4.z)) + add : -INFINITY;
+      t[c + 3] = there && key < n4.w ? __fmul_rn(t[c + 3], __fmul_rn(sk, z4.w)) + add : -INFINITY;
     }
     st.best[k][half][quarter][lane] = column_max(t, lane);
   }
@@ -550,7 +534,13 @@ __device__ __noinline__ void wide_softmax() {
       }
       if (mixed) {  // rows that do not see this key
 #pragma unroll
-        for (int c = 0; c < 32; ++c) t[c] = there && key < st.sees[col + c] ? t[c] : -INFINITY;
+        for (int c = 0; c < 32; c += 4) {
+          const int4 n4 = *reinterpret_cast<const int4*>(st.sees + col + c);
+          t[c] = there && key < n4.x ? t[c] : -INFINITY;
+          t[c + 1] = there && key < n4.y ? t[c + 1] : -INFINITY;
+          t[c + 2] = there && key < n4.z ? t[c + 2] : -INFINITY;
+          t[c + 3] = there && key < n4.w ? t[c + 3] : -INFINITY;
+        }
       }
       float mx = -INFINITY, mw = -INFINITY;
 #pragma unroll
@@ -990,7 +980,7 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
 template <int D, bool SHARED, bool HALF>
 cudaError_t launch_wide(AttendArgs a, cudaStream_t stream) {
   using C = Wide<D, SHARED>;
-  const PlanShape p = plan_of(a, C::R, 128, 152, 2, 8);
+  const PlanShape p = plan_of(a, C::R, 128, 152, 2, 8, 0);
   auto* kernel = attend_wide_kernel<D, SHARED, HALF>;
   cudaError_t e = allow_dynamic_smem((const void*)kernel, C::SMEM);
   if (e != cudaSuccess) return e;

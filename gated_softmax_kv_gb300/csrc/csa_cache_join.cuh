@@ -30,6 +30,56 @@ __device__ __forceinline__ uint32_t lo_f16x2(uint32_t w) { return e4m3x2_to_f16x
 __device__ __forceinline__ uint32_t hi_f16x2(uint32_t w) {
   return e4m3x2_to_f16x2((uint16_t)(w >> 16));
 }
+// A query row as fp16, times a power of two that puts its largest finite value
+// into [2^14, 2^15) (as far as 2^126 reaches). A lane holds V vectors of it.
+// The magnitudes are compared as integers, two to an instruction: without the
+// sign, the bits grow with the value, infinities and NaN above every finite one.
+template <bool HALF, int V>
+__device__ __forceinline__ uint32_t finite_max(const uint4 (&x)[V]) {
+  constexpr uint32_t INF = HALF ? 0x7C00u : 0x7F80u;
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    m = __vmaxu2(m, __vmaxu2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu));
+    m = __vmaxu2(m, __vmaxu2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu));
+  }
+  m = max(m >> 16, m & 0xFFFFu);
+  if (__any_sync(0xFFFFFFFFu, m >= INF)) {
+    m = 0;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const uint32_t u[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t b = (u[e >> 1] >> (16 * (e & 1))) & 0x7FFFu;
+        if (b < INF) m = max(m, b);
+      }
+    }
+  }
+  return __reduce_max_sync(0xFFFFFFFFu, m);
+}
+// The power: the bits of finite_max to the exponent.
+template <bool HALF>
+__device__ __forceinline__ int query_lift(uint32_t amax) {
+  if (amax == 0) return 0;
+  const float v = HALF ? __half2float(__ushort_as_half((unsigned short)amax)) : __uint_as_float(amax << 16);
+  return min(14 + 127 - (int)(__float_as_uint(v) >> 23), 126);
+}
+template <bool HALF>
+__device__ __forceinline__ uint4 lifted(const uint4& x, float f) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float2 v;
+    if (HALF)
+      v = __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
+    else
+      v = make_float2(bf16_lo(u[e]), bf16_hi(u[e]));
+    r[e] = pack_f16x2(v.x * f, v.y * f);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
 // 0xFF in the bytes that hold a NaN.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);

@@ -19,6 +19,7 @@ struct PlanShape {
   int32_t workers;
   int32_t least;     // fewest chunks a worker takes
   bool whole;        // items are not cut: one unit each
+  int32_t split;     // thread blocks of a cluster, which is then a worker (whole items)
 };
 
 struct SeqWork {
@@ -101,16 +102,22 @@ __device__ __forceinline__ Place locate(const AttendArgs& a, const PlanShape& p,
 // The plan of a call, on the host. Items of at most `few` chunks, as the table's
 // width shows, are not worth cutting: no workspace, no joining kernel, and as
 // many workers as there can be items, up to four for each that is resident.
-inline PlanShape plan_of(const AttendArgs& a, int rows, int keys, int resident, int least, int few) {
+// Where so few items leave SMs free, the blocks of a cluster share an item's
+// keys, `groups` chunks a block at a time (0: the kernel has no clusters); four
+// such steps cost less than the second kernel.
+inline PlanShape plan_of(const AttendArgs& a, int rows, int keys, int resident, int least, int few, int groups) {
   PlanShape p;
   p.row_bits = log2_of(rows);
   p.key_bits = log2_of(keys);
   p.least = least;
   p.workers = resident;
   const int64_t chunks = (((int64_t)a.max_pages << a.c.page_bits) + keys - 1) / keys;
-  p.whole = chunks <= few;
+  const int64_t items = ((a.tokens * a.group) / rows + a.nseq) * a.kv;
+  p.split = 1;
+  while (p.split < 8 && groups > 0 && items * p.split * 2 <= 152 && chunks > p.split * groups) p.split *= 2;
+  p.whole = chunks <= few || (p.split > 1 && chunks <= 4 * p.split * groups);
+  if (!p.whole) p.split = 1;
   if (p.whole) {
-    const int64_t items = ((a.tokens * a.group) / rows + a.nseq) * a.kv;
     p.workers = (int32_t)(items < 4 * resident ? items : 4 * resident);
     p.least = 1;
   }
