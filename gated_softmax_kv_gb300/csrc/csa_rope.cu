@@ -8,7 +8,10 @@
 // fp32 rate here). The top 32 bits go through sincospif.
 //
 // The kernels are copies with some arithmetic, bound by memory. A thread keeps
-// its columns for its whole loop, so F is worked out once per thread.
+// its columns for its whole loop, so F is worked out once per thread. 66533 rows
+// of 512 bf16 columns, 64 of them turned, take 22 us (6.2 TB/s, 92% of the
+// copy rate); 32768 tokens of 8 fp16 heads of 128 columns, all turned, 26.5 us
+// (75%). A decoding step (16 tokens of 64 heads) takes 4 us, a launch's latency.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -290,12 +293,13 @@ __device__ __forceinline__ int64_t warp_position(const RopeArgs& a, int64_t t, i
 }
 
 // Rows that share nothing (one head, or a decoding step): whole warps turn 32
-// pairs of T rows at a time, a lane a pair, so that a row's sines cost one pass
-// of a warp; the other half of the CTA's warps copy what is not turned, 16 bytes
-// a thread and T of them in flight. One kernel whose lanes did either cost 455
-// instructions a warp and row of 512 bf16 columns, 64 of them turned (58 us for
-// 66533 rows); this one about a third of that.
-template <typename E, bool HALF, int T>
+// pairs of a row at a time, a lane a pair, so that a row's sines cost one pass of
+// a warp; the other half of the CTA's warps copy what is not turned, 16 bytes a
+// thread. One kernel whose lanes did either cost 455 instructions a warp and row
+// of 512 bf16 columns, 64 of them turned (58 us for 66533 rows); this one about a
+// third of that (22 us). Four rows a warp and thread at once measured the same
+// there, and 20.5 us against 17.8 for rows of 128 columns.
+template <typename E, bool HALF>
 __global__ void __launch_bounds__(256) rope_rows_kernel(const RopeArgs a, int32_t blocks_of_pairs, int32_t copied) {
   grid_dependency_wait();
   allow_dependent_launch();
@@ -316,27 +320,17 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(const RopeArgs a, int32_
     const E* x = static_cast<const E*>(a.x) + col;
     E* y = static_cast<E*>(a.y) + col;
     const float sign = a.transpose ? -1.0f : 1.0f;
-    for (int64_t r = (id - block * each) * T; r < rows; r += each * T) {
-      uint32_t va[T], vb[T];
-      int64_t token[T];
-      int head[T];
-#pragma unroll
-      for (int j = 0; j < T; ++j) {
-        const int64_t row = min(r + j, rows - 1);
-        token[j] = a.heads == 1 ? row : row / a.heads;
-        head[j] = (int)(row - token[j] * a.heads);
-        if (on) load_pair<E, HALF>(x + token[j] * a.xt + head[j] * a.xh, pairs, va[j], vb[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < T; ++j) {
-        const int64_t pos = warp_position(a, token[j], lane);
-        float c, s;
-        turn_of(f, pos, a.amplitude, sign, &c, &s);
-        const float2 p = pair_value<E, HALF>(va[j], vb[j]);
-        if (on && r + j < rows)
-          store_pair<E, HALF>(y + token[j] * a.yt + head[j] * a.yh, pairs,
-                              make_float2(fmaf(-p.y, s, p.x * c), fmaf(p.x, s, p.y * c)));
-      }
+    for (int64_t r = id - block * each; r < rows; r += each) {
+      const int64_t token = a.heads == 1 ? r : r / a.heads;
+      const int head = (int)(r - token * a.heads);
+      uint32_t va, vb;
+      if (on) load_pair<E, HALF>(x + token * a.xt + head * a.xh, pairs, va, vb);
+      float c, s;
+      turn_of(f, warp_position(a, token, lane), a.amplitude, sign, &c, &s);
+      const float2 p = pair_value<E, HALF>(va, vb);
+      if (on)
+        store_pair<E, HALF>(y + token * a.yt + head * a.yh, pairs,
+                            make_float2(fmaf(-p.y, s, p.x * c), fmaf(p.x, s, p.y * c)));
     }
   } else {
     const uint32_t id = blockIdx.x * 128 + threadIdx.x - 128, lanes = gridDim.x * 128 / copied;
@@ -346,20 +340,11 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(const RopeArgs a, int32_
     const int col = c < a.offset ? c : c + a.rope;
     const E* x = static_cast<const E*>(a.x) + col;
     E* y = static_cast<E*>(a.y) + col;
-    for (int64_t r = first; r < rows; r += (int64_t)lanes * T) {
-      uint4 v[T];
-      E* to[T];
-#pragma unroll
-      for (int j = 0; j < T; ++j) {
-        const int64_t row = r + (int64_t)j * lanes;
-        const int64_t token = a.heads == 1 ? row : row / a.heads;
-        const int head = (int)(row - token * a.heads);
-        to[j] = y + token * a.yt + head * a.yh;
-        if (row < rows) v[j] = ld_stream(reinterpret_cast<const uint16_t*>(x + token * a.xt + head * a.xh));
-      }
-#pragma unroll
-      for (int j = 0; j < T; ++j)
-        if (r + (int64_t)j * lanes < rows) *reinterpret_cast<uint4*>(to[j]) = v[j];
+    for (int64_t r = first; r < rows; r += lanes) {
+      const int64_t token = a.heads == 1 ? r : r / a.heads;
+      const int head = (int)(r - token * a.heads);
+      *reinterpret_cast<uint4*>(y + token * a.yt + head * a.yh) =
+          ld_stream(reinterpret_cast<const uint16_t*>(x + token * a.xt + head * a.xh));
     }
   }
 }
@@ -406,11 +391,15 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
   if (bytes % 16 == 0 && cols % N == 0) {
     constexpr int WIDE = HALF ? N : N / 2;
     const int copied = a.in_place ? 0 : (a.d - a.rope) / N;
-    // Heads share a token's sines, four at a time, where that still leaves every
-    // SM its threads.
+    // Heads share a token's sines, four at a time, where the rows' turned pairs are
+    // enough work for that (in warps of 32 pairs). Measured as a graph, rows kernel
+    // against this: 8 heads of 128 fp16 columns, all turned, 256 tokens (4096 warps)
+    // 2.9 us / 3.7, 512 tokens 4.3 / 3.7, 2048 tokens 8.2 / 3.9; 64 heads of 512, 64
+    // turned, 16 tokens (1024) 2.2 / 2.7, 64 tokens (4096) 3.9 / 2.9; all of 512
+    // turned, 16 tokens (8192) 4.2 / 2.8, 256 tokens 23.9 / 7.3.
     const int chunks = a.rope / (2 * WIDE) + copied, groups = (a.heads + 3) / 4;
     const int64_t most = 152 * 4;
-    if (a.heads >= 4 && a.tokens * groups * chunks >= (int64_t)152 * 1024) {
+    if (a.heads >= 4 && a.tokens * a.heads * ((a.rope / 2 + 31) / 32) >= 4096) {
       int64_t blocks = (a.tokens * groups * chunks + 255) / 256;
       if (blocks > most) blocks = most;
       const int64_t least = (chunks + 255) / 256;  // at least one whole row of chunks
@@ -418,20 +407,18 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
       return launch_dependent(rope_heads_kernel<T, HALF>, dim3((unsigned)blocks), dim3(256), 0, stream, a,
                               (int32_t)chunks, (int32_t)groups);
     }
-    // Four rows a warp where there are enough of them to fill the GPU.
     const int64_t rows = a.tokens * a.heads;
     const int pairs32 = (a.rope / 2 + 31) / 32, turners = copied ? 4 : 8;
-    const bool four = rows * pairs32 >= (int64_t)152 * 64;
-    int64_t blocks = (rows * pairs32 + turners * (four ? 4 : 1) - 1) / (turners * (four ? 4 : 1));
-    const int64_t copies = (rows * copied + (four ? 511 : 127)) / (four ? 512 : 128);
+    int64_t blocks = (rows * pairs32 + turners - 1) / turners;
+    const int64_t copies = (rows * copied + 127) / 128;
     if (blocks < copies) blocks = copies;
     if (blocks > 2 * most) blocks = 2 * most;
     const int64_t least = (pairs32 + turners - 1) / turners > (copied + 127) / 128
                               ? (pairs32 + turners - 1) / turners
                               : (copied + 127) / 128;  // every block of pairs, a whole row of copies
     if (blocks < least) blocks = least;
-    return launch_dependent(four ? rope_rows_kernel<T, HALF, 4> : rope_rows_kernel<T, HALF, 1>,
-                            dim3((unsigned)blocks), dim3(256), 0, stream, a, (int32_t)pairs32, (int32_t)copied);
+    return launch_dependent(rope_rows_kernel<T, HALF>, dim3((unsigned)blocks), dim3(256), 0, stream, a,
+                            (int32_t)pairs32, (int32_t)copied);
   }
   const int64_t items = a.tokens * a.heads * (a.rope / 2 + (a.in_place ? 0 : a.d - a.rope));
   int64_t blocks = (items + 255) / 256;
