@@ -12,7 +12,7 @@
 // ahead, widen them to fp16 (exact) and store them to a ring of panels (128 keys
 // x 128 columns) in shared memory in the 128-byte swizzle; a panel is the
 // K-major operand of S^T and, unchanged, the M-major operand of O^T, so a row
-// that is key and value is stored once. One thread issues the matrix
+// that is key and value is stored once. A warp of its own issues the matrix
 // instructions. Softmax warps own a key a thread: they read S^T from TMEM, form
 // the weights and store P^T [key][row], the N-major operand.
 //
@@ -20,6 +20,16 @@
 // when passed, fp16 weights that carry the value scale. Where scales lie
 // within 2^30 and the references within 2^60 of one another, the weight is the
 // softmax term times two factors; beyond, it takes an exponential of its own.
+//
+// What bounds it: shared memory and the chain. A tile of 128 keys of 512 columns
+// costs 64 instructions of 128 x 64 x 16 (3.1 K cycles at 6 KB of operands and
+// 128 bytes a cycle each), 128 KB of stores (1 K) and the softmax (2.4 K); heads
+// of 512 have room for one tile in the ring, so refill, S^T, softmax and O^T
+// follow one another: 8.8 K cycles a tile. Seven producer warps measured best (six
+// 201 us, eight 238, seven 192). Measured: 64 sequences of 10400 rows on average,
+// 64 heads over one row of 512: 186 us (446 TFLOP/s), joining 15 us; one sequence
+// of 65536 rows 44 us; 255 queries each of four sequences of up to 4099 rows, 16
+// heads over two of 128 columns, 83 us.
 //
 // Every wait on an mbarrier is bounded: a wait that runs out marks the CTA,
 // whose later waits then return at once, and its results become NaN.

@@ -101,10 +101,12 @@ __device__ __forceinline__ Place locate(const AttendArgs& a, const PlanShape& p,
 
 // The plan of a call, on the host. Items of at most `few` chunks, as the table's
 // width shows, are not worth cutting: no workspace, no joining kernel, and as
-// many workers as there can be items, up to four for each that is resident.
+// many workers as there can be items, up to four for each that is resident (300
+// rows by 16 heads: 20 us a call, cut and joined 26).
 // Where so few items leave SMs free, the blocks of a cluster share an item's
-// keys, `groups` chunks a block at a time (0: the kernel has no clusters); four
-// such steps cost less than the second kernel.
+// keys, `groups` chunks a block at a time (0: the kernel has no clusters): the same
+// rows take 13.9 us by 8 blocks, 21.5 by one. A step is 2 us; four cost no more
+// than the second kernel (5 us) and its workspace.
 inline PlanShape plan_of(const AttendArgs& a, int rows, int keys, int resident, int least, int few, int groups) {
   PlanShape p;
   p.row_bits = log2_of(rows);
