@@ -58,9 +58,10 @@ extern "C" csa_status_t csa_cache_attend(const csa_cache_t* cache, const void* q
   // The rows kernel passes over the keys once for 16 rows, the wide one for 64.
   // Measured (32 sequences of 4096 rows, as a graph, rows against wide kernel):
   // shared rows of 512 columns, 16 rows 34 us / 62, 32 rows 56 / 62, 64 rows
-  // 102 / 64; two heads of 128 columns, 30 / 49, 46 / 49, 76 / 49. Heads of 64
-  // columns have no wide kernel: a panel of the wide one has 128.
-  const bool wide = cache->head_dim >= 128 && num_tokens * a.group > (int64_t)32 * num_seqs;
+  // 102 / 64; two heads of 128 columns, 30 / 49, 46 / 49, 76 / 49; of 64 columns,
+  // which fill half of the wide kernel's panels, 26 / 47, 38 / 49, 62 / 48.
+  const int64_t most_rows = cache->head_dim == 64 ? 48 : 32;
+  const bool wide = num_tokens * a.group > most_rows * num_seqs;
   const cudaError_t e = wide ? csa::launch_attend_wide(a, dtype == CSA_FP16, shared != 0, stream)
                              : csa::launch_attend_rows(a, dtype == CSA_FP16, shared != 0, stream);
   return e == cudaSuccess ? CSA_OK : csa::record_cuda_error(e);

@@ -25,8 +25,7 @@ struct AttendArgs {
 
 // Tiles of up to 16 query rows on mma.sync (csa_cache_attend_rows.cu).
 cudaError_t launch_attend_rows(const AttendArgs& a, bool half, bool shared, cudaStream_t stream);
-// Tiles of 64 query rows on tcgen05, head_dim 128 and more
-// (csa_cache_attend_wide.cu).
+// Tiles of 64 query rows on tcgen05 (csa_cache_attend_wide.cu).
 cudaError_t launch_attend_wide(const AttendArgs& a, bool half, bool shared, cudaStream_t stream);
 
 }  // namespace csa

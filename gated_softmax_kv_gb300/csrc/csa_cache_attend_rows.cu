@@ -672,7 +672,10 @@ cudaError_t launch_tile(AttendArgs a, cudaStream_t stream) {
 template <int D, bool SHARED, bool HALF>
 cudaError_t launch_rows(const AttendArgs& a, cudaStream_t stream) {
   // A tile of 8 rows holds a group of up to 8 heads; larger groups, and more
-  // than one token a sequence, fill 16 rows for one pass over the keys.
+  // than one token a sequence, fill 16 rows for one pass over the keys. Measured
+  // (32 sequences, tiles of 8 against 16): 8 cache heads of 128 with 8 heads each
+  // 78 us / 122, with 16 each 141 / 123; one of 512 with 8 heads 29 / 34, with 16
+  // heads 43 / 35.
   if (a.group <= 8 && (int64_t)a.group * a.tokens <= (int64_t)8 * a.nseq)
     return launch_tile<D, SHARED, 1, HALF>(a, stream);
   return launch_tile<D, SHARED, 2, HALF>(a, stream);

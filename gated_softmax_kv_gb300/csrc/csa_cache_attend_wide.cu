@@ -5,6 +5,7 @@
 // at a time, transposed so that the accumulator's lanes are keys, then columns:
 //   S^T [128 keys x R] = K [128 x D] Q^T        (TMEM, two buffers)
 //   O^T [D x R] += V^T [D x 128] P^T            (TMEM, D / 128 tiles of 128 x R)
+// Heads of 64 columns fill half a panel; the other half holds them again.
 // TMEM's 512 columns hold 2 R + R D / 128 of them. The rows are the N of both
 // products, so 64 heads fill the tensor core as well as 128 do.
 //
@@ -195,7 +196,7 @@ extern __shared__ __align__(1024) uint8_t wide_smem[];
 template <int D, bool SHARED>
 struct Wide {
   static constexpr int R = 64;                      // query rows of a tile
-  static constexpr int PP = D / 128;                // panels of 128 keys
+  static constexpr int PP = (D + 127) / 128;        // panels of 128 keys; of D = 64 the columns come twice
   static constexpr int SW = R / 8;                  // softmax warps: 4 for each 32 rows
   static constexpr int PW = 7;                      // producer warps
   static constexpr int THREADS = (SW + PW + 1) * 32;  // 16 warps: 128 registers a thread
@@ -363,7 +364,7 @@ struct Issue {
       const uint64_t k = operand(at.ring + slot * C::PANEL, 16);
       const uint64_t q = operand(at.q + pp * 2 * C::QSLAB, 16);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < (D < 128 ? 4 : 8); ++j)
         tc_mma(tmem + C::S0 + b * C::R, k + ((j >> 2) * C::SLAB + (j & 3) * 32) / 16,
                q + ((j >> 2) * C::QSLAB + (j & 3) * 32) / 16, C::IDESC_S, pp > 0 || j > 0);
       if (!SHARED) tc_commit(at.empty + 8 * slot);
@@ -680,6 +681,7 @@ __device__ __noinline__ void wide_result() {
   barrier_of(3, C::SW * 32);
   for (int pp = 0; pp < C::PP; ++pp) {
     const int d = pp * 128 + mine;
+    if (pp * 128 + quarter * 32 >= D) continue;  // the second copy of 64 columns
     int bad = 0x7FFFFFFF;  // first row whose value in column d is NaN
     if (nans && !SHARED)
       for (int64_t key = mixed0; key < mixed1; ++key) {
@@ -826,7 +828,7 @@ __device__ __noinline__ void wide_produce() {
         const int32_t first = __shfl_sync(0xFFFFFFFFu, kib, p * 8 + (e >> 2));
         const bool ok = first >= 0 && e * 4 + kb < left;
         there |= (uint32_t)ok << k;
-        src[k] = pool + (ok ? (int64_t)first << 10 : 0) + ((e & 3) * 4 + kb) * D + chunk * 16;
+        src[k] = pool + (ok ? (int64_t)first << 10 : 0) + ((e & 3) * 4 + kb) * D + (chunk * 16) % D;
       }
     }
     mask = there;
@@ -1035,6 +1037,7 @@ cudaError_t launch_dim(const AttendArgs& a, bool half, bool shared, cudaStream_t
 
 cudaError_t launch_attend_wide(const AttendArgs& a, bool half, bool shared, cudaStream_t stream) {
   switch (a.c.d) {
+    case 64: return launch_dim<64>(a, half, shared, stream);
     case 128: return launch_dim<128>(a, half, shared, stream);
     case 256: return launch_dim<256>(a, half, shared, stream);
     default: return launch_dim<512>(a, half, shared, stream);

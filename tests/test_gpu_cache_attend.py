@@ -232,7 +232,8 @@ def test_strides_streams_and_repeats(gsk):
 
 
 @pytest.mark.parametrize("D,shared,kv,group,n", [(128, False, 2, 8, 5000), (512, True, 1, 16, 3000), (512, True, 1, 64, 4000),
-                                                 (64, True, 1, 1, 9000), (512, True, 1, 128, 2000), (128, True, 1, 128, 6000)])
+                                                 (64, True, 1, 1, 9000), (512, True, 1, 128, 2000), (128, True, 1, 128, 6000),
+                                                 (64, True, 2, 128, 4000), (64, False, 1, 80, 5000)])
 def test_long_sequences_are_split_and_joined(gsk, D, shared, kv, group, n):
     """One long sequence next to short ones, against a 64-bit product on the GPU."""
     lens = [n, 3, 0, 700]
@@ -350,7 +351,8 @@ def test_a_pool_past_32_bits(gsk):
 
 @pytest.mark.parametrize("D,shared,kv,group,queries", [(64, True, 1, 2, 1), (64, False, 2, 3, 5), (128, False, 2, 8, 1),
                                                        (256, True, 1, 4, 3), (512, False, 1, 5, 1), (512, True, 1, 64, 1),
-                                                       (128, False, 1, 8, 20), (256, False, 1, 64, 1)])
+                                                       (128, False, 1, 8, 20), (256, False, 1, 64, 1), (64, True, 1, 64, 2),
+                                                       (64, False, 2, 70, 1)])
 def test_short_and_wide_tables(gsk, D, shared, kv, group, queries):
     """Items are cut or not by the width of the table: the same sequences under a
     table just wide enough, and under ones that have room for far more rows."""
