@@ -28,8 +28,8 @@
 // of 512 have room for one tile in the ring, so refill, S^T, softmax and O^T
 // follow one another: 8.8 K cycles a tile. Seven producer warps measured best (six
 // 201 us, eight 238, seven 192). Measured: 64 sequences of 10400 rows on average,
-// 64 heads over one row of 512: 186 us (446 TFLOP/s), joining 15 us; one sequence
-// of 65536 rows 44 us; 255 queries each of four sequences of up to 4099 rows, 16
+// 64 heads over one row of 512: 186 us (450 TFLOP/s), joining 13 us; one sequence
+// of 65536 rows 43 us, joining 8; 255 queries each of four sequences of up to 4099 rows, 16
 // heads over two of 128 columns, 83 us.
 //
 // Every wait on an mbarrier is bounded: a wait that runs out marks the CTA,

@@ -189,18 +189,18 @@ __device__ __forceinline__ void add_parts(const float* first, const float* rest,
   }
 }
 
-// Joins the shared items (64 sequences' tiles of 64 x 512 sums in 15 us, one in 152
-// parts in 13; 32 sequences' of 8 x 128 in 5): every CTA reads the list, and all pieces of all items
+// Joins the shared items (64 sequences' tiles of 64 x 512 sums in 13 us, one in 152
+// parts in 8; 32 sequences' of 8 x 128 in 5): every CTA reads the list, and all pieces of all items
 // are spread over the grid. An item of few parts (a batch: two or three) is
 // streamed, four columns a thread. Of a long one (a sequence alone on the GPU
-// has up to 152 parts) four threads take a quarter of the parts each, and are
-// added up in order.
+// has up to 152 parts) sixteen threads take a sixteenth of the parts each, and are
+// added up in order (four: 13 us).
 template <int D, int ROWS, bool HALF>
 __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a, int workers) {
   constexpr int SLOT = ROWS * (D + 4), QUADS = ROWS * D / 4, FEW = 12;
   __shared__ int32_t list[512], start[513];
-  __shared__ float4 sum[4][64];
-  __shared__ float4 stat[4][64];
+  __shared__ float4 sum[16][16];
+  __shared__ float4 stat[16][16];
   grid_dependency_wait();
   allow_dependent_launch();
   const Shared* items = shared_items<ROWS, D>(a, workers);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
     const int w = threadIdx.x * 2 + k;
     parts[k] = w < workers ? __ldg(&items[w].parts) : 0;
     before.x += parts[k] > 0;
-    before.y += parts[k] > FEW ? QUADS / 64 : parts[k] > 0 ? (QUADS + 255) / 256 : 0;
+    before.y += parts[k] > FEW ? QUADS / 16 : parts[k] > 0 ? (QUADS + 255) / 256 : 0;
   }
   const int2 mine = before;
 #pragma unroll
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
     if (parts[k] > 0) {
       list[at_item] = threadIdx.x * 2 + k;
       start[at_item++] = at_piece;
-      at_piece += parts[k] > FEW ? QUADS / 64 : (QUADS + 255) / 256;
+      at_piece += parts[k] > FEW ? QUADS / 16 : (QUADS + 255) / 256;
     }
   __syncthreads();
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
@@ -268,16 +268,16 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
       write_row<D, HALF>(a, row_of(a, item.s, item.tile, item.h, ROWS, row), at % D, r, o);
       continue;
     }
-    const int v = threadIdx.x & 63, quarter = threadIdx.x >> 6;
-    const int at = (piece * 64 + v) * 4, row = at / D;
-    const int each = (item.parts + 3) / 4, i0 = quarter * each, i1 = min(i0 + each, item.parts);
-    add_parts<8, ROWS, D>(first, rest, i0, i1, at, row, r, o);
+    const int v = threadIdx.x & 15, share = threadIdx.x >> 4;
+    const int at = (piece * 16 + v) * 4, row = at / D;
+    const int each = (item.parts + 15) / 16, i0 = share * each, i1 = min(i0 + each, item.parts);
+    add_parts<5, ROWS, D>(first, rest, i0, i1, at, row, r, o);
     __syncthreads();
-    sum[quarter][v] = o;
-    stat[quarter][v] = make_float4(r.m, r.mp, r.l, 0.0f);
+    sum[share][v] = o;
+    stat[share][v] = make_float4(r.m, r.mp, r.l, 0.0f);
     __syncthreads();
-    if (quarter == 0) {
-      for (int k = 1; k < 4; ++k) {
+    if (share == 0) {
+      for (int k = 1; k < 16; ++k) {
         const float4 st = stat[k][v], x = sum[k][v];
         const float m = fmaxf(r.m, st.x), mp = fmaxf(r.mp, st.y);
         r.l = r.l * exp2f(r.m - m) + st.z * exp2f(st.x - m);

@@ -106,7 +106,7 @@ csa_status_t csa_cache_append(const csa_cache_t* cache, const void* rows, int32_
  * lse fp32 [num_tokens, num_q_heads] (may be null) are written in full for
  * tokens below cu_q[num_seqs]; tokens behind it are left as they were.
  * Logits, softmax statistics and sums are fp32; the weights enter the second
- * product as 16-bit values (csa_cache_attend.cu).
+ * product as 16-bit values (csa_cache_attend_rows.cu).
  *
  * Results are the same from call to call; the order of sums depends on the
  * sizes and lengths of the call alone. Workspace comes from the library's
