@@ -212,6 +212,23 @@ struct Wide {
   static constexpr int HEAD = (int)(sizeof(State) + 1023) / 1024 * 1024;
   static constexpr int SMEM = HEAD + NS * PANEL + Q + P + 1024;
   static constexpr int KV = (32 + PW - 1) / PW;     // steps of 4 keys a warp and panel
+  // Step k of producer warp pw is keys 4 e .. 4 e + 3 of the tile, e = step_of(k, pw).
+  // The warps for which a last step would be one too many repeat their own before
+  // it, so that no two warps ever store, or clean, the same keys.
+  static __host__ __device__ constexpr int step_of(int k, int pw) {
+    return k * PW + pw < 32 ? k * PW + pw : (k - 1) * PW + pw;
+  }
+  static constexpr bool each_step_by_one_warp() {
+    int owner[32] = {}, steps = 0;
+    for (int pw = 0; pw < PW; ++pw)
+      for (int k = 0; k < KV; ++k) {
+        const int e = step_of(k, pw);
+        if (e < 0 || e >= 32 || (owner[e] != 0 && owner[e] != pw + 1)) return false;
+        steps += owner[e] == 0;
+        owner[e] = pw + 1;
+      }
+    return steps == 32;
+  }
   // Panels in flight in registers. Heads of one panel (128 columns) have less to
   // wait for and the lookups in every panel: one measured 82 us, two 87 (1020
   // queries of 16 heads over 16396 rows); of four panels two measured less.
@@ -738,7 +755,7 @@ __device__ __noinline__ void wide_clean(uint8_t* panel, int chunk, int kb, int p
   auto& st = *reinterpret_cast<typename C::State*>(wide_smem);
 #pragma unroll 1
   for (int k = 0; k < C::KV; ++k) {
-    const int e = min(k * C::PW + pw, 31), c16 = ((chunk & 3) * 2) ^ ((e * 4 + kb) & 7);
+    const int e = C::step_of(k, pw), c16 = ((chunk & 3) * 2) ^ ((e * 4 + kb) & 7);
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       uint4* v = reinterpret_cast<uint4*>(panel + e * 512 + ((c16 ^ i) << 4));
@@ -794,12 +811,10 @@ __device__ __noinline__ void wide_produce() {
     return (int32_t)((((((int64_t)page * item.heads + head) << item.page_bits) + slot) * D) >> 10);
   };
   int32_t kib = locate16(0, pages), kib_next = -1;
-  // Step k of this warp is keys 4 e .. 4 e + 3 of the tile, e = k PW + pw (the
-  // last step of some warps is one too many and repeats the one before).
   int line[C::KV];  // where the step's first 8 values go in a panel
 #pragma unroll
   for (int k = 0; k < C::KV; ++k) {
-    const int e = min(k * C::PW + pw, 31);
+    const int e = C::step_of(k, pw);
     line[k] = (chunk >> 2) * C::SLAB + (e * 4 + kb) * 128 + ((((chunk & 3) * 2) ^ ((e * 4 + kb) & 7)) << 4);
   }
   const uint8_t* const pool = item.data;
@@ -824,7 +839,7 @@ __device__ __noinline__ void wide_produce() {
       there = 0;
 #pragma unroll
       for (int k = 0; k < C::KV; ++k) {
-        const int e = min(k * C::PW + pw, 31);
+        const int e = C::step_of(k, pw);
         const int32_t first = __shfl_sync(0xFFFFFFFFu, kib, p * 8 + (e >> 2));
         const bool ok = first >= 0 && e * 4 + kb < left;
         there |= (uint32_t)ok << k;
@@ -1011,6 +1026,7 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
 template <int D, bool SHARED, bool HALF>
 cudaError_t launch_wide(AttendArgs a, cudaStream_t stream) {
   using C = Wide<D, SHARED>;
+  static_assert(C::each_step_by_one_warp(), "producer warps share keys of a panel");
   const PlanShape p = plan_of(a, C::R, 128, 152, 2, 8, 0);
   auto* kernel = attend_wide_kernel<D, SHARED, HALF>;
   cudaError_t e = allow_dynamic_smem((const void*)kernel, C::SMEM);
