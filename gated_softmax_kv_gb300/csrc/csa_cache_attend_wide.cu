@@ -188,7 +188,11 @@ struct WideState {
   float lscale[R], oscale[R], factor[R];
   float best[2][R / 32][4][32];
   float part[R * 4];
-  int32_t sees_least, sees_most, far_refs, nan_rows, dead, first_nan;
+  // Whether a row's references are too far apart for weights in two factors: one
+  // of each half of the rows, written and read by that half's four warps alone,
+  // which their own barrier orders.
+  int32_t far_refs[R / 32];
+  int32_t sees_least, sees_most, nan_rows, dead, first_nan;
   uint32_t tmem;
 };
 extern __shared__ __align__(1024) uint8_t wide_smem[];
@@ -472,7 +476,7 @@ __device__ __noinline__ void wide_raise(uint32_t s_at, float sk, float lv, bool 
     st.mpref[c] = y;
     st.rl[c] = x - y + kLift;
     st.rf[c] = exp2f(x - y + kLift);
-    if (!(fabsf(x - y) <= 60.0f)) st.far_refs = 1;
+    if (!(fabsf(x - y) <= 60.0f)) st.far_refs[half] = 1;
   }
   barrier_of(1 + half, 128);
   if (i > 0) {
@@ -596,7 +600,7 @@ __device__ __noinline__ void wide_softmax() {
     tc_before();  // S^T is read
     __syncwarp();
     if (lane == 0) mbar_arrive(at.s_empty + 8 * b);
-    const bool far = __any_sync(0xFFFFFFFFu, far_key) || *(volatile int32_t*)&st.far_refs;
+    const bool far = __any_sync(0xFFFFFFFFu, far_key) || *(volatile int32_t*)&st.far_refs[half];
     uint32_t w[16];
     if (!far) {
       const float2 kf2 = make_float2(kf, kf);
@@ -965,7 +969,7 @@ __global__ void __launch_bounds__(Wide<D, SHARED>::THREADS, 1)
     if (threadIdx.x == 0) {
       st.sees_least = 0x7FFFFFFF;
       st.sees_most = 0;
-      st.far_refs = 0;
+      for (int k = 0; k < C::R / 32; ++k) st.far_refs[k] = 0;
       st.nan_rows = 0;
       st.first_nan = 0x7FFFFFFF;
     }

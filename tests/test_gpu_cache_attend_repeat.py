@@ -32,3 +32,29 @@ def test_nan_and_missing_rows_at_a_tiles_end(gsk, D, shared, group, n):  # noqa:
     for _ in range(20):
         again = s.run(gsk)
         assert same(again[0], out) and same(again[1], lse)
+
+
+@pytest.mark.parametrize("far", [0, 1])
+@pytest.mark.parametrize("D,shared", [(64, False), (128, False), (128, True), (256, True), (512, True), (512, False)])
+def test_one_half_of_a_tile_sees_only_zeros(gsk, D, shared, far):  # noqa: F811
+    """A tile is two tokens of 32 heads. One token sees nothing but a block of
+    zeros, which the writer gives the scale 2^-120: its two references are 120
+    powers of two apart. The other sees ordinary rows too, and its bits are those
+    that it has beside a token that sees them as well."""
+    lens = [700, 130, 2000]
+    s = Setup(lens, [2] * 3, 32, 1, D, shared, 64, 16, seed=D)
+    for t in s.table:
+        s.bytes[t[0], :, :16] = 0
+        s.scales[t[0], :, 0] = 2.0 ** -120
+    near = [2 * i + 1 - far for i in range(3)]
+    s.visible = [n for n in lens for _ in range(2)]
+    want = s.check(gsk)
+    for i in range(3):
+        s.visible[2 * i + far] = 11 + i
+    out, lse = s.check(gsk)
+    assert (out[[2 * i + far for i in range(3)]] == 0).all()
+    assert same(out[near], want[0][near]) and same(lse[near], want[1][near])
+    args, visible = s.args(), i32(s.visible)
+    for _ in range(50):
+        again = gsk.csa_cache_attend(s.q, *args, shared=shared, visible=visible)
+        assert same(again[0], out) and same(again[1], lse)
