@@ -625,9 +625,10 @@ __device__ __noinline__ void wide_softmax() {
       for (int c = 0; c < 32; c += 2) {
         l[c] += ex2_approx_ftz(t[c]);
         l[c + 1] += ex2_approx_ftz(t[c + 1]);
-        // a zero scale's log2 is -inf: weight 0
-        w[c / 2] = pack_f16x2(ex2_approx_ftz(t[c] + (st.rl[col + c] + lv)),
-                              ex2_approx_ftz(t[c + 1] + (st.rl[col + c + 1] + lv)));
+        // A zero scale's log2 is -inf: weight 0. So has a row that does not see the
+        // key, whose scale may then be anything.
+        w[c / 2] = pack_f16x2(t[c] == -INFINITY ? 0.0f : ex2_approx_ftz(t[c] + (st.rl[col + c] + lv)),
+                              t[c + 1] == -INFINITY ? 0.0f : ex2_approx_ftz(t[c + 1] + (st.rl[col + c + 1] + lv)));
       }
     }
     if (!o_free && tc > 0) mbar_wait(at.p_empty, (tc - 1) & 1, dead);  // P^T's old contents are used

@@ -100,7 +100,9 @@ csa_status_t csa_cache_append(const csa_cache_t* cache, const void* rows, int32_
  * visible [num_tokens] (int32) may be null: every row of the sequence is
  * seen. A compressed row that ends at token (j + 1) * ratio - 1 is in the
  * past of the query at position p when j < (p + 1) / ratio. Rows that a query
- * does not see have no influence on it, whatever they hold (NaN included).
+ * does not see take no part in its sums, whatever they and their scales hold
+ * (NaN and infinities included). Only roundings can differ: queries that are
+ * worked on together rescale their sums at the same rows.
  * A query that sees no row, or whose logits are all -inf (those below -6e37
  * count as -inf), gets out 0 and lse -inf. out [num_tokens, num_q_heads, head_dim] in q's type, contiguous, and
  * lse fp32 [num_tokens, num_q_heads] (may be null) are written in full for
