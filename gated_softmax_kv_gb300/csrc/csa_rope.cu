@@ -5,7 +5,8 @@
 // 64-bit fixed point, so the phase of position p is p * F modulo 2^64: the
 // reduction to one turn is the integer product's own overflow, exact for any
 // position, with no fp64 arithmetic per element (fp64 runs at 1/64 of the
-// fp32 rate here). The top 32 bits go through sincospif.
+// fp32 rate here). What is off is F, by turns_of's rounding, times p. The top
+// 32 bits go through sincospif.
 //
 // The kernels are copies with some arithmetic, bound by memory. A thread keeps
 // its columns for its whole loop, so F is worked out once per thread. 66533 rows
@@ -152,8 +153,10 @@ __device__ __forceinline__ void store_pair(E* p, int half, float2 v) {
 
 // f / (2 pi) modulo 1 as a 64-bit fraction, from the bits of f: with f =
 // m 2^(e-52), m a 53-bit integer, and K = floor(2^66 / (2 pi)), the product's
-// high word (m 2^11) K / 2^64 times 2^(e-1) is 2^64 f / (2 pi), within 2^-61
-// relative before the shift drops what is below 2^-64 turns.
+// high word (m 2^11) K / 2^64 times 2^(e-1) is 2^64 f / (2 pi). K lacks less than
+// 2^-63 of itself and the high word, at least 2^62.3, less than one: together
+// below 2^-61 relative, f 2^-61 / (2 pi) turns. A shift to the right drops less
+// than 2^-64 turns, one to the left (f >= 4) or none (f >= 2) nothing.
 __device__ __forceinline__ uint64_t turns_of(double f) {
   const uint64_t b = (uint64_t)__double_as_longlong(f);
   const int e = (int)((b >> 52) & 0x7FF) - 1023;

@@ -22,12 +22,17 @@
  * static capacity) have position 0.
  *
  * Angles: frequencies are radians a position in fp64. The kernel holds them
- * in turns as 64-bit fixed-point numbers and multiplies modulo 2^64, so the
- * reduction to one turn is exact whatever the position; the angle used is
- * within 2^-32 turns of p * freqs[i] as long as |p| < 2^31 (and then rounded to
- * fp32 in half turns, |angle| <= 1: 2^-25). Frequencies must
- * be finite and below 2^62 in magnitude. Products and sums are fp32, rounded
- * once to the tensor's type.
+ * in turns as 64-bit fixed-point numbers, within 2^-64 + |freqs[i]| 2^-61 / (2 pi)
+ * turns, and multiplies them by the position modulo 2^64: that product and its
+ * reduction to one turn are exact. The angle used is within
+ *
+ *   |p| (2^-64 + |freqs[i]| 2^-61 / (2 pi)) + 2^-33 turns
+ *
+ * of p * freqs[i]: below 2^-31 for |freqs[i]| <= 1 and |p| <= 2^31, below 2^-12 for
+ * |freqs[i]| = 2^20 there (and then rounded to fp32 in half turns, |angle| <= 1:
+ * 2^-25). Frequencies must be finite and below 2^62 in magnitude; where the
+ * bound passes half a turn, the angle says nothing. Products and sums are fp32,
+ * rounded once to the tensor's type.
  *
  * x and y are [tokens, heads, head_dim], the last dimension contiguous, the
  * other two with strides in elements. Input strides may be 0 (a broadcast
