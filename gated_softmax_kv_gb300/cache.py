@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 
 from .binding import _check, _check_detail, _raise, load
-from .launch import on_device, output_overlaps
+from .launch import changed, on_device, output_overlaps
 
 CACHE_STATUS = {1: "a sequence index outside the table", 2: "an index twice, or both child and parent",
                 4: "a child that holds rows or pages", 8: "fewer free pages than needed",
@@ -188,6 +188,7 @@ def csa_cache_attend(q, cache, scales, page_table, seq_lens, cu_q, kv_heads: int
         qt = 0
     if H <= 1:
         qh = 0
+    given = [t for t in (out, lse) if t is not None]
     with on_device(dev, stream) as launch:
         if out is None:
             out = _types.empty_like(q, **_types.contiguous)
@@ -211,6 +212,8 @@ def csa_cache_attend(q, cache, scales, page_table, seq_lens, cu_q, kv_heads: int
         if st != 0:
             _raise(st)
         launch.used(q, cache, scales, page_table, seq_lens, cu_q, visible, out, lse)
+    if given:
+        changed(*given)
     return out, lse
 
 

@@ -1,5 +1,6 @@
 """What the bindings of rope.py and cache.py share around a launch: the
-device, the stream, the life of the tensors and the overlap of an output."""
+device, the stream, the life of the tensors, and an output of the caller's: its
+overlap, and what autograd is told of it."""
 from __future__ import annotations
 
 from . import binding
@@ -69,6 +70,13 @@ def on_device(dev: int, stream=None) -> _Launch:
     if stream is None and _current_device() == dev:
         return _Launch(binding._stream_handle(None, dev))
     return _GuardedLaunch(dev, stream)
+
+
+def changed(*tensors):
+    """Tells autograd that a kernel wrote over tensors of the caller, so that a
+    graph that saved their old values refuses its backward pass."""
+    import torch
+    torch.autograd.graph.increment_version(tensors)
 
 
 def _span(t):

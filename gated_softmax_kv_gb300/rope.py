@@ -6,7 +6,7 @@ import math
 from typing import Optional
 
 from .binding import _check, _check_detail, _raise, load
-from .launch import on_device, output_overlaps
+from .launch import changed, on_device, output_overlaps
 
 LAYOUTS = {"interleaved": 0, "half": 1}
 _codes = {}
@@ -79,6 +79,7 @@ def csa_rope(x, freqs, positions=None, *, cu_seqlens_comp=None, ratio: int = 1, 
         raise ValueError("x has no heads or no columns")
     if last != 1 and D > 1:
         raise ValueError("the last dimension of x must be contiguous")
+    given = out is not None
     with on_device(dev, stream) as launch:
         if out is None:
             out = torch.empty_like(x, memory_format=torch.contiguous_format)
@@ -98,6 +99,8 @@ def csa_rope(x, freqs, positions=None, *, cu_seqlens_comp=None, ratio: int = 1, 
         if st != 0:
             _raise(st)
         launch.used(x, out, freqs, positions, cu_seqlens_comp)
+    if given:
+        changed(out)
     return out
 
 
