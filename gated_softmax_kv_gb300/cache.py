@@ -112,7 +112,8 @@ def _rows(t, name, dtypes, dev):
 def csa_cache_append(rows, cache, scales, page_table, seq_lens, cu_rows, stream=None) -> None:
     """Quantises rows [num_rows, num_heads, head_dim] (bf16, fp16 or fp32) into
     the cache: sequence s gets rows cu_rows[s] .. cu_rows[s + 1] - 1 behind its
-    seq_lens[s] rows. seq_lens is not changed: add the lengths afterwards."""
+    seq_lens[s] rows. seq_lens is not changed: add the lengths afterwards. Not
+    recorded by autograd."""
     try:
         dev = cache.get_device()
         (pages, heads, page, D), (sp, sh, blocks) = cache.shape, scales.shape
@@ -156,7 +157,9 @@ def csa_cache_attend(q, cache, scales, page_table, seq_lens, cu_q, kv_heads: int
     shared=True they are the values too, else the next kv_heads heads are.
     visible (int32 [tokens]): rows that each query sees, all where None. lse
     (natural logarithm, fp32 [tokens, heads]) lets the result be merged with
-    attention over other rows. Tokens at or behind cu_q[-1] are not written."""
+    attention over other rows. Tokens at or behind cu_q[-1] are not written.
+    Not recorded by autograd: out and lse carry no gradient to q, whether or not
+    it requires one (the 8-bit rows have none to take)."""
     try:
         dev = cache.get_device()
         (pages, heads, page, D), (sp, sh, blocks) = cache.shape, scales.shape

@@ -66,3 +66,12 @@ def test_attention_into_a_saved_tensor(gsk):
     with torch.inference_mode():
         hold = torch.zeros_like(q)
         gsk.csa_cache_attend(q, *args, out=hold)
+
+
+def test_attention_carries_no_gradient(gsk):
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = torch.zeros(2, 2, 16, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16().requires_grad_()
+    out, lse = gsk.csa_cache_attend(q, cache, torch.ones(2, 2, 1, device="cuda"), i32([[0]]), i32([5]), i32([0, 2]), 1, 0.125)
+    assert not out.requires_grad and not lse.requires_grad
+    assert "Not recorded by autograd" in gsk.csa_cache_attend.__doc__
