@@ -14,9 +14,10 @@
 // four instructions, and V is transposed by byte permutes of the four keys
 // that a thread's operand holds.
 //
-// Numerics. Queries are scaled row by row by a power of two into fp16 (exact
-// down to 2^-39 of the row's largest value); the logits are fp32, in units of
-// log2. With z_j the logit and s_j the value block's scale, the sum of weights
+// Numerics. Queries are scaled row by row by a power of two into fp16, the row's
+// largest value into [2^14, 2^15): exact for values down to 2^-31 of it (bf16) or
+// 2^-28 (fp16), below that off by at most half a subnormal step, 2^-25, which is
+// 2^-39 of it. The logits are fp32, in units of log2. With z_j the logit and s_j the value block's scale, the sum of weights
 // is sum 2^(z_j - m) in fp32, and the weights of the second product are
 // w_j = 2^(z_j + log2 s_j - m') in fp16: m' follows z + log2 s, so the scale is
 // part of the weight and far apart scales cost no precision. Both references
