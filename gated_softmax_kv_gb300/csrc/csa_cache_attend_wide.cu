@@ -28,9 +28,10 @@
 // of 512 have room for one tile in the ring, so refill, S^T, softmax and O^T
 // follow one another: 8.8 K cycles a tile. Seven producer warps measured best (six
 // 201 us, eight 238, seven 192). Measured: 64 sequences of 10400 rows on average,
-// 64 heads over one row of 512: 186 us (450 TFLOP/s), joining 13 us; one sequence
-// of 65536 rows 43 us, joining 8; 255 queries each of four sequences of up to 4099 rows, 16
-// heads over two of 128 columns, 83 us.
+// 64 heads over one row of 512: 188 us (451 TFLOP/s), joining 14 us; one sequence
+// of 65536 rows 44 us, joining 8; 255 queries each of four sequences of up to 4099 rows, 16
+// heads over two of 128 columns, 82 us, joining 8; 2048 queries of 64 heads over 4096
+// rows of 512, 2061 us (500 TFLOP/s).
 //
 // Every wait on an mbarrier is bounded: a wait that runs out marks the CTA,
 // whose later waits then return at once, and its results become NaN.

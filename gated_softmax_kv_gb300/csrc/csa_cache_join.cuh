@@ -189,7 +189,7 @@ __device__ __forceinline__ void add_parts(const float* first, const float* rest,
   }
 }
 
-// Joins the shared items (64 sequences' tiles of 64 x 512 sums in 13 us, one in 152
+// Joins the shared items (64 sequences' tiles of 64 x 512 sums in 14 us, one in 152
 // parts in 8; 32 sequences' of 8 x 128 in 5): every CTA reads the list, and all pieces of all items
 // are spread over the grid. An item of few parts (a batch: two or three) is
 // streamed, four columns a thread. Of a long one (a sequence alone on the GPU
