@@ -1,5 +1,6 @@
 """Thin torch.autograd wrappers: `compressor` over the Compressor's two C-ABI
-calls, and `rope` over csa_rope and its transpose.
+calls, `rope` over csa_rope and its transpose, and `norm_rope` over
+csa_norm_rope and its gradient.
 
 `compressor(...)` returns `out` and, on backward, calls csa_compress_bwd for
 dkv, dscore and dape (cuDNN-frontend "CSA Fused Compressor", sections
@@ -13,6 +14,7 @@ from typing import Optional
 import torch
 
 from .binding import csa_compress_bwd, csa_compress_fwd
+from .norm_rope import csa_norm_rope, csa_norm_rope_bwd
 from .rope import csa_rope
 
 
@@ -86,3 +88,39 @@ def rope(x: torch.Tensor, freqs: torch.Tensor, positions: Optional[torch.Tensor]
     the stream it was made on and would make the capture wait for it)."""
     return RopeFunction.apply(x, freqs, positions, cu_seqlens_comp, ratio, offset, layout,
                               amplitude, transpose)
+
+
+def _rows_contiguous(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """Kernels read rows whose last dimension is contiguous."""
+    return t if t is None or t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
+
+
+class NormRopeFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, q_weight, k, k_weight, freqs, positions, cu_seqlens_comp, how):
+        ctx.save_for_backward(q, q_weight, k, k_weight, freqs, positions, cu_seqlens_comp)
+        ctx.how = how
+        return csa_norm_rope(q, q_weight, freqs, positions, k=k, k_weight=k_weight,
+                             cu_seqlens_comp=cu_seqlens_comp, **how)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, k_grad):
+        q, q_weight, k, k_weight, freqs, positions, cuc = ctx.saved_tensors
+        dq, dqw, dk, dkw = csa_norm_rope_bwd(q, q_weight, freqs, _rows_contiguous(grad), positions, k=k,
+                                             k_weight=k_weight, k_grad=_rows_contiguous(k_grad),
+                                             cu_seqlens_comp=cuc, **ctx.how)
+        return dq, dqw, dk, dkw, None, None, None, None
+
+
+def norm_rope(q: torch.Tensor, q_weight: torch.Tensor, freqs: torch.Tensor,
+              positions: Optional[torch.Tensor] = None, *, k: Optional[torch.Tensor] = None,
+              k_weight: Optional[torch.Tensor] = None, cu_seqlens_comp: Optional[torch.Tensor] = None,
+              ratio: int = 1, offset: int = 0, layout: str = "interleaved", amplitude: float = 1.0,
+              eps: float = 1e-6):
+    """Differentiable csa_norm_rope (same arguments, no in-place form): (out,
+    k_out), k_out None without k, with gradients of q, k and their weights; freqs
+    and positions are constants. The gradient is not itself differentiable.
+    Captured into a CUDA graph under the condition that `rope` states."""
+    how = dict(ratio=ratio, offset=offset, layout=layout, amplitude=amplitude, eps=eps)
+    return NormRopeFunction.apply(q, q_weight, k, k_weight, freqs, positions, cu_seqlens_comp, how)
