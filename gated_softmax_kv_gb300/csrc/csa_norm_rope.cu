@@ -465,7 +465,8 @@ csa_status_t call(const csa_norm_rope_t* how, const csa_norm_side_t* q, const cs
     return CSA_ERR_ALIGN;
   NormArgs a = {};
   const int vec = n.dtype == CSA_FP32 ? 4 : 8;
-  bool vectors = n.head_dim % vec == 0 && n.offset % vec == 0 &&
+  // at most 128 vectors: 32 lanes of 4
+  bool vectors = n.head_dim % vec == 0 && n.head_dim / vec <= 128 && n.offset % vec == 0 &&
                  n.rope_dim % (n.layout == CSA_ROPE_HALF ? 2 * vec : vec) == 0;
   for (int i = 0; i < 2; ++i) {
     const csa_norm_side_t* s = i ? k : q;

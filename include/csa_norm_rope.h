@@ -76,7 +76,8 @@ typedef struct csa_norm_rope {
  * layout known, 2 <= rope_dim even, the part inside head_dim <= 1024
  * (UNSUPPORTED); sizes, strides, eps >= 0 and finite, distinct output elements
  * (RANGE); null pointers (NULL); pointers aligned to their element (ALIGN).
- * 16-byte aligned rows and parts take the vector kernel. k may be null.
+ * 16-byte aligned rows and parts take the vector kernel (head_dim <= 512 in fp32).
+ * k may be null.
  */
 csa_status_t csa_norm_rope(const csa_norm_rope_t* how, const csa_norm_side_t* q,
                            const csa_norm_side_t* k, cudaStream_t stream);

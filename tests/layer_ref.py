@@ -18,11 +18,12 @@ def norm_rope(x, w, freqs, positions, eps, **kw):
 
     r: a lane sums at most 32 squares and 5 shuffles follow, the mean and eps add two
     roundings: 40 U of the sum, 20 U of its root; the root and the quotient add 2 ulp, 4 U: 24 U.
-    Two more products, then the turn."""
+    Two more products, then the turn. Columns that are not turned have no pair (mag 0): theirs are
+    the norm's roundings, 26 U of the value itself, which in a pair is at most mag."""
     r = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
     y, mag = cache_ref.rope(x * r * w, freqs, positions, kw.get("offset", 0), kw.get("layout", "interleaved"),
                             kw.get("amplitude", 1.0), False)
-    return y, (TURN + 26 * U) * mag
+    return y, TURN * mag + 26 * U * np.maximum(mag, np.abs(y))
 
 
 def norm_rope_grad(x, w, g, freqs, positions, eps, **kw):
