@@ -1,6 +1,6 @@
 """Thin torch.autograd wrappers: `compressor` over the Compressor's two C-ABI
-calls, `rope` over csa_rope and its transpose, and `norm_rope` over
-csa_norm_rope and its gradient.
+calls, `rope` over csa_rope and its transpose, `norm_rope` over csa_norm_rope
+and `prompt_attend` over csa_prompt_attend and their gradients.
 
 `compressor(...)` returns `out` and, on backward, calls csa_compress_bwd for
 dkv, dscore and dape (cuDNN-frontend "CSA Fused Compressor", sections
@@ -15,6 +15,7 @@ import torch
 
 from .binding import csa_compress_bwd, csa_compress_fwd
 from .norm_rope import csa_norm_rope, csa_norm_rope_bwd
+from .prompt import csa_prompt_attend, csa_prompt_attend_bwd
 from .rope import csa_rope
 
 
@@ -124,3 +125,47 @@ def norm_rope(q: torch.Tensor, q_weight: torch.Tensor, freqs: torch.Tensor,
     Captured into a CUDA graph under the condition that `rope` states."""
     how = dict(ratio=ratio, offset=offset, layout=layout, amplitude=amplitude, eps=eps)
     return NormRopeFunction.apply(q, q_weight, k, k_weight, freqs, positions, cu_seqlens_comp, how)
+
+
+def _vectors_apart(t: torch.Tensor) -> bool:
+    """Whether csa_prompt_attend_bwd takes a gradient as it lies in memory: 16-byte
+    aligned rows, no dimension broadcast."""
+    return (t.stride(2) == 1 and t.data_ptr() % 16 == 0
+            and all(t.shape[i] == 1 or t.stride(i) > 0 and t.stride(i) % 8 == 0 for i in (0, 1)))
+
+
+class PromptAttendFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_q, cu_k, sm_scale: float, window):
+        rest = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out, lse = csa_prompt_attend(q, k, v, cu_q, sm_scale, cu_k=cu_k, window=window, rest=rest)
+        ctx.save_for_backward(q, k, v, cu_q, cu_k, out, lse, rest)
+        ctx.how = (sm_scale, window)
+        ctx.set_materialize_grads(False)
+        return out, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, grad_lse):
+        if grad is None and grad_lse is None:
+            return None, None, None, None, None, None, None
+        q, k, v, cu_q, cu_k, out, lse, rest = ctx.saved_tensors
+        sm_scale, window = ctx.how
+        if grad is None:
+            grad = torch.zeros_like(out)
+        elif not _vectors_apart(grad):
+            grad = grad.clone(memory_format=torch.contiguous_format)
+        if grad_lse is not None:
+            grad_lse = grad_lse.contiguous()
+        dq, dk, dv = csa_prompt_attend_bwd(q, k, v, out, lse, grad, cu_q, sm_scale, cu_k=cu_k, window=window,
+                                           rest=rest, grad_lse=grad_lse)
+        return dq, dk, dv, None, None, None, None
+
+
+def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, sm_scale: float, *,
+                  cu_k: Optional[torch.Tensor] = None, window: Optional[int] = None):
+    """Differentiable csa_prompt_attend (same arguments, no outputs of the caller's):
+    (out, lse), both with gradients to q, k and v. A gradient that arrives broadcast
+    or unaligned is copied first. The gradient is not itself differentiable.
+    Captured into a CUDA graph under the condition that `rope` states."""
+    return PromptAttendFunction.apply(q, k, v, cu_q, cu_k, sm_scale, window)

@@ -1,6 +1,6 @@
 """Python binding of the C ABI in include/csa_compress.h (argument marshalling only);
-rope.py, norm_rope.py and cache.py bind csa_rope.h, csa_norm_rope.h and csa_cache.h
-over the library loaded here.
+rope.py, norm_rope.py, prompt.py and cache.py bind csa_rope.h, csa_norm_rope.h,
+csa_prompt.h and csa_cache.h over the library loaded here.
 
 Every computation runs in libcsa_compress.so; this module checks tensor
 dtypes/devices/shapes, derives the sizes the C calls want from tensor shapes,
@@ -58,6 +58,10 @@ def load() -> ctypes.CDLL:
     lib.csa_rope.restype = ctypes.c_int
     for fn in (lib.csa_norm_rope, lib.csa_norm_rope_bwd):
         fn.argtypes, fn.restype = [vp] * 4, ctypes.c_int
+    lib.csa_prompt_attend.argtypes = [vp, vp, vp, vp, i32, vp]
+    lib.csa_prompt_attend.restype = ctypes.c_int
+    lib.csa_prompt_attend_bwd.argtypes = [vp] * 5 + [i64, i64] + [vp] * 5
+    lib.csa_prompt_attend_bwd.restype = ctypes.c_int
     lib.csa_cache_append.argtypes = [vp, vp, i32, i64, i64, i64, vp, i32, i32, vp, vp, vp]
     lib.csa_cache_append.restype = ctypes.c_int
     lib.csa_cache_attend.argtypes = [vp, vp, i32, i64, i32, i64, i64, i32, i32, ctypes.c_float, vp,

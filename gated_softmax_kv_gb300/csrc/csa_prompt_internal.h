@@ -1,0 +1,51 @@
+// Shared by the translation units of causal attention over packed sequences
+// (csa_prompt.cu and its kernels). Not installed, not part of the ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "csa_prompt.h"
+
+namespace csa {
+
+struct PromptArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* g;      // grad
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  void* out;
+  void* rest;
+  float* lse;
+  const float* grad_lse;
+  void* dq;
+  void* dk;
+  void* dv;
+  int64_t qt, qh, kt, kh, vt, vh, gt, gh;  // strides in elements
+  int32_t num_q, num_k;
+  int32_t nseq, heads, kv, group, d, window;
+  int32_t fill;
+  float scale;
+};
+
+// A sequence's rows, checked: an empty one where the lists do not make sense.
+struct Span {
+  int32_t q0, nq, k0, nk;
+};
+__device__ __forceinline__ Span span_of(const PromptArgs& a, int s) {
+  Span w;
+  w.q0 = __ldg(a.cu_q + s);
+  w.k0 = __ldg(a.cu_k + s);
+  const int32_t q1 = __ldg(a.cu_q + s + 1), k1 = __ldg(a.cu_k + s + 1);
+  const bool ok = w.q0 >= 0 && w.q0 <= q1 && q1 <= a.num_q && w.k0 >= 0 && w.k0 <= k1 && k1 <= a.num_k;
+  w.nq = ok ? q1 - w.q0 : 0;
+  w.nk = ok ? k1 - w.k0 : 0;
+  return w;
+}
+
+cudaError_t launch_prompt(const PromptArgs& a, bool half, cudaStream_t stream);
+cudaError_t launch_prompt_bwd(const PromptArgs& a, bool half, cudaStream_t stream);
+
+}  // namespace csa
