@@ -1,14 +1,45 @@
 // Causal attention over packed sequences (declared in include/csa_prompt.h): the
-// calls' checks. Kernels: csa_prompt_simple.cu.
+// calls' checks. Kernels: csa_prompt_fwd.cu, csa_prompt_simple.cu.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "csa_cache_internal.h"
 #include "csa_internal.h"
 #include "csa_prompt_internal.h"
+#include "csa_prompt_tile.cuh"
 
 namespace csa {
+
+// The encoder is a driver call, looked up once through the runtime.
+cudaError_t rows_map(CUtensorMap* map, const void* base, bool half, int32_t d, int32_t heads, int64_t tokens, int64_t ts,
+                     int64_t hs, int32_t heads_box, int32_t tokens_box) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);  // its type alone: nothing links against the driver
+  static std::atomic<void*> known{nullptr};
+  void* fn = known.load();
+  if (!fn) {
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    known.store(fn);
+  }
+  const Encode encode = reinterpret_cast<Encode>(fn);
+  // a tensor without rows is never loaded from, but has a map; strides of single
+  // elements are never stepped
+  static const uint4 none = {};
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)(tokens > 0 ? tokens : 1)};
+  const cuuint64_t strides[2] = {(cuuint64_t)(hs > 0 ? hs : 8) * 2, (cuuint64_t)(ts > 0 ? ts : 8) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)heads_box, (cuuint32_t)tokens_box}, steps[3] = {1, 1, 1};
+  const CUresult r = encode(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                            const_cast<void*>(tokens > 0 ? base : &none), dims, strides, box, steps,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 namespace {
 

@@ -164,12 +164,6 @@ __global__ void __launch_bounds__(128) keys_kernel(const PromptArgs a) {
 
 }  // namespace
 
-cudaError_t launch_prompt(const PromptArgs& a, bool half, cudaStream_t stream) {
-  const dim3 grid(152 * 16), block(128);
-  return half ? launch_dependent(rows_kernel<__half, false>, grid, block, 0, stream, a)
-              : launch_dependent(rows_kernel<Bf16, false>, grid, block, 0, stream, a);
-}
-
 cudaError_t launch_prompt_bwd(const PromptArgs& a, bool half, cudaStream_t stream) {
   const dim3 grid(152 * 16), block(128);
   cudaError_t e = half ? launch_dependent(rows_kernel<__half, true>, grid, block, 0, stream, a)
