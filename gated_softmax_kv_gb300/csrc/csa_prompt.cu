@@ -1,5 +1,5 @@
 // Causal attention over packed sequences (declared in include/csa_prompt.h): the
-// calls' checks. Kernels: csa_prompt_fwd.cu, csa_prompt_simple.cu.
+// calls' checks. Kernels: csa_prompt_fwd.cu, csa_prompt_bwd.cu.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

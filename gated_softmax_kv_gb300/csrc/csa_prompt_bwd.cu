@@ -1,0 +1,842 @@
+// Causal attention over packed sequences, the gradient: tcgen05.
+//
+// Three kernels. prompt_delta_kernel reads out and grad once and writes, for each
+// (token, head), lse in log2 units and delta = sum grad out - grad_lse. Then two passes
+// over the pairs, each with sums of its own and in a fixed order:
+//   prompt_keys_kernel, 128 keys of a key head a CTA, over the tiles of query rows
+//   that see them (keys are the accumulators' lanes, so that P and dS are written
+//   as first operands in tensor memory):
+//     S^T = K Q^T   dP^T = V G^T   dV += P^T G   dK += dS^T Q
+//   prompt_rows_kernel, 128 query rows a CTA, over the keys that they see:
+//     S = Q K^T     dP = G V^T     dQ += dS K
+// Seven products where one pass with atomic sums of dQ would need five; in return
+// results do not depend on timing, and there is no fp32 copy of dQ to clear, add to
+// and convert.
+//
+// In both, one warp issues the matrix instructions, one the copies, and eight warps
+// form P and dS: a lane of the accumulators a thread, half of the columns each. The
+// products of a tile go between the two phases of the arithmetic: keys kernel: dV of
+// tile j and S of j + 1 while dS(j) is formed, dK(j) and dP(j + 1) while P(j + 1) is;
+// rows kernel: dQ(j), dP(j + 1) and S(j + 2) while dS(j + 1) is.
+//
+// fp16: P is lifted by 2^15 and dS, whose size is that of the gradients, by a power
+// of two that the largest grad and v allow (prompt_delta_kernel finds them), so that
+// the small ones keep their bits; bf16 needs neither.
+//
+// Infinities and NaN of rows that do not see the keys are cleaned from the operands
+// as in the forward (csa_prompt_fwd.cu). Waits are bounded as there.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "csa_cache_internal.h"
+#include "csa_internal.h"
+#include "csa_prompt_tile.cuh"
+
+namespace csa {
+
+namespace {
+
+struct BwdArgs {
+  PromptArgs a;
+  float2* stats;    // [num_q * heads]: -(lse log2 e - lift), -delta
+  uint32_t* sizes;  // fp16: bits of the largest |grad row|, |v row|, |grad_lse|
+};
+
+template <bool HALF>
+constexpr float kPLift = HALF ? 15.0f : 0.0f;
+
+// fp16: |dP - delta| <= 2 |grad| |v| + |grad_lse| < 2^x, so that times 2^-x and a
+// weight of at most 2^15 it stays below 2^15. bf16: x = 0.
+template <bool HALF>
+__device__ __forceinline__ int gradient_exponent(const BwdArgs& b) {
+  if (!HALF) return 0;
+  const float g = __uint_as_float(__ldg(b.sizes)), v = __uint_as_float(__ldg(b.sizes + 1)), l = __uint_as_float(__ldg(b.sizes + 2));
+  const float most = fmaf(2.0f * g, v, l);
+  if (!(most > 0.0f) || !isfinite(most)) return 0;
+  int x;
+  frexpf(most * 1.01f, &x);
+  return min(max(x, -100), 100);
+}
+
+// ---- delta -------------------------------------------------------------------
+
+// A warp a token, for all of its heads: 8 columns a lane, so 8 or 16 lanes a head.
+// fp16: further warps look at v's rows.
+template <bool HALF>
+__global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant__ BwdArgs b) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const PromptArgs& a = b.a;
+  const int lane = threadIdx.x & 31;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), warps = (int64_t)gridDim.x * 4;
+  const int each = a.d <= 64 ? 8 : 16, per = 32 / each;  // lanes of a head, heads of a round
+  const int sub = lane / each, col = (lane % each) * 8;
+  float most_g = 0.0f, most_v = 0.0f, most_l = 0.0f;
+  auto total = [&](float v) {
+    for (int o = each >> 1; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+  };
+  auto unpack = [&](const void* base, int64_t at, float (&f)[8]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = value16<HALF>((uint16_t)w[i]);
+      f[2 * i + 1] = value16<HALF>((uint16_t)(w[i] >> 16));
+    }
+  };
+  for (int64_t t = id; t < a.num_q; t += warps) {
+    // the token's sequence: the last one that begins at or before it
+    int lo = 0, span = a.nseq;
+    while (span > 1) {
+      const int step = (span + 31) / 32, at = lo + lane * step;
+      const bool before = lane * step < span && __ldg(a.cu_q + at) <= t;
+      const unsigned who = __ballot_sync(0xFFFFFFFFu, before);
+      const int k = who ? 31 - __clz(who) : 0;
+      span = min(step, span - k * step);
+      lo += k * step;
+    }
+    const Span w = span_of(a, lo);
+    const bool in = t >= w.q0 && t < (int64_t)w.q0 + w.nq;
+    const int hi = w.nk - w.nq + (int)(t - w.q0) + 1;
+    const bool single = in && (a.window == 1 || hi == 1);
+    for (int h0 = 0; h0 < a.heads; h0 += per) {
+      const int h = h0 + sub;
+      const bool there = in && h < a.heads;
+      const int64_t row = t * a.heads + h;
+      float dot = 0.0f, size = 0.0f;
+      if (there && col < a.d) {
+        float g[8], o[8], e[8] = {};
+        unpack(a.g, t * a.gt + h * a.gh + col, g);
+        unpack(a.out, row * a.d + col, o);
+        if (a.rest) unpack(a.rest, row * a.d + col, e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dot = fmaf(g[i], e[i], fmaf(g[i], o[i], dot));
+          size = fmaf(g[i], g[i], size);
+        }
+      }
+      dot = total(dot);
+      if (HALF) size = total(size);
+      if (there && lane % each == 0) {
+        const float dl = a.grad_lse ? __ldg(a.grad_lse + row) : 0.0f, lse = a.lse[row];
+        b.stats[row] = make_float2(lse == -INFINITY ? -INFINITY : kPLift<HALF> - lse * kLog2e, single ? dl : dl - dot);
+        if (HALF) {
+          // NaN compares above every number as bits, which gradient_exponent takes for no size
+          const float s = sqrtf(size);
+          most_g = s != s || s > most_g ? s : most_g;
+          most_l = dl != dl || fabsf(dl) > most_l ? fabsf(dl) : most_l;
+        }
+      }
+    }
+  }
+  if (HALF) {
+    for (int64_t t = id; t < a.num_k; t += warps)
+      for (int h0 = 0; h0 < a.kv; h0 += per) {
+        const int h = h0 + sub;
+        float size = 0.0f;
+        if (h < a.kv && col < a.d) {
+          float v[8];
+          unpack(a.v, t * a.vt + h * a.vh + col, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) size = isfinite(v[i]) ? fmaf(v[i], v[i], size) : size;
+        }
+        size = sqrtf(total(size));
+        most_v = fmaxf(most_v, size);
+      }
+    const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most_g) & 0x7FFFFFFFu);
+    const uint32_t v = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most_v));
+    const uint32_t l = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most_l) & 0x7FFFFFFFu);
+    if (lane == 0) {
+      atomicMax(b.sizes, g);
+      atomicMax(b.sizes + 1, v);
+      atomicMax(b.sizes + 2, l);
+    }
+  }
+}
+
+// ---- what both passes share ---------------------------------------------------
+
+template <int DP_, bool HALF_>
+struct Bwd {
+  static constexpr int DP = DP_;
+  static constexpr bool HALF = HALF_;
+  static constexpr int SLAB = 16384;
+  static constexpr int TILE = DP / 64 * SLAB;
+  static constexpr int HEAD = 8192;  // barriers and the rows' numbers
+  static constexpr int THREADS = 384;
+  static constexpr int MATH_REGS = 208, OTHER_REGS = 88;  // 2 * 208 + 88 = 3 * 168
+  static constexpr uint32_t TYPES = HALF ? 0u : (1u << 7) | (1u << 10);
+  // both operands K-major, N = 128; the second N-major, N = DP
+  static constexpr uint32_t IDESC_S = (1u << 4) | TYPES | ((128u >> 3) << 17) | (8u << 24);
+  static constexpr uint32_t IDESC_D = (1u << 4) | TYPES | (1u << 16) | ((uint32_t)(DP >> 3) << 17) | (8u << 24);
+};
+
+extern __shared__ __align__(1024) uint8_t bwd_smem[];
+
+// D [128 x 128] = A B^T over the columns of two operands in shared memory.
+template <class C>
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b) {
+  const uint64_t x = operand(a, 16), y = operand(b, 16);
+#pragma unroll
+  for (int j = 0; j < C::DP / 16; ++j) {
+    const int at = ((j >> 2) * C::SLAB + (j & 3) * 32) / 16;
+    tc_mma(d, x + at, y + at, C::IDESC_S, j > 0);
+  }
+}
+// D [128 x DP] += A B, A in tensor memory, its first 64 columns (16-bit) at `a` and the
+// other 64 at a + 64: each half in the place of the 64 logits that it was formed from.
+template <class C>
+__device__ __forceinline__ void product_add(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  const uint64_t y = operand(b, C::SLAB);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) tc_mma_ts(d, a + (j < 4 ? 8 * j : 32 + 8 * j), y + j * 128, C::IDESC_D, add || j > 0);
+}
+
+// 64 values of a lane as 32 words of tensor memory.
+template <bool HALF>
+__device__ __forceinline__ void store_half(uint32_t at, const float* v) {
+#pragma unroll
+  for (int k = 0; k < 64; k += 32) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack16<HALF>(v[k + 2 * i], v[k + 2 * i + 1]);
+    tc_store16_async(at + k / 2, w);
+  }
+  tc_store_wait();
+}
+__device__ __forceinline__ void load_half(uint32_t at, float* v) {
+  tc_load32_async(at, v);
+  tc_load32_async(at + 32, v + 32);
+  tc_load_wait();
+  tc_loaded(v);
+  tc_loaded(v + 32);
+}
+
+// 32 columns of a row of a result.
+template <bool HALF>
+__device__ __forceinline__ void store_columns(void* to, int64_t at, int d, int col, const float* v) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = pack16<HALF>(v[2 * i], v[2 * i + 1]);
+  uint16_t* p = static_cast<uint16_t*>(to) + at + col;
+  if (d % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (col + 16 * i < d) st_sector(p + 16 * i, w + 8 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + 8 * i < d) *reinterpret_cast<uint4*>(p + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+}
+
+// Copies under way land before a CTA that gave up ends: the last `stages` of a ring.
+__device__ __forceinline__ void drain(uint32_t full, int stages, int issued) {
+  for (int j = max(0, issued - stages); j < issued; ++j)
+    for (int k = 0; k < kPolls && !mbar_try(full + 8 * (j % stages), (j / stages) & 1); ++k) {
+    }
+}
+
+template <class C>
+__device__ __forceinline__ void load_tile(uint32_t to, const CUtensorMap* map, int head, int token, uint32_t bar) {
+  for (int p = 0; p < C::DP / 64; ++p) tma_load(to + p * C::SLAB, map, p * 64, head, token, bar);
+}
+
+// ---- dK and dV ----------------------------------------------------------------
+
+struct KeysState {
+  alignas(16) float lse[2][128];    // of a tile's rows: -(lse log2 e - lift)
+  alignas(16) float delta[2][128];  // -delta, times 2^-x for fp16
+  alignas(16) int32_t lo[2][128];   // keys that they see
+  alignas(16) int32_t hi[2][128];
+  uint64_t kv_full, q_full[2], q_empty[2], g_full[2], g_empty[2], r_full[2], s_full, p_full, dp_full, ds_full, done;
+  int32_t dead, bad;
+  uint32_t tmem;
+};
+static_assert(sizeof(KeysState) <= 8192, "HEAD");
+
+struct KeysWork {
+  Span w;
+  int32_t k0, kvh, off;    // first key of the CTA within the sequence
+  int32_t t0, tp, rows, n; // first query token, tokens and rows of a tile, tiles
+  int32_t t1;              // behind the last query token
+};
+
+// Whether some row of tile j does not see some key of the CTA, or is not there.
+__device__ __forceinline__ bool keys_mixed(const PromptArgs& a, const KeysWork& x, int j) {
+  const int64_t ta = (int64_t)x.t0 + (int64_t)j * x.tp, tb = ta + x.tp - 1;
+  return x.k0 + 128 > x.off + ta + 1 || tb >= x.w.nq || (a.window && x.k0 < x.off + tb + 1 - a.window);
+}
+
+// Infinities and NaN of grad that were cleaned away, for 32 columns of a key's dv.
+template <bool HALF>
+__device__ __noinline__ void give_back_grad(const PromptArgs& a, const KeysWork& x, int key, int col, float* o) {
+  for (int j = 0; j < x.n; ++j) {
+    if (!keys_mixed(a, x, j)) continue;
+    for (int i = 0; i < x.tp; ++i) {
+      const int t = x.t0 + j * x.tp + i;
+      const int64_t hi = (int64_t)x.off + t + 1;
+      if (t >= x.w.nq || key >= hi || (a.window && key < hi - a.window)) continue;
+      for (int h = x.kvh * a.group; h < (x.kvh + 1) * a.group; ++h) {
+        const uint16_t* g = static_cast<const uint16_t*>(a.g) + (int64_t)(x.w.q0 + t) * a.gt + h * a.gh + col;
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (col + c < a.d) {
+            const float f = value16<HALF>(__ldg(g + c));
+            if (!isfinite(f)) o[c] += f;
+          }
+      }
+    }
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    prompt_keys_kernel(const __grid_constant__ BwdArgs b, const __grid_constant__ CUtensorMap mq,
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                       const __grid_constant__ CUtensorMap mg) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const PromptArgs& a = b.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  {
+    const int64_t words = (int64_t)a.kv * a.d / 8;
+    fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dk));
+    fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dv));
+  }
+  // earlier slots first: a sequence's first keys are seen by the most rows
+  KeysWork x;
+  const int64_t slot = blockIdx.x / a.kv;
+  x.kvh = (int)(blockIdx.x - slot * a.kv);
+  const int s = seq_of_slot(a.cu_k, a.nseq, 128, slot, lane);
+  x.w = span_of(a, s);
+  const int64_t local = slot - first_slot(a.cu_k, s, 128);
+  if (local < 0 || local * 128 >= x.w.nk) return;
+  x.k0 = (int)local * 128;
+  x.off = x.w.nk - x.w.nq;
+  x.tp = 128 / a.group;
+  x.rows = x.tp * a.group;
+  x.t0 = max(0, x.k0 - x.off);
+  x.t1 = x.w.nq;
+  if (a.window) x.t1 = (int)min((int64_t)x.t1, (int64_t)min(x.k0 + 128, x.w.nk) - 1 - x.off + a.window);
+  x.n = x.t1 > x.t0 ? (x.t1 - x.t0 + x.tp - 1) / x.tp : 0;
+  const int n = x.n;
+
+  uint8_t* const base = bwd_smem + ((1024u - (smem_at(bwd_smem) & 1023u)) & 1023u);
+  auto& st = *reinterpret_cast<KeysState*>(base);
+  uint8_t* const q_ptr = base + C::HEAD + 2 * C::TILE;
+  uint8_t* const g_ptr = q_ptr + 2 * C::TILE;
+  const uint32_t k_at = smem_at(base + C::HEAD), v_at = k_at + C::TILE, q_at = smem_at(q_ptr), g_at = smem_at(g_ptr);
+  const uint32_t kv_full = smem_at(&st.kv_full), q_full = smem_at(st.q_full), q_empty = smem_at(st.q_empty),
+                 g_full = smem_at(st.g_full), g_empty = smem_at(st.g_empty), r_full = smem_at(st.r_full),
+                 s_full = smem_at(&st.s_full), p_full = smem_at(&st.p_full), dp_full = smem_at(&st.dp_full),
+                 ds_full = smem_at(&st.ds_full), done = smem_at(&st.done);
+  volatile int32_t* const dead = &st.dead;
+  if (threadIdx.x == 0) {
+    st.dead = st.bad = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 1);
+      mbar_init(q_empty + 8 * i, 1);
+      mbar_init(g_full + 8 * i, 1);
+      mbar_init(g_empty + 8 * i, 1);
+      mbar_init(r_full + 8 * i, 1);
+    }
+    mbar_init(kv_full, 1);
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(done, 1);
+    mbar_init(p_full, 8);
+    mbar_init(ds_full, 8);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // rows of a tile that no head uses are never copied to, and must not hold NaN
+  if (x.rows < 128) {
+    for (int i = threadIdx.x; i < 4 * (C::DP / 64) * (128 - x.rows) * 8; i += C::THREADS) {
+      const int part = i / ((128 - x.rows) * 8), at = i - part * (128 - x.rows) * 8;
+      *reinterpret_cast<uint4*>(q_ptr + part * C::SLAB + x.rows * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async();
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_at(&st.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *(volatile uint32_t*)&st.tmem;
+  const uint32_t S = tmem, DP = tmem + 128, DV = tmem + 256, DK = tmem + 256 + C::DP;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+    if (warp == 9) {  // ---- copies
+      if (lane == 0 && n > 0) {
+        const int bytes = C::DP / 64 * 128 * x.rows;
+        mbar_expect(kv_full, 2 * C::TILE);
+        load_tile<C>(k_at, &mk, x.kvh, x.w.k0 + x.k0, kv_full);
+        load_tile<C>(v_at, &mv, x.kvh, x.w.k0 + x.k0, kv_full);
+        for (int j = 0; j < n; ++j) {
+          const int stage = j & 1, token = x.w.q0 + x.t0 + j * x.tp;
+          mbar_wait(q_empty + 8 * stage, ((j >> 1) & 1) ^ 1, dead);
+          if (*dead) {
+            drain(kv_full, 1, 1);
+            drain(q_full, 2, j);
+            drain(g_full, 2, j);
+            break;
+          }
+          mbar_expect(q_full + 8 * stage, bytes);
+          load_tile<C>(q_at + stage * C::TILE, &mq, x.kvh * a.group, token, q_full + 8 * stage);
+          mbar_wait(g_empty + 8 * stage, ((j >> 1) & 1) ^ 1, dead);
+          if (*dead) {
+            drain(kv_full, 1, 1);
+            drain(q_full, 2, j + 1);
+            drain(g_full, 2, j);
+            break;
+          }
+          mbar_expect(g_full + 8 * stage, bytes);
+          load_tile<C>(g_at + stage * C::TILE, &mg, x.kvh * a.group, token, g_full + 8 * stage);
+        }
+      }
+    } else if (warp == 10) {  // ---- the rows' numbers, with the tile of q
+      const float f = C::HALF ? exp2f((float)-gradient_exponent<C::HALF>(b)) : 1.0f;
+      for (int j = 0; j < n; ++j) {
+        const int stage = j & 1;
+        float2 v[4];
+        int hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 32 + lane, t = x.t0 + j * x.tp + r / a.group;
+          const bool there = r < x.rows && t < x.w.nq;
+          hi[i] = there ? x.off + t + 1 : 0;
+          v[i] = there ? __ldg(b.stats + (int64_t)(x.w.q0 + t) * a.heads + x.kvh * a.group + r % a.group)
+                       : make_float2(-INFINITY, 0.0f);
+        }
+        mbar_wait(q_empty + 8 * stage, ((j >> 1) & 1) ^ 1, dead);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 32 + lane;
+          st.lse[stage][r] = v[i].x;
+          st.delta[stage][r] = v[i].y * f;
+          st.hi[stage][r] = hi[i];
+          st.lo[stage][r] = a.window ? max(0, hi[i] - a.window) : 0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(r_full + 8 * stage);
+      }
+    } else if (warp == 8) {  // ---- matrix instructions
+      if (n > 0) {
+        mbar_wait(kv_full, 0, dead);
+        auto scores = [&](int j) {
+          mbar_wait(q_full + 8 * (j & 1), (j >> 1) & 1, dead);
+          tc_after();
+          __syncwarp();
+          product<C>(S, k_at, q_at + (j & 1) * C::TILE);
+          tc_commit(s_full);
+        };
+        auto weights = [&](int j) {  // dP
+          mbar_wait(g_full + 8 * (j & 1), (j >> 1) & 1, dead);
+          tc_after();
+          __syncwarp();
+          product<C>(DP, v_at, g_at + (j & 1) * C::TILE);
+          tc_commit(dp_full);
+        };
+        scores(0);
+        weights(0);
+        for (int j = 0; j < n; ++j) {
+          mbar_wait(p_full, j & 1, dead);
+          tc_after();
+          __syncwarp();
+          product_add<C>(DV, S, g_at + (j & 1) * C::TILE, j > 0);
+          tc_commit(g_empty + 8 * (j & 1));
+          if (j + 1 < n) scores(j + 1);
+          mbar_wait(ds_full, j & 1, dead);
+          tc_after();
+          __syncwarp();
+          product_add<C>(DK, DP, q_at + (j & 1) * C::TILE, j > 0);
+          tc_commit(q_empty + 8 * (j & 1));
+          if (j + 1 < n) weights(j + 1);
+        }
+        tc_commit(done);
+      }
+    }
+  } else {  // ---- P and dS: a key a thread, half of a tile's rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MATH_REGS));
+    const int half = warp >> 2, col = half * 64, key = x.k0 + (threadIdx.x & 127);
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int e = gradient_exponent<C::HALF>(b);
+    const float c = a.scale * kLog2e, f = C::HALF ? exp2f((float)-e) : 1.0f;
+    const float2 c2 = make_float2(c, c), f2 = make_float2(f, f);
+    for (int j = 0; j < n; ++j) {
+      const int stage = j & 1;
+      const bool some = keys_mixed(a, x, j);
+      mbar_wait(r_full + 8 * stage, (j >> 1) & 1, dead);
+      mbar_wait(s_full, j & 1, dead);
+      tc_after();
+      float p[64], d[64];
+      load_half(S + lanes + col, p);
+#pragma unroll
+      for (int k = 0; k < 64; k += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(&st.lse[stage][col + k]);
+        const float2 za = fma2_rn(make_float2(p[k], p[k + 1]), c2, make_float2(l.x, l.y));
+        const float2 zb = fma2_rn(make_float2(p[k + 2], p[k + 3]), c2, make_float2(l.z, l.w));
+        p[k] = ex2_approx_ftz(za.x);
+        p[k + 1] = ex2_approx_ftz(za.y);
+        p[k + 2] = ex2_approx_ftz(zb.x);
+        p[k + 3] = ex2_approx_ftz(zb.y);
+      }
+      if (some) {
+#pragma unroll
+        for (int k = 0; k < 64; k += 4) {
+          const int4 l = *reinterpret_cast<const int4*>(&st.lo[stage][col + k]), h = *reinterpret_cast<const int4*>(&st.hi[stage][col + k]);
+          p[k] = key >= l.x && key < h.x ? p[k] : 0.0f;
+          p[k + 1] = key >= l.y && key < h.y ? p[k + 1] : 0.0f;
+          p[k + 2] = key >= l.z && key < h.z ? p[k + 2] : 0.0f;
+          p[k + 3] = key >= l.w && key < h.w ? p[k + 3] : 0.0f;
+        }
+      }
+      store_half<C::HALF>(S + lanes + col, p);
+      if (some) {
+        mbar_wait(g_full + 8 * stage, (j >> 1) & 1, dead);
+        clean_operand<C::HALF>(g_ptr + stage * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
+      }
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+
+      mbar_wait(dp_full, j & 1, dead);
+      tc_after();
+      load_half(DP + lanes + col, d);
+#pragma unroll
+      for (int k = 0; k < 64; k += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(&st.delta[stage][col + k]);
+        float2 da, db;
+        if constexpr (C::HALF) {
+          da = fma2_rn(make_float2(d[k], d[k + 1]), f2, make_float2(l.x, l.y));
+          db = fma2_rn(make_float2(d[k + 2], d[k + 3]), f2, make_float2(l.z, l.w));
+        } else {
+          da = add2_rn(make_float2(d[k], d[k + 1]), make_float2(l.x, l.y));
+          db = add2_rn(make_float2(d[k + 2], d[k + 3]), make_float2(l.z, l.w));
+        }
+        if (some) {  // rows that see one key: dP does not count; rows that see none of it: nothing does
+          const int4 lo = *reinterpret_cast<const int4*>(&st.lo[stage][col + k]), hi = *reinterpret_cast<const int4*>(&st.hi[stage][col + k]);
+          da.x = hi.x - lo.x == 1 ? l.x : da.x;
+          da.y = hi.y - lo.y == 1 ? l.y : da.y;
+          db.x = hi.z - lo.z == 1 ? l.z : db.x;
+          db.y = hi.w - lo.w == 1 ? l.w : db.y;
+          da.x = key >= lo.x && key < hi.x ? da.x : 0.0f;
+          da.y = key >= lo.y && key < hi.y ? da.y : 0.0f;
+          db.x = key >= lo.z && key < hi.z ? db.x : 0.0f;
+          db.y = key >= lo.w && key < hi.w ? db.y : 0.0f;
+        }
+        const float2 sa = mul2_rn(make_float2(p[k], p[k + 1]), da), sb = mul2_rn(make_float2(p[k + 2], p[k + 3]), db);
+        d[k] = sa.x;
+        d[k + 1] = sa.y;
+        d[k + 2] = sb.x;
+        d[k + 3] = sb.y;
+      }
+      store_half<C::HALF>(DP + lanes + col, d);
+      if (some) clean_operand<C::HALF>(q_ptr + stage * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    // group 0 stores dV, group 1 dK
+    if (n > 0) mbar_wait(done, 0, dead);
+    tc_after();
+    barrier_of(1, 256);  // all of both groups' cleaning is known
+    const bool there = key < x.w.nk;
+    const int64_t row = ((int64_t)(x.w.k0 + key) * a.kv + x.kvh) * a.d;
+    float factor = half ? a.scale * (C::HALF ? exp2f((float)(e - 15)) : 1.0f) : (C::HALF ? exp2f(-15.0f) : 1.0f);
+    if (*dead) factor = NAN;
+    const bool bad = half == 0 && *(volatile int32_t*)&st.bad != 0;
+#pragma unroll 1
+    for (int k = 0; k < C::DP; k += 32) {
+      float o[32];
+      if (n > 0) tc_load32((half ? DK : DV) + lanes + k, o);
+      if (!there || k >= a.d) continue;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * factor : 0.0f;
+      if (bad) {
+        float again[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) again[i] = o[i];
+        give_back_grad<C::HALF>(a, x, key, k, again);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = again[i];
+      }
+      store_columns<C::HALF>(half ? a.dk : a.dv, row, a.d, k, o);
+    }
+    tc_before();
+  }
+  __syncthreads();
+  tc_after();
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ---- dQ -------------------------------------------------------------------------
+
+constexpr int kKeyStages = 3, kValueStages = 2;
+
+struct RowsState {
+  uint64_t q_full, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], s_full[2], dp_full,
+      ds_full, done;
+  int32_t dead, bad;
+  uint32_t tmem;
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    prompt_rows_kernel(const __grid_constant__ BwdArgs b, const __grid_constant__ CUtensorMap mq,
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                       const __grid_constant__ CUtensorMap mg) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const PromptArgs& a = b.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  fill_rest(a.cu_q, a.nseq, a.num_q, (int64_t)a.heads * a.d / 8, static_cast<uint4*>(a.dq));
+  // later slots first: a sequence's last tiles see the most keys
+  const int tp = 128 / a.group, rows = tp * a.group;
+  const uint32_t id = gridDim.x - 1 - blockIdx.x;
+  const int64_t slot = id / a.kv;
+  const int kvh = (int)(id - slot * a.kv);
+  const int s = seq_of_slot(a.cu_q, a.nseq, tp, slot, lane);
+  const Span w = span_of(a, s);
+  const int64_t local = slot - first_slot(a.cu_q, s, tp);
+  if (local < 0 || local * tp >= w.nq) return;
+  const int t0 = (int)local * tp, t1 = min(t0 + tp, w.nq), off = w.nk - w.nq;
+  const int kb0 = (a.window ? (int)max((int64_t)0, (int64_t)off + t0 + 1 - a.window) : 0) / 128;
+  const int n = off + t1 > 0 ? (off + t1 + 127) / 128 - kb0 : 0;
+
+  uint8_t* const base = bwd_smem + ((1024u - (smem_at(bwd_smem) & 1023u)) & 1023u);
+  auto& st = *reinterpret_cast<RowsState*>(base);
+  uint8_t* const k_ptr = base + 1024 + 2 * C::TILE;
+  const uint32_t q_at = smem_at(base + 1024), g_at = q_at + C::TILE, k_at = smem_at(k_ptr), v_at = k_at + kKeyStages * C::TILE;
+  const uint32_t q_full = smem_at(&st.q_full), k_full = smem_at(st.k_full), k_empty = smem_at(st.k_empty),
+                 v_full = smem_at(st.v_full), v_empty = smem_at(st.v_empty), s_full = smem_at(st.s_full),
+                 dp_full = smem_at(&st.dp_full), ds_full = smem_at(&st.ds_full), done = smem_at(&st.done);
+  volatile int32_t* const dead = &st.dead;
+  if (threadIdx.x == 0) {
+    st.dead = st.bad = 0;
+    for (int i = 0; i < kKeyStages; ++i) {
+      mbar_init(k_full + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < kValueStages; ++i) {
+      mbar_init(v_full + 8 * i, 1);
+      mbar_init(v_empty + 8 * i, 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(s_full, 1);
+    mbar_init(s_full + 8, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(done, 1);
+    mbar_init(ds_full, 8);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_at(&st.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *(volatile uint32_t*)&st.tmem;
+  const uint32_t S = tmem, DP = tmem + 256, DQ = tmem + 384;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+    if (warp == 9) {  // ---- copies of q, grad and keys
+      if (lane == 0 && n > 0) {
+        mbar_expect(q_full, 2 * (C::DP / 64) * 128 * rows);
+        load_tile<C>(q_at, &mq, kvh * a.group, w.q0 + t0, q_full);
+        load_tile<C>(g_at, &mg, kvh * a.group, w.q0 + t0, q_full);
+        for (int j = 0; j < n; ++j) {
+          const int i = j % kKeyStages;
+          mbar_wait(k_empty + 8 * i, ((j / kKeyStages) & 1) ^ 1, dead);
+          if (*dead) {
+            drain(q_full, 1, 1);
+            drain(k_full, kKeyStages, j);
+            break;
+          }
+          mbar_expect(k_full + 8 * i, C::TILE);
+          load_tile<C>(k_at + i * C::TILE, &mk, kvh, w.k0 + (kb0 + j) * 128, k_full + 8 * i);
+        }
+      }
+    } else if (warp == 10) {  // ---- copies of values
+      if (lane == 0) {
+        for (int j = 0; j < n; ++j) {
+          const int i = j % kValueStages;
+          mbar_wait(v_empty + 8 * i, ((j / kValueStages) & 1) ^ 1, dead);
+          if (*dead) {
+            drain(v_full, kValueStages, j);
+            break;
+          }
+          mbar_expect(v_full + 8 * i, C::TILE);
+          load_tile<C>(v_at + i * C::TILE, &mv, kvh, w.k0 + (kb0 + j) * 128, v_full + 8 * i);
+        }
+      }
+    } else if (warp == 8) {  // ---- matrix instructions
+      if (n > 0) {
+        mbar_wait(q_full, 0, dead);
+        auto scores = [&](int j) {
+          mbar_wait(k_full + 8 * (j % kKeyStages), (j / kKeyStages) & 1, dead);
+          tc_after();
+          __syncwarp();
+          product<C>(S + 128 * (j & 1), q_at, k_at + (j % kKeyStages) * C::TILE);
+          tc_commit(s_full + 8 * (j & 1));
+        };
+        auto weights = [&](int j) {  // dP
+          mbar_wait(v_full + 8 * (j % kValueStages), (j / kValueStages) & 1, dead);
+          tc_after();
+          __syncwarp();
+          product<C>(DP, g_at, v_at + (j % kValueStages) * C::TILE);
+          tc_commit(v_empty + 8 * (j % kValueStages));
+          tc_commit(dp_full);
+        };
+        scores(0);
+        weights(0);
+        if (n > 1) scores(1);
+        for (int j = 0; j < n; ++j) {
+          mbar_wait(ds_full, j & 1, dead);
+          tc_after();
+          __syncwarp();
+          product_add<C>(DQ, S + 128 * (j & 1), k_at + (j % kKeyStages) * C::TILE, j > 0);
+          tc_commit(k_empty + 8 * (j % kKeyStages));
+          if (j + 1 < n) weights(j + 1);
+          if (j + 2 < n) scores(j + 2);
+        }
+        tc_commit(done);
+      }
+    }
+  } else {  // ---- dS: a row a thread, half of a block's keys
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MATH_REGS));
+    const int half = warp >> 2, col = half * 64, r = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int token = t0 + r / a.group;
+    const bool there = r < rows && token < w.nq;
+    const int hi = there ? off + token + 1 : 0;
+    const int lo = a.window ? max(0, hi - a.window) : 0;
+    const int64_t row = (int64_t)(w.q0 + token) * a.heads + kvh * a.group + r % a.group;
+    const float2 stats = there ? __ldg(b.stats + row) : make_float2(-INFINITY, 0.0f);
+    const int e = gradient_exponent<C::HALF>(b);
+    const float c = a.scale * kLog2e, f = C::HALF ? exp2f((float)-e) : 1.0f, delta = stats.y * f;
+    const bool single = hi - lo == 1;
+    const float2 c2 = make_float2(c, c), f2 = make_float2(f, f), l2 = make_float2(stats.x, stats.x), d2 = make_float2(delta, delta);
+    for (int j = 0; j < n; ++j) {
+      const int first = (kb0 + j) * 128;
+      // some row of the tile does not see some key of the block
+      const bool some = first + 128 > off + t0 + 1 || (a.window && (int64_t)first < (int64_t)off + t1 - a.window);
+      const uint32_t s_at = S + 128 * (j & 1) + lanes + col;
+      mbar_wait(s_full + 8 * (j & 1), (j >> 1) & 1, dead);
+      tc_after();
+      float p[64], d[64];
+      load_half(s_at, p);
+#pragma unroll
+      for (int k = 0; k < 64; k += 2) {
+        const float2 z = fma2_rn(make_float2(p[k], p[k + 1]), c2, l2);
+        p[k] = ex2_approx_ftz(z.x);
+        p[k + 1] = ex2_approx_ftz(z.y);
+      }
+      mbar_wait(dp_full, j & 1, dead);
+      tc_after();
+      load_half(DP + lanes + col, d);
+#pragma unroll
+      for (int k = 0; k < 64; k += 2) {
+        float2 v = make_float2(d[k], d[k + 1]);
+        if constexpr (C::HALF)
+          v = fma2_rn(v, f2, d2);
+        else
+          v = add2_rn(v, d2);
+        if (some && single) v = d2;
+        v = mul2_rn(make_float2(p[k], p[k + 1]), v);
+        d[k] = v.x;
+        d[k + 1] = v.y;
+      }
+      if (some) {
+        const int h = hi - first - col, l = lo - first - col;
+#pragma unroll
+        for (int k = 0; k < 64; ++k) d[k] = k < h && k >= l ? d[k] : 0.0f;
+      }
+      store_half<C::HALF>(s_at, d);
+      if (some) clean_operand<C::HALF>(k_ptr + (j % kKeyStages) * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
+      tc_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    if (n > 0) mbar_wait(done, 0, dead);
+    tc_after();
+    float factor = a.scale * (C::HALF ? exp2f((float)(e - 15)) : 1.0f);
+    if (*dead) factor = NAN;
+#pragma unroll 1
+    for (int k = half * (C::DP / 2); k < (half + 1) * (C::DP / 2); k += 32) {
+      float o[32];
+      if (n > 0) tc_load32(DQ + lanes + k, o);
+      if (!there || k >= a.d) continue;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * factor : 0.0f;
+      store_columns<C::HALF>(a.dq, row * a.d, a.d, k, o);
+    }
+    tc_before();
+  }
+  __syncthreads();
+  tc_after();
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+template <class C>
+cudaError_t launch_passes(const BwdArgs& b, cudaStream_t stream) {
+  const PromptArgs& a = b.a;
+  constexpr int KEYS_SMEM = 1024 + C::HEAD + 6 * C::TILE, ROWS_SMEM = 2048 + (2 + kKeyStages + kValueStages) * C::TILE;
+  const int tp = 128 / a.group;
+  CUtensorMap mq, mk, mv, mg;
+  cudaError_t e = rows_map(&mq, a.q, C::HALF, a.d, a.heads, a.num_q, a.qt, a.qh, a.group, tp);
+  if (e == cudaSuccess) e = rows_map(&mg, a.g, C::HALF, a.d, a.heads, a.num_q, a.gt, a.gh, a.group, tp);
+  if (e == cudaSuccess) e = rows_map(&mk, a.k, C::HALF, a.d, a.kv, a.num_k, a.kt, a.kh, 1, 128);
+  if (e == cudaSuccess) e = rows_map(&mv, a.v, C::HALF, a.d, a.kv, a.num_k, a.vt, a.vh, 1, 128);
+  auto* keys = prompt_keys_kernel<C>;
+  auto* rows = prompt_rows_kernel<C>;
+  if (e == cudaSuccess) e = allow_dynamic_smem((const void*)keys, KEYS_SMEM);
+  if (e == cudaSuccess) e = allow_dynamic_smem((const void*)rows, ROWS_SMEM);
+  if (e != cudaSuccess) return e;
+  if (a.num_k > 0) {
+    const int64_t blocks = ((int64_t)a.num_k / 128 + a.nseq) * a.kv;
+    e = launch_dependent(keys, dim3((unsigned)blocks), dim3(C::THREADS), KEYS_SMEM, stream, b, mq, mk, mv, mg);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t blocks = ((int64_t)a.num_q / tp + a.nseq) * a.kv;
+  return launch_dependent(rows, dim3((unsigned)blocks), dim3(C::THREADS), ROWS_SMEM, stream, b, mq, mk, mv, mg);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_bwd(const PromptArgs& a, bool half, cudaStream_t stream) {
+  BwdArgs b;
+  b.a = a;
+  const size_t stats = sizeof(float2) * (size_t)a.num_q * a.heads;
+  void* ws = nullptr;
+  cudaError_t e = workspace_take(&ws, stats + 16, stream);
+  if (e != cudaSuccess) return e;
+  b.stats = static_cast<float2*>(ws);
+  b.sizes = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + stats);
+  if (half) e = cudaMemsetAsync(b.sizes, 0, 16, stream);
+  if (e == cudaSuccess) {
+    const int64_t most = half && a.num_k > a.num_q ? a.num_k : a.num_q;
+    int64_t blocks = (most + 3) / 4;
+    if (blocks > 152 * 16) blocks = 152 * 16;
+    e = half ? launch_dependent(prompt_delta_kernel<true>, dim3((unsigned)blocks), dim3(128), 0, stream, b)
+             : launch_dependent(prompt_delta_kernel<false>, dim3((unsigned)blocks), dim3(128), 0, stream, b);
+  }
+  if (e == cudaSuccess) {
+    if (a.d <= 64)
+      e = half ? launch_passes<Bwd<64, true>>(b, stream) : launch_passes<Bwd<64, false>>(b, stream);
+    else
+      e = half ? launch_passes<Bwd<128, true>>(b, stream) : launch_passes<Bwd<128, false>>(b, stream);
+  }
+  const cudaError_t ef = workspace_give(ws, stream);
+  return e != cudaSuccess ? e : ef;
+}
+
+}  // namespace csa
