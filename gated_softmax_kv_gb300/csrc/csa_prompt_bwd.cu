@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant
   const int sub = lane / each, col = (lane % each) * 8;
   float most_g = 0.0f, most_v = 0.0f, most_l = 0.0f;
   auto total = [&](float v) {
+#pragma unroll 1
     for (int o = each >> 1; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
   };
@@ -87,6 +88,7 @@ __global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant
       f[2 * i + 1] = value16<HALF>((uint16_t)(w[i] >> 16));
     }
   };
+#pragma unroll 1
   for (int64_t t = id; t < a.num_q; t += warps) {
     // the token's sequence: the last one that begins at or before it
     int lo = 0, span = a.nseq;
@@ -102,6 +104,7 @@ __global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant
     const bool in = t >= w.q0 && t < (int64_t)w.q0 + w.nq;
     const int hi = w.nk - w.nq + (int)(t - w.q0) + 1;
     const bool single = in && (a.window == 1 || hi == 1);
+#pragma unroll 4
     for (int h0 = 0; h0 < a.heads; h0 += per) {
       const int h = h0 + sub;
       const bool there = in && h < a.heads;
@@ -133,7 +136,9 @@ __global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant
     }
   }
   if (HALF) {
+#pragma unroll 1
     for (int64_t t = id; t < a.num_k; t += warps)
+#pragma unroll 1
       for (int h0 = 0; h0 < a.kv; h0 += per) {
         const int h = h0 + sub;
         float size = 0.0f;
@@ -178,41 +183,25 @@ extern __shared__ __align__(1024) uint8_t bwd_smem[];
 
 // D [128 x 128] = A B^T over the columns of two operands in shared memory.
 template <class C>
-__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void product(uint32_t leader, uint32_t d, uint32_t a, uint32_t b) {
   const uint64_t x = operand(a, 16), y = operand(b, 16);
 #pragma unroll
-  for (int j = 0; j < C::DP / 16; ++j) {
-    const int at = ((j >> 2) * C::SLAB + (j & 3) * 32) / 16;
-    tc_mma(d, x + at, y + at, C::IDESC_S, j > 0);
-  }
+  for (int p = 0; p < C::DP / 64; ++p) tc_mma4<2>(leader, d, x + p * (C::SLAB / 16), y + p * (C::SLAB / 16), C::IDESC_S, p > 0);
 }
-// D [128 x DP] += A B, A in tensor memory, its first 64 columns (16-bit) at `a` and the
-// other 64 at a + 64: each half in the place of the 64 logits that it was formed from.
+// D [128 x DP] += A B, A in tensor memory, the 16-bit weights of 64 of the 128 at `a`,
+// in the place of the logits that they were formed from; half: which 64.
 template <class C>
-__device__ __forceinline__ void product_add(uint32_t d, uint32_t a, uint32_t b, bool add) {
-  const uint64_t y = operand(b, C::SLAB);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) tc_mma_ts(d, a + (j < 4 ? 8 * j : 32 + 8 * j), y + j * 128, C::IDESC_D, add || j > 0);
+__device__ __forceinline__ void product_add(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, int half, bool add) {
+  tc_mma4_ts<128>(leader, d, a + 64 * half, operand(b, C::SLAB) + 512 * half, C::IDESC_D, add);
 }
 
-// 64 values of a lane as 32 words of tensor memory.
+// 32 values of a lane as 16 words of tensor memory, without waiting.
 template <bool HALF>
-__device__ __forceinline__ void store_half(uint32_t at, const float* v) {
+__device__ __forceinline__ void store_part(uint32_t at, const float* v) {
+  uint32_t w[16];
 #pragma unroll
-  for (int k = 0; k < 64; k += 32) {
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack16<HALF>(v[k + 2 * i], v[k + 2 * i + 1]);
-    tc_store16_async(at + k / 2, w);
-  }
-  tc_store_wait();
-}
-__device__ __forceinline__ void load_half(uint32_t at, float* v) {
-  tc_load32_async(at, v);
-  tc_load32_async(at + 32, v + 32);
-  tc_load_wait();
-  tc_loaded(v);
-  tc_loaded(v + 32);
+  for (int i = 0; i < 16; ++i) w[i] = pack16<HALF>(v[2 * i], v[2 * i + 1]);
+  tc_store16_async(at, w);
 }
 
 // 32 columns of a row of a result.
@@ -235,13 +224,16 @@ __device__ __forceinline__ void store_columns(void* to, int64_t at, int d, int c
 
 // Copies under way land before a CTA that gave up ends: the last `stages` of a ring.
 __device__ __forceinline__ void drain(uint32_t full, int stages, int issued) {
+#pragma unroll 1
   for (int j = max(0, issued - stages); j < issued; ++j)
+#pragma unroll 1
     for (int k = 0; k < kPolls && !mbar_try(full + 8 * (j % stages), (j / stages) & 1); ++k) {
     }
 }
 
 template <class C>
 __device__ __forceinline__ void load_tile(uint32_t to, const CUtensorMap* map, int head, int token, uint32_t bar) {
+#pragma unroll 1
   for (int p = 0; p < C::DP / 64; ++p) tma_load(to + p * C::SLAB, map, p * 64, head, token, bar);
 }
 
@@ -252,7 +244,7 @@ struct KeysState {
   alignas(16) float delta[2][128];  // -delta, times 2^-x for fp16
   alignas(16) int32_t lo[2][128];   // keys that they see
   alignas(16) int32_t hi[2][128];
-  uint64_t kv_full, q_full[2], q_empty[2], g_full[2], g_empty[2], r_full[2], s_full, p_full, dp_full, ds_full, done;
+  uint64_t kv_full, q_full[2], q_empty[2], g_full[2], g_empty[2], r_full[2], s_full, p_full[2], dp_full, ds_full[2], done;
   int32_t dead, bad;
   uint32_t tmem;
 };
@@ -274,12 +266,15 @@ __device__ __forceinline__ bool keys_mixed(const PromptArgs& a, const KeysWork& 
 // Infinities and NaN of grad that were cleaned away, for 32 columns of a key's dv.
 template <bool HALF>
 __device__ __noinline__ void give_back_grad(const PromptArgs& a, const KeysWork& x, int key, int col, float* o) {
+#pragma unroll 1
   for (int j = 0; j < x.n; ++j) {
     if (!keys_mixed(a, x, j)) continue;
+#pragma unroll 1
     for (int i = 0; i < x.tp; ++i) {
       const int t = x.t0 + j * x.tp + i;
       const int64_t hi = (int64_t)x.off + t + 1;
       if (t >= x.w.nq || key >= hi || (a.window && key < hi - a.window)) continue;
+#pragma unroll 1
       for (int h = x.kvh * a.group; h < (x.kvh + 1) * a.group; ++h) {
         const uint16_t* g = static_cast<const uint16_t*>(a.g) + (int64_t)(x.w.q0 + t) * a.gt + h * a.gh + col;
 #pragma unroll
@@ -293,6 +288,121 @@ __device__ __noinline__ void give_back_grad(const PromptArgs& a, const KeysWork&
   }
 }
 
+// What the arithmetic of the keys kernel's tiles needs.
+struct KeysMath {
+  uint8_t *q_ptr, *g_ptr;
+  volatile int32_t* dead;
+  uint32_t s_at, dp_at, r_full, s_full, g_full, p_full, dp_full, ds_full;
+  int col, key;
+  float c, f;
+};
+
+// P and dS of tile j for a key and 64 rows; SOME: some row does not see some key. In
+// two parts of 32 rows: the second's logits arrive while the first's are used.
+template <class C, bool SOME>
+__device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, int j) {
+  constexpr bool HALF = C::HALF;
+  const int stage = j & 1, key = m.key, lane = threadIdx.x & 31;
+  const float2 c2 = make_float2(m.c, m.c), f2 = make_float2(m.f, m.f);
+  mbar_wait(m.r_full + 8 * stage, (j >> 1) & 1, m.dead);
+  if constexpr (SOME) {
+    mbar_wait(m.g_full + 8 * stage, (j >> 1) & 1, m.dead);
+    clean_operand<HALF>(m.g_ptr + stage * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
+  }
+  mbar_wait(m.s_full, j & 1, m.dead);
+  tc_after();
+  float p[64], d[64];
+  tc_load32_async(m.s_at, p);
+  tc_load_wait();
+  tc_loaded(p);
+  tc_load32_async(m.s_at + 32, p + 32);
+#pragma unroll
+  for (int part = 0; part < 64; part += 32) {
+    if (part) {
+      tc_load_wait();
+      tc_loaded(p + 32);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const int k = part + i;
+      const float4 l = *reinterpret_cast<const float4*>(&st.lse[stage][m.col + k]);
+      const float2 za = fma2_rn(make_float2(p[k], p[k + 1]), c2, make_float2(l.x, l.y));
+      const float2 zb = fma2_rn(make_float2(p[k + 2], p[k + 3]), c2, make_float2(l.z, l.w));
+      p[k] = ex2_approx_ftz(za.x);
+      p[k + 1] = ex2_approx_ftz(za.y);
+      p[k + 2] = ex2_approx_ftz(zb.x);
+      p[k + 3] = ex2_approx_ftz(zb.y);
+      if constexpr (SOME) {
+        const int4 lo = *reinterpret_cast<const int4*>(&st.lo[stage][m.col + k]), hi = *reinterpret_cast<const int4*>(&st.hi[stage][m.col + k]);
+        p[k] = key >= lo.x && key < hi.x ? p[k] : 0.0f;
+        p[k + 1] = key >= lo.y && key < hi.y ? p[k + 1] : 0.0f;
+        p[k + 2] = key >= lo.z && key < hi.z ? p[k + 2] : 0.0f;
+        p[k + 3] = key >= lo.w && key < hi.w ? p[k + 3] : 0.0f;
+      }
+    }
+    store_part<HALF>(m.s_at + part / 2, p + part);
+  }
+  tc_store_wait();
+  tc_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(m.p_full);
+
+  if constexpr (SOME) clean_operand<HALF>(m.q_ptr + stage * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
+  mbar_wait(m.dp_full, j & 1, m.dead);
+  tc_after();
+  tc_load32_async(m.dp_at, d);
+  tc_load_wait();
+  tc_loaded(d);
+  tc_load32_async(m.dp_at + 32, d + 32);
+#pragma unroll
+  for (int part = 0; part < 64; part += 32) {
+    if (part) {
+      tc_load_wait();
+      tc_loaded(d + 32);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const int k = part + i;
+      const float4 l = *reinterpret_cast<const float4*>(&st.delta[stage][m.col + k]);
+      float2 da, db;
+      if constexpr (HALF) {
+        da = fma2_rn(make_float2(d[k], d[k + 1]), f2, make_float2(l.x, l.y));
+        db = fma2_rn(make_float2(d[k + 2], d[k + 3]), f2, make_float2(l.z, l.w));
+      } else {
+        da = add2_rn(make_float2(d[k], d[k + 1]), make_float2(l.x, l.y));
+        db = add2_rn(make_float2(d[k + 2], d[k + 3]), make_float2(l.z, l.w));
+      }
+      if constexpr (SOME) {  // rows that see one key: dP does not count; rows that see none of it: nothing does
+        const int4 lo = *reinterpret_cast<const int4*>(&st.lo[stage][m.col + k]), hi = *reinterpret_cast<const int4*>(&st.hi[stage][m.col + k]);
+        da.x = hi.x - lo.x == 1 ? l.x : da.x;
+        da.y = hi.y - lo.y == 1 ? l.y : da.y;
+        db.x = hi.z - lo.z == 1 ? l.z : db.x;
+        db.y = hi.w - lo.w == 1 ? l.w : db.y;
+        da.x = key >= lo.x && key < hi.x ? da.x : 0.0f;
+        da.y = key >= lo.y && key < hi.y ? da.y : 0.0f;
+        db.x = key >= lo.z && key < hi.z ? db.x : 0.0f;
+        db.y = key >= lo.w && key < hi.w ? db.y : 0.0f;
+      }
+      const float2 sa = mul2_rn(make_float2(p[k], p[k + 1]), da), sb = mul2_rn(make_float2(p[k + 2], p[k + 3]), db);
+      d[k] = sa.x;
+      d[k + 1] = sa.y;
+      d[k + 2] = sb.x;
+      d[k + 3] = sb.y;
+    }
+    store_part<HALF>(m.dp_at + part / 2, d + part);
+  }
+  tc_store_wait();
+  tc_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(m.ds_full);
+}
+// Kept out of the loop: with both forms in it the instruction cache held neither
+// (8192 tokens of 32 heads of 128: 875 us).
+template <class C>
+__device__ __noinline__ void keys_step_some(KeysState& st, const KeysMath& m, int j) {
+  keys_step<C, true>(st, m, j);
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     prompt_keys_kernel(const __grid_constant__ BwdArgs b, const __grid_constant__ CUtensorMap mq,
@@ -304,8 +414,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   {
     const int64_t words = (int64_t)a.kv * a.d / 8;
-    fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dk));
-    fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dv));
+    const int64_t from = (int64_t)blockIdx.x * C::THREADS + threadIdx.x, step = (int64_t)gridDim.x * C::THREADS;
+    fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dk), from, step);
+    fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dv), from, step);
   }
   // earlier slots first: a sequence's first keys are seen by the most rows
   KeysWork x;
@@ -332,11 +443,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t k_at = smem_at(base + C::HEAD), v_at = k_at + C::TILE, q_at = smem_at(q_ptr), g_at = smem_at(g_ptr);
   const uint32_t kv_full = smem_at(&st.kv_full), q_full = smem_at(st.q_full), q_empty = smem_at(st.q_empty),
                  g_full = smem_at(st.g_full), g_empty = smem_at(st.g_empty), r_full = smem_at(st.r_full),
-                 s_full = smem_at(&st.s_full), p_full = smem_at(&st.p_full), dp_full = smem_at(&st.dp_full),
-                 ds_full = smem_at(&st.ds_full), done = smem_at(&st.done);
+                 s_full = smem_at(&st.s_full), p_full = smem_at(st.p_full), dp_full = smem_at(&st.dp_full),
+                 ds_full = smem_at(st.ds_full), done = smem_at(&st.done);
   volatile int32_t* const dead = &st.dead;
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1);
       mbar_init(q_empty + 8 * i, 1);
@@ -348,12 +460,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
     mbar_init(done, 1);
-    mbar_init(p_full, 8);
-    mbar_init(ds_full, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(p_full + 8 * i, 4);
+      mbar_init(ds_full + 8 * i, 4);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // rows of a tile that no head uses are never copied to, and must not hold NaN
   if (x.rows < 128) {
+#pragma unroll 1
     for (int i = threadIdx.x; i < 4 * (C::DP / 64) * (128 - x.rows) * 8; i += C::THREADS) {
       const int part = i / ((128 - x.rows) * 8), at = i - part * (128 - x.rows) * 8;
       *reinterpret_cast<uint4*>(q_ptr + part * C::SLAB + x.rows * 128 + at * 16) = make_uint4(0, 0, 0, 0);
@@ -378,6 +493,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         mbar_expect(kv_full, 2 * C::TILE);
         load_tile<C>(k_at, &mk, x.kvh, x.w.k0 + x.k0, kv_full);
         load_tile<C>(v_at, &mv, x.kvh, x.w.k0 + x.k0, kv_full);
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int stage = j & 1, token = x.w.q0 + x.t0 + j * x.tp;
           mbar_wait(q_empty + 8 * stage, ((j >> 1) & 1) ^ 1, dead);
@@ -402,6 +518,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     } else if (warp == 10) {  // ---- the rows' numbers, with the tile of q
       const float f = C::HALF ? exp2f((float)-gradient_exponent<C::HALF>(b)) : 1.0f;
+#pragma unroll 1
       for (int j = 0; j < n; ++j) {
         const int stage = j & 1;
         float2 v[4];
@@ -427,39 +544,43 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (lane == 0) mbar_arrive(r_full + 8 * stage);
       }
     } else if (warp == 8) {  // ---- matrix instructions
-      if (n > 0) {
+      const int tiles = (int)uniform((uint32_t)n);
+      const uint32_t leader = tc_leader(), base_t = uniform(tmem), S = base_t, DP = base_t + 128, DV = base_t + 256,
+                     DK = base_t + 256 + C::DP;
+      if (tiles > 0) {
         mbar_wait(kv_full, 0, dead);
         auto scores = [&](int j) {
           mbar_wait(q_full + 8 * (j & 1), (j >> 1) & 1, dead);
           tc_after();
-          __syncwarp();
-          product<C>(S, k_at, q_at + (j & 1) * C::TILE);
-          tc_commit(s_full);
+          product<C>(leader, S, k_at, q_at + (j & 1) * C::TILE);
+          tc_commit_by(leader, s_full);
         };
         auto weights = [&](int j) {  // dP
           mbar_wait(g_full + 8 * (j & 1), (j >> 1) & 1, dead);
           tc_after();
-          __syncwarp();
-          product<C>(DP, v_at, g_at + (j & 1) * C::TILE);
-          tc_commit(dp_full);
+          product<C>(leader, DP, v_at, g_at + (j & 1) * C::TILE);
+          tc_commit_by(leader, dp_full);
+        };
+        auto add = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t ready, int j) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            mbar_wait(ready + 8 * half, j & 1, dead);
+            tc_after();
+            product_add<C>(leader, d, x, y, half, j > 0 || half > 0);
+          }
         };
         scores(0);
         weights(0);
-        for (int j = 0; j < n; ++j) {
-          mbar_wait(p_full, j & 1, dead);
-          tc_after();
-          __syncwarp();
-          product_add<C>(DV, S, g_at + (j & 1) * C::TILE, j > 0);
-          tc_commit(g_empty + 8 * (j & 1));
-          if (j + 1 < n) scores(j + 1);
-          mbar_wait(ds_full, j & 1, dead);
-          tc_after();
-          __syncwarp();
-          product_add<C>(DK, DP, q_at + (j & 1) * C::TILE, j > 0);
-          tc_commit(q_empty + 8 * (j & 1));
-          if (j + 1 < n) weights(j + 1);
+#pragma unroll 1
+        for (int j = 0; j < tiles; ++j) {
+          add(DV, S, g_at + (j & 1) * C::TILE, p_full, j);
+          tc_commit_by(leader, g_empty + 8 * (j & 1));
+          if (j + 1 < tiles) scores(j + 1);
+          add(DK, DP, q_at + (j & 1) * C::TILE, ds_full, j);
+          tc_commit_by(leader, q_empty + 8 * (j & 1));
+          if (j + 1 < tiles) weights(j + 1);
         }
-        tc_commit(done);
+        tc_commit_by(leader, done);
       }
     }
   } else {  // ---- P and dS: a key a thread, half of a tile's rows
@@ -468,80 +589,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int e = gradient_exponent<C::HALF>(b);
     const float c = a.scale * kLog2e, f = C::HALF ? exp2f((float)-e) : 1.0f;
-    const float2 c2 = make_float2(c, c), f2 = make_float2(f, f);
+    const KeysMath m = {q_ptr, g_ptr, dead, S + lanes + col, DP + lanes + col, r_full, s_full, g_full, p_full + 8 * half, dp_full, ds_full + 8 * half, col, key, c, f};
+#pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      const int stage = j & 1;
-      const bool some = keys_mixed(a, x, j);
-      mbar_wait(r_full + 8 * stage, (j >> 1) & 1, dead);
-      mbar_wait(s_full, j & 1, dead);
-      tc_after();
-      float p[64], d[64];
-      load_half(S + lanes + col, p);
-#pragma unroll
-      for (int k = 0; k < 64; k += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(&st.lse[stage][col + k]);
-        const float2 za = fma2_rn(make_float2(p[k], p[k + 1]), c2, make_float2(l.x, l.y));
-        const float2 zb = fma2_rn(make_float2(p[k + 2], p[k + 3]), c2, make_float2(l.z, l.w));
-        p[k] = ex2_approx_ftz(za.x);
-        p[k + 1] = ex2_approx_ftz(za.y);
-        p[k + 2] = ex2_approx_ftz(zb.x);
-        p[k + 3] = ex2_approx_ftz(zb.y);
-      }
-      if (some) {
-#pragma unroll
-        for (int k = 0; k < 64; k += 4) {
-          const int4 l = *reinterpret_cast<const int4*>(&st.lo[stage][col + k]), h = *reinterpret_cast<const int4*>(&st.hi[stage][col + k]);
-          p[k] = key >= l.x && key < h.x ? p[k] : 0.0f;
-          p[k + 1] = key >= l.y && key < h.y ? p[k + 1] : 0.0f;
-          p[k + 2] = key >= l.z && key < h.z ? p[k + 2] : 0.0f;
-          p[k + 3] = key >= l.w && key < h.w ? p[k + 3] : 0.0f;
-        }
-      }
-      store_half<C::HALF>(S + lanes + col, p);
-      if (some) {
-        mbar_wait(g_full + 8 * stage, (j >> 1) & 1, dead);
-        clean_operand<C::HALF>(g_ptr + stage * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
-      }
-      tc_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
-
-      mbar_wait(dp_full, j & 1, dead);
-      tc_after();
-      load_half(DP + lanes + col, d);
-#pragma unroll
-      for (int k = 0; k < 64; k += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(&st.delta[stage][col + k]);
-        float2 da, db;
-        if constexpr (C::HALF) {
-          da = fma2_rn(make_float2(d[k], d[k + 1]), f2, make_float2(l.x, l.y));
-          db = fma2_rn(make_float2(d[k + 2], d[k + 3]), f2, make_float2(l.z, l.w));
-        } else {
-          da = add2_rn(make_float2(d[k], d[k + 1]), make_float2(l.x, l.y));
-          db = add2_rn(make_float2(d[k + 2], d[k + 3]), make_float2(l.z, l.w));
-        }
-        if (some) {  // rows that see one key: dP does not count; rows that see none of it: nothing does
-          const int4 lo = *reinterpret_cast<const int4*>(&st.lo[stage][col + k]), hi = *reinterpret_cast<const int4*>(&st.hi[stage][col + k]);
-          da.x = hi.x - lo.x == 1 ? l.x : da.x;
-          da.y = hi.y - lo.y == 1 ? l.y : da.y;
-          db.x = hi.z - lo.z == 1 ? l.z : db.x;
-          db.y = hi.w - lo.w == 1 ? l.w : db.y;
-          da.x = key >= lo.x && key < hi.x ? da.x : 0.0f;
-          da.y = key >= lo.y && key < hi.y ? da.y : 0.0f;
-          db.x = key >= lo.z && key < hi.z ? db.x : 0.0f;
-          db.y = key >= lo.w && key < hi.w ? db.y : 0.0f;
-        }
-        const float2 sa = mul2_rn(make_float2(p[k], p[k + 1]), da), sb = mul2_rn(make_float2(p[k + 2], p[k + 3]), db);
-        d[k] = sa.x;
-        d[k + 1] = sa.y;
-        d[k + 2] = sb.x;
-        d[k + 3] = sb.y;
-      }
-      store_half<C::HALF>(DP + lanes + col, d);
-      if (some) clean_operand<C::HALF>(q_ptr + stage * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
-      tc_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      if (keys_mixed(a, x, j))
+        keys_step_some<C>(st, m, j);
+      else
+        keys_step<C, false>(st, m, j);
     }
     // group 0 stores dV, group 1 dK
     if (n > 0) mbar_wait(done, 0, dead);
@@ -582,7 +636,7 @@ constexpr int kKeyStages = 3, kValueStages = 2;
 
 struct RowsState {
   uint64_t q_full, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], s_full[2], dp_full,
-      ds_full, done;
+      ds_full[2], done;
   int32_t dead, bad;
   uint32_t tmem;
 };
@@ -596,7 +650,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   allow_dependent_launch();
   const PromptArgs& a = b.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  fill_rest(a.cu_q, a.nseq, a.num_q, (int64_t)a.heads * a.d / 8, static_cast<uint4*>(a.dq));
+  fill_rest(a.cu_q, a.nseq, a.num_q, (int64_t)a.heads * a.d / 8, static_cast<uint4*>(a.dq),
+            (int64_t)blockIdx.x * C::THREADS + threadIdx.x, (int64_t)gridDim.x * C::THREADS);
   // later slots first: a sequence's last tiles see the most keys
   const int tp = 128 / a.group, rows = tp * a.group;
   const uint32_t id = gridDim.x - 1 - blockIdx.x;
@@ -616,14 +671,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t q_at = smem_at(base + 1024), g_at = q_at + C::TILE, k_at = smem_at(k_ptr), v_at = k_at + kKeyStages * C::TILE;
   const uint32_t q_full = smem_at(&st.q_full), k_full = smem_at(st.k_full), k_empty = smem_at(st.k_empty),
                  v_full = smem_at(st.v_full), v_empty = smem_at(st.v_empty), s_full = smem_at(st.s_full),
-                 dp_full = smem_at(&st.dp_full), ds_full = smem_at(&st.ds_full), done = smem_at(&st.done);
+                 dp_full = smem_at(&st.dp_full), ds_full = smem_at(st.ds_full), done = smem_at(&st.done);
   volatile int32_t* const dead = &st.dead;
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
+#pragma unroll 1
     for (int i = 0; i < kKeyStages; ++i) {
       mbar_init(k_full + 8 * i, 1);
       mbar_init(k_empty + 8 * i, 1);
     }
+#pragma unroll 1
     for (int i = 0; i < kValueStages; ++i) {
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_empty + 8 * i, 1);
@@ -633,7 +690,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     mbar_init(s_full + 8, 1);
     mbar_init(dp_full, 1);
     mbar_init(done, 1);
-    mbar_init(ds_full, 8);
+    mbar_init(ds_full, 4);
+    mbar_init(ds_full + 8, 4);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) {
@@ -653,6 +711,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         mbar_expect(q_full, 2 * (C::DP / 64) * 128 * rows);
         load_tile<C>(q_at, &mq, kvh * a.group, w.q0 + t0, q_full);
         load_tile<C>(g_at, &mg, kvh * a.group, w.q0 + t0, q_full);
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int i = j % kKeyStages;
           mbar_wait(k_empty + 8 * i, ((j / kKeyStages) & 1) ^ 1, dead);
@@ -667,6 +726,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     } else if (warp == 10) {  // ---- copies of values
       if (lane == 0) {
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
           const int i = j % kValueStages;
           mbar_wait(v_empty + 8 * i, ((j / kValueStages) & 1) ^ 1, dead);
@@ -679,36 +739,42 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
     } else if (warp == 8) {  // ---- matrix instructions
-      if (n > 0) {
+      const int tiles = (int)uniform((uint32_t)n);
+      const uint32_t leader = tc_leader(), base_t = uniform(tmem), S = base_t, DP = base_t + 256, DQ = base_t + 384;
+      if (tiles > 0) {
         mbar_wait(q_full, 0, dead);
         auto scores = [&](int j) {
           mbar_wait(k_full + 8 * (j % kKeyStages), (j / kKeyStages) & 1, dead);
           tc_after();
-          __syncwarp();
-          product<C>(S + 128 * (j & 1), q_at, k_at + (j % kKeyStages) * C::TILE);
-          tc_commit(s_full + 8 * (j & 1));
+          product<C>(leader, S + 128 * (j & 1), q_at, k_at + (j % kKeyStages) * C::TILE);
+          tc_commit_by(leader, s_full + 8 * (j & 1));
         };
         auto weights = [&](int j) {  // dP
           mbar_wait(v_full + 8 * (j % kValueStages), (j / kValueStages) & 1, dead);
           tc_after();
-          __syncwarp();
-          product<C>(DP, g_at, v_at + (j % kValueStages) * C::TILE);
-          tc_commit(v_empty + 8 * (j % kValueStages));
-          tc_commit(dp_full);
+          product<C>(leader, DP, g_at, v_at + (j % kValueStages) * C::TILE);
+          tc_commit_by(leader, v_empty + 8 * (j % kValueStages));
+          tc_commit_by(leader, dp_full);
+        };
+        auto add = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t ready, int j) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            mbar_wait(ready + 8 * half, j & 1, dead);
+            tc_after();
+            product_add<C>(leader, d, x, y, half, j > 0 || half > 0);
+          }
         };
         scores(0);
         weights(0);
-        if (n > 1) scores(1);
-        for (int j = 0; j < n; ++j) {
-          mbar_wait(ds_full, j & 1, dead);
-          tc_after();
-          __syncwarp();
-          product_add<C>(DQ, S + 128 * (j & 1), k_at + (j % kKeyStages) * C::TILE, j > 0);
-          tc_commit(k_empty + 8 * (j % kKeyStages));
-          if (j + 1 < n) weights(j + 1);
-          if (j + 2 < n) scores(j + 2);
+        if (tiles > 1) scores(1);
+#pragma unroll 1
+        for (int j = 0; j < tiles; ++j) {
+          add(DQ, S + 128 * (j & 1), k_at + (j % kKeyStages) * C::TILE, ds_full, j);
+          tc_commit_by(leader, k_empty + 8 * (j % kKeyStages));
+          if (j + 1 < tiles) weights(j + 1);
+          if (j + 2 < tiles) scores(j + 2);
         }
-        tc_commit(done);
+        tc_commit_by(leader, done);
       }
     }
   } else {  // ---- dS: a row a thread, half of a block's keys
@@ -725,6 +791,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const float c = a.scale * kLog2e, f = C::HALF ? exp2f((float)-e) : 1.0f, delta = stats.y * f;
     const bool single = hi - lo == 1;
     const float2 c2 = make_float2(c, c), f2 = make_float2(f, f), l2 = make_float2(stats.x, stats.x), d2 = make_float2(delta, delta);
+#pragma unroll 1
     for (int j = 0; j < n; ++j) {
       const int first = (kb0 + j) * 128;
       // some row of the tile does not see some key of the block
@@ -733,38 +800,55 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_wait(s_full + 8 * (j & 1), (j >> 1) & 1, dead);
       tc_after();
       float p[64], d[64];
-      load_half(s_at, p);
+      tc_load32_async(s_at, p);
+      tc_load32_async(s_at + 32, p + 32);
+      tc_load_wait();
+      tc_loaded(p);
+      tc_loaded(p + 32);
 #pragma unroll
       for (int k = 0; k < 64; k += 2) {
         const float2 z = fma2_rn(make_float2(p[k], p[k + 1]), c2, l2);
         p[k] = ex2_approx_ftz(z.x);
         p[k + 1] = ex2_approx_ftz(z.y);
       }
+      if (some) clean_operand<C::HALF>(k_ptr + (j % kKeyStages) * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
       mbar_wait(dp_full, j & 1, dead);
       tc_after();
-      load_half(DP + lanes + col, d);
+      tc_load32_async(DP + lanes + col, d);
+      tc_load_wait();
+      tc_loaded(d);
+      tc_load32_async(DP + lanes + col + 32, d + 32);
+      // in two parts, as in keys_step
 #pragma unroll
-      for (int k = 0; k < 64; k += 2) {
-        float2 v = make_float2(d[k], d[k + 1]);
-        if constexpr (C::HALF)
-          v = fma2_rn(v, f2, d2);
-        else
-          v = add2_rn(v, d2);
-        if (some && single) v = d2;
-        v = mul2_rn(make_float2(p[k], p[k + 1]), v);
-        d[k] = v.x;
-        d[k + 1] = v.y;
-      }
-      if (some) {
-        const int h = hi - first - col, l = lo - first - col;
+      for (int part = 0; part < 64; part += 32) {
+        if (part) {
+          tc_load_wait();
+          tc_loaded(d + 32);
+        }
 #pragma unroll
-        for (int k = 0; k < 64; ++k) d[k] = k < h && k >= l ? d[k] : 0.0f;
+        for (int i = 0; i < 32; i += 2) {
+          const int k = part + i;
+          float2 v = make_float2(d[k], d[k + 1]);
+          if constexpr (C::HALF)
+            v = fma2_rn(v, f2, d2);
+          else
+            v = add2_rn(v, d2);
+          if (some && single) v = d2;
+          v = mul2_rn(make_float2(p[k], p[k + 1]), v);
+          d[k] = v.x;
+          d[k + 1] = v.y;
+        }
+        if (some) {
+          const int h = hi - first - col - part, l = lo - first - col - part;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) d[part + k] = k < h && k >= l ? d[part + k] : 0.0f;
+        }
+        store_part<C::HALF>(s_at + part / 2, d + part);
       }
-      store_half<C::HALF>(s_at, d);
-      if (some) clean_operand<C::HALF>(k_ptr + (j % kKeyStages) * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
+      tc_store_wait();
       tc_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      if (lane == 0) mbar_arrive(ds_full + 8 * half);
     }
     if (n > 0) mbar_wait(done, 0, dead);
     tc_after();

@@ -9,10 +9,15 @@
 // PV of tile t and then its next Q K^T, take as long as the softmax of the other.
 //
 // Roles: four warps a tile for its softmax and its result, one warp for the matrix
-// instructions, one for TMA. Tiles of K and V come in a ring, in the order in which
-// the instructions use them. Where only one tile has rows (single tokens, short
-// prompts) both softmax groups work on it, on alternate blocks of keys, and add up
-// at the end.
+// instructions, one for TMA, one that finds the work. Tiles of K and V come in a ring,
+// in the order in which the instructions use them. Where only one tile has rows (single
+// tokens, short prompts) both softmax groups work on it, on alternate blocks of keys,
+// and add up at the end.
+//
+// A CTA that is done takes over the work of one that has not started (cluster launch
+// control), so that the copies and first products of its next item run beside the
+// result of this one. Grids that leave SMs idle are launched as clusters instead,
+// whose CTAs share an item's keys and add up through distributed shared memory.
 //
 // The reference that logits are taken from rises only when they pass it by 2^8, so
 // that O is seldom scaled: weights are at most 2^8. fp16 weights are lifted by
@@ -47,7 +52,8 @@ struct Fwd {
   static constexpr int THREADS = 384;
   // Registers: 384 threads at 168, dealt out again by role (2 * 208 + 88 = 3 * 168).
   static constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
-  static constexpr int SMEM = 2048 + (2 + NS) * TILE;
+  static constexpr int HEAD = 2048;  // barriers and the item
+  static constexpr int SMEM = 1024 + HEAD + (2 + NS) * TILE;
   static constexpr uint32_t S0 = 0, O0 = 256;     // TMEM columns: S of the two tiles, O of the two
   static constexpr uint32_t TYPES = HALF ? 0u : (1u << 7) | (1u << 10);
   // fp32 accumulator, M = 128; N = 128 keys; N = DP columns, the second operand N-major
@@ -56,30 +62,47 @@ struct Fwd {
   static constexpr float LIFT = HALF ? 7.0f : 0.0f;
 };
 
+// An item of work: the query rows of up to two tiles, and the keys that they see.
+struct alignas(16) Item {
+  int32_t q0, nq, k0, off;   // first row of the sequence in q and k; its queries; key index of query 0
+  int32_t t0, last;          // first and last token
+  int32_t kvh;               // key head
+  int32_t kb0, n0, n1, step; // first block of keys, blocks of each tile, 2: the groups share tile 0
+  int32_t pad;               // n0 < 0: there is no more work
+};
+
 template <int NS>
 struct State {
-  uint64_t full[NS], empty[NS], q_full, s_full[2], p_full[2], o_full[2];
+  Item item[2];
+  alignas(16) uint32_t stolen[4];
+  uint64_t full[NS], empty[NS], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], item_full[2], item_empty[2], steal, pair_full, pair_empty;
   int32_t dead, bad;
   uint32_t tmem;
+  float ref[128], sum[128];  // group 1's, for group 0; in a cluster: the CTA's
 };
 
-// The CTA's work, the same in every thread.
-struct Work {
-  Span w;
-  int32_t t0, tp, rows;       // first token, tokens of a tile, its rows in use
-  int32_t kvh, off;           // key head; key index of query 0
-  int32_t kb0, n[2], step;    // first block of keys, blocks of each tile, 2: the groups share tile 0
-  int32_t last;               // last token of the CTA
+// A place in the ring, and the parity of its barriers.
+template <int NS>
+struct Place {
+  int stage;
+  uint32_t parity;
+  __device__ __forceinline__ void next(int n) {
+    stage += n;
+    if (stage >= NS) {
+      stage -= NS;
+      parity ^= 1;
+    }
+  }
 };
 
-// Position in the ring of the keys and values of block b.
-__device__ __forceinline__ int keys_at(int b, int step) { return step == 1 ? 2 * b : b == 0 ? 0 : 2 * b - 1; }
+// The order of the ring: K0 V0 K1 V1 ... or, where the groups take alternate blocks, K0
+// K1 V0 K2 V1 ...: the position of block b's values.
 __device__ __forceinline__ int values_at(int b, int n, int step) {
   return step == 1 ? 2 * b + 1 : b < n - 1 ? 2 * b + 2 : 2 * n - 1;
 }
 
 // Whether some row of tokens ta .. tb does not see all of block b.
-__device__ __forceinline__ bool mixed(const PromptArgs& a, const Work& x, int b, int ta, int tb) {
+__device__ __forceinline__ bool mixed(const PromptArgs& a, const Item& x, int b, int ta, int tb) {
   const int first = (x.kb0 + b) * 128;
   return first + 128 > x.off + ta + 1 || (a.window && (int64_t)first < (int64_t)x.off + tb + 1 - a.window);
 }
@@ -89,12 +112,14 @@ extern __shared__ __align__(1024) uint8_t fwd_smem[];
 // Infinities and NaN of V that were cleaned away, for 32 columns of a row that sees
 // keys lo .. hi - 1.
 template <bool HALF>
-__device__ __noinline__ void give_back(const PromptArgs& a, const Work& x, int lo, int hi, int col, float* o) {
-  for (int b = 0; b < max(x.n[0], x.n[1]); ++b) {
+__device__ __noinline__ void give_back(const PromptArgs& a, const Item& x, int lo, int hi, int col, float* o) {
+#pragma unroll 1
+  for (int b = 0; b < max(x.n0, x.n1); ++b) {
     if (!mixed(a, x, b, x.t0, x.last)) continue;
     const int k0 = max(lo, (x.kb0 + b) * 128), k1 = min(hi, (x.kb0 + b) * 128 + 128);
+#pragma unroll 1
     for (int k = k0; k < k1; ++k) {
-      const uint16_t* v = static_cast<const uint16_t*>(a.v) + (int64_t)(x.w.k0 + k) * a.vt + x.kvh * a.vh + col;
+      const uint16_t* v = static_cast<const uint16_t*>(a.v) + (int64_t)(x.k0 + k) * a.vt + x.kvh * a.vh + col;
 #pragma unroll
       for (int c = 0; c < 32; ++c)
         if (col + c < a.d) {
@@ -105,68 +130,122 @@ __device__ __noinline__ void give_back(const PromptArgs& a, const Work& x, int l
   }
 }
 
+// How a launch deals out its work.
+struct FwdShape {
+  int32_t tiles;  // of a CTA: 1 or 2
+  int32_t split;  // CTAs that share an item's keys: a cluster
+};
+
+// Item `id`, by a warp; n0 < 0 where the slot has none. Later slots first: a sequence's
+// last tiles see the most keys.
+__device__ __forceinline__ Item item_of(const PromptArgs& a, const FwdShape& shape, uint32_t id, uint32_t ids, int part,
+                                        int lane) {
+  Item x;
+  const int tp = 128 / a.group, b = shape.tiles * tp;
+  id = ids - 1 - id;
+  const int64_t slot = id / a.kv;
+  x.kvh = (int)(id - slot * a.kv);
+  const int s = seq_of_slot(a.cu_q, a.nseq, b, slot, lane);
+  const Span w = span_of(a, s);
+  const int64_t local = slot - first_slot(a.cu_q, s, b);
+  x.q0 = w.q0;
+  x.nq = w.nq;
+  x.k0 = w.k0;
+  x.off = w.nk - w.nq;
+  x.n0 = -1;
+  x.n1 = 0;
+  if (local < 0 || local * b >= w.nq) return x;
+  x.t0 = (int)local * b;
+  x.last = min(x.t0 + b, w.nq) - 1;
+  x.kb0 = (a.window ? (int)max((int64_t)0, (int64_t)x.off + x.t0 + 1 - a.window) : 0) / 128;
+  auto blocks = [&](int ta) {
+    const int tb = min(ta + tp - 1, x.last), end = x.off + tb + 1;
+    return tb >= ta && end > 0 ? (end + 127) / 128 - x.kb0 : 0;
+  };
+  x.n0 = blocks(x.t0);
+  x.n1 = blocks(x.t0 + tp);
+  x.step = 1;
+  if (shape.split > 1) {
+    const int per = (x.n0 + shape.split - 1) / shape.split;
+    x.kb0 += part * per;
+    x.n0 = max(0, min(per, x.n0 - part * per));
+  }
+  if (x.t0 + tp > x.last && x.n0 > 1) {
+    x.step = 2;
+    x.n1 = x.n0;
+  }
+  return x;
+}
+
+// 32 columns of a row of a result.
+template <class C>
+__device__ __forceinline__ void put_columns(const PromptArgs& a, int64_t row, int k, const float* o) {
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = pack16<C::HALF>(o[2 * i], o[2 * i + 1]);
+  auto put = [&](void* to) {
+    uint16_t* p = static_cast<uint16_t*>(to) + row * a.d + k;
+    if (a.d % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (k + 16 * i < a.d) st_sector(p + 16 * i, w + 8 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k + 8 * i < a.d)
+          *reinterpret_cast<uint4*>(p + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  };
+  put(a.out);
+  if (a.rest) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      w[i] = pack16<C::HALF>(o[2 * i] - value16<C::HALF>((uint16_t)w[i]), o[2 * i + 1] - value16<C::HALF>((uint16_t)(w[i] >> 16)));
+    put(a.rest);
+  }
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
-    prompt_fwd_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap mq,
+    prompt_fwd_kernel(const __grid_constant__ PromptArgs a, const FwdShape shape, const __grid_constant__ CUtensorMap mq,
                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   grid_dependency_wait();
   allow_dependent_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (a.fill & CSA_FILL_OUT) {
-    const int64_t words = (int64_t)a.heads * a.d / 8;
-    fill_rest(a.cu_q, a.nseq, a.num_q, words, static_cast<uint4*>(a.out));
-    if (a.rest) fill_rest(a.cu_q, a.nseq, a.num_q, words, static_cast<uint4*>(a.rest));
-  }
-  if (a.fill & CSA_FILL_LSE) fill_rest(a.cu_q, a.nseq, a.num_q, a.heads, -INFINITY, a.lse);
-
-  // later slots first: a sequence's last tiles see the most keys
-  Work x;
-  const uint32_t id = gridDim.x - 1 - blockIdx.x;
-  const int64_t slot = id / a.kv;
-  x.kvh = (int)(id - slot * a.kv);
-  x.tp = 128 / a.group;
-  x.rows = x.tp * a.group;
-  const int s = seq_of_slot(a.cu_q, a.nseq, 2 * x.tp, slot, lane);
-  x.w = span_of(a, s);
-  const int64_t local = slot - first_slot(a.cu_q, s, 2 * x.tp);
-  if (local < 0 || local * 2 * x.tp >= x.w.nq) return;
-  x.t0 = (int)local * 2 * x.tp;
-  x.last = min(x.t0 + 2 * x.tp, x.w.nq) - 1;
-  x.off = x.w.nk - x.w.nq;
-  {
-    const int first = a.window ? (int)max((int64_t)0, (int64_t)x.off + x.t0 + 1 - a.window) : 0;
-    x.kb0 = first / 128;
-    for (int t = 0; t < 2; ++t) {
-      const int ta = x.t0 + t * x.tp, tb = min(ta + x.tp, x.w.nq) - 1, end = x.off + tb + 1;
-      x.n[t] = tb >= ta && end > 0 ? (end + 127) / 128 - x.kb0 : 0;
-    }
-    x.step = 1;
-    if (x.t0 + x.tp >= x.w.nq && x.n[0] > 1) {
-      x.step = 2;
-      x.n[1] = x.n[0];
-    }
-  }
-  const int n = max(x.n[0], x.n[1]);
-
   uint8_t* const base = fwd_smem + ((1024u - (smem_at(fwd_smem) & 1023u)) & 1023u);
   auto& st = *reinterpret_cast<State<C::NS>*>(base);
-  uint8_t* const q_ptr = base + 1024;
+  static_assert(sizeof(State<C::NS>) <= C::HEAD, "HEAD");
+  uint8_t* const q_ptr = base + C::HEAD;
   uint8_t* const ring_ptr = q_ptr + 2 * C::TILE;
   const uint32_t q_at = smem_at(q_ptr), ring = smem_at(ring_ptr);
   const uint32_t full = smem_at(st.full), empty = smem_at(st.empty), q_full = smem_at(&st.q_full),
-                 s_full = smem_at(st.s_full), p_full = smem_at(st.p_full), o_full = smem_at(st.o_full);
+                 q_empty = smem_at(&st.q_empty), s_full = smem_at(st.s_full), p_full = smem_at(st.p_full),
+                 o_full = smem_at(st.o_full), item_full = smem_at(st.item_full), item_empty = smem_at(st.item_empty),
+                 steal = smem_at(&st.steal), pair_full = smem_at(&st.pair_full), pair_empty = smem_at(&st.pair_empty);
   volatile int32_t* const dead = &st.dead;
+  const int tp = 128 / a.group, rows = tp * a.group;
+  const uint32_t ids = gridDim.x / shape.split, first_id = blockIdx.x / shape.split;
+  const int part = (int)(blockIdx.x - first_id * shape.split);  // of the item, in a cluster
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
+#pragma unroll 1
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
     }
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(steal, 1);
+    mbar_init(pair_full, 4);
+    mbar_init(pair_empty, 4);
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full + 8 * t, 1);
-      mbar_init(p_full + 8 * t, 4);
+      mbar_init(p_full + 16 * t, 4);
+      mbar_init(p_full + 16 * t + 8, 4);
       mbar_init(o_full + 8 * t, 1);
+      mbar_init(item_full + 8 * t, 1);
+      mbar_init(item_empty + 8 * t, 10);  // eight softmax warps, copies, matrix instructions
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -179,95 +258,235 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&st.tmem;
 
+  // The k-th item, for a whole warp; its slot may be filled again after that.
+  auto take = [&](int k) -> Item {
+    mbar_wait(item_full + 8 * (k & 1), (k >> 1) & 1, dead);
+    Item x = st.item[k & 1];
+    if (*dead) x.n0 = -1;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_empty + 8 * (k & 1));
+    return x;
+  };
+
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
-    if (warp == 9) {  // ---- copies
-      if (lane == 0 && n > 0) {
+    if (warp == 10) {  // ---- work
+      uint32_t id = first_id;
+      int k = 0;
+#pragma unroll 1
+      for (int stolen = 0;; ++stolen) {
+        if (part == 0) {  // this item's share of the rows of no sequence
+          if (a.fill & CSA_FILL_OUT) {
+            const int64_t words = (int64_t)a.heads * a.d / 8;
+            fill_rest(a.cu_q, a.nseq, a.num_q, words, static_cast<uint4*>(a.out), id * 32 + lane, (int64_t)ids * 32);
+            if (a.rest) fill_rest(a.cu_q, a.nseq, a.num_q, words, static_cast<uint4*>(a.rest), id * 32 + lane, (int64_t)ids * 32);
+          }
+          if (a.fill & CSA_FILL_LSE) fill_rest(a.cu_q, a.nseq, a.num_q, a.heads, -INFINITY, a.lse, id * 32 + lane, (int64_t)ids * 32);
+        }
+        const Item x = item_of(a, shape, id, ids, part, lane);
+        if (x.n0 >= 0) {
+          mbar_wait(item_empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
+          if (lane == 0) {
+            st.item[k & 1] = x;
+            mbar_arrive(item_full + 8 * (k & 1));
+          }
+          ++k;
+        }
+        if (shape.split > 1 || *dead) break;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_expect(steal, 16);
+          asm volatile(
+              "fence.proxy.async.shared::cta;\n\t"
+              "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                  smem_at(st.stolen)),
+              "r"(steal)
+              : "memory");
+        }
+        mbar_wait(steal, stolen & 1, dead);
+        uint32_t got, next;
+        asm volatile(
+            "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+            : "=r"(got), "=r"(next)
+            : "r"(smem_at(st.stolen))
+            : "memory");
+        if (!got || *dead) break;
+        id = next;
+      }
+      mbar_wait(item_empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
+      if (lane == 0) {
+        st.item[k & 1].n0 = -1;
+        mbar_arrive(item_full + 8 * (k & 1));
+      }
+    } else if (warp == 9) {  // ---- copies
+      Place<C::NS> at = {0, 0};
+      uint32_t loaded = 0;  // items with keys
+      int copies = 0;
+      if (lane == 0) {
         tma_prefetch(&mq);
         tma_prefetch(&mk);
         tma_prefetch(&mv);
-        const int tiles = x.step == 1 && x.n[1] > 0 ? 2 : 1;
-        mbar_expect(q_full, tiles * (C::DP / 64) * 128 * x.rows);
-        for (int t = 0; t < tiles; ++t)
-          for (int p = 0; p < C::DP / 64; ++p)
-            tma_load(q_at + t * C::TILE + p * C::SLAB, &mq, p * 64, x.kvh * a.group, x.w.q0 + x.t0 + t * x.tp, q_full);
-        for (int i = 0; i < 2 * n; ++i) {
-          bool value;
-          int b;
-          if (x.step == 1) {
-            value = i & 1;
-            b = i / 2;
-          } else {  // K0 K1 V0 K2 V1 ...
-            value = i == 2 * n - 1 || (i > 1 && (i & 1) == 0);
-            b = i == 2 * n - 1 ? n - 1 : value ? i / 2 - 1 : (i + 1) / 2;
-          }
-          const uint32_t stage = i % C::NS;
-          mbar_wait(empty + 8 * stage, ((i / C::NS) & 1) ^ 1, dead);
-          if (*dead) {
-            // copies under way land before the CTA ends
-            for (int j = max(0, i - C::NS); j < i; ++j)
-              for (int k = 0; k < kPolls && !mbar_try(full + 8 * (j % C::NS), (j / C::NS) & 1); ++k) {
-              }
-            for (int k = 0; k < kPolls && !mbar_try(q_full, 0); ++k) {
+      }
+#pragma unroll 1
+      for (int k = 0;; ++k) {
+        const Item x = take(k);
+        if (x.n0 < 0) break;
+        const int n = max(x.n0, x.n1);
+        if (n == 0) continue;
+        if (lane == 0) {
+          const int tiles = x.step == 1 && x.n1 > 0 ? 2 : 1;
+          mbar_wait(q_empty, (loaded & 1) ^ 1, dead);
+          mbar_expect(q_full, tiles * (C::DP / 64) * 128 * rows);
+#pragma unroll 1
+          for (int t = 0; t < tiles; ++t)
+#pragma unroll 1
+            for (int p = 0; p < C::DP / 64; ++p)
+              tma_load(q_at + t * C::TILE + p * C::SLAB, &mq, p * 64, x.kvh * a.group, x.q0 + x.t0 + t * tp, q_full);
+#pragma unroll 1
+          for (int i = 0; i < 2 * n && !*dead; ++i) {
+            bool value;
+            int b;
+            if (x.step == 1) {
+              value = i & 1;
+              b = i / 2;
+            } else {  // K0 K1 V0 K2 V1 ...
+              value = i == 2 * n - 1 || (i > 1 && (i & 1) == 0);
+              b = i == 2 * n - 1 ? n - 1 : value ? i / 2 - 1 : (i + 1) / 2;
             }
-            break;
+            mbar_wait(empty + 8 * at.stage, at.parity ^ 1, dead);
+            mbar_expect(full + 8 * at.stage, C::TILE);
+#pragma unroll 1
+            for (int p = 0; p < C::DP / 64; ++p)
+              tma_load(ring + at.stage * C::TILE + p * C::SLAB, value ? &mv : &mk, p * 64, x.kvh, x.k0 + (x.kb0 + b) * 128,
+                       full + 8 * at.stage);
+            ++copies;
+            at.next(1);
           }
-          mbar_expect(full + 8 * stage, C::TILE);
-          for (int p = 0; p < C::DP / 64; ++p)
-            tma_load(ring + stage * C::TILE + p * C::SLAB, value ? &mv : &mk, p * 64, x.kvh, x.w.k0 + (x.kb0 + b) * 128,
-                     full + 8 * stage);
+          if (*dead) {  // copies under way land before the CTA ends
+#pragma unroll 1
+            for (int j = max(0, copies - C::NS); j < copies; ++j)
+#pragma unroll 1
+              for (int i = 0; i < kPolls && !mbar_try(full + 8 * (j % C::NS), (j / C::NS) & 1); ++i) {
+              }
+#pragma unroll 1
+            for (int i = 0; i < kPolls && !mbar_try(q_full, loaded & 1); ++i) {
+            }
+          }
         }
+        __syncwarp();
+        ++loaded;
       }
     } else if (warp == 8) {  // ---- matrix instructions
-      if (n > 0) {
-        mbar_wait(q_full, 0, dead);
-        auto ready = [&](int i) { mbar_wait(full + 8 * (i % C::NS), (i / C::NS) & 1, dead); };
-        auto scores = [&](int t, int b) {  // S of tile t and block b
-          const uint64_t q = operand(q_at + (x.step == 1 ? t : 0) * C::TILE, 16);
-          const uint64_t k = operand(ring + (keys_at(b, x.step) % C::NS) * C::TILE, 16);
-  #pragma unroll
-          for (int j = 0; j < C::DP / 16; ++j) {
-            const int at = ((j >> 2) * C::SLAB + (j & 3) * 32) / 16;
-            tc_mma(tmem + C::S0 + 128 * t, q + at, k + at, C::IDESC_S, j > 0);
-          }
-          tc_commit(s_full + 8 * t);
+      // Issuing them is a warp's whole work: what it counts stays in registers, with no
+      // divisions and no waits that are known to have passed (a tile 1900 -> 1100 cycles).
+      const uint32_t leader = tc_leader(), tm = uniform(tmem);
+      const uint64_t q_op = operand(q_at, 16), k_op = operand(ring, 16), v_op = operand(ring, C::SLAB);
+      Place<C::NS> start = {0, 0};
+      uint32_t loaded = 0, copies = 0, rounds[2] = {0, 0};
+#pragma unroll 1
+      for (int k = 0;; ++k) {
+        const Item x = take(k);
+        const int n0 = (int)uniform((uint32_t)x.n0), n1 = (int)uniform((uint32_t)x.n1), step = (int)uniform((uint32_t)x.step);
+        if (n0 < 0) break;
+        const int n = max(n0, n1);
+        if (n == 0) continue;
+        mbar_wait(q_full, loaded & 1, dead);
+        ++loaded;
+        // keys and values of the next block to come, of either tile
+        Place<C::NS> key = start, value = start;
+        value.next(step);
+        auto scores = [&](int t, int at) {  // S of tile t and the keys at a place of the ring
+          const uint64_t q = q_op + (step == 1 ? t : 0) * (C::TILE / 16), kk = k_op + at * (C::TILE / 16);
+#pragma unroll
+          for (int p = 0; p < C::DP / 64; ++p)
+            tc_mma4<2>(leader, tm + C::S0 + 128 * t, q + p * (C::SLAB / 16), kk + p * (C::SLAB / 16), C::IDESC_S, p > 0);
+          tc_commit_by(leader, s_full + 8 * t);
         };
-        for (int t = 0; t < 2; ++t) {
-          const int b = x.step == 1 ? 0 : t;
-          if (x.n[t] == 0) continue;
-          if (t == 0 || x.step == 2 || x.n[0] == 0) ready(keys_at(b, x.step));
+        auto ready = [&](const Place<C::NS>& p) {
+          mbar_wait(full + 8 * p.stage, p.parity, dead);
           tc_after();
-          __syncwarp();
-          scores(t, b);
-          if (x.step == 2 || t == 1 || x.n[1] == 0) tc_commit(empty + 8 * (keys_at(b, x.step) % C::NS));
-        }
-        const int rounds = x.step == 1 ? n : (n + 1) / 2;
-        for (int r = 0; r < rounds; ++r)
-          for (int t = 0; t < 2; ++t) {
-            const int b = x.step == 1 ? r : 2 * r + t, next = b + x.step;
-            if (b >= x.n[t]) continue;
-            // step 1: tile 1 is the last to use a block, unless it has fewer (no rows)
-            const bool done = x.step == 2 || t == 1 || b >= x.n[1], done_next = x.step == 2 || t == 1 || next >= x.n[1];
-            const int vi = values_at(b, n, x.step);
-            ready(vi);
-            mbar_wait(p_full + 8 * t, r & 1, dead);
+        };
+        auto weigh = [&](int t, int at, bool first) {  // O of tile t += its weights and the values at a place
+          const uint64_t v = v_op + at * (C::TILE / 16);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            mbar_wait(p_full + 16 * t + 8 * h, rounds[t] & 1, dead);
             tc_after();
-            __syncwarp();
-            const uint64_t v = operand(ring + (vi % C::NS) * C::TILE, C::SLAB);
-  #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              tc_mma_ts(tmem + C::O0 + C::DP * t, tmem + C::S0 + 128 * t + 8 * j, v + j * 128, C::IDESC_O, r > 0 || j > 0);
-            if (done) tc_commit(empty + 8 * (vi % C::NS));
-            if (next < x.n[t]) {
-              ready(keys_at(next, x.step));
-              tc_after();
-              __syncwarp();
-              scores(t, next);
-              if (done_next) tc_commit(empty + 8 * (keys_at(next, x.step) % C::NS));
+            tc_mma4_ts<128>(leader, tm + C::O0 + C::DP * t, tm + C::S0 + 128 * t + 32 * h, v + 512 * h, C::IDESC_O, !first || h > 0);
+          }
+          ++rounds[t];
+        };
+        ready(key);
+        if (step == 1) {
+          if (n0 > 0) scores(0, key.stage);
+          if (n1 > 0) scores(1, key.stage);
+          tc_commit_by(leader, empty + 8 * key.stage);
+          if (n == 1) tc_commit_by(leader, q_empty);
+          key.next(2);
+#pragma unroll 1
+          for (int b = 0; b < n; ++b) {
+            ready(value);
+            const bool more = b + 1 < n;
+            if (b < n0) {
+              weigh(0, value.stage, b == 0);
+              if (b + 1 < n0) {
+                ready(key);
+                scores(0, key.stage);
+              } else {
+                tc_commit_by(leader, o_full);
+              }
+            }
+            if (b < n1) {
+              weigh(1, value.stage, b == 0);
+              tc_commit_by(leader, empty + 8 * value.stage);
+              if (b + 1 < n1) {
+                if (b + 1 >= n0) ready(key);
+                scores(1, key.stage);
+              } else {
+                tc_commit_by(leader, o_full + 8);
+              }
             } else {
-              tc_commit(o_full + 8 * t);
+              tc_commit_by(leader, empty + 8 * value.stage);
+            }
+            if (more) tc_commit_by(leader, empty + 8 * key.stage);
+            if (b + 2 == n) tc_commit_by(leader, q_empty);
+            key.next(2);
+            value.next(2);
+          }
+        } else {  // n >= 2: tile 0 has the even blocks, 1 the odd ones
+          scores(0, key.stage);
+          tc_commit_by(leader, empty + 8 * key.stage);
+          key.next(1);
+          ready(key);
+          scores(1, key.stage);
+          tc_commit_by(leader, empty + 8 * key.stage);
+          if (n == 2) tc_commit_by(leader, q_empty);
+          key.next(2);
+#pragma unroll 1
+          for (int b = 0; b < n; b += 2) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (b + t >= n) break;
+              ready(value);
+              weigh(t, value.stage, b == 0);
+              tc_commit_by(leader, empty + 8 * value.stage);
+              value.next(b + t + 2 == n ? 1 : 2);
+              if (b + t + 2 < n) {
+                ready(key);
+                scores(t, key.stage);
+                tc_commit_by(leader, empty + 8 * key.stage);
+                if (b + t + 3 == n) tc_commit_by(leader, q_empty);
+                key.next(2);
+              } else {
+                tc_commit_by(leader, o_full + 8 * t);
+              }
             }
           }
+        }
+        copies += 2 * n;
+        start = {(int)(copies % C::NS), (copies / C::NS) & 1};
       }
     }
   } else {  // ---- softmax and result: a row a thread
@@ -275,182 +494,248 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int t = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + C::S0 + 128 * t, o_at = tmem + lanes + C::O0 + C::DP * t;
-    const int tile = x.step == 1 ? t : 0;
-    const int ta = x.t0 + tile * x.tp, tb = min(ta + x.tp, x.w.nq) - 1;
-    const int token = ta + r / a.group;
-    const bool there = r < x.rows && token < x.w.nq;
-    const int hi = there ? x.off + token + 1 : 0;
-    const int lo = a.window ? (int)max((int64_t)0, (int64_t)x.off + token + 1 - a.window) : 0;
     const float c = a.scale * kLog2e;
-    float ref = -INFINITY;  // in log2 units
-    float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
-    int round = 0;
-    for (int b = x.step == 1 ? 0 : t; b < x.n[t]; b += x.step, ++round) {
-      mbar_wait(s_full + 8 * t, round & 1, dead);
+    const int in_tile = r / a.group, head = r - in_tile * a.group;
+    uint32_t rounds = 0, results = 0, copies = 0, pairs = 0;
+#pragma unroll 1
+    for (int k = 0;; ++k) {
+      const Item x = take(k);
+      if (x.n0 < 0) break;
+      const int n = max(x.n0, x.n1), mine = t ? x.n1 : x.n0;
+      const int ta = x.t0 + (x.step == 1 ? t * tp : 0), tb = min(ta + tp - 1, x.last);
+      const int token = ta + in_tile;
+      const bool there = r < rows && token <= tb;
+      const int hi = there ? x.off + token + 1 : 0;
+      const int lo = a.window ? (int)max((int64_t)0, (int64_t)x.off + token + 1 - a.window) : 0;
+      float ref = -INFINITY;  // in log2 units
+      float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
+#pragma unroll 1
+      for (int b = x.step == 1 ? 0 : t; b < mine; b += x.step) {
+        if (mixed(a, x, b, x.t0, x.last)) {
+          const uint32_t at = copies + values_at(b, n, x.step);
+          mbar_wait(full + 8 * (at % C::NS), (at / C::NS) & 1, dead);
+          clean_operand<C::HALF>(ring_ptr + (at % C::NS) * C::TILE, C::TILE, r, 128, &st.bad);
+        }
+        mbar_wait(s_full + 8 * t, rounds & 1, dead);
+        ++rounds;
+        tc_after();
+        float v[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc_load32_async(s_at + 32 * i, v + 32 * i);
+        tc_load_wait();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc_loaded(v + 32 * i);
+        if (mixed(a, x, b, ta, tb)) {
+          const int k0 = (x.kb0 + b) * 128;
+          const int h = hi - k0, w = lo - k0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) v[i] = i < h && i >= w ? v[i] : -INFINITY;
+        }
+        float m0 = fmaxf(v[0], v[1]), m1 = fmaxf(v[2], v[3]);
+#pragma unroll
+        for (int i = 4; i < 128; i += 4) {
+          m0 = fmaxf(m0, fmaxf(v[i], v[i + 1]));
+          m1 = fmaxf(m1, fmaxf(v[i + 2], v[i + 3]));
+        }
+        const float z = fmaxf(m0, m1) * c;
+        const bool raise = z > ref + 8.0f;
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+          const float f = raise ? ex2_approx_ftz(ref - z) : 1.0f;
+          if (raise) ref = z;
+          l0.x *= f;
+          l0.y *= f;
+          l1.x *= f;
+          l1.y *= f;
+          if (b >= x.step) {  // the products before are done: S of this block came after them
+#pragma unroll 1
+            for (int i = 0; i < C::DP; i += 32) {
+              float o[32];
+              tc_load32(o_at + i, o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] *= f;
+              tc_store32(o_at + i, o);
+            }
+          }
+        }
+        const float back = C::LIFT - (ref == -INFINITY ? 0.0f : ref);
+#pragma unroll
+        for (int i = 0; i < 128; i += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float2 za = fma2_rn(make_float2(v[i + j], v[i + j + 1]), make_float2(c, c), make_float2(back, back));
+            const float2 zb = fma2_rn(make_float2(v[i + j + 2], v[i + j + 3]), make_float2(c, c), make_float2(back, back));
+            const float2 pa = make_float2(ex2_approx_ftz(za.x), ex2_approx_ftz(za.y));
+            const float2 pb = make_float2(ex2_approx_ftz(zb.x), ex2_approx_ftz(zb.y));
+            l0 = add2_rn(l0, pa);
+            l1 = add2_rn(l1, pb);
+            p[j / 2] = pack16<C::HALF>(pa.x, pa.y);
+            p[j / 2 + 1] = pack16<C::HALF>(pb.x, pb.y);
+          }
+          tc_store16_async(s_at + i / 2, p);
+          if (i & 32) {  // 64 weights: their products begin
+            tc_store_wait();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * (i / 64));
+          }
+        }
+      }
+      copies += 2 * n;
+      float l = (l0.x + l0.y) + (l1.x + l1.y);
+      if (mine > 0) mbar_wait(o_full + 8 * t, results++ & 1, dead);
       tc_after();
-      if (mixed(a, x, b, x.t0, x.last)) {
-        const int vi = values_at(b, n, x.step);
-        mbar_wait(full + 8 * (vi % C::NS), (vi / C::NS) & 1, dead);
-        clean_operand<C::HALF>(ring_ptr + (vi % C::NS) * C::TILE, C::TILE, r, 128, &st.bad);
-      }
-      float v[128];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tc_load32_async(s_at + 32 * k, v + 32 * k);
-      tc_load_wait();
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tc_loaded(v + 32 * k);
-      if (mixed(a, x, b, ta, tb)) {
-        const int k0 = (x.kb0 + b) * 128;
-        const int h = hi - k0, w = lo - k0;
-#pragma unroll
-        for (int k = 0; k < 128; ++k) v[k] = k < h && k >= w ? v[k] : -INFINITY;
-      }
-      float m0 = fmaxf(v[0], v[1]), m1 = fmaxf(v[2], v[3]);
-#pragma unroll
-      for (int k = 4; k < 128; k += 4) {
-        m0 = fmaxf(m0, fmaxf(v[k], v[k + 1]));
-        m1 = fmaxf(m1, fmaxf(v[k + 2], v[k + 3]));
-      }
-      const float z = fmaxf(m0, m1) * c;
-      const bool raise = z > ref + 8.0f;
-      if (__any_sync(0xFFFFFFFFu, raise)) {
-        const float f = raise ? ex2_approx_ftz(ref - z) : 1.0f;
-        if (raise) ref = z;
-        l0.x *= f;
-        l0.y *= f;
-        l1.x *= f;
-        l1.y *= f;
-        if (round > 0) {  // the products before are done: S of this block came after them
-#pragma unroll 1
-          for (int k = 0; k < C::DP; k += 32) {
-            float o[32];
-            tc_load32(o_at + k, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f;
-            tc_store32(o_at + k, o);
-          }
+      // O = fa O of tile 0 + fb O of tile 1, where both groups have worked on the same rows
+      float fa = 1.0f, fb = 0.0f;
+      if (x.step == 2) {
+        if (t == 1) {
+          st.ref[r] = ref;
+          st.sum[r] = l;
+        }
+        if (t == 1) {
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pair_full);
+        } else {
+          mbar_wait(pair_full, pairs & 1, dead);
+          tc_after();
+          const float other = st.ref[r], top = fmaxf(ref, other), safe = top == -INFINITY ? 0.0f : top;
+          fa = ex2_approx_ftz(ref - safe);
+          fb = ex2_approx_ftz(other - safe);
+          l = l * fa + st.sum[r] * fb;
+          ref = top;
         }
       }
-      const float back = C::LIFT - (ref == -INFINITY ? 0.0f : ref);
-#pragma unroll
-      for (int k = 0; k < 128; k += 32) {
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float2 za = fma2_rn(make_float2(v[k + i], v[k + i + 1]), make_float2(c, c), make_float2(back, back));
-          const float2 zb = fma2_rn(make_float2(v[k + i + 2], v[k + i + 3]), make_float2(c, c), make_float2(back, back));
-          const float2 pa = make_float2(ex2_approx_ftz(za.x), ex2_approx_ftz(za.y));
-          const float2 pb = make_float2(ex2_approx_ftz(zb.x), ex2_approx_ftz(zb.y));
-          l0 = add2_rn(l0, pa);
-          l1 = add2_rn(l1, pb);
-          p[i / 2] = pack16<C::HALF>(pa.x, pa.y);
-          p[i / 2 + 1] = pack16<C::HALF>(pb.x, pb.y);
+      if (t == 0 || (x.step == 1 && shape.split == 1)) {
+        const bool some = !(l == 0.0f);
+        const bool whole = shape.split == 1;
+        const float f = *dead ? NAN : !whole ? 1.0f : some ? 1.0f / l : 0.0f;
+        fa *= f;
+        fb *= f;
+        const int64_t row = (int64_t)(x.q0 + token) * a.heads + x.kvh * a.group + head;
+        if (whole) {
+          if (there) a.lse[row] = *dead ? NAN : some ? (ref - C::LIFT + log2f(l)) * kLn2 : -INFINITY;
+        } else {
+          st.ref[r] = *dead ? NAN : ref;
+          st.sum[r] = l;
         }
-        tc_store16_async(s_at + k / 2, p);
-      }
-      tc_store_wait();
-      tc_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + 8 * t);
-    }
-    float l = (l0.x + l0.y) + (l1.x + l1.y);
-    if (round > 0) mbar_wait(o_full + 8 * t, 0, dead);
-    tc_after();
-    float f = 1.0f;  // O's factor
-    if (x.step == 2) {
-      // group 1's reference, sum and O by way of the ring, whose operands have all been
-      // used; columns apart by 128 rows
-      float* const share = reinterpret_cast<float*>(ring_ptr);
-      barrier_of(1, 256);
-      if (t == 1) {
-        share[r] = ref;
-        share[128 + r] = l;
-        if (round > 0) {
+        const bool bad = *(volatile int32_t*)&st.bad != 0;
 #pragma unroll 1
-          for (int k = 0; k < C::DP; k += 32) {
-            float o[32];
-            tc_load32(o_at + k, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) share[256 + (k + i) * 128 + r] = o[i];
-          }
-        }
-      }
-      barrier_of(1, 256);
-      if (t == 0) {
-        const float other = share[r], top = fmaxf(ref, other), safe = top == -INFINITY ? 0.0f : top;
-        const float fa = ex2_approx_ftz(ref - safe), fb = ex2_approx_ftz(other - safe);
-        l = l * fa + share[128 + r] * fb;
-        ref = top;
-#pragma unroll 1
-        for (int k = 0; k < C::DP; k += 32) {
+        for (int i = 0; i < C::DP; i += 32) {
           float o[32];
-          tc_load32(o_at + k, o);
+          if (mine > 0) {
+            tc_load32(o_at + i, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = o[i] * fa + share[256 + (k + i) * 128 + r] * fb;
-          tc_store32(o_at + k, o);
-        }
-      }
-    }
-    if (x.step == 1 || t == 0) {
-      const bool some = !(l == 0.0f);
-      f = some ? 1.0f / l : 0.0f;
-      if (*dead) f = NAN;
-      const int64_t row = (int64_t)(x.w.q0 + token) * a.heads + x.kvh * a.group + r % a.group;
-      if (there) a.lse[row] = *dead ? NAN : some ? (ref - C::LIFT + log2f(l)) * kLn2 : -INFINITY;
-      const bool bad = *(volatile int32_t*)&st.bad != 0;
-#pragma unroll 1
-      for (int k = 0; k < C::DP; k += 32) {
-        float o[32];
-        if (round > 0) tc_load32(o_at + k, o);
-        if (!there || k >= a.d) continue;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = some || *dead ? o[i] * f : 0.0f;
-        if (round == 0) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = *dead ? NAN : 0.0f;
-        }
-        if (bad) {
-          float again[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) again[i] = o[i];
-          give_back<C::HALF>(a, x, lo, hi, k, again);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = again[i];
-        }
-        uint32_t w[16], low[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          w[i] = pack16<C::HALF>(o[2 * i], o[2 * i + 1]);
-          low[i] = pack16<C::HALF>(o[2 * i] - value16<C::HALF>((uint16_t)w[i]), o[2 * i + 1] - value16<C::HALF>((uint16_t)(w[i] >> 16)));
-        }
-        auto put = [&](void* to, const uint32_t* v) {
-          uint16_t* p = static_cast<uint16_t*>(to) + row * a.d + k;
-          if (a.d % 16 == 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (k + 16 * i < a.d) st_sector(p + 16 * i, v + 8 * i);
+            for (int j = 0; j < 32; ++j) o[j] *= fa;
           } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (k + 8 * i < a.d)
-                *reinterpret_cast<uint4*>(p + 8 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int j = 0; j < 32; ++j) o[j] = *dead ? NAN : 0.0f;
           }
-        };
-        put(a.out, w);
-        if (a.rest) put(a.rest, low);
+          if (x.step == 2) {
+            float q[32];
+            tc_load32(o_at + C::DP + i, q);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = fmaf(q[j], fb, o[j]);
+          }
+          if (!some && !*dead) {  // no weight: 0, whatever O holds
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+          }
+          if (bad && there && i < a.d) {
+            float again[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) again[j] = o[j];
+            give_back<C::HALF>(a, x, lo, hi, i, again);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = again[j];
+          }
+          if (!whole) {  // for the cluster; every operand of the ring has been used
+            float* const share = reinterpret_cast<float*>(ring_ptr) + i * 128 + r;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) share[j * 128] = o[j];
+          } else if (there && i < a.d) {
+            put_columns<C>(a, row, i, o);
+          }
+        }
+      }
+      tc_before();
+      if (x.step == 2) {  // tile 1's O and sums have been read
+        if (t == 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pair_empty);
+        } else {
+          mbar_wait(pair_empty, pairs & 1, dead);
+        }
+        ++pairs;
       }
     }
-    tc_before();
   }
+  __syncwarp();
   __syncthreads();
   tc_after();
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (shape.split > 1) {
+    // Each CTA of the cluster joins its share of the columns: 32 at a time, a row a thread.
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const Item x = item_of(a, shape, first_id, ids, 0, lane);
+    if (x.n0 >= 0 && warp < 4) {
+      const int r = threadIdx.x, token = x.t0 + r / a.group;
+      const bool there = r < rows && token <= x.last;
+      const int64_t row = (int64_t)(x.q0 + token) * a.heads + x.kvh * a.group + r % a.group;
+      auto remote = [&](const void* p, int rank) {
+        uint32_t at;
+        float v;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_at(p)), "r"(rank));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at));
+        return v;
+      };
+      float top = -INFINITY, l = 0.0f;
+#pragma unroll 1
+      for (int z = 0; z < shape.split; ++z) {
+        const float ref = remote(&st.ref[r], z);
+        top = ref != ref || ref > top ? ref : top;  // NaN stays
+        if (top != top) break;
+      }
+      const float safe = top == -INFINITY ? 0.0f : top;
+#pragma unroll 1
+      for (int z = 0; z < shape.split; ++z) l += ex2_approx_ftz(remote(&st.ref[r], z) - safe) * remote(&st.sum[r], z);
+      const bool some = !(l == 0.0f);
+      const float f = some ? 1.0f / l : 0.0f;
+      if (part == 0 && there) a.lse[row] = some ? (top - C::LIFT + log2f(l)) * kLn2 : -INFINITY;
+#pragma unroll 1
+      for (int i = part * 32; i < a.d; i += shape.split * 32) {
+        float o[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+#pragma unroll 1
+        for (int z = 0; z < shape.split; ++z) {
+          const float fz = ex2_approx_ftz(remote(&st.ref[r], z) - safe) * f;
+          if (remote(&st.sum[r], z) == 0.0f) continue;
+          const float* share = reinterpret_cast<const float*>(ring_ptr) + i * 128 + r;
+#pragma unroll 8
+          for (int j = 0; j < 32; ++j) o[j] = fmaf(remote(share + j * 128, z), fz, o[j]);
+        }
+        if (there) put_columns<C>(a, row, i, o);
+      }
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
 }
 
 template <class C>
 cudaError_t launch_fwd_of(const PromptArgs& a, cudaStream_t stream) {
   const int tp = 128 / a.group;
-  const int64_t blocks = ((int64_t)a.num_q / (2 * tp) + a.nseq) * a.kv;
+  auto items = [&](int tiles) { return ((int64_t)a.num_q / (tiles * tp) + a.nseq) * a.kv; };
+  // One tile a CTA, on which both softmax groups work, where two would leave SMs without
+  // any; then, where there are SMs to spare and keys enough (four blocks a CTA), clusters.
+  FwdShape shape = {items(2) > 152 ? 2 : 1, 1};
+  if (shape.tiles == 1) {
+    int64_t keys = a.num_k / a.nseq;
+    if (a.window && keys > (int64_t)a.window + tp) keys = (int64_t)a.window + tp;
+    while (shape.split < 8 && items(1) * shape.split * 2 <= 152 && keys >= (int64_t)shape.split * 2 * 512) shape.split *= 2;
+  }
+  const int64_t blocks = items(shape.tiles) * shape.split;
   CUtensorMap mq, mk, mv;
   cudaError_t e = rows_map(&mq, a.q, C::HALF, a.d, a.heads, a.num_q, a.qt, a.qh, a.group, tp);
   if (e == cudaSuccess) e = rows_map(&mk, a.k, C::HALF, a.d, a.kv, a.num_k, a.kt, a.kh, 1, 128);
@@ -458,7 +743,10 @@ cudaError_t launch_fwd_of(const PromptArgs& a, cudaStream_t stream) {
   auto* kernel = prompt_fwd_kernel<C>;
   if (e == cudaSuccess) e = allow_dynamic_smem((const void*)kernel, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, dim3((unsigned)blocks), dim3(C::THREADS), C::SMEM, stream, a, mq, mk, mv);
+  if (shape.split > 1)
+    return launch_clusters(kernel, dim3((unsigned)blocks), dim3(C::THREADS), C::SMEM, (unsigned)shape.split, stream, a, shape, mq,
+                           mk, mv);
+  return launch_dependent(kernel, dim3((unsigned)blocks), dim3(C::THREADS), C::SMEM, stream, a, shape, mq, mk, mv);
 }
 
 }  // namespace

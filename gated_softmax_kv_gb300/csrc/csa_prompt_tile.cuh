@@ -39,20 +39,22 @@ __device__ __forceinline__ int seq_of_slot(const int32_t* cu, int nseq, int b, i
   return lo;
 }
 
-// Rows of no sequence: [0, cu[0]) and [cu[nseq], n), a thread's share of `words`
-// 16-byte vectors of zeros a row.
-__device__ __forceinline__ void fill_rest(const int32_t* cu, int nseq, int32_t n, int64_t words, uint4* to) {
+// Rows of no sequence: [0, cu[0]) and [cu[nseq], n), a thread's share (every `step`-th
+// from `from` on) of `words` 16-byte vectors of zeros a row.
+__device__ __forceinline__ void fill_rest(const int32_t* cu, int nseq, int32_t n, int64_t words, uint4* to, int64_t from,
+                                          int64_t step) {
   const int64_t a = min(max(__ldg(cu), 0), n), b = max((int64_t)min(max(__ldg(cu + nseq), 0), n), a);
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (a + n - b) * words;
-       i += (int64_t)gridDim.x * blockDim.x) {
+#pragma unroll 1
+  for (int64_t i = from; i < (a + n - b) * words; i += step) {
     const int64_t row = i / words;
     to[row < a ? i : i + (b - a) * words] = make_uint4(0, 0, 0, 0);
   }
 }
-__device__ __forceinline__ void fill_rest(const int32_t* cu, int nseq, int32_t n, int32_t heads, float v, float* to) {
+__device__ __forceinline__ void fill_rest(const int32_t* cu, int nseq, int32_t n, int32_t heads, float v, float* to,
+                                          int64_t from, int64_t step) {
   const int64_t a = min(max(__ldg(cu), 0), n), b = max((int64_t)min(max(__ldg(cu + nseq), 0), n), a);
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (a + n - b) * heads;
-       i += (int64_t)gridDim.x * blockDim.x)
+#pragma unroll 1
+  for (int64_t i = from; i < (a + n - b) * heads; i += step)
     to[i / heads < a ? i : i + (b - a) * heads] = v;
 }
 
@@ -77,6 +79,7 @@ __device__ __forceinline__ bool all_finite(uint4 v) {
 template <bool HALF>
 __device__ __noinline__ void clean_operand(uint8_t* at, int bytes, int thread, int threads, volatile int32_t* found) {
   bool any = false;
+#pragma unroll 1
   for (int i = thread * 16; i < bytes; i += threads * 16) {
     uint4* p = reinterpret_cast<uint4*>(at + i);
     const uint4 v = *p;

@@ -32,7 +32,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 // Bounded: after kPolls the CTA is marked dead and no further wait waits.
 __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int32_t* dead) {
-  if (mbar_try(bar, parity)) return;
+#pragma unroll 1
   for (int i = 0; i < kPolls; ++i) {
     if (mbar_try(bar, parity)) return;
     if (*dead) return;
@@ -114,15 +114,52 @@ __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// The same with a first operand in tensor memory: lanes
-// are rows, a column holds two 16-bit values.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+// The same for a warp that elects its lane once (tc_leader) and keeps it: an election
+// for each instruction made the issue, not the tensor core, the bound of the prompt
+// kernels (a tile of the keys kernel 3060 cycles, its products 2048).
+__device__ __forceinline__ uint32_t tc_leader() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void tc_commit_by(uint32_t leader, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
       : "memory");
 }
+// Four steps of 16 along the products' inner dimension, STEP (in units of 16 bytes) apart
+// in the operands of shared memory; together, so that their predicates and operands are
+// worked out once.
+#define CSA_MMA4(A_DECL, A_REG, A_NEXT, A_ARG, STEP)                                                         \
+  asm volatile(                                                                                               \
+      "{\n\t.reg .pred p, q, t;\n\t" A_DECL                                                                  \
+      ".reg .b64 b1, b2, b3;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"  \
+      "add.s64 b1, %2, %6;\n\tadd.s64 b2, b1, %6;\n\tadd.s64 b3, b2, %6;\n\t" A_NEXT                         \
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], " A_REG("%1") ", %2, %3, p;\n\t"                          \
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], " A_REG("a1") ", b1, %3, t;\n\t"                          \
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], " A_REG("a2") ", b2, %3, t;\n\t"                          \
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], " A_REG("a3") ", b3, %3, t;\n\t}" ::"r"(d),               \
+      A_ARG(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader), "n"(STEP)                                \
+      : "memory")
+#define CSA_SMEM_A(x) x
+#define CSA_TMEM_A(x) "[" x "]"
+template <int STEP>
+__device__ __forceinline__ void tc_mma4(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  CSA_MMA4(".reg .b64 a1, a2, a3;\n\t", CSA_SMEM_A, "add.s64 a1, %1, %6;\n\tadd.s64 a2, a1, %6;\n\tadd.s64 a3, a2, %6;\n\t",
+           "l", STEP);
+}
+// With a first operand in tensor memory: lanes are rows, a column holds two 16-bit
+// values, a step has eight.
+template <int STEP>
+__device__ __forceinline__ void tc_mma4_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  CSA_MMA4(".reg .b32 a1, a2, a3;\n\t", CSA_TMEM_A, "add.s32 a1, %1, 8;\n\tadd.s32 a2, a1, 8;\n\tadd.s32 a3, a2, 8;\n\t", "r",
+           STEP);
+}
+#undef CSA_MMA4
+#undef CSA_SMEM_A
+#undef CSA_TMEM_A
 // 32 columns of a warp's 32 lanes, without waiting; tc_loaded(v) must follow
 // tc_load_wait() before v is used (it ties the values to the wait).
 #define CSA_R32(r)                                                                                               \
