@@ -223,10 +223,8 @@ __device__ __forceinline__ void store_columns(void* to, int64_t at, int d, int c
 }
 
 // Copies under way land before a CTA that gave up ends: the last `stages` of a ring.
-__device__ __forceinline__ void drain(uint32_t full, int stages, int issued) {
-#pragma unroll 1
-  for (int j = max(0, issued - stages); j < issued; ++j)
-#pragma unroll 1
+__device__ __forceinline__ void drain(uint32_t full, int stages, uint32_t issued) {
+  for (uint32_t j = issued > (uint32_t)stages ? issued - stages : 0; j < issued; ++j)
     for (int k = 0; k < kPolls && !mbar_try(full + 8 * (j % stages), (j / stages) & 1); ++k) {
     }
 }
@@ -239,35 +237,38 @@ __device__ __forceinline__ void load_tile(uint32_t to, const CUtensorMap* map, i
 
 // ---- dK and dV ----------------------------------------------------------------
 
+struct alignas(16) KeysItem {
+  Span w;
+  int32_t k0, kvh, off;  // first key within the sequence; key head; key index of query 0
+  int32_t t0, tp, n0;    // first query token, tokens of a tile, tiles
+  int32_t pad[2];
+  __device__ __forceinline__ bool keys() const { return n0 > 0; }
+};
+
 struct KeysState {
   alignas(16) float lse[2][128];    // of a tile's rows: -(lse log2 e - lift)
   alignas(16) float delta[2][128];  // -delta, times 2^-x for fp16
   alignas(16) int32_t lo[2][128];   // keys that they see
   alignas(16) int32_t hi[2][128];
-  uint64_t kv_full, q_full[2], q_empty[2], g_full[2], g_empty[2], r_full[2], s_full, p_full[2], dp_full, ds_full[2], done;
+  KeysItem item[2];
+  WorkState work;
+  uint64_t kv_full, kv_empty, q_full[2], q_empty[2], g_full[2], g_empty[2], r_full[2], s_full, p_full[2], dp_full, ds_full[2], done;
   int32_t dead, bad;
   uint32_t tmem;
 };
 static_assert(sizeof(KeysState) <= 8192, "HEAD");
 
-struct KeysWork {
-  Span w;
-  int32_t k0, kvh, off;    // first key of the CTA within the sequence
-  int32_t t0, tp, rows, n; // first query token, tokens and rows of a tile, tiles
-  int32_t t1;              // behind the last query token
-};
-
 // Whether some row of tile j does not see some key of the CTA, or is not there.
-__device__ __forceinline__ bool keys_mixed(const PromptArgs& a, const KeysWork& x, int j) {
+__device__ __forceinline__ bool keys_mixed(const PromptArgs& a, const KeysItem& x, int j) {
   const int64_t ta = (int64_t)x.t0 + (int64_t)j * x.tp, tb = ta + x.tp - 1;
   return x.k0 + 128 > x.off + ta + 1 || tb >= x.w.nq || (a.window && x.k0 < x.off + tb + 1 - a.window);
 }
 
 // Infinities and NaN of grad that were cleaned away, for 32 columns of a key's dv.
 template <bool HALF>
-__device__ __noinline__ void give_back_grad(const PromptArgs& a, const KeysWork& x, int key, int col, float* o) {
+__device__ __noinline__ void give_back_grad(const PromptArgs& a, const KeysItem& x, int key, int col, float* o) {
 #pragma unroll 1
-  for (int j = 0; j < x.n; ++j) {
+  for (int j = 0; j < x.n0; ++j) {
     if (!keys_mixed(a, x, j)) continue;
 #pragma unroll 1
     for (int i = 0; i < x.tp; ++i) {
@@ -297,10 +298,10 @@ struct KeysMath {
   float c, f;
 };
 
-// P and dS of tile j for a key and 64 rows; SOME: some row does not see some key. In
+// P and dS of the CTA's j-th tile for a key and 64 rows; SOME: some row does not see some key. In
 // two parts of 32 rows: the second's logits arrive while the first's are used.
 template <class C, bool SOME>
-__device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, int j) {
+__device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, uint32_t j) {
   constexpr bool HALF = C::HALF;
   const int stage = j & 1, key = m.key, lane = threadIdx.x & 31;
   const float2 c2 = make_float2(m.c, m.c), f2 = make_float2(m.f, m.f);
@@ -399,7 +400,7 @@ __device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, int 
 // Kept out of the loop: with both forms in it the instruction cache held neither
 // (8192 tokens of 32 heads of 128: 875 us).
 template <class C>
-__device__ __noinline__ void keys_step_some(KeysState& st, const KeysMath& m, int j) {
+__device__ __noinline__ void keys_step_some(KeysState& st, const KeysMath& m, uint32_t j) {
   keys_step<C, true>(st, m, j);
 }
 
@@ -412,39 +413,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   allow_dependent_launch();
   const PromptArgs& a = b.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  {
-    const int64_t words = (int64_t)a.kv * a.d / 8;
-    const int64_t from = (int64_t)blockIdx.x * C::THREADS + threadIdx.x, step = (int64_t)gridDim.x * C::THREADS;
-    fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dk), from, step);
-    fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dv), from, step);
-  }
-  // earlier slots first: a sequence's first keys are seen by the most rows
-  KeysWork x;
-  const int64_t slot = blockIdx.x / a.kv;
-  x.kvh = (int)(blockIdx.x - slot * a.kv);
-  const int s = seq_of_slot(a.cu_k, a.nseq, 128, slot, lane);
-  x.w = span_of(a, s);
-  const int64_t local = slot - first_slot(a.cu_k, s, 128);
-  if (local < 0 || local * 128 >= x.w.nk) return;
-  x.k0 = (int)local * 128;
-  x.off = x.w.nk - x.w.nq;
-  x.tp = 128 / a.group;
-  x.rows = x.tp * a.group;
-  x.t0 = max(0, x.k0 - x.off);
-  x.t1 = x.w.nq;
-  if (a.window) x.t1 = (int)min((int64_t)x.t1, (int64_t)min(x.k0 + 128, x.w.nk) - 1 - x.off + a.window);
-  x.n = x.t1 > x.t0 ? (x.t1 - x.t0 + x.tp - 1) / x.tp : 0;
-  const int n = x.n;
-
+  const int tp = 128 / a.group, rows = tp * a.group;
   uint8_t* const base = bwd_smem + ((1024u - (smem_at(bwd_smem) & 1023u)) & 1023u);
   auto& st = *reinterpret_cast<KeysState*>(base);
   uint8_t* const q_ptr = base + C::HEAD + 2 * C::TILE;
   uint8_t* const g_ptr = q_ptr + 2 * C::TILE;
   const uint32_t k_at = smem_at(base + C::HEAD), v_at = k_at + C::TILE, q_at = smem_at(q_ptr), g_at = smem_at(g_ptr);
-  const uint32_t kv_full = smem_at(&st.kv_full), q_full = smem_at(st.q_full), q_empty = smem_at(st.q_empty),
-                 g_full = smem_at(st.g_full), g_empty = smem_at(st.g_empty), r_full = smem_at(st.r_full),
-                 s_full = smem_at(&st.s_full), p_full = smem_at(st.p_full), dp_full = smem_at(&st.dp_full),
-                 ds_full = smem_at(st.ds_full), done = smem_at(&st.done);
+  const uint32_t kv_full = smem_at(&st.kv_full), kv_empty = smem_at(&st.kv_empty), q_full = smem_at(st.q_full),
+                 q_empty = smem_at(st.q_empty), g_full = smem_at(st.g_full), g_empty = smem_at(st.g_empty),
+                 r_full = smem_at(st.r_full), s_full = smem_at(&st.s_full), p_full = smem_at(st.p_full),
+                 dp_full = smem_at(&st.dp_full), ds_full = smem_at(st.ds_full), done = smem_at(&st.done);
   volatile int32_t* const dead = &st.dead;
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
@@ -455,23 +433,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(g_full + 8 * i, 1);
       mbar_init(g_empty + 8 * i, 1);
       mbar_init(r_full + 8 * i, 1);
-    }
-    mbar_init(kv_full, 1);
-    mbar_init(s_full, 1);
-    mbar_init(dp_full, 1);
-    mbar_init(done, 1);
-    for (int i = 0; i < 2; ++i) {
       mbar_init(p_full + 8 * i, 4);
       mbar_init(ds_full + 8 * i, 4);
     }
+    mbar_init(kv_full, 1);
+    mbar_init(kv_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(done, 1);
+    init_work(st.work, 11);  // eight warps of the arithmetic, copies, the rows' numbers, matrix instructions
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // rows of a tile that no head uses are never copied to, and must not hold NaN
-  if (x.rows < 128) {
+  if (rows < 128) {
 #pragma unroll 1
-    for (int i = threadIdx.x; i < 4 * (C::DP / 64) * (128 - x.rows) * 8; i += C::THREADS) {
-      const int part = i / ((128 - x.rows) * 8), at = i - part * (128 - x.rows) * 8;
-      *reinterpret_cast<uint4*>(q_ptr + part * C::SLAB + x.rows * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < 4 * (C::DP / 64) * (128 - rows) * 8; i += C::THREADS) {
+      const int slab = i / ((128 - rows) * 8), at = i - slab * (128 - rows) * 8;
+      *reinterpret_cast<uint4*>(q_ptr + slab * C::SLAB + rows * 128 + at * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_async();
   }
@@ -483,148 +461,202 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&st.tmem;
-  const uint32_t S = tmem, DP = tmem + 128, DV = tmem + 256, DK = tmem + 256 + C::DP;
+  auto take = [&](int k) { return take_work(st.work, st.item, k, lane, dead); };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
-    if (warp == 9) {  // ---- copies
-      if (lane == 0 && n > 0) {
-        const int bytes = C::DP / 64 * 128 * x.rows;
-        mbar_expect(kv_full, 2 * C::TILE);
-        load_tile<C>(k_at, &mk, x.kvh, x.w.k0 + x.k0, kv_full);
-        load_tile<C>(v_at, &mv, x.kvh, x.w.k0 + x.k0, kv_full);
+    if (warp == 11) {  // ---- work
+      find_work(st.work, st.item, blockIdx.x, false, lane, dead, [&](uint32_t id) {
+        const int64_t words = (int64_t)a.kv * a.d / 8, from = id * 32 + lane, step = (int64_t)gridDim.x * 32;
+        fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dk), from, step);
+        fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dv), from, step);
+        // earlier slots first: a sequence's first keys are seen by the most rows
+        KeysItem x;
+        const int64_t slot = id / a.kv;
+        x.kvh = (int)(id - slot * a.kv);
+        const int s = seq_of_slot(a.cu_k, a.nseq, 128, slot, lane);
+        x.w = span_of(a, s);
+        x.n0 = -1;
+        const int64_t local = slot - first_slot(a.cu_k, s, 128);
+        if (local < 0 || local * 128 >= x.w.nk) return x;
+        x.k0 = (int)local * 128;
+        x.off = x.w.nk - x.w.nq;
+        x.tp = tp;
+        x.t0 = max(0, x.k0 - x.off);
+        int t1 = x.w.nq;  // behind the last query that sees a key
+        if (a.window) t1 = (int)min((int64_t)t1, (int64_t)min(x.k0 + 128, x.w.nk) - 1 - x.off + a.window);
+        x.n0 = t1 > x.t0 ? (t1 - x.t0 + tp - 1) / tp : 0;
+        return x;
+      });
+    } else if (warp == 9) {  // ---- copies
+      uint32_t tiles = 0, loaded = 0;
+      const int bytes = C::DP / 64 * 128 * rows;
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-          const int stage = j & 1, token = x.w.q0 + x.t0 + j * x.tp;
-          mbar_wait(q_empty + 8 * stage, ((j >> 1) & 1) ^ 1, dead);
-          if (*dead) {
-            drain(kv_full, 1, 1);
-            drain(q_full, 2, j);
-            drain(g_full, 2, j);
-            break;
+      for (int k = 0;; ++k) {
+        const KeysItem x = take(k);
+        if (x.n0 < 0) break;
+        if (x.n0 == 0) continue;
+        if (lane == 0) {
+          mbar_wait(kv_empty, (loaded & 1) ^ 1, dead);
+          mbar_expect(kv_full, 2 * C::TILE);
+          load_tile<C>(k_at, &mk, x.kvh, x.w.k0 + x.k0, kv_full);
+          load_tile<C>(v_at, &mv, x.kvh, x.w.k0 + x.k0, kv_full);
+#pragma unroll 1
+          for (int j = 0; j < x.n0 && !*dead; ++j, ++tiles) {
+            const uint32_t stage = tiles & 1, parity = ((tiles >> 1) & 1) ^ 1;
+            const int token = x.w.q0 + x.t0 + j * tp;
+            mbar_wait(q_empty + 8 * stage, parity, dead);
+            mbar_expect(q_full + 8 * stage, bytes);
+            load_tile<C>(q_at + stage * C::TILE, &mq, x.kvh * a.group, token, q_full + 8 * stage);
+            mbar_wait(g_empty + 8 * stage, parity, dead);
+            mbar_expect(g_full + 8 * stage, bytes);
+            load_tile<C>(g_at + stage * C::TILE, &mg, x.kvh * a.group, token, g_full + 8 * stage);
           }
-          mbar_expect(q_full + 8 * stage, bytes);
-          load_tile<C>(q_at + stage * C::TILE, &mq, x.kvh * a.group, token, q_full + 8 * stage);
-          mbar_wait(g_empty + 8 * stage, ((j >> 1) & 1) ^ 1, dead);
           if (*dead) {
-            drain(kv_full, 1, 1);
-            drain(q_full, 2, j + 1);
-            drain(g_full, 2, j);
-            break;
+            drain(kv_full, 1, loaded + 1);
+            drain(q_full, 2, tiles);
+            drain(g_full, 2, tiles);
           }
-          mbar_expect(g_full + 8 * stage, bytes);
-          load_tile<C>(g_at + stage * C::TILE, &mg, x.kvh * a.group, token, g_full + 8 * stage);
         }
+        __syncwarp();
+        ++loaded;
       }
     } else if (warp == 10) {  // ---- the rows' numbers, with the tile of q
       const float f = C::HALF ? exp2f((float)-gradient_exponent<C::HALF>(b)) : 1.0f;
+      uint32_t tiles = 0;
+      int token[4], head[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        token[i] = (i * 32 + lane) / a.group;
+        head[i] = i * 32 + lane - token[i] * a.group;
+      }
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        const int stage = j & 1;
-        float2 v[4];
-        int hi[4];
+      for (int k = 0;; ++k) {
+        const KeysItem x = take(k);
+        if (x.n0 < 0) break;
+#pragma unroll 1
+        for (int j = 0; j < x.n0; ++j, ++tiles) {
+          const uint32_t stage = tiles & 1;
+          float2 v[4];
+          int hi[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = i * 32 + lane, t = x.t0 + j * x.tp + r / a.group;
-          const bool there = r < x.rows && t < x.w.nq;
-          hi[i] = there ? x.off + t + 1 : 0;
-          v[i] = there ? __ldg(b.stats + (int64_t)(x.w.q0 + t) * a.heads + x.kvh * a.group + r % a.group)
-                       : make_float2(-INFINITY, 0.0f);
-        }
-        mbar_wait(q_empty + 8 * stage, ((j >> 1) & 1) ^ 1, dead);
+          for (int i = 0; i < 4; ++i) {
+            const int t = x.t0 + j * tp + token[i];
+            const bool there = i * 32 + lane < rows && t < x.w.nq;
+            hi[i] = there ? x.off + t + 1 : 0;
+            v[i] = there ? __ldg(b.stats + (int64_t)(x.w.q0 + t) * a.heads + x.kvh * a.group + head[i]) : make_float2(-INFINITY, 0.0f);
+          }
+          mbar_wait(q_empty + 8 * stage, ((tiles >> 1) & 1) ^ 1, dead);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = i * 32 + lane;
-          st.lse[stage][r] = v[i].x;
-          st.delta[stage][r] = v[i].y * f;
-          st.hi[stage][r] = hi[i];
-          st.lo[stage][r] = a.window ? max(0, hi[i] - a.window) : 0;
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 32 + lane;
+            st.lse[stage][r] = v[i].x;
+            st.delta[stage][r] = v[i].y * f;
+            st.hi[stage][r] = hi[i];
+            st.lo[stage][r] = a.window ? max(0, hi[i] - a.window) : 0;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(r_full + 8 * stage);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(r_full + 8 * stage);
       }
     } else if (warp == 8) {  // ---- matrix instructions
-      const int tiles = (int)uniform((uint32_t)n);
-      const uint32_t leader = tc_leader(), base_t = uniform(tmem), S = base_t, DP = base_t + 128, DV = base_t + 256,
-                     DK = base_t + 256 + C::DP;
-      if (tiles > 0) {
-        mbar_wait(kv_full, 0, dead);
-        auto scores = [&](int j) {
-          mbar_wait(q_full + 8 * (j & 1), (j >> 1) & 1, dead);
-          tc_after();
-          product<C>(leader, S, k_at, q_at + (j & 1) * C::TILE);
-          tc_commit_by(leader, s_full);
-        };
-        auto weights = [&](int j) {  // dP
-          mbar_wait(g_full + 8 * (j & 1), (j >> 1) & 1, dead);
-          tc_after();
-          product<C>(leader, DP, v_at, g_at + (j & 1) * C::TILE);
-          tc_commit_by(leader, dp_full);
-        };
-        auto add = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t ready, int j) {
+      const uint32_t leader = tc_leader(), tm = uniform(tmem), S = tm, DP = tm + 128, DV = tm + 256, DK = tm + 256 + C::DP;
+      uint32_t tiles = 0, items = 0;
+      auto scores = [&](uint32_t j) {
+        mbar_wait(q_full + 8 * (j & 1), (j >> 1) & 1, dead);
+        tc_after();
+        product<C>(leader, S, k_at, q_at + (j & 1) * C::TILE);
+        tc_commit_by(leader, s_full);
+      };
+      auto weights = [&](uint32_t j) {  // dP
+        mbar_wait(g_full + 8 * (j & 1), (j >> 1) & 1, dead);
+        tc_after();
+        product<C>(leader, DP, v_at, g_at + (j & 1) * C::TILE);
+        tc_commit_by(leader, dp_full);
+      };
+      auto add = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t ready, uint32_t j, bool first) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            mbar_wait(ready + 8 * half, j & 1, dead);
-            tc_after();
-            product_add<C>(leader, d, x, y, half, j > 0 || half > 0);
-          }
-        };
-        scores(0);
-        weights(0);
+        for (int half = 0; half < 2; ++half) {
+          mbar_wait(ready + 8 * half, j & 1, dead);
+          tc_after();
+          product_add<C>(leader, d, x, y, half, !first || half > 0);
+        }
+      };
 #pragma unroll 1
-        for (int j = 0; j < tiles; ++j) {
-          add(DV, S, g_at + (j & 1) * C::TILE, p_full, j);
-          tc_commit_by(leader, g_empty + 8 * (j & 1));
-          if (j + 1 < tiles) scores(j + 1);
-          add(DK, DP, q_at + (j & 1) * C::TILE, ds_full, j);
-          tc_commit_by(leader, q_empty + 8 * (j & 1));
-          if (j + 1 < tiles) weights(j + 1);
+      for (int k = 0;; ++k) {
+        const KeysItem x = take(k);
+        const int n = (int)uniform((uint32_t)x.n0);
+        if (n < 0) break;
+        if (n == 0) continue;
+        mbar_wait(kv_full, items & 1, dead);
+        ++items;
+        scores(tiles);
+        weights(tiles);
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++tiles) {
+          if (j == max(0, n - 3)) want_work(st.work, lane);
+          add(DV, S, g_at + (tiles & 1) * C::TILE, p_full, tiles, j == 0);
+          tc_commit_by(leader, g_empty + 8 * (tiles & 1));
+          if (j + 1 < n) scores(tiles + 1);
+          add(DK, DP, q_at + (tiles & 1) * C::TILE, ds_full, tiles, j == 0);
+          tc_commit_by(leader, q_empty + 8 * (tiles & 1));
+          if (j + 1 < n)
+            weights(tiles + 1);
+          else
+            tc_commit_by(leader, kv_empty);
         }
         tc_commit_by(leader, done);
       }
     }
   } else {  // ---- P and dS: a key a thread, half of a tile's rows
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MATH_REGS));
-    const int half = warp >> 2, col = half * 64, key = x.k0 + (threadIdx.x & 127);
+    const int half = warp >> 2, col = half * 64;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int e = gradient_exponent<C::HALF>(b);
-    const float c = a.scale * kLog2e, f = C::HALF ? exp2f((float)-e) : 1.0f;
-    const KeysMath m = {q_ptr, g_ptr, dead, S + lanes + col, DP + lanes + col, r_full, s_full, g_full, p_full + 8 * half, dp_full, ds_full + 8 * half, col, key, c, f};
+    KeysMath m = {q_ptr, g_ptr, dead, tmem + lanes + col, tmem + 128 + lanes + col, r_full, s_full, g_full, p_full + 8 * half,
+                  dp_full, ds_full + 8 * half, col, 0, a.scale * kLog2e, C::HALF ? exp2f((float)-e) : 1.0f};
+    uint32_t tiles = 0, items = 0;
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      if (keys_mixed(a, x, j))
-        keys_step_some<C>(st, m, j);
-      else
-        keys_step<C, false>(st, m, j);
-    }
-    // group 0 stores dV, group 1 dK
-    if (n > 0) mbar_wait(done, 0, dead);
-    tc_after();
-    barrier_of(1, 256);  // all of both groups' cleaning is known
-    const bool there = key < x.w.nk;
-    const int64_t row = ((int64_t)(x.w.k0 + key) * a.kv + x.kvh) * a.d;
-    float factor = half ? a.scale * (C::HALF ? exp2f((float)(e - 15)) : 1.0f) : (C::HALF ? exp2f(-15.0f) : 1.0f);
-    if (*dead) factor = NAN;
-    const bool bad = half == 0 && *(volatile int32_t*)&st.bad != 0;
+    for (int k = 0;; ++k) {
+      const KeysItem x = take(k);
+      if (x.n0 < 0) break;
+      m.key = x.k0 + (threadIdx.x & 127);
 #pragma unroll 1
-    for (int k = 0; k < C::DP; k += 32) {
-      float o[32];
-      if (n > 0) tc_load32((half ? DK : DV) + lanes + k, o);
-      if (!there || k >= a.d) continue;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * factor : 0.0f;
-      if (bad) {
-        float again[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) again[i] = o[i];
-        give_back_grad<C::HALF>(a, x, key, k, again);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = again[i];
+      for (int j = 0; j < x.n0; ++j, ++tiles) {
+        if (keys_mixed(a, x, j))
+          keys_step_some<C>(st, m, tiles);
+        else
+          keys_step<C, false>(st, m, tiles);
       }
-      store_columns<C::HALF>(half ? a.dk : a.dv, row, a.d, k, o);
+      // group 0 stores dV, group 1 dK
+      if (x.n0 > 0) mbar_wait(done, items++ & 1, dead);
+      tc_after();
+      const bool there = m.key < x.w.nk;
+      const int64_t row = ((int64_t)(x.w.k0 + m.key) * a.kv + x.kvh) * a.d;
+      float factor = half ? a.scale * (C::HALF ? exp2f((float)(e - 15)) : 1.0f) : (C::HALF ? exp2f(-15.0f) : 1.0f);
+      if (*dead) factor = NAN;
+      // what the other group has found is known: its last dS came after, and `done` after that
+      const bool bad = half == 0 && *(volatile int32_t*)&st.bad != 0;
+#pragma unroll 1
+      for (int i = 0; i < C::DP; i += 32) {
+        float o[32];
+        if (x.n0 > 0) tc_load32(tmem + 256 + half * C::DP + lanes + i, o);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) o[c] = x.n0 > 0 ? o[c] * factor : 0.0f;
+        if (bad && there && i < a.d) {
+          float again[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) again[c] = o[c];
+          give_back_grad<C::HALF>(a, x, m.key, i, again);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = again[c];
+        }
+        if (there && i < a.d) store_columns<C::HALF>(half ? a.dk : a.dv, row, a.d, i, o);
+      }
+      tc_before();
     }
-    tc_before();
   }
+  __syncwarp();
   __syncthreads();
   tc_after();
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -634,12 +666,106 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
 constexpr int kKeyStages = 3, kValueStages = 2;
 
+struct alignas(16) RowsItem {
+  Span w;
+  int32_t t0, t1, kvh, off;  // tokens t0 .. t1 - 1; key head; key index of query 0
+  int32_t kb0, n0;           // first block of keys, blocks
+  int32_t pad[2];
+  __device__ __forceinline__ bool keys() const { return n0 > 0; }
+};
+
 struct RowsState {
-  uint64_t q_full, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], s_full[2], dp_full,
-      ds_full[2], done;
+  RowsItem item[2];
+  WorkState work;
+  uint64_t q_full, q_empty, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], s_full[2],
+      dp_full, ds_full[2], done;
   int32_t dead, bad;
   uint32_t tmem;
 };
+static_assert(sizeof(RowsState) <= 1024, "in front of the tiles");
+
+// Whether some row of the item does not see some key of block j.
+__device__ __forceinline__ bool rows_mixed(const PromptArgs& a, const RowsItem& x, int j) {
+  const int first = (x.kb0 + j) * 128;
+  return first + 128 > x.off + x.t0 + 1 || (a.window && (int64_t)first < (int64_t)x.off + x.t1 - a.window);
+}
+
+// What the arithmetic of a row's blocks needs.
+struct RowsMath {
+  uint8_t* k_ptr;
+  volatile int32_t* dead;
+  uint32_t s_at, dp_at, s_full, dp_full, ds_full;
+  int32_t* bad;
+  int lo, hi;  // keys that the row sees, from this thread's half of block 0 on
+  bool single;
+  float c, f, lse, delta;
+};
+
+// dS of the CTA's j-th block for a row and 64 keys, the first of them `first` behind the
+// item's first; SOME: some row does not see some key.
+template <class C, bool SOME>
+__device__ __forceinline__ void rows_step(const RowsMath& m, uint32_t j, uint32_t k_stage, int first) {
+  const int lane = threadIdx.x & 31;
+  const float2 c2 = make_float2(m.c, m.c), f2 = make_float2(m.f, m.f), l2 = make_float2(m.lse, m.lse),
+               d2 = make_float2(m.delta, m.delta);
+  const uint32_t s_at = m.s_at + 128 * (j & 1);
+  mbar_wait(m.s_full + 8 * (j & 1), (j >> 1) & 1, m.dead);
+  tc_after();
+  float p[64], d[64];
+  tc_load32_async(s_at, p);
+  tc_load32_async(s_at + 32, p + 32);
+  tc_load_wait();
+  tc_loaded(p);
+  tc_loaded(p + 32);
+#pragma unroll
+  for (int k = 0; k < 64; k += 2) {
+    const float2 z = fma2_rn(make_float2(p[k], p[k + 1]), c2, l2);
+    p[k] = ex2_approx_ftz(z.x);
+    p[k + 1] = ex2_approx_ftz(z.y);
+  }
+  if constexpr (SOME) clean_operand<C::HALF>(m.k_ptr + k_stage * C::TILE, C::TILE, threadIdx.x, 256, m.bad);
+  mbar_wait(m.dp_full, j & 1, m.dead);
+  tc_after();
+  tc_load32_async(m.dp_at, d);
+  tc_load_wait();
+  tc_loaded(d);
+  tc_load32_async(m.dp_at + 32, d + 32);
+#pragma unroll
+  for (int part = 0; part < 64; part += 32) {
+    if (part) {
+      tc_load_wait();
+      tc_loaded(d + 32);
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const int k = part + i;
+      float2 v = make_float2(d[k], d[k + 1]);
+      if constexpr (C::HALF)
+        v = fma2_rn(v, f2, d2);
+      else
+        v = add2_rn(v, d2);
+      if constexpr (SOME) {
+        if (m.single) v = d2;  // a row that sees one key: dP does not count
+      }
+      v = mul2_rn(make_float2(p[k], p[k + 1]), v);
+      d[k] = v.x;
+      d[k + 1] = v.y;
+      if constexpr (SOME) {
+        d[k] = first + k < m.hi && first + k >= m.lo ? d[k] : 0.0f;
+        d[k + 1] = first + k + 1 < m.hi && first + k + 1 >= m.lo ? d[k + 1] : 0.0f;
+      }
+    }
+    store_part<C::HALF>(s_at + part / 2, d + part);
+  }
+  tc_store_wait();
+  tc_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(m.ds_full);
+}
+template <class C>
+__device__ __noinline__ void rows_step_some(const RowsMath& m, uint32_t j, uint32_t k_stage, int first) {
+  rows_step<C, true>(m, j, k_stage, first);
+}
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
@@ -650,28 +776,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   allow_dependent_launch();
   const PromptArgs& a = b.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  fill_rest(a.cu_q, a.nseq, a.num_q, (int64_t)a.heads * a.d / 8, static_cast<uint4*>(a.dq),
-            (int64_t)blockIdx.x * C::THREADS + threadIdx.x, (int64_t)gridDim.x * C::THREADS);
-  // later slots first: a sequence's last tiles see the most keys
   const int tp = 128 / a.group, rows = tp * a.group;
-  const uint32_t id = gridDim.x - 1 - blockIdx.x;
-  const int64_t slot = id / a.kv;
-  const int kvh = (int)(id - slot * a.kv);
-  const int s = seq_of_slot(a.cu_q, a.nseq, tp, slot, lane);
-  const Span w = span_of(a, s);
-  const int64_t local = slot - first_slot(a.cu_q, s, tp);
-  if (local < 0 || local * tp >= w.nq) return;
-  const int t0 = (int)local * tp, t1 = min(t0 + tp, w.nq), off = w.nk - w.nq;
-  const int kb0 = (a.window ? (int)max((int64_t)0, (int64_t)off + t0 + 1 - a.window) : 0) / 128;
-  const int n = off + t1 > 0 ? (off + t1 + 127) / 128 - kb0 : 0;
-
   uint8_t* const base = bwd_smem + ((1024u - (smem_at(bwd_smem) & 1023u)) & 1023u);
   auto& st = *reinterpret_cast<RowsState*>(base);
   uint8_t* const k_ptr = base + 1024 + 2 * C::TILE;
   const uint32_t q_at = smem_at(base + 1024), g_at = q_at + C::TILE, k_at = smem_at(k_ptr), v_at = k_at + kKeyStages * C::TILE;
-  const uint32_t q_full = smem_at(&st.q_full), k_full = smem_at(st.k_full), k_empty = smem_at(st.k_empty),
-                 v_full = smem_at(st.v_full), v_empty = smem_at(st.v_empty), s_full = smem_at(st.s_full),
-                 dp_full = smem_at(&st.dp_full), ds_full = smem_at(st.ds_full), done = smem_at(&st.done);
+  const uint32_t q_full = smem_at(&st.q_full), q_empty = smem_at(&st.q_empty), k_full = smem_at(st.k_full),
+                 k_empty = smem_at(st.k_empty), v_full = smem_at(st.v_full), v_empty = smem_at(st.v_empty),
+                 s_full = smem_at(st.s_full), dp_full = smem_at(&st.dp_full), ds_full = smem_at(st.ds_full), done = smem_at(&st.done);
   volatile int32_t* const dead = &st.dead;
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
@@ -686,12 +798,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(v_empty + 8 * i, 1);
     }
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     mbar_init(s_full, 1);
     mbar_init(s_full + 8, 1);
     mbar_init(dp_full, 1);
     mbar_init(done, 1);
     mbar_init(ds_full, 4);
     mbar_init(ds_full + 8, 4);
+    init_work(st.work, 11);  // eight warps of the arithmetic, two of copies, matrix instructions
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) {
@@ -702,77 +816,126 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&st.tmem;
-  const uint32_t S = tmem, DP = tmem + 256, DQ = tmem + 384;
+  auto take = [&](int k) { return take_work(st.work, st.item, k, lane, dead); };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
-    if (warp == 9) {  // ---- copies of q, grad and keys
-      if (lane == 0 && n > 0) {
-        mbar_expect(q_full, 2 * (C::DP / 64) * 128 * rows);
-        load_tile<C>(q_at, &mq, kvh * a.group, w.q0 + t0, q_full);
-        load_tile<C>(g_at, &mg, kvh * a.group, w.q0 + t0, q_full);
+    if (warp == 11) {  // ---- work
+      find_work(st.work, st.item, blockIdx.x, false, lane, dead, [&](uint32_t id) {
+        fill_rest(a.cu_q, a.nseq, a.num_q, (int64_t)a.heads * a.d / 8, static_cast<uint4*>(a.dq), id * 32 + lane,
+                  (int64_t)gridDim.x * 32);
+        // later slots first: a sequence's last tiles see the most keys
+        RowsItem x;
+        id = gridDim.x - 1 - id;
+        const int64_t slot = id / a.kv;
+        x.kvh = (int)(id - slot * a.kv);
+        const int s = seq_of_slot(a.cu_q, a.nseq, tp, slot, lane);
+        x.w = span_of(a, s);
+        x.n0 = -1;
+        const int64_t local = slot - first_slot(a.cu_q, s, tp);
+        if (local < 0 || local * tp >= x.w.nq) return x;
+        x.t0 = (int)local * tp;
+        x.t1 = min(x.t0 + tp, x.w.nq);
+        x.off = x.w.nk - x.w.nq;
+        x.kb0 = (a.window ? (int)max((int64_t)0, (int64_t)x.off + x.t0 + 1 - a.window) : 0) / 128;
+        x.n0 = x.off + x.t1 > 0 ? (x.off + x.t1 + 127) / 128 - x.kb0 : 0;
+        return x;
+      });
+    } else if (warp == 9) {  // ---- copies of q, grad and keys
+      Place<kKeyStages> at = {0, 0};
+      uint32_t loaded = 0, tiles = 0;
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-          const int i = j % kKeyStages;
-          mbar_wait(k_empty + 8 * i, ((j / kKeyStages) & 1) ^ 1, dead);
-          if (*dead) {
-            drain(q_full, 1, 1);
-            drain(k_full, kKeyStages, j);
-            break;
+      for (int k = 0;; ++k) {
+        const RowsItem x = take(k);
+        if (x.n0 < 0) break;
+        if (x.n0 == 0) continue;
+        if (lane == 0) {
+          mbar_wait(q_empty, (loaded & 1) ^ 1, dead);
+          mbar_expect(q_full, 2 * (C::DP / 64) * 128 * rows);
+          load_tile<C>(q_at, &mq, x.kvh * a.group, x.w.q0 + x.t0, q_full);
+          load_tile<C>(g_at, &mg, x.kvh * a.group, x.w.q0 + x.t0, q_full);
+#pragma unroll 1
+          for (int j = 0; j < x.n0 && !*dead; ++j, ++tiles) {
+            mbar_wait(k_empty + 8 * at.stage, at.parity ^ 1, dead);
+            mbar_expect(k_full + 8 * at.stage, C::TILE);
+            load_tile<C>(k_at + at.stage * C::TILE, &mk, x.kvh, x.w.k0 + (x.kb0 + j) * 128, k_full + 8 * at.stage);
+            at.next(1);
           }
-          mbar_expect(k_full + 8 * i, C::TILE);
-          load_tile<C>(k_at + i * C::TILE, &mk, kvh, w.k0 + (kb0 + j) * 128, k_full + 8 * i);
+          if (*dead) {
+            drain(q_full, 1, loaded + 1);
+            drain(k_full, kKeyStages, tiles);
+          }
         }
+        __syncwarp();
+        ++loaded;
       }
     } else if (warp == 10) {  // ---- copies of values
-      if (lane == 0) {
+      Place<kValueStages> at = {0, 0};
+      uint32_t tiles = 0;
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-          const int i = j % kValueStages;
-          mbar_wait(v_empty + 8 * i, ((j / kValueStages) & 1) ^ 1, dead);
-          if (*dead) {
-            drain(v_full, kValueStages, j);
-            break;
+      for (int k = 0;; ++k) {
+        const RowsItem x = take(k);
+        if (x.n0 < 0) break;
+        if (lane == 0) {
+#pragma unroll 1
+          for (int j = 0; j < x.n0 && !*dead; ++j, ++tiles) {
+            mbar_wait(v_empty + 8 * at.stage, at.parity ^ 1, dead);
+            mbar_expect(v_full + 8 * at.stage, C::TILE);
+            load_tile<C>(v_at + at.stage * C::TILE, &mv, x.kvh, x.w.k0 + (x.kb0 + j) * 128, v_full + 8 * at.stage);
+            at.next(1);
           }
-          mbar_expect(v_full + 8 * i, C::TILE);
-          load_tile<C>(v_at + i * C::TILE, &mv, kvh, w.k0 + (kb0 + j) * 128, v_full + 8 * i);
+          if (*dead) drain(v_full, kValueStages, tiles);
         }
+        __syncwarp();
       }
     } else if (warp == 8) {  // ---- matrix instructions
-      const int tiles = (int)uniform((uint32_t)n);
-      const uint32_t leader = tc_leader(), base_t = uniform(tmem), S = base_t, DP = base_t + 256, DQ = base_t + 384;
-      if (tiles > 0) {
-        mbar_wait(q_full, 0, dead);
-        auto scores = [&](int j) {
-          mbar_wait(k_full + 8 * (j % kKeyStages), (j / kKeyStages) & 1, dead);
-          tc_after();
-          product<C>(leader, S + 128 * (j & 1), q_at, k_at + (j % kKeyStages) * C::TILE);
-          tc_commit_by(leader, s_full + 8 * (j & 1));
-        };
-        auto weights = [&](int j) {  // dP
-          mbar_wait(v_full + 8 * (j % kValueStages), (j / kValueStages) & 1, dead);
-          tc_after();
-          product<C>(leader, DP, g_at, v_at + (j % kValueStages) * C::TILE);
-          tc_commit_by(leader, v_empty + 8 * (j % kValueStages));
-          tc_commit_by(leader, dp_full);
-        };
-        auto add = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t ready, int j) {
+      const uint32_t leader = tc_leader(), tm = uniform(tmem), S = tm, DP = tm + 256, DQ = tm + 384;
+      Place<kKeyStages> key = {0, 0}, used = {0, 0};  // of the next S, of the next dQ
+      Place<kValueStages> value = {0, 0};
+      uint32_t scored = 0, added = 0, items = 0;
+      auto scores = [&]() {
+        mbar_wait(k_full + 8 * key.stage, key.parity, dead);
+        tc_after();
+        product<C>(leader, S + 128 * (scored & 1), q_at, k_at + key.stage * C::TILE);
+        tc_commit_by(leader, s_full + 8 * (scored & 1));
+        ++scored;
+        key.next(1);
+      };
+      auto weights = [&]() {  // dP
+        mbar_wait(v_full + 8 * value.stage, value.parity, dead);
+        tc_after();
+        product<C>(leader, DP, g_at, v_at + value.stage * C::TILE);
+        tc_commit_by(leader, v_empty + 8 * value.stage);
+        tc_commit_by(leader, dp_full);
+        value.next(1);
+      };
+#pragma unroll 1
+      for (int k = 0;; ++k) {
+        const RowsItem x = take(k);
+        const int n = (int)uniform((uint32_t)x.n0);
+        if (n < 0) break;
+        if (n == 0) continue;
+        mbar_wait(q_full, items & 1, dead);
+        ++items;
+        scores();
+        weights();
+        if (n > 1) scores();
+        if (n == 1) tc_commit_by(leader, q_empty);
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          if (j == max(0, n - 3)) want_work(st.work, lane);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            mbar_wait(ready + 8 * half, j & 1, dead);
+            mbar_wait(ds_full + 8 * half, added & 1, dead);
             tc_after();
-            product_add<C>(leader, d, x, y, half, j > 0 || half > 0);
+            product_add<C>(leader, DQ, S + 128 * (added & 1), k_at + used.stage * C::TILE, half, j > 0 || half > 0);
           }
-        };
-        scores(0);
-        weights(0);
-        if (tiles > 1) scores(1);
-#pragma unroll 1
-        for (int j = 0; j < tiles; ++j) {
-          add(DQ, S + 128 * (j & 1), k_at + (j % kKeyStages) * C::TILE, ds_full, j);
-          tc_commit_by(leader, k_empty + 8 * (j % kKeyStages));
-          if (j + 1 < tiles) weights(j + 1);
-          if (j + 2 < tiles) scores(j + 2);
+          ++added;
+          tc_commit_by(leader, k_empty + 8 * used.stage);
+          used.next(1);
+          if (j + 1 < n) weights();
+          if (j + 2 < n) scores();
+          if (j + 2 == n) tc_commit_by(leader, q_empty);
         }
         tc_commit_by(leader, done);
       }
@@ -781,90 +944,47 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MATH_REGS));
     const int half = warp >> 2, col = half * 64, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int token = t0 + r / a.group;
-    const bool there = r < rows && token < w.nq;
-    const int hi = there ? off + token + 1 : 0;
-    const int lo = a.window ? max(0, hi - a.window) : 0;
-    const int64_t row = (int64_t)(w.q0 + token) * a.heads + kvh * a.group + r % a.group;
-    const float2 stats = there ? __ldg(b.stats + row) : make_float2(-INFINITY, 0.0f);
-    const int e = gradient_exponent<C::HALF>(b);
-    const float c = a.scale * kLog2e, f = C::HALF ? exp2f((float)-e) : 1.0f, delta = stats.y * f;
-    const bool single = hi - lo == 1;
-    const float2 c2 = make_float2(c, c), f2 = make_float2(f, f), l2 = make_float2(stats.x, stats.x), d2 = make_float2(delta, delta);
+    const int in_tile = r / a.group, head = r - in_tile * a.group, e = gradient_exponent<C::HALF>(b);
+    RowsMath m = {k_ptr, dead, tmem + lanes + col, tmem + 256 + lanes + col, s_full, dp_full, ds_full + 8 * half, &st.bad, 0, 0, false,
+                  a.scale * kLog2e, C::HALF ? exp2f((float)-e) : 1.0f, 0.0f, 0.0f};
+    uint32_t tiles = 0, items = 0;
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      const int first = (kb0 + j) * 128;
-      // some row of the tile does not see some key of the block
-      const bool some = first + 128 > off + t0 + 1 || (a.window && (int64_t)first < (int64_t)off + t1 - a.window);
-      const uint32_t s_at = S + 128 * (j & 1) + lanes + col;
-      mbar_wait(s_full + 8 * (j & 1), (j >> 1) & 1, dead);
-      tc_after();
-      float p[64], d[64];
-      tc_load32_async(s_at, p);
-      tc_load32_async(s_at + 32, p + 32);
-      tc_load_wait();
-      tc_loaded(p);
-      tc_loaded(p + 32);
-#pragma unroll
-      for (int k = 0; k < 64; k += 2) {
-        const float2 z = fma2_rn(make_float2(p[k], p[k + 1]), c2, l2);
-        p[k] = ex2_approx_ftz(z.x);
-        p[k + 1] = ex2_approx_ftz(z.y);
+    for (int k = 0;; ++k) {
+      const RowsItem x = take(k);
+      if (x.n0 < 0) break;
+      const int token = x.t0 + in_tile;
+      const bool there = r < rows && token < x.t1;
+      const int64_t row = (int64_t)(x.w.q0 + token) * a.heads + x.kvh * a.group + head;
+      const float2 stats = there ? __ldg(b.stats + row) : make_float2(-INFINITY, 0.0f);
+      const int hi = there ? x.off + token + 1 : 0, lo = a.window ? max(0, hi - a.window) : 0;
+      m.hi = hi - x.kb0 * 128 - col;
+      m.lo = lo - x.kb0 * 128 - col;
+      m.single = hi - lo == 1;
+      m.lse = stats.x;
+      m.delta = stats.y * m.f;
+#pragma unroll 1
+      for (int j = 0; j < x.n0; ++j, ++tiles) {
+        if (rows_mixed(a, x, j))
+          rows_step_some<C>(m, tiles, tiles % kKeyStages, j * 128);
+        else
+          rows_step<C, false>(m, tiles, 0, 0);
       }
-      if (some) clean_operand<C::HALF>(k_ptr + (j % kKeyStages) * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
-      mbar_wait(dp_full, j & 1, dead);
+      if (x.n0 > 0) mbar_wait(done, items++ & 1, dead);
       tc_after();
-      tc_load32_async(DP + lanes + col, d);
-      tc_load_wait();
-      tc_loaded(d);
-      tc_load32_async(DP + lanes + col + 32, d + 32);
-      // in two parts, as in keys_step
+      float factor = a.scale * (C::HALF ? exp2f((float)(e - 15)) : 1.0f);
+      if (*dead) factor = NAN;
+#pragma unroll 1
+      for (int i = half * (C::DP / 2); i < (half + 1) * (C::DP / 2); i += 32) {
+        float o[32];
+        if (x.n0 > 0) tc_load32(tmem + 384 + lanes + i, o);
 #pragma unroll
-      for (int part = 0; part < 64; part += 32) {
-        if (part) {
-          tc_load_wait();
-          tc_loaded(d + 32);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const int k = part + i;
-          float2 v = make_float2(d[k], d[k + 1]);
-          if constexpr (C::HALF)
-            v = fma2_rn(v, f2, d2);
-          else
-            v = add2_rn(v, d2);
-          if (some && single) v = d2;
-          v = mul2_rn(make_float2(p[k], p[k + 1]), v);
-          d[k] = v.x;
-          d[k + 1] = v.y;
-        }
-        if (some) {
-          const int h = hi - first - col - part, l = lo - first - col - part;
-#pragma unroll
-          for (int k = 0; k < 32; ++k) d[part + k] = k < h && k >= l ? d[part + k] : 0.0f;
-        }
-        store_part<C::HALF>(s_at + part / 2, d + part);
+        for (int c = 0; c < 32; ++c) o[c] = x.n0 > 0 ? o[c] * factor : 0.0f;
+        if (there && i < a.d) store_columns<C::HALF>(a.dq, row * a.d, a.d, i, o);
       }
-      tc_store_wait();
       tc_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full + 8 * half);
     }
-    if (n > 0) mbar_wait(done, 0, dead);
-    tc_after();
-    float factor = a.scale * (C::HALF ? exp2f((float)(e - 15)) : 1.0f);
-    if (*dead) factor = NAN;
-#pragma unroll 1
-    for (int k = half * (C::DP / 2); k < (half + 1) * (C::DP / 2); k += 32) {
-      float o[32];
-      if (n > 0) tc_load32(DQ + lanes + k, o);
-      if (!there || k >= a.d) continue;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * factor : 0.0f;
-      store_columns<C::HALF>(a.dq, row * a.d, a.d, k, o);
-    }
-    tc_before();
   }
+  __syncwarp();
   __syncthreads();
   tc_after();
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

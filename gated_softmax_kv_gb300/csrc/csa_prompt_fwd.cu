@@ -49,6 +49,8 @@ struct Fwd {
   static constexpr int SLAB = 16384;              // 128 rows x 64 columns
   static constexpr int TILE = DP / 64 * SLAB;
   static constexpr int NS = DP == 128 ? 5 : 8;    // tiles of the ring
+  static constexpr int SHARE = DP + 4;            // floats of a row that a cluster shares
+  static_assert(128 * SHARE * 4 <= NS * TILE, "a cluster shares its sums in the ring");
   static constexpr int THREADS = 384;
   // Registers: 384 threads at 168, dealt out again by role (2 * 208 + 88 = 3 * 168).
   static constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
@@ -69,30 +71,17 @@ struct alignas(16) Item {
   int32_t kvh;               // key head
   int32_t kb0, n0, n1, step; // first block of keys, blocks of each tile, 2: the groups share tile 0
   int32_t pad;               // n0 < 0: there is no more work
+  __device__ __forceinline__ bool keys() const { return n0 > 0 || n1 > 0; }
 };
 
 template <int NS>
 struct State {
   Item item[2];
-  alignas(16) uint32_t stolen[4];
-  uint64_t full[NS], empty[NS], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], item_full[2], item_empty[2], steal, pair_full, pair_empty;
+  WorkState work;
+  uint64_t full[NS], empty[NS], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], pair_full, pair_empty;
   int32_t dead, bad;
   uint32_t tmem;
   float ref[128], sum[128];  // group 1's, for group 0; in a cluster: the CTA's
-};
-
-// A place in the ring, and the parity of its barriers.
-template <int NS>
-struct Place {
-  int stage;
-  uint32_t parity;
-  __device__ __forceinline__ void next(int n) {
-    stage += n;
-    if (stage >= NS) {
-      stage -= NS;
-      parity ^= 1;
-    }
-  }
 };
 
 // The order of the ring: K0 V0 K1 V1 ... or, where the groups take alternate blocks, K0
@@ -220,8 +209,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t q_at = smem_at(q_ptr), ring = smem_at(ring_ptr);
   const uint32_t full = smem_at(st.full), empty = smem_at(st.empty), q_full = smem_at(&st.q_full),
                  q_empty = smem_at(&st.q_empty), s_full = smem_at(st.s_full), p_full = smem_at(st.p_full),
-                 o_full = smem_at(st.o_full), item_full = smem_at(st.item_full), item_empty = smem_at(st.item_empty),
-                 steal = smem_at(&st.steal), pair_full = smem_at(&st.pair_full), pair_empty = smem_at(&st.pair_empty);
+                 o_full = smem_at(st.o_full), pair_full = smem_at(&st.pair_full), pair_empty = smem_at(&st.pair_empty);
   volatile int32_t* const dead = &st.dead;
   const int tp = 128 / a.group, rows = tp * a.group;
   const uint32_t ids = gridDim.x / shape.split, first_id = blockIdx.x / shape.split;
@@ -235,7 +223,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    mbar_init(steal, 1);
     mbar_init(pair_full, 4);
     mbar_init(pair_empty, 4);
 #pragma unroll 1
@@ -244,9 +231,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(p_full + 16 * t, 4);
       mbar_init(p_full + 16 * t + 8, 4);
       mbar_init(o_full + 8 * t, 1);
-      mbar_init(item_full + 8 * t, 1);
-      mbar_init(item_empty + 8 * t, 10);  // eight softmax warps, copies, matrix instructions
     }
+    init_work(st.work, 10);  // eight softmax warps, copies, matrix instructions
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) {
@@ -258,68 +244,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   tc_after();
   const uint32_t tmem = *(volatile uint32_t*)&st.tmem;
 
-  // The k-th item, for a whole warp; its slot may be filled again after that.
-  auto take = [&](int k) -> Item {
-    mbar_wait(item_full + 8 * (k & 1), (k >> 1) & 1, dead);
-    Item x = st.item[k & 1];
-    if (*dead) x.n0 = -1;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(item_empty + 8 * (k & 1));
-    return x;
-  };
-
+  auto take = [&](int k) { return take_work(st.work, st.item, k, lane, dead); };
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == 10) {  // ---- work
-      uint32_t id = first_id;
-      int k = 0;
-#pragma unroll 1
-      for (int stolen = 0;; ++stolen) {
+      find_work(st.work, st.item, first_id, shape.split > 1, lane, dead, [&](uint32_t id) {
         if (part == 0) {  // this item's share of the rows of no sequence
+          const int64_t from = id * 32 + lane, step = (int64_t)ids * 32;
           if (a.fill & CSA_FILL_OUT) {
             const int64_t words = (int64_t)a.heads * a.d / 8;
-            fill_rest(a.cu_q, a.nseq, a.num_q, words, static_cast<uint4*>(a.out), id * 32 + lane, (int64_t)ids * 32);
-            if (a.rest) fill_rest(a.cu_q, a.nseq, a.num_q, words, static_cast<uint4*>(a.rest), id * 32 + lane, (int64_t)ids * 32);
+            fill_rest(a.cu_q, a.nseq, a.num_q, words, static_cast<uint4*>(a.out), from, step);
+            if (a.rest) fill_rest(a.cu_q, a.nseq, a.num_q, words, static_cast<uint4*>(a.rest), from, step);
           }
-          if (a.fill & CSA_FILL_LSE) fill_rest(a.cu_q, a.nseq, a.num_q, a.heads, -INFINITY, a.lse, id * 32 + lane, (int64_t)ids * 32);
+          if (a.fill & CSA_FILL_LSE) fill_rest(a.cu_q, a.nseq, a.num_q, a.heads, -INFINITY, a.lse, from, step);
         }
-        const Item x = item_of(a, shape, id, ids, part, lane);
-        if (x.n0 >= 0) {
-          mbar_wait(item_empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
-          if (lane == 0) {
-            st.item[k & 1] = x;
-            mbar_arrive(item_full + 8 * (k & 1));
-          }
-          ++k;
-        }
-        if (shape.split > 1 || *dead) break;
-        __syncwarp();
-        if (lane == 0) {
-          mbar_expect(steal, 16);
-          asm volatile(
-              "fence.proxy.async.shared::cta;\n\t"
-              "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                  smem_at(st.stolen)),
-              "r"(steal)
-              : "memory");
-        }
-        mbar_wait(steal, stolen & 1, dead);
-        uint32_t got, next;
-        asm volatile(
-            "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
-            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
-            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
-            : "=r"(got), "=r"(next)
-            : "r"(smem_at(st.stolen))
-            : "memory");
-        if (!got || *dead) break;
-        id = next;
-      }
-      mbar_wait(item_empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
-      if (lane == 0) {
-        st.item[k & 1].n0 = -1;
-        mbar_arrive(item_full + 8 * (k & 1));
-      }
+        return item_of(a, shape, id, ids, part, lane);
+      });
     } else if (warp == 9) {  // ---- copies
       Place<C::NS> at = {0, 0};
       uint32_t loaded = 0;  // items with keys
@@ -427,6 +367,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           key.next(2);
 #pragma unroll 1
           for (int b = 0; b < n; ++b) {
+            if (b == max(0, n - 3)) want_work(st.work, lane);
             ready(value);
             const bool more = b + 1 < n;
             if (b < n0) {
@@ -466,6 +407,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           key.next(2);
 #pragma unroll 1
           for (int b = 0; b < n; b += 2) {
+            if (b == (max(0, n - 6) & ~1)) want_work(st.work, lane);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (b + t >= n) break;
@@ -650,9 +592,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int j = 0; j < 32; ++j) o[j] = again[j];
           }
           if (!whole) {  // for the cluster; every operand of the ring has been used
-            float* const share = reinterpret_cast<float*>(ring_ptr) + i * 128 + r;
+            if (there) {
+              float* const share = reinterpret_cast<float*>(ring_ptr) + r * C::SHARE + i;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) share[j * 128] = o[j];
+              for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(share + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            }
           } else if (there && i < a.d) {
             put_columns<C>(a, row, i, o);
           }
@@ -675,48 +619,63 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   tc_after();
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   if (shape.split > 1) {
-    // Each CTA of the cluster joins its share of the columns: 32 at a time, a row a thread.
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // The CTAs of the cluster join the rows that are there, eight columns a thread.
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     const Item x = item_of(a, shape, first_id, ids, 0, lane);
-    if (x.n0 >= 0 && warp < 4) {
-      const int r = threadIdx.x, token = x.t0 + r / a.group;
-      const bool there = r < rows && token <= x.last;
-      const int64_t row = (int64_t)(x.q0 + token) * a.heads + x.kvh * a.group + r % a.group;
-      auto remote = [&](const void* p, int rank) {
-        uint32_t at;
-        float v;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_at(p)), "r"(rank));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at));
-        return v;
-      };
-      float top = -INFINITY, l = 0.0f;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const int there = x.n0 >= 0 ? (x.last - x.t0 + 1) * a.group : 0, vectors = a.d / 8;
+    const uint32_t refs = smem_at(st.ref), sums = smem_at(st.sum);
+    auto at_rank = [&](uint32_t at, int rank) {
+      uint32_t r;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+      return r;
+    };
+    auto remote = [&](uint32_t at, int rank) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at_rank(at, rank)));
+      return v;
+    };
 #pragma unroll 1
-      for (int z = 0; z < shape.split; ++z) {
-        const float ref = remote(&st.ref[r], z);
-        top = ref != ref || ref > top ? ref : top;  // NaN stays
-        if (top != top) break;
+    for (int u = part * C::THREADS + threadIdx.x; u < there * vectors; u += shape.split * C::THREADS) {
+      const int r = u / vectors, col = (u - r * vectors) * 8;
+      const uint32_t from = ring + (r * C::SHARE + col) * 4;
+      float ref[8], sum[8], o[8], l = 0.0f, top = -INFINITY;
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        ref[z] = z < shape.split ? remote(refs + 4 * r, z) : -INFINITY;
+        sum[z] = z < shape.split ? remote(sums + 4 * r, z) : 0.0f;
+        o[z] = 0.0f;
+        top = top != top || ref[z] <= top ? top : ref[z];  // NaN stays
       }
       const float safe = top == -INFINITY ? 0.0f : top;
-#pragma unroll 1
-      for (int z = 0; z < shape.split; ++z) l += ex2_approx_ftz(remote(&st.ref[r], z) - safe) * remote(&st.sum[r], z);
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        if (sum[z] == 0.0f) continue;  // no key, or no CTA
+        const float f = ex2_approx_ftz(ref[z] - safe);
+        l = fmaf(f, sum[z], l);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 4)
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3])
+                       : "r"(at_rank(from, z) + 4 * i));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], f, o[i]);
+      }
       const bool some = !(l == 0.0f);
       const float f = some ? 1.0f / l : 0.0f;
-      if (part == 0 && there) a.lse[row] = some ? (top - C::LIFT + log2f(l)) * kLn2 : -INFINITY;
-#pragma unroll 1
-      for (int i = part * 32; i < a.d; i += shape.split * 32) {
-        float o[32];
+      const int64_t row = (int64_t)(x.q0 + x.t0 + r / a.group) * a.heads + x.kvh * a.group + r % a.group;
+      if (col == 0) a.lse[row] = some ? (top - C::LIFT + log2f(l)) * kLn2 : -INFINITY;
+      uint32_t w[4], low[4];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-#pragma unroll 1
-        for (int z = 0; z < shape.split; ++z) {
-          const float fz = ex2_approx_ftz(remote(&st.ref[r], z) - safe) * f;
-          if (remote(&st.sum[r], z) == 0.0f) continue;
-          const float* share = reinterpret_cast<const float*>(ring_ptr) + i * 128 + r;
-#pragma unroll 8
-          for (int j = 0; j < 32; ++j) o[j] = fmaf(remote(share + j * 128, z), fz, o[j]);
-        }
-        if (there) put_columns<C>(a, row, i, o);
+      for (int i = 0; i < 8; ++i) o[i] = some ? o[i] * f : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = pack16<C::HALF>(o[2 * i], o[2 * i + 1]);
+        low[i] = pack16<C::HALF>(o[2 * i] - value16<C::HALF>((uint16_t)w[i]), o[2 * i + 1] - value16<C::HALF>((uint16_t)(w[i] >> 16)));
       }
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.d + col) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (a.rest) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.rest) + row * a.d + col) = make_uint4(low[0], low[1], low[2], low[3]);
     }
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -728,12 +687,17 @@ cudaError_t launch_fwd_of(const PromptArgs& a, cudaStream_t stream) {
   const int tp = 128 / a.group;
   auto items = [&](int tiles) { return ((int64_t)a.num_q / (tiles * tp) + a.nseq) * a.kv; };
   // One tile a CTA, on which both softmax groups work, where two would leave SMs without
-  // any; then, where there are SMs to spare and keys enough (four blocks a CTA), clusters.
+  // any (as a graph, two tiles against one: 4 x 255 queries on 4354 keys, 16 heads over 2,
+  // 57 us / 43; 1000 tokens 20.8 / 17.1; 2000 tokens, 252 items of one, 31.7 / 32.8). Then,
+  // where SMs are to spare and each CTA keeps two blocks of keys, clusters (one CTA, 2, 4, 8:
+  // a token over 8192 keys, 8 key heads, 64 us / 37 / 23 / 17, over 1024 13.6 / 11.9 / 10.1
+  // / 10.0). More than 128 CTAs in clusters do not all reside (38 items of 300 queries on
+  // 2300 keys: 26 / 22, and 33 with 152 CTAs; 32 of 8192 keys 66 / 39 / 29, and 50 with 256).
   FwdShape shape = {items(2) > 152 ? 2 : 1, 1};
   if (shape.tiles == 1) {
     int64_t keys = a.num_k / a.nseq;
     if (a.window && keys > (int64_t)a.window + tp) keys = (int64_t)a.window + tp;
-    while (shape.split < 8 && items(1) * shape.split * 2 <= 152 && keys >= (int64_t)shape.split * 2 * 512) shape.split *= 2;
+    while (shape.split < 8 && items(1) * shape.split * 2 <= 128 && keys >= (int64_t)shape.split * 2 * 256) shape.split *= 2;
   }
   const int64_t blocks = items(shape.tiles) * shape.split;
   CUtensorMap mq, mk, mv;

@@ -58,6 +58,105 @@ __device__ __forceinline__ void fill_rest(const int32_t* cu, int nseq, int32_t n
     to[i / heads < a ? i : i + (b - a) * heads] = v;
 }
 
+// ---- items of work -----------------------------------------------------------
+//
+// A warp of its own finds the items (type Item, n0 < 0: none): first the CTA's own, then
+// those of CTAs that have not started and are cancelled for it (cluster launch control),
+// until there are none. It looks for the next one when the warp of the matrix
+// instructions says that the last is near its end (want_work), no earlier: an item
+// taken at once would wait behind a long one while other SMs run dry (4096 tokens, 32
+// heads of 128, dK and dV: 254 us instead of 197).
+
+struct WorkState {
+  alignas(16) uint32_t stolen[4];
+  uint64_t full[2], empty[2], steal, want;
+};
+
+__device__ __forceinline__ void init_work(WorkState& w, int takers) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(smem_at(&w.full[i]), 1);
+    mbar_init(smem_at(&w.empty[i]), takers);
+  }
+  mbar_init(smem_at(&w.steal), 1);
+  mbar_init(smem_at(&w.want), 1);
+}
+
+template <class Item, class Find>
+__device__ __forceinline__ void find_work(WorkState& w, Item* slots, uint32_t id, bool once, int lane, volatile int32_t* dead,
+                                          Find find) {
+  const uint32_t full = smem_at(w.full), empty = smem_at(w.empty), steal = smem_at(&w.steal), stolen = smem_at(w.stolen);
+  int k = 0;
+  uint32_t wanted = 0;
+#pragma unroll 1
+  for (int n = 0;; ++n) {
+    const Item x = find(id);
+    if (x.n0 >= 0) {
+      mbar_wait(empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
+      if (lane == 0) {
+        slots[k & 1] = x;
+        mbar_arrive(full + 8 * (k & 1));
+      }
+      ++k;
+    }
+    if (once || *dead) break;
+    if (x.keys()) mbar_wait(smem_at(&w.want), wanted++ & 1, dead);
+    __syncwarp();
+    if (lane == 0) {
+      mbar_expect(steal, 16);
+      asm volatile(
+          "fence.proxy.async.shared::cta;\n\t"
+          "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(stolen),
+          "r"(steal)
+          : "memory");
+    }
+    mbar_wait(steal, n & 1, dead);
+    uint32_t got;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(got), "=r"(id)
+        : "r"(stolen)
+        : "memory");
+    if (!got || *dead) break;
+  }
+  mbar_wait(empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
+  if (lane == 0) {
+    slots[k & 1].n0 = -1;
+    mbar_arrive(full + 8 * (k & 1));
+  }
+}
+
+// Once for each item with work for the matrix instructions (Item::keys).
+__device__ __forceinline__ void want_work(WorkState& w, int lane) {
+  if (lane == 0) mbar_arrive(smem_at(&w.want));
+}
+
+// The k-th item, for a whole warp; its slot may be filled again after that.
+template <class Item>
+__device__ __forceinline__ Item take_work(WorkState& w, const Item* slots, int k, int lane, volatile int32_t* dead) {
+  mbar_wait(smem_at(&w.full[k & 1]), (k >> 1) & 1, dead);
+  Item x = slots[k & 1];
+  if (*dead) x.n0 = -1;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_at(&w.empty[k & 1]));
+  return x;
+}
+
+// A place in the ring, and the parity of its barriers.
+template <int NS>
+struct Place {
+  int stage;
+  uint32_t parity;
+  __device__ __forceinline__ void next(int n) {
+    stage += n;
+    if (stage >= NS) {
+      stage -= NS;
+      parity ^= 1;
+    }
+  }
+};
+
 // Half a word pair whose exponent is all ones: infinity or NaN.
 template <bool HALF>
 __device__ __forceinline__ uint32_t finite_mask(uint32_t w) {
