@@ -17,7 +17,8 @@
 // form P and dS: a lane of the accumulators a thread, half of the columns each. The
 // products of a tile go between the two phases of the arithmetic: keys kernel: dV of
 // tile j and S of j + 1 while dS(j) is formed, dK(j) and dP(j + 1) while P(j + 1) is;
-// rows kernel: dQ(j), dP(j + 1) and S(j + 2) while dS(j + 1) is.
+// rows kernel, where there is room for two tiles of dP: dQ(j), dP(j + 2) and S(j + 2)
+// while dS(j + 1) is.
 //
 // fp16: P is lifted by 2^15 and dS, whose size is that of the gradients, by a power
 // of two that the largest grad and v allow (prompt_delta_kernel finds them), so that
@@ -575,6 +576,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         tc_commit_by(leader, dp_full);
       };
       auto add = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t ready, uint32_t j, bool first) {
+        // An item's first product writes over the last one's sums: both groups of the
+        // arithmetic have read them when both have formed something of this item.
+        if (first) mbar_wait(ready + 8, j & 1, dead);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           mbar_wait(ready + 8 * half, j & 1, dead);
@@ -677,8 +681,8 @@ struct alignas(16) RowsItem {
 struct RowsState {
   RowsItem item[2];
   WorkState work;
-  uint64_t q_full, q_empty, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], s_full[2],
-      dp_full, ds_full[2], done;
+  uint64_t q_full, q_empty, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], s_full,
+      s_empty, dp_full[2], ds_full[2][2], done;  // ds_full: the arithmetic may be a block ahead
   int32_t dead, bad;
   uint32_t tmem;
 };
@@ -694,7 +698,7 @@ __device__ __forceinline__ bool rows_mixed(const PromptArgs& a, const RowsItem& 
 struct RowsMath {
   uint8_t* k_ptr;
   volatile int32_t* dead;
-  uint32_t s_at, dp_at, s_full, dp_full, ds_full;
+  uint32_t s_at, dp_at, s_full, s_empty, dp_full, ds_full;
   int32_t* bad;
   int lo, hi;  // keys that the row sees, from this thread's half of block 0 on
   bool single;
@@ -708,15 +712,18 @@ __device__ __forceinline__ void rows_step(const RowsMath& m, uint32_t j, uint32_
   const int lane = threadIdx.x & 31;
   const float2 c2 = make_float2(m.c, m.c), f2 = make_float2(m.f, m.f), l2 = make_float2(m.lse, m.lse),
                d2 = make_float2(m.delta, m.delta);
-  const uint32_t s_at = m.s_at + 128 * (j & 1);
-  mbar_wait(m.s_full + 8 * (j & 1), (j >> 1) & 1, m.dead);
+  const uint32_t dp_at = m.dp_at + 128 * (j & 1);
+  mbar_wait(m.s_full, j & 1, m.dead);
   tc_after();
   float p[64], d[64];
-  tc_load32_async(s_at, p);
-  tc_load32_async(s_at + 32, p + 32);
+  tc_load32_async(m.s_at, p);
+  tc_load32_async(m.s_at + 32, p + 32);
   tc_load_wait();
   tc_loaded(p);
   tc_loaded(p + 32);
+  tc_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(m.s_empty);
 #pragma unroll
   for (int k = 0; k < 64; k += 2) {
     const float2 z = fma2_rn(make_float2(p[k], p[k + 1]), c2, l2);
@@ -724,12 +731,12 @@ __device__ __forceinline__ void rows_step(const RowsMath& m, uint32_t j, uint32_
     p[k + 1] = ex2_approx_ftz(z.y);
   }
   if constexpr (SOME) clean_operand<C::HALF>(m.k_ptr + k_stage * C::TILE, C::TILE, threadIdx.x, 256, m.bad);
-  mbar_wait(m.dp_full, j & 1, m.dead);
+  mbar_wait(m.dp_full + 8 * (j & 1), (j >> 1) & 1, m.dead);
   tc_after();
-  tc_load32_async(m.dp_at, d);
+  tc_load32_async(dp_at, d);
   tc_load_wait();
   tc_loaded(d);
-  tc_load32_async(m.dp_at + 32, d + 32);
+  tc_load32_async(dp_at + 32, d + 32);
 #pragma unroll
   for (int part = 0; part < 64; part += 32) {
     if (part) {
@@ -755,12 +762,12 @@ __device__ __forceinline__ void rows_step(const RowsMath& m, uint32_t j, uint32_
         d[k + 1] = first + k + 1 < m.hi && first + k + 1 >= m.lo ? d[k + 1] : 0.0f;
       }
     }
-    store_part<C::HALF>(s_at + part / 2, d + part);
+    store_part<C::HALF>(dp_at + part / 2, d + part);
   }
   tc_store_wait();
   tc_before();
   __syncwarp();
-  if (lane == 0) mbar_arrive(m.ds_full);
+  if (lane == 0) mbar_arrive(m.ds_full + 16 * (j & 1));
 }
 template <class C>
 __device__ __noinline__ void rows_step_some(const RowsMath& m, uint32_t j, uint32_t k_stage, int first) {
@@ -783,7 +790,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t q_at = smem_at(base + 1024), g_at = q_at + C::TILE, k_at = smem_at(k_ptr), v_at = k_at + kKeyStages * C::TILE;
   const uint32_t q_full = smem_at(&st.q_full), q_empty = smem_at(&st.q_empty), k_full = smem_at(st.k_full),
                  k_empty = smem_at(st.k_empty), v_full = smem_at(st.v_full), v_empty = smem_at(st.v_empty),
-                 s_full = smem_at(st.s_full), dp_full = smem_at(&st.dp_full), ds_full = smem_at(st.ds_full), done = smem_at(&st.done);
+                 s_full = smem_at(&st.s_full), s_empty = smem_at(&st.s_empty), dp_full = smem_at(st.dp_full),
+                 ds_full = smem_at(st.ds_full), done = smem_at(&st.done);
   volatile int32_t* const dead = &st.dead;
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
@@ -800,11 +808,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(s_full, 1);
-    mbar_init(s_full + 8, 1);
+    mbar_init(s_empty, 8);
     mbar_init(dp_full, 1);
+    mbar_init(dp_full + 8, 1);
     mbar_init(done, 1);
-    mbar_init(ds_full, 4);
-    mbar_init(ds_full + 8, 4);
+    for (int i = 0; i < 4; ++i) mbar_init(ds_full + 8 * i, 4);
     init_work(st.work, 11);  // eight warps of the arithmetic, two of copies, matrix instructions
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -889,24 +897,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
       }
     } else if (warp == 8) {  // ---- matrix instructions
-      const uint32_t leader = tc_leader(), tm = uniform(tmem), S = tm, DP = tm + 256, DQ = tm + 384;
+      const uint32_t leader = tc_leader(), tm = uniform(tmem), S = tm, DP = tm + 128, DQ = tm + 384;
       Place<kKeyStages> key = {0, 0}, used = {0, 0};  // of the next S, of the next dQ
       Place<kValueStages> value = {0, 0};
-      uint32_t scored = 0, added = 0, items = 0;
+      uint32_t scored = 0, weighed = 0, added = 0, items = 0;
       auto scores = [&]() {
         mbar_wait(k_full + 8 * key.stage, key.parity, dead);
+        mbar_wait(s_empty, (scored & 1) ^ 1, dead);
         tc_after();
-        product<C>(leader, S + 128 * (scored & 1), q_at, k_at + key.stage * C::TILE);
-        tc_commit_by(leader, s_full + 8 * (scored & 1));
+        product<C>(leader, S, q_at, k_at + key.stage * C::TILE);
+        tc_commit_by(leader, s_full);
         ++scored;
         key.next(1);
       };
       auto weights = [&]() {  // dP
         mbar_wait(v_full + 8 * value.stage, value.parity, dead);
         tc_after();
-        product<C>(leader, DP, g_at, v_at + value.stage * C::TILE);
+        product<C>(leader, DP + 128 * (weighed & 1), g_at, v_at + value.stage * C::TILE);
         tc_commit_by(leader, v_empty + 8 * value.stage);
-        tc_commit_by(leader, dp_full);
+        tc_commit_by(leader, dp_full + 8 * (weighed & 1));
+        ++weighed;
         value.next(1);
       };
 #pragma unroll 1
@@ -919,23 +929,31 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ++items;
         scores();
         weights();
-        if (n > 1) scores();
-        if (n == 1) tc_commit_by(leader, q_empty);
+        if (n > 1) {
+          weights();
+          scores();
+        }
+        if (n <= 2) tc_commit_by(leader, q_empty);
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
           if (j == max(0, n - 3)) want_work(st.work, lane);
+          const uint32_t ready = ds_full + 16 * (added & 1), parity = (added >> 1) & 1;
+          // the item's first product writes over sums that both groups have to have read
+          if (j == 0) mbar_wait(ready + 8, parity, dead);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            mbar_wait(ds_full + 8 * half, added & 1, dead);
+            mbar_wait(ready + 8 * half, parity, dead);
             tc_after();
-            product_add<C>(leader, DQ, S + 128 * (added & 1), k_at + used.stage * C::TILE, half, j > 0 || half > 0);
+            product_add<C>(leader, DQ, DP + 128 * (added & 1), k_at + used.stage * C::TILE, half, j > 0 || half > 0);
           }
           ++added;
           tc_commit_by(leader, k_empty + 8 * used.stage);
           used.next(1);
-          if (j + 1 < n) weights();
-          if (j + 2 < n) scores();
-          if (j + 2 == n) tc_commit_by(leader, q_empty);
+          if (j + 2 < n) {
+            weights();
+            scores();
+            if (j + 3 == n) tc_commit_by(leader, q_empty);
+          }
         }
         tc_commit_by(leader, done);
       }
@@ -945,7 +963,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int half = warp >> 2, col = half * 64, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int in_tile = r / a.group, head = r - in_tile * a.group, e = gradient_exponent<C::HALF>(b);
-    RowsMath m = {k_ptr, dead, tmem + lanes + col, tmem + 256 + lanes + col, s_full, dp_full, ds_full + 8 * half, &st.bad, 0, 0, false,
+    RowsMath m = {k_ptr, dead, tmem + lanes + col, tmem + 128 + lanes + col, s_full, s_empty, dp_full, ds_full + 8 * half, &st.bad, 0, 0, false,
                   a.scale * kLog2e, C::HALF ? exp2f((float)-e) : 1.0f, 0.0f, 0.0f};
     uint32_t tiles = 0, items = 0;
 #pragma unroll 1
