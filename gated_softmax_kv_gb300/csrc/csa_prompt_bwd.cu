@@ -253,7 +253,7 @@ struct KeysState {
   alignas(16) int32_t hi[2][128];
   KeysItem item[2];
   WorkState work;
-  uint64_t kv_full, kv_empty, q_full[2], q_empty[2], g_full[2], g_empty[2], r_full[2], s_full, p_full[2], dp_full, ds_full[2], done;
+  uint64_t kv_full, kv_empty, q_full[2], q_empty[2], g_full[2], g_empty[2], r_full[2], s_full, p_full[2], dp_full, ds_full[2], done, clean[2];
   int32_t dead, bad;
   uint32_t tmem;
 };
@@ -292,9 +292,8 @@ __device__ __noinline__ void give_back_grad(const PromptArgs& a, const KeysItem&
 
 // What the arithmetic of the keys kernel's tiles needs.
 struct KeysMath {
-  uint8_t *q_ptr, *g_ptr;
   volatile int32_t* dead;
-  uint32_t s_at, dp_at, r_full, s_full, g_full, p_full, dp_full, ds_full;
+  uint32_t s_at, dp_at, r_full, s_full, p_full, dp_full, ds_full;
   int col, key;
   float c, f;
 };
@@ -307,10 +306,6 @@ __device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, uint
   const int stage = j & 1, key = m.key, lane = threadIdx.x & 31;
   const float2 c2 = make_float2(m.c, m.c), f2 = make_float2(m.f, m.f);
   mbar_wait(m.r_full + 8 * stage, (j >> 1) & 1, m.dead);
-  if constexpr (SOME) {
-    mbar_wait(m.g_full + 8 * stage, (j >> 1) & 1, m.dead);
-    clean_operand<HALF>(m.g_ptr + stage * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
-  }
   mbar_wait(m.s_full, j & 1, m.dead);
   tc_after();
   float p[64], d[64];
@@ -349,7 +344,6 @@ __device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, uint
   __syncwarp();
   if (lane == 0) mbar_arrive(m.p_full);
 
-  if constexpr (SOME) clean_operand<HALF>(m.q_ptr + stage * C::TILE, C::TILE, threadIdx.x, 256, &st.bad);
   mbar_wait(m.dp_full, j & 1, m.dead);
   tc_after();
   tc_load32_async(m.dp_at, d);
@@ -423,12 +417,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t kv_full = smem_at(&st.kv_full), kv_empty = smem_at(&st.kv_empty), q_full = smem_at(st.q_full),
                  q_empty = smem_at(st.q_empty), g_full = smem_at(st.g_full), g_empty = smem_at(st.g_empty),
                  r_full = smem_at(st.r_full), s_full = smem_at(&st.s_full), p_full = smem_at(st.p_full),
-                 dp_full = smem_at(&st.dp_full), ds_full = smem_at(st.ds_full), done = smem_at(&st.done);
+                 dp_full = smem_at(&st.dp_full), ds_full = smem_at(st.ds_full), done = smem_at(&st.done),
+                 clean = smem_at(st.clean);
   volatile int32_t* const dead = &st.dead;
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
+      mbar_init(clean + 8 * i, 1);
       mbar_init(q_full + 8 * i, 1);
       mbar_init(q_empty + 8 * i, 1);
       mbar_init(g_full + 8 * i, 1);
@@ -522,7 +518,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
         ++loaded;
       }
-    } else if (warp == 10) {  // ---- the rows' numbers, with the tile of q
+    } else if (warp == 10) {  // ---- the rows' numbers, with the tile of q; cleaning
       const float f = C::HALF ? exp2f((float)-gradient_exponent<C::HALF>(b)) : 1.0f;
       uint32_t tiles = 0;
       int token[4], head[4];
@@ -558,11 +554,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(r_full + 8 * stage);
+          if (keys_mixed(a, x, j)) {  // infinities and NaN of rows that do not see every key
+            const uint32_t parity = (tiles >> 1) & 1;
+            mbar_wait(q_full + 8 * stage, parity, dead);
+            clean_operand<C::HALF>(q_ptr + stage * C::TILE, C::TILE, lane, &st.bad);
+            mbar_wait(g_full + 8 * stage, parity, dead);
+            clean_operand<C::HALF>(g_ptr + stage * C::TILE, C::TILE, lane, &st.bad);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(clean + 8 * stage);
+          }
         }
       }
     } else if (warp == 8) {  // ---- matrix instructions
       const uint32_t leader = tc_leader(), tm = uniform(tmem), S = tm, DP = tm + 128, DV = tm + 256, DK = tm + 256 + C::DP;
-      uint32_t tiles = 0, items = 0;
+      uint32_t tiles = 0, items = 0, cleaned = 0;  // cleaned: a parity a stage
       auto scores = [&](uint32_t j) {
         mbar_wait(q_full + 8 * (j & 1), (j >> 1) & 1, dead);
         tc_after();
@@ -599,6 +604,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++tiles) {
           if (j == max(0, n - 3)) want_work(st.work, lane);
+          if (keys_mixed(a, x, j)) {
+            mbar_wait(clean + 8 * (tiles & 1), (cleaned >> (tiles & 1)) & 1, dead);
+            cleaned ^= 1u << (tiles & 1);
+            tc_after();
+          }
           add(DV, S, g_at + (tiles & 1) * C::TILE, p_full, tiles, j == 0);
           tc_commit_by(leader, g_empty + 8 * (tiles & 1));
           if (j + 1 < n) scores(tiles + 1);
@@ -617,8 +627,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int half = warp >> 2, col = half * 64;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int e = gradient_exponent<C::HALF>(b);
-    KeysMath m = {q_ptr, g_ptr, dead, tmem + lanes + col, tmem + 128 + lanes + col, r_full, s_full, g_full, p_full + 8 * half,
-                  dp_full, ds_full + 8 * half, col, 0, a.scale * kLog2e, C::HALF ? exp2f((float)-e) : 1.0f};
+    KeysMath m = {dead, tmem + lanes + col, tmem + 128 + lanes + col, r_full, s_full, p_full + 8 * half, dp_full,
+                  ds_full + 8 * half, col, 0, a.scale * kLog2e, C::HALF ? exp2f((float)-e) : 1.0f};
     uint32_t tiles = 0, items = 0;
 #pragma unroll 1
     for (int k = 0;; ++k) {
@@ -639,7 +649,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int64_t row = ((int64_t)(x.w.k0 + m.key) * a.kv + x.kvh) * a.d;
       float factor = half ? a.scale * (C::HALF ? exp2f((float)(e - 15)) : 1.0f) : (C::HALF ? exp2f(-15.0f) : 1.0f);
       if (*dead) factor = NAN;
-      // what the other group has found is known: its last dS came after, and `done` after that
+      // cleaned before the products that `done` stands for
       const bool bad = half == 0 && *(volatile int32_t*)&st.bad != 0;
 #pragma unroll 1
       for (int i = 0; i < C::DP; i += 32) {
@@ -681,8 +691,8 @@ struct alignas(16) RowsItem {
 struct RowsState {
   RowsItem item[2];
   WorkState work;
-  uint64_t q_full, q_empty, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], s_full,
-      s_empty, dp_full[2], ds_full[2][2], done;  // ds_full: the arithmetic may be a block ahead
+  uint64_t q_full, q_empty, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], clean[kKeyStages],
+      s_full, s_empty, dp_full[2], ds_full[2][2], done;  // ds_full: the arithmetic may be a block ahead
   int32_t dead, bad;
   uint32_t tmem;
 };
@@ -696,10 +706,8 @@ __device__ __forceinline__ bool rows_mixed(const PromptArgs& a, const RowsItem& 
 
 // What the arithmetic of a row's blocks needs.
 struct RowsMath {
-  uint8_t* k_ptr;
   volatile int32_t* dead;
   uint32_t s_at, dp_at, s_full, s_empty, dp_full, ds_full;
-  int32_t* bad;
   int lo, hi;  // keys that the row sees, from this thread's half of block 0 on
   bool single;
   float c, f, lse, delta;
@@ -708,7 +716,7 @@ struct RowsMath {
 // dS of the CTA's j-th block for a row and 64 keys, the first of them `first` behind the
 // item's first; SOME: some row does not see some key.
 template <class C, bool SOME>
-__device__ __forceinline__ void rows_step(const RowsMath& m, uint32_t j, uint32_t k_stage, int first) {
+__device__ __forceinline__ void rows_step(const RowsMath& m, uint32_t j, int first) {
   const int lane = threadIdx.x & 31;
   const float2 c2 = make_float2(m.c, m.c), f2 = make_float2(m.f, m.f), l2 = make_float2(m.lse, m.lse),
                d2 = make_float2(m.delta, m.delta);
@@ -730,7 +738,6 @@ __device__ __forceinline__ void rows_step(const RowsMath& m, uint32_t j, uint32_
     p[k] = ex2_approx_ftz(z.x);
     p[k + 1] = ex2_approx_ftz(z.y);
   }
-  if constexpr (SOME) clean_operand<C::HALF>(m.k_ptr + k_stage * C::TILE, C::TILE, threadIdx.x, 256, m.bad);
   mbar_wait(m.dp_full + 8 * (j & 1), (j >> 1) & 1, m.dead);
   tc_after();
   tc_load32_async(dp_at, d);
@@ -770,8 +777,8 @@ __device__ __forceinline__ void rows_step(const RowsMath& m, uint32_t j, uint32_
   if (lane == 0) mbar_arrive(m.ds_full + 16 * (j & 1));
 }
 template <class C>
-__device__ __noinline__ void rows_step_some(const RowsMath& m, uint32_t j, uint32_t k_stage, int first) {
-  rows_step<C, true>(m, j, k_stage, first);
+__device__ __noinline__ void rows_step_some(const RowsMath& m, uint32_t j, int first) {
+  rows_step<C, true>(m, j, first);
 }
 
 template <class C>
@@ -791,12 +798,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t q_full = smem_at(&st.q_full), q_empty = smem_at(&st.q_empty), k_full = smem_at(st.k_full),
                  k_empty = smem_at(st.k_empty), v_full = smem_at(st.v_full), v_empty = smem_at(st.v_empty),
                  s_full = smem_at(&st.s_full), s_empty = smem_at(&st.s_empty), dp_full = smem_at(st.dp_full),
-                 ds_full = smem_at(st.ds_full), done = smem_at(&st.done);
+                 ds_full = smem_at(st.ds_full), done = smem_at(&st.done), clean = smem_at(st.clean);
   volatile int32_t* const dead = &st.dead;
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
 #pragma unroll 1
     for (int i = 0; i < kKeyStages; ++i) {
+      mbar_init(clean + 8 * i, 1);
       mbar_init(k_full + 8 * i, 1);
       mbar_init(k_empty + 8 * i, 1);
     }
@@ -813,7 +821,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     mbar_init(dp_full + 8, 1);
     mbar_init(done, 1);
     for (int i = 0; i < 4; ++i) mbar_init(ds_full + 8 * i, 4);
-    init_work(st.work, 11);  // eight warps of the arithmetic, two of copies, matrix instructions
+    init_work(st.work, 11);  // eight warps of the arithmetic, copies, cleaning, matrix instructions
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) {
@@ -849,8 +857,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         x.n0 = x.off + x.t1 > 0 ? (x.off + x.t1 + 127) / 128 - x.kb0 : 0;
         return x;
       });
-    } else if (warp == 9) {  // ---- copies of q, grad and keys
+    } else if (warp == 9) {  // ---- copies
       Place<kKeyStages> at = {0, 0};
+      Place<kValueStages> value = {0, 0};
       uint32_t loaded = 0, tiles = 0;
 #pragma unroll 1
       for (int k = 0;; ++k) {
@@ -868,39 +877,44 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             mbar_expect(k_full + 8 * at.stage, C::TILE);
             load_tile<C>(k_at + at.stage * C::TILE, &mk, x.kvh, x.w.k0 + (x.kb0 + j) * 128, k_full + 8 * at.stage);
             at.next(1);
+            mbar_wait(v_empty + 8 * value.stage, value.parity ^ 1, dead);
+            mbar_expect(v_full + 8 * value.stage, C::TILE);
+            load_tile<C>(v_at + value.stage * C::TILE, &mv, x.kvh, x.w.k0 + (x.kb0 + j) * 128, v_full + 8 * value.stage);
+            value.next(1);
           }
           if (*dead) {
             drain(q_full, 1, loaded + 1);
             drain(k_full, kKeyStages, tiles);
+            drain(v_full, kValueStages, tiles);
           }
         }
         __syncwarp();
         ++loaded;
       }
-    } else if (warp == 10) {  // ---- copies of values
-      Place<kValueStages> at = {0, 0};
-      uint32_t tiles = 0;
+    } else if (warp == 10) {  // ---- infinities and NaN of keys that not every row sees
+      Place<kKeyStages> at = {0, 0};
 #pragma unroll 1
       for (int k = 0;; ++k) {
         const RowsItem x = take(k);
         if (x.n0 < 0) break;
-        if (lane == 0) {
 #pragma unroll 1
-          for (int j = 0; j < x.n0 && !*dead; ++j, ++tiles) {
-            mbar_wait(v_empty + 8 * at.stage, at.parity ^ 1, dead);
-            mbar_expect(v_full + 8 * at.stage, C::TILE);
-            load_tile<C>(v_at + at.stage * C::TILE, &mv, x.kvh, x.w.k0 + (x.kb0 + j) * 128, v_full + 8 * at.stage);
-            at.next(1);
+        for (int j = 0; j < x.n0; ++j) {
+          // every block is waited for: a parity tells only whether the one before it in its
+          // place has come
+          mbar_wait(k_full + 8 * at.stage, at.parity, dead);
+          if (rows_mixed(a, x, j)) {
+            clean_operand<C::HALF>(k_ptr + at.stage * C::TILE, C::TILE, lane, &st.bad);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(clean + 8 * at.stage);
           }
-          if (*dead) drain(v_full, kValueStages, tiles);
+          at.next(1);
         }
-        __syncwarp();
       }
     } else if (warp == 8) {  // ---- matrix instructions
       const uint32_t leader = tc_leader(), tm = uniform(tmem), S = tm, DP = tm + 128, DQ = tm + 384;
       Place<kKeyStages> key = {0, 0}, used = {0, 0};  // of the next S, of the next dQ
       Place<kValueStages> value = {0, 0};
-      uint32_t scored = 0, weighed = 0, added = 0, items = 0;
+      uint32_t scored = 0, weighed = 0, added = 0, items = 0, cleaned = 0;  // cleaned: a parity a stage
       auto scores = [&]() {
         mbar_wait(k_full + 8 * key.stage, key.parity, dead);
         mbar_wait(s_empty, (scored & 1) ^ 1, dead);
@@ -938,6 +952,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int j = 0; j < n; ++j) {
           if (j == max(0, n - 3)) want_work(st.work, lane);
           const uint32_t ready = ds_full + 16 * (added & 1), parity = (added >> 1) & 1;
+          if (rows_mixed(a, x, j)) {
+            mbar_wait(clean + 8 * used.stage, (cleaned >> used.stage) & 1, dead);
+            cleaned ^= 1u << used.stage;
+          }
           // the item's first product writes over sums that both groups have to have read
           if (j == 0) mbar_wait(ready + 8, parity, dead);
 #pragma unroll
@@ -963,7 +981,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int half = warp >> 2, col = half * 64, r = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int in_tile = r / a.group, head = r - in_tile * a.group, e = gradient_exponent<C::HALF>(b);
-    RowsMath m = {k_ptr, dead, tmem + lanes + col, tmem + 128 + lanes + col, s_full, s_empty, dp_full, ds_full + 8 * half, &st.bad, 0, 0, false,
+    RowsMath m = {dead, tmem + lanes + col, tmem + 128 + lanes + col, s_full, s_empty, dp_full, ds_full + 8 * half, 0, 0, false,
                   a.scale * kLog2e, C::HALF ? exp2f((float)-e) : 1.0f, 0.0f, 0.0f};
     uint32_t tiles = 0, items = 0;
 #pragma unroll 1
@@ -983,9 +1001,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
       for (int j = 0; j < x.n0; ++j, ++tiles) {
         if (rows_mixed(a, x, j))
-          rows_step_some<C>(m, tiles, tiles % kKeyStages, j * 128);
+          rows_step_some<C>(m, tiles, j * 128);
         else
-          rows_step<C, false>(m, tiles, 0, 0);
+          rows_step<C, false>(m, tiles, 0);
       }
       if (x.n0 > 0) mbar_wait(done, items++ & 1, dead);
       tc_after();

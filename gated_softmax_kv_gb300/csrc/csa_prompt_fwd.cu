@@ -25,8 +25,8 @@
 // weights are of what is not rounded yet.
 //
 // Blocks that some row of the CTA does not see in full are cleaned of infinities and
-// NaN in V, which a weight of 0 would not keep out; rows that do see one get it back
-// from memory at the end.
+// NaN in V, which a weight of 0 would not keep out, by a warp of its own; rows that do
+// see one get it back from memory at the end.
 //
 // Every wait on an mbarrier is bounded: a wait that runs out marks the CTA, whose
 // later waits return at once and whose results become NaN.
@@ -42,10 +42,11 @@ namespace csa {
 
 namespace {
 
-template <int DP_, bool HALF_>
+template <int DP_, bool HALF_, bool WINDOW_>
 struct Fwd {
   static constexpr int DP = DP_;                  // columns, padded to a slab of 64
   static constexpr bool HALF = HALF_;
+  static constexpr bool WINDOW = WINDOW_;
   static constexpr int SLAB = 16384;              // 128 rows x 64 columns
   static constexpr int TILE = DP / 64 * SLAB;
   static constexpr int NS = DP == 128 ? 5 : 8;    // tiles of the ring
@@ -78,22 +79,33 @@ template <int NS>
 struct State {
   Item item[2];
   WorkState work;
-  uint64_t full[NS], empty[NS], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], pair_full, pair_empty;
+  uint64_t full[NS], empty[NS], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], pair_full, pair_empty, clean[NS];
   int32_t dead, bad;
   uint32_t tmem;
   float ref[128], sum[128];  // group 1's, for group 0; in a cluster: the CTA's
 };
 
 // The order of the ring: K0 V0 K1 V1 ... or, where the groups take alternate blocks, K0
-// K1 V0 K2 V1 ...: the position of block b's values.
-__device__ __forceinline__ int values_at(int b, int n, int step) {
-  return step == 1 ? 2 * b + 1 : b < n - 1 ? 2 * b + 2 : 2 * n - 1;
+// K1 V0 K2 V1 ...: the block of an item's i-th tile, and whether it is of values.
+__device__ __forceinline__ int tile_at(int i, int n, int step, bool& value) {
+  if (step == 1) {
+    value = i & 1;
+    return i / 2;
+  }
+  value = i == 2 * n - 1 || (i > 1 && (i & 1) == 0);
+  return i == 2 * n - 1 ? n - 1 : value ? i / 2 - 1 : (i + 1) / 2;
 }
 
-// Whether some row of tokens ta .. tb does not see all of block b.
-__device__ __forceinline__ bool mixed(const PromptArgs& a, const Item& x, int b, int ta, int tb) {
-  const int first = (x.kb0 + b) * 128;
-  return first + 128 > x.off + ta + 1 || (a.window && (int64_t)first < (int64_t)x.off + tb + 1 - a.window);
+// The blocks [from, to) that every row of tokens ta .. tb sees in full.
+struct Seen {
+  int from, to;
+  __device__ __forceinline__ bool all(int b) const { return b >= from && b < to; }
+};
+__device__ __forceinline__ Seen seen_by(const PromptArgs& a, const Item& x, int ta, int tb) {
+  Seen s;
+  s.to = max(x.off + ta + 1, 0) / 128 - x.kb0;
+  s.from = a.window ? (int)((max((int64_t)x.off + tb + 1 - a.window, (int64_t)0) + 127) / 128) - x.kb0 : 0;
+  return s;
 }
 
 extern __shared__ __align__(1024) uint8_t fwd_smem[];
@@ -102,9 +114,10 @@ extern __shared__ __align__(1024) uint8_t fwd_smem[];
 // keys lo .. hi - 1.
 template <bool HALF>
 __device__ __noinline__ void give_back(const PromptArgs& a, const Item& x, int lo, int hi, int col, float* o) {
+  const Seen seen = seen_by(a, x, x.t0, x.last);
 #pragma unroll 1
   for (int b = 0; b < max(x.n0, x.n1); ++b) {
-    if (!mixed(a, x, b, x.t0, x.last)) continue;
+    if (seen.all(b)) continue;
     const int k0 = max(lo, (x.kb0 + b) * 128), k1 = min(hi, (x.kb0 + b) * 128 + 128);
 #pragma unroll 1
     for (int k = k0; k < k1; ++k) {
@@ -209,7 +222,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t q_at = smem_at(q_ptr), ring = smem_at(ring_ptr);
   const uint32_t full = smem_at(st.full), empty = smem_at(st.empty), q_full = smem_at(&st.q_full),
                  q_empty = smem_at(&st.q_empty), s_full = smem_at(st.s_full), p_full = smem_at(st.p_full),
-                 o_full = smem_at(st.o_full), pair_full = smem_at(&st.pair_full), pair_empty = smem_at(&st.pair_empty);
+                 o_full = smem_at(st.o_full), pair_full = smem_at(&st.pair_full), pair_empty = smem_at(&st.pair_empty),
+                 clean = smem_at(st.clean);
   volatile int32_t* const dead = &st.dead;
   const int tp = 128 / a.group, rows = tp * a.group;
   const uint32_t ids = gridDim.x / shape.split, first_id = blockIdx.x / shape.split;
@@ -220,6 +234,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
+      mbar_init(clean + 8 * i, 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -232,7 +247,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(p_full + 16 * t + 8, 4);
       mbar_init(o_full + 8 * t, 1);
     }
-    init_work(st.work, 10);  // eight softmax warps, copies, matrix instructions
+    init_work(st.work, 11);  // eight softmax warps, copies, cleaning, matrix instructions
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) {
@@ -260,6 +275,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         return item_of(a, shape, id, ids, part, lane);
       });
+    } else if (warp == 11) {  // ---- infinities and NaN of values that not every row sees
+      // Every tile of the ring is waited for, keys too: a parity tells only whether the
+      // tile before it in its place has come.
+      Place<C::NS> at = {0, 0};
+#pragma unroll 1
+      for (int k = 0;; ++k) {
+        const Item x = take(k);
+        if (x.n0 < 0) break;
+        const int n = max(x.n0, x.n1);
+        const Seen seen = seen_by(a, x, x.t0, x.last);
+#pragma unroll 1
+        for (int i = 0; i < 2 * n; ++i) {
+          bool value;
+          const int b = tile_at(i, n, x.step, value);
+          mbar_wait(full + 8 * at.stage, at.parity, dead);
+          if (value && !seen.all(b)) {
+            clean_operand<C::HALF>(ring_ptr + at.stage * C::TILE, C::TILE, lane, &st.bad);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(clean + 8 * at.stage);
+          }
+          at.next(1);
+        }
+      }
     } else if (warp == 9) {  // ---- copies
       Place<C::NS> at = {0, 0};
       uint32_t loaded = 0;  // items with keys
@@ -287,14 +325,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
           for (int i = 0; i < 2 * n && !*dead; ++i) {
             bool value;
-            int b;
-            if (x.step == 1) {
-              value = i & 1;
-              b = i / 2;
-            } else {  // K0 K1 V0 K2 V1 ...
-              value = i == 2 * n - 1 || (i > 1 && (i & 1) == 0);
-              b = i == 2 * n - 1 ? n - 1 : value ? i / 2 - 1 : (i + 1) / 2;
-            }
+            const int b = tile_at(i, n, x.step, value);
             mbar_wait(empty + 8 * at.stage, at.parity ^ 1, dead);
             mbar_expect(full + 8 * at.stage, C::TILE);
 #pragma unroll 1
@@ -324,7 +355,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const uint32_t leader = tc_leader(), tm = uniform(tmem);
       const uint64_t q_op = operand(q_at, 16), k_op = operand(ring, 16), v_op = operand(ring, C::SLAB);
       Place<C::NS> start = {0, 0};
-      uint32_t loaded = 0, copies = 0, rounds[2] = {0, 0};
+      uint32_t loaded = 0, copies = 0, cleaned = 0, rounds[2] = {0, 0};  // cleaned: a parity a stage
 #pragma unroll 1
       for (int k = 0;; ++k) {
         const Item x = take(k);
@@ -332,6 +363,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (n0 < 0) break;
         const int n = max(n0, n1);
         if (n == 0) continue;
+        const Seen seen = seen_by(a, x, x.t0, x.last);
+        const int seen_from = (int)uniform((uint32_t)seen.from), seen_to = (int)uniform((uint32_t)seen.to);
         mbar_wait(q_full, loaded & 1, dead);
         ++loaded;
         // keys and values of the next block to come, of either tile
@@ -347,6 +380,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         auto ready = [&](const Place<C::NS>& p) {
           mbar_wait(full + 8 * p.stage, p.parity, dead);
           tc_after();
+        };
+        auto valued = [&](int b) {  // the values of block b are there, and clean
+          ready(value);
+          if (b < seen_from || b >= seen_to) {
+            mbar_wait(clean + 8 * value.stage, (cleaned >> value.stage) & 1, dead);
+            cleaned ^= 1u << value.stage;
+            tc_after();
+          }
         };
         auto weigh = [&](int t, int at, bool first) {  // O of tile t += its weights and the values at a place
           const uint64_t v = v_op + at * (C::TILE / 16);
@@ -368,7 +409,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
           for (int b = 0; b < n; ++b) {
             if (b == max(0, n - 3)) want_work(st.work, lane);
-            ready(value);
+            valued(b);
             const bool more = b + 1 < n;
             if (b < n0) {
               weigh(0, value.stage, b == 0);
@@ -411,7 +452,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (b + t >= n) break;
-              ready(value);
+              valued(b + t);
               weigh(t, value.stage, b == 0);
               tc_commit_by(leader, empty + 8 * value.stage);
               value.next(b + t + 2 == n ? 1 : 2);
@@ -438,26 +479,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const uint32_t s_at = tmem + lanes + C::S0 + 128 * t, o_at = tmem + lanes + C::O0 + C::DP * t;
     const float c = a.scale * kLog2e;
     const int in_tile = r / a.group, head = r - in_tile * a.group;
-    uint32_t rounds = 0, results = 0, copies = 0, pairs = 0;
+    uint32_t rounds = 0, results = 0, pairs = 0;
 #pragma unroll 1
     for (int k = 0;; ++k) {
       const Item x = take(k);
       if (x.n0 < 0) break;
-      const int n = max(x.n0, x.n1), mine = t ? x.n1 : x.n0;
+      const int mine = t ? x.n1 : x.n0;
       const int ta = x.t0 + (x.step == 1 ? t * tp : 0), tb = min(ta + tp - 1, x.last);
       const int token = ta + in_tile;
       const bool there = r < rows && token <= tb;
       const int hi = there ? x.off + token + 1 : 0;
       const int lo = a.window ? (int)max((int64_t)0, (int64_t)x.off + token + 1 - a.window) : 0;
+      const Seen seen = seen_by(a, x, ta, tb);
       float ref = -INFINITY;  // in log2 units
       float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
 #pragma unroll 1
       for (int b = x.step == 1 ? 0 : t; b < mine; b += x.step) {
-        if (mixed(a, x, b, x.t0, x.last)) {
-          const uint32_t at = copies + values_at(b, n, x.step);
-          mbar_wait(full + 8 * (at % C::NS), (at / C::NS) & 1, dead);
-          clean_operand<C::HALF>(ring_ptr + (at % C::NS) * C::TILE, C::TILE, r, 128, &st.bad);
-        }
         mbar_wait(s_full + 8 * t, rounds & 1, dead);
         ++rounds;
         tc_after();
@@ -467,18 +504,38 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         tc_load_wait();
 #pragma unroll
         for (int i = 0; i < 4; ++i) tc_loaded(v + 32 * i);
-        if (mixed(a, x, b, ta, tb)) {
-          const int k0 = (x.kb0 + b) * 128;
-          const int h = hi - k0, w = lo - k0;
+        // With a window, most of a block is hidden: which 32 columns some row of the warp
+        // sees, the others cost nothing (5003 tokens of 64 heads of 64, window 128: 140 us, so
+        // 95). Without one the branches cost more than they save (16384 tokens: 632 us, 674).
+        uint32_t some_see = 15;
+        if (!seen.all(b)) {
+          const int k0 = (x.kb0 + b) * 128, h = hi - k0, w = lo - k0;
+          if constexpr (C::WINDOW) some_see = 0;
 #pragma unroll
-          for (int i = 0; i < 128; ++i) v[i] = i < h && i >= w ? v[i] : -INFINITY;
-        }
-        float m0 = fmaxf(v[0], v[1]), m1 = fmaxf(v[2], v[3]);
+          for (int g = 0; g < 4; ++g) {
+            if constexpr (C::WINDOW) {
+              if (!__any_sync(0xFFFFFFFFu, h > 32 * g && w < 32 * g + 32 && h > w)) continue;
+              some_see |= 1u << g;
+            }
+            if (!__any_sync(0xFFFFFFFFu, h < 32 * g + 32 || w > 32 * g)) continue;
+            // bit i: column 32 g + i is seen
+            const int from = max(w - 32 * g, 0), to = min(h - 32 * g, 32);
+            const uint32_t bits = to > from ? (0xFFFFFFFFu >> (32 - (to - from))) << from : 0;
 #pragma unroll
-        for (int i = 4; i < 128; i += 4) {
-          m0 = fmaxf(m0, fmaxf(v[i], v[i + 1]));
-          m1 = fmaxf(m1, fmaxf(v[i + 2], v[i + 3]));
+            for (int i = 0; i < 32; ++i) v[32 * g + i] = bits >> i & 1 ? v[32 * g + i] : -INFINITY;
+          }
         }
+        float m0 = -INFINITY, m1 = -INFINITY;
+        auto largest = [&](int g) {
+#pragma unroll
+          for (int i = 32 * g; i < 32 * g + 32; i += 4) {
+            m0 = fmaxf(m0, fmaxf(v[i], v[i + 1]));
+            m1 = fmaxf(m1, fmaxf(v[i + 2], v[i + 3]));
+          }
+        };
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (!C::WINDOW || (some_see >> g & 1)) largest(g);
         const float z = fmaxf(m0, m1) * c;
         const bool raise = z > ref + 8.0f;
         if (__any_sync(0xFFFFFFFFu, raise)) {
@@ -500,30 +557,36 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
         const float back = C::LIFT - (ref == -INFINITY ? 0.0f : ref);
-#pragma unroll
-        for (int i = 0; i < 128; i += 32) {
+        auto weights = [&](int g, bool any) {  // of 32 columns
           uint32_t p[16];
+          if (any) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float2 za = fma2_rn(make_float2(v[i + j], v[i + j + 1]), make_float2(c, c), make_float2(back, back));
-            const float2 zb = fma2_rn(make_float2(v[i + j + 2], v[i + j + 3]), make_float2(c, c), make_float2(back, back));
-            const float2 pa = make_float2(ex2_approx_ftz(za.x), ex2_approx_ftz(za.y));
-            const float2 pb = make_float2(ex2_approx_ftz(zb.x), ex2_approx_ftz(zb.y));
-            l0 = add2_rn(l0, pa);
-            l1 = add2_rn(l1, pb);
-            p[j / 2] = pack16<C::HALF>(pa.x, pa.y);
-            p[j / 2 + 1] = pack16<C::HALF>(pb.x, pb.y);
+            for (int j = 0; j < 32; j += 4) {
+              const int i = 32 * g + j;
+              const float2 za = fma2_rn(make_float2(v[i], v[i + 1]), make_float2(c, c), make_float2(back, back));
+              const float2 zb = fma2_rn(make_float2(v[i + 2], v[i + 3]), make_float2(c, c), make_float2(back, back));
+              const float2 pa = make_float2(ex2_approx_ftz(za.x), ex2_approx_ftz(za.y));
+              const float2 pb = make_float2(ex2_approx_ftz(zb.x), ex2_approx_ftz(zb.y));
+              l0 = add2_rn(l0, pa);
+              l1 = add2_rn(l1, pb);
+              p[j / 2] = pack16<C::HALF>(pa.x, pa.y);
+              p[j / 2 + 1] = pack16<C::HALF>(pb.x, pb.y);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) p[j] = 0;
           }
-          tc_store16_async(s_at + i / 2, p);
-          if (i & 32) {  // 64 weights: their products begin
+          tc_store16_async(s_at + 16 * g, p);
+          if (g & 1) {  // 64 weights: their products begin
             tc_store_wait();
             tc_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * (i / 64));
+            if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * (g / 2));
           }
-        }
+        };
+#pragma unroll
+        for (int g = 0; g < 4; ++g) weights(g, !C::WINDOW || (some_see >> g & 1));
       }
-      copies += 2 * n;
       float l = (l0.x + l0.y) + (l1.x + l1.y);
       if (mine > 0) mbar_wait(o_full + 8 * t, results++ & 1, dead);
       tc_after();
@@ -713,11 +776,16 @@ cudaError_t launch_fwd_of(const PromptArgs& a, cudaStream_t stream) {
   return launch_dependent(kernel, dim3((unsigned)blocks), dim3(C::THREADS), C::SMEM, stream, a, shape, mq, mk, mv);
 }
 
+template <int DP, bool WINDOW>
+cudaError_t launch_fwd(const PromptArgs& a, bool half, cudaStream_t stream) {
+  return half ? launch_fwd_of<Fwd<DP, true, WINDOW>>(a, stream) : launch_fwd_of<Fwd<DP, false, WINDOW>>(a, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_prompt(const PromptArgs& a, bool half, cudaStream_t stream) {
-  if (a.d <= 64) return half ? launch_fwd_of<Fwd<64, true>>(a, stream) : launch_fwd_of<Fwd<64, false>>(a, stream);
-  return half ? launch_fwd_of<Fwd<128, true>>(a, stream) : launch_fwd_of<Fwd<128, false>>(a, stream);
+  if (a.window) return a.d <= 64 ? launch_fwd<64, true>(a, half, stream) : launch_fwd<128, true>(a, half, stream);
+  return a.d <= 64 ? launch_fwd<64, false>(a, half, stream) : launch_fwd<128, false>(a, half, stream);
 }
 
 }  // namespace csa

@@ -166,28 +166,38 @@ __device__ __forceinline__ uint32_t finite_mask(uint32_t w) {
   if ((w & (E << 16)) != (E << 16)) keep |= 0xFFFF0000u;
   return keep;
 }
+// Whether some half of the words does: an exponent of ones carries into the half's
+// sign bit, which has been cleared.
 template <bool HALF>
-__device__ __forceinline__ bool all_finite(uint4 v) {
-  return (finite_mask<HALF>(v.x) & finite_mask<HALF>(v.y) & finite_mask<HALF>(v.z) & finite_mask<HALF>(v.w)) ==
-         0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t infinite_bits(uint4 v) {
+  constexpr uint32_t E = HALF ? 0x7C007C00u : 0x7F807F80u, ONE = HALF ? 0x04000400u : 0x00800080u;
+  return (((v.x & E) + ONE) | ((v.y & E) + ONE) | ((v.z & E) + ONE) | ((v.w & E) + ONE)) & 0x80008000u;
 }
 
-// Zeros for infinities and NaN in an operand's `bytes` of shared memory, by `threads`
-// threads of which this is one; *found is set where there were any. A weight of 0 keeps
-// a finite value out of a sum, but not these.
+// Zeros for infinities and NaN in `bytes` (a multiple of 4096) of an operand in shared
+// memory, by a warp; *found is set where there were any. A weight of 0 keeps a finite
+// value out of a sum, but not these. A warp of its own does this ahead of the products: as
+// a part of the softmax it cost 3600 cycles a block (5003 tokens of 64 heads of 64 with a
+// window of 128: 140 us).
 template <bool HALF>
-__device__ __noinline__ void clean_operand(uint8_t* at, int bytes, int thread, int threads, volatile int32_t* found) {
+__device__ __forceinline__ void clean_operand(uint8_t* at, int bytes, int lane, volatile int32_t* found) {
   bool any = false;
 #pragma unroll 1
-  for (int i = thread * 16; i < bytes; i += threads * 16) {
-    uint4* p = reinterpret_cast<uint4*>(at + i);
-    const uint4 v = *p;
-    if (!all_finite<HALF>(v)) {
+  for (int i = lane * 16; i < bytes; i += 4096) {
+    uint4 v[8];
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = *reinterpret_cast<const uint4*>(at + i + k * 512);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bits |= infinite_bits<HALF>(v[k]);
+    if (bits) {
       *found = 1;
-      __threadfence_block();
-      *p = make_uint4(v.x & finite_mask<HALF>(v.x), v.y & finite_mask<HALF>(v.y), v.z & finite_mask<HALF>(v.z),
-                      v.w & finite_mask<HALF>(v.w));
       any = true;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<uint4*>(at + i + k * 512) =
+            make_uint4(v[k].x & finite_mask<HALF>(v[k].x), v[k].y & finite_mask<HALF>(v[k].y), v[k].z & finite_mask<HALF>(v[k].z),
+                       v[k].w & finite_mask<HALF>(v[k].w));
     }
   }
   if (__any_sync(0xFFFFFFFFu, any)) fence_async();
