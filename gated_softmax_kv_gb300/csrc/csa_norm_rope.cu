@@ -5,8 +5,8 @@
 // it, so a mean over the head is log2(G) shuffles and each byte is read once. For
 // the half layout a lane's vectors come in pairs half a part apart, so that both
 // columns of a pair are its own. A group keeps its columns for its whole loop:
-// frequencies and weights are worked out once, and the sines of a token serve
-// HEADS heads of it, whose loads are issued before the sines are worked out.
+// weights are read once. The lanes share a token's sines through shared memory, and
+// they serve a span of its heads, whose first loads are issued before the sines.
 //
 // The gradient reads x and grad once, works r out again, and sums its part of dw
 // in registers over the loop; the groups' sums meet in shared memory in a fixed
@@ -39,7 +39,8 @@ struct Side {
   int64_t xt, xh, gt, gh, yt, yh;
   int64_t items;   // tokens x groups of heads
   int32_t heads;
-  int32_t groups;  // of heads, a token
+  int32_t span;    // heads of an item
+  int32_t groups;  // items of a token
   int32_t blocks;  // CTAs of this side
 };
 
@@ -57,15 +58,56 @@ struct NormArgs {
   float amplitude, eps;
 };
 
+// N values of E as they are loaded: 16 bytes, or for the half layout of 16-bit types 8,
+// since a lane has two vectors of each pair (fewer registers: 16384 tokens of 40 heads of
+// 128, forward 86 us, backward 154 with 16 bytes).
+template <typename E, int N>
+struct Chunk {
+  using Raw = uint4;
+  static __device__ __forceinline__ Raw none() { return make_uint4(0, 0, 0, 0); }
+  static __device__ __forceinline__ void unpack(Raw w, float2 (&v)[N / 2]) {
+    if constexpr (sizeof(E) == 4) {
+      v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+      v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+    } else {
+      v[0] = Elem<E>::unpack(w.x);
+      v[1] = Elem<E>::unpack(w.y);
+      v[2] = Elem<E>::unpack(w.z);
+      v[3] = Elem<E>::unpack(w.w);
+    }
+  }
+  static __device__ __forceinline__ Raw pack(const float2 (&v)[N / 2]) {
+    if constexpr (sizeof(E) == 4)
+      return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+    else
+      return make_uint4(Elem<E>::pack(v[0]), Elem<E>::pack(v[1]), Elem<E>::pack(v[2]), Elem<E>::pack(v[3]));
+  }
+};
+template <typename E>
+struct Chunk<E, sizeof(E) == 2 ? 4 : -1> {
+  using Raw = uint2;
+  static __device__ __forceinline__ Raw none() { return make_uint2(0, 0); }
+  static __device__ __forceinline__ void unpack(Raw w, float2 (&v)[2]) {
+    v[0] = Elem<E>::unpack(w.x);
+    v[1] = Elem<E>::unpack(w.y);
+  }
+  static __device__ __forceinline__ Raw pack(const float2 (&v)[2]) { return make_uint2(Elem<E>::pack(v[0]), Elem<E>::pack(v[1])); }
+};
+template <typename E, bool HALF>
+constexpr int kChunk = HALF && sizeof(E) == 2 ? 4 : Vec<E>::N;
+
 template <typename E>
 __device__ __forceinline__ float weight_at(const NormArgs& a, const Side& s, int c) {
   return a.weight32 ? __ldg(static_cast<const float*>(s.weight) + c) : Elem<E>::load(static_cast<const E*>(s.weight) + c);
 }
 
-// Sum over the G lanes of a group (a power of two), the same in each.
+// Sum over the G = 4 .. 32 lanes of a group, the same in each.
 __device__ __forceinline__ float group_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
+  if (lanes > 16) v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+  if (lanes > 8) v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+  if (lanes > 4) v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+  v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+  return v + __shfl_xor_sync(0xFFFFFFFFu, v, 1);
 }
 
 // Which columns a lane has: col[k] of its vector k, -1 for none; its first pair of
@@ -103,21 +145,24 @@ __device__ __forceinline__ void columns_of(const NormArgs& a, int lane, int (&co
   }
 }
 
-// The turn of a group's vectors, and its transpose (sn negated): vectors 2j and
-// 2j + 1 are the two halves of the same pairs, or a vector has whole pairs.
-template <int N, int K, bool HALF>
-__device__ __forceinline__ void turn_vectors(float (&v)[K][N], const int (&pair)[K], const float (&cs)[K][N / 2],
-                                             const float (&sn)[K][N / 2], float sign) {
+// The turn of a group's vectors, or its transpose: vectors 2j and 2j + 1 are the two
+// halves of the same pairs, or a vector has whole pairs. Sines are those of the vector's
+// N / 2 pairs, or of the first and second half of the N pairs of two vectors.
+template <int N, int K, bool HALF, bool TRANSPOSE>
+__device__ __forceinline__ void turn_vectors(float2 (&v)[K][N / 2], const int (&pair)[K], const float (&cs)[K][N / 2],
+                                             const float (&sn)[K][N / 2]) {
   if constexpr (HALF) {
 #pragma unroll
     for (int k = 0; k < K; k += 2)
       if (pair[k] >= 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float c = cs[k + i / (N / 2)][i % (N / 2)], s = sign * sn[k + i / (N / 2)][i % (N / 2)];
-          const float x = v[k][i], y = v[k + 1][i];
-          v[k][i] = fmaf(-y, s, x * c);
-          v[k + 1][i] = fmaf(x, s, y * c);
+        for (int i = 0; i < N / 2; ++i) {
+          const int h = k + 2 * i / (N / 2), j = 2 * i % (N / 2);
+          const float2 c = make_float2(cs[h][j], cs[h][j + 1]);
+          const float2 s = TRANSPOSE ? make_float2(-sn[h][j], -sn[h][j + 1]) : make_float2(sn[h][j], sn[h][j + 1]);
+          const float2 n = make_float2(-s.x, -s.y), x = v[k][i], y = v[k + 1][i];
+          v[k][i] = fma2_rn(y, n, mul2_rn(x, c));
+          v[k + 1][i] = fma2_rn(x, s, mul2_rn(y, c));
         }
       }
   } else {
@@ -126,19 +171,38 @@ __device__ __forceinline__ void turn_vectors(float (&v)[K][N], const int (&pair)
       if (pair[k] >= 0) {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-          const float c = cs[k][i], s = sign * sn[k][i];
-          const float x = v[k][2 * i], y = v[k][2 * i + 1];
-          v[k][2 * i] = fmaf(-y, s, x * c);
-          v[k][2 * i + 1] = fmaf(x, s, y * c);
+          const float c = cs[k][i], s = TRANSPOSE ? -sn[k][i] : sn[k][i];
+          const float2 x = v[k][i];
+          v[k][i] = make_float2(fmaf(-x.y, s, x.x * c), fmaf(x.x, s, x.y * c));
         }
       }
   }
 }
 
-template <typename E, int K, bool HALF, bool BWD>
+// The last segment that begins at or before token t, by the 32 lanes of a group that is
+// a warp: two dependent loads for up to 1024 segments.
+__device__ __forceinline__ int64_t warp_position_of(const NormArgs& a, int64_t t, int lane) {
+  if (a.positions) return position_of(a, t);
+  int lo = 0, span = a.nseq;
+  while (span > 1) {
+    const int step = (span + 31) / 32, at = lo + lane * step;
+    const bool before = lane * step < span && __ldg(a.cu + at) <= t;
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, before);
+    const int k = who ? 31 - __clz(who) : 0;
+    span = min(step, span - k * step);
+    lo += k * step;
+  }
+  return t >= __ldg(a.cu + a.nseq) ? 0 : (t - __ldg(a.cu + lo)) * a.ratio;
+}
+
+// H: heads that a group has in flight; an item is a token and a.span of a side's heads.
+template <typename E, int K, int H, bool HALF, bool BWD>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int N = Vec<E>::N;
-  constexpr int H = BWD ? 2 : K >= 4 ? 2 : 4;  // heads of an item
+  constexpr int N = kChunk<E, HALF>;
+  using V = Chunk<E, N>;
+  using Raw = typename V::Raw;
+  // frequencies in turns, then each group's sines of its token
+  extern __shared__ __align__(16) uint64_t freq[];
   __shared__ float sums[BWD ? kMaxHeadDim : 1];
   grid_dependency_wait();
   allow_dependent_launch();
@@ -146,93 +210,117 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   const Side& s = a.side[second];
   const int block = (int)blockIdx.x - (second ? a.side[0].blocks : 0);
   const int lane = threadIdx.x & (a.lanes - 1), group = threadIdx.x / a.lanes, groups = kThreads / a.lanes;
+  const int pairs = a.rope / 2;
+  float2* const turns = reinterpret_cast<float2*>(freq + ((pairs + 1) & ~1)) + group * pairs;
+  for (int i = threadIdx.x; i < pairs; i += kThreads) freq[i] = turns_of(__ldg(a.freqs + i));
   int col[K], pair[K];
   columns_of<N, K, HALF>(a, lane, col, pair);
-  uint64_t f[K][N / 2];
-  float w[K][N];
+  float2 w[K][N / 2];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
+  for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int i = 0; i < N / 2; ++i)
-      f[k][i] = pair[k] >= 0 ? turns_of(__ldg(a.freqs + pair[k] + (HALF ? (k & 1) * (N / 2) : 0) + i)) : 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[k][i] = col[k] >= 0 ? weight_at<E>(a, s, col[k] + i) : 0.0f;
-  }
-  float dw[BWD ? K : 1][N];
+      w[k][i] = col[k] >= 0 ? make_float2(weight_at<E>(a, s, col[k] + 2 * i), weight_at<E>(a, s, col[k] + 2 * i + 1))
+                            : make_float2(0.0f, 0.0f);
+  float2 dw[BWD ? K : 1][N / 2];
 #pragma unroll
   for (int k = 0; k < (BWD ? K : 1); ++k)
 #pragma unroll
-    for (int i = 0; i < N; ++i) dw[k][i] = 0.0f;
+    for (int i = 0; i < N / 2; ++i) dw[k][i] = make_float2(0.0f, 0.0f);
+  __syncthreads();
   const float inv_d = 1.0f / (float)a.d;
   const int64_t step = (int64_t)s.blocks * groups;
+  const int batches = (s.span + H - 1) / H;
   // every group of a warp makes the same number of rounds: shuffles need all lanes
   const int64_t rounds = (s.items + step - 1) / step;
   for (int64_t n = 0; n < rounds; ++n) {
     const int64_t it = n * step + (int64_t)block * groups + group;
     const bool on = it < s.items;
     const int64_t token = on ? it / s.groups : 0;
-    const int head = on ? (int)(it - token * s.groups) * H : 0;
-    const int heads = on ? min(H, s.heads - head) : 0;
-    uint4 xr[H][K], gr[BWD ? H : 1][K];
+    const int first = on ? (int)(it - token * s.groups) * s.span : 0;
+    const int heads = on ? min(s.span, s.heads - first) : 0;
+    const E* const x0 = static_cast<const E*>(s.x) + token * s.xt + first * s.xh;
+    const E* const g0 = BWD ? static_cast<const E*>(s.grad) + token * s.gt + first * s.gh : nullptr;
+    E* const y0 = static_cast<E*>(s.y) + token * s.yt + first * s.yh;
+    Raw xr[H][K], gr[BWD ? H : 1][K];
+    auto load = [&](int h0) {
 #pragma unroll
-    for (int h = 0; h < H; ++h)
+      for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const bool there = h < heads && col[k] >= 0;
-        xr[h][k] = there ? *reinterpret_cast<const uint4*>(static_cast<const E*>(s.x) + token * s.xt + (head + h) * s.xh + col[k])
-                         : make_uint4(0, 0, 0, 0);
-        if constexpr (BWD)
-          gr[h][k] = there ? *reinterpret_cast<const uint4*>(static_cast<const E*>(s.grad) + token * s.gt + (head + h) * s.gh + col[k])
-                           : make_uint4(0, 0, 0, 0);
-      }
+        for (int k = 0; k < K; ++k) {
+          const bool there = h0 + h < heads && col[k] >= 0;
+          xr[h][k] = there ? *reinterpret_cast<const Raw*>(x0 + (h0 + h) * s.xh + col[k]) : V::none();
+          if constexpr (BWD)
+            gr[h][k] = there ? *reinterpret_cast<const Raw*>(g0 + (h0 + h) * s.gh + col[k]) : V::none();
+        }
+    };
+    load(0);
+    // the token's sines, a pair a lane at a time, for all of its heads
+    const int64_t pos = a.lanes == 32 ? warp_position_of(a, token, lane) : position_of(a, token);
+    __syncwarp();
+    for (int i = lane; i < pairs; i += a.lanes) {
+      float2 t;
+      turn_of(freq[i], pos, a.amplitude, 1.0f, &t.x, &t.y);
+      turns[i] = t;
+    }
+    __syncwarp();
     float cs[K][N / 2], sn[K][N / 2];
-    const int64_t pos = on ? position_of(a, token) : 0;
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if (pair[k] >= 0) {
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) turn_of(f[k][i], pos, a.amplitude, 1.0f, &cs[k][i], &sn[k][i]);
+        for (int i = 0; i < N / 2; ++i) {
+          const float2 t = turns[pair[k] + (HALF ? (k & 1) * (N / 2) : 0) + i];
+          cs[k][i] = t.x;
+          sn[k][i] = t.y;
+        }
       }
+#pragma unroll 1
+    for (int b = 0; b < batches; ++b) {
+      if (b > 0) load(b * H);
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      float x[K][N], sum = 0.0f;
+      for (int h = 0; h < H; ++h) {
+        float2 x[K][N / 2], sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        Vec<E>::unpack(xr[h][k], x[k]);
+        for (int k = 0; k < K; ++k) {
+          V::unpack(xr[h][k], x[k]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum = fmaf(x[k][i], x[k][i], sum);
-      }
-      const float r = 1.0f / sqrtf(fmaf(group_sum(sum, a.lanes), inv_d, a.eps));
-      if constexpr (!BWD) {
+          for (int i = 0; i < N / 2; ++i) sum = fma2_rn(x[k][i], x[k][i], sum);
+        }
+        // rsqrtf is within 2 ulp
+        const float r = rsqrtf(fmaf(group_sum(sum.x + sum.y, a.lanes), inv_d, a.eps));
+        const float2 r2 = make_float2(r, r);
+        const bool there = b * H + h < heads;
+        if constexpr (!BWD) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+          for (int k = 0; k < K; ++k)
 #pragma unroll
-          for (int i = 0; i < N; ++i) x[k][i] = x[k][i] * r * w[k][i];
-        turn_vectors<N, K, HALF>(x, pair, cs, sn, 1.0f);
-      } else {
-        float g[K][N], along = 0.0f;
+            for (int i = 0; i < N / 2; ++i) x[k][i] = mul2_rn(mul2_rn(x[k][i], r2), w[k][i]);
+          turn_vectors<N, K, HALF, false>(x, pair, cs, sn);
+        } else {
+          float2 g[K][N / 2], along = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int k = 0; k < K; ++k) Vec<E>::unpack(gr[h][k], g[k]);
-        turn_vectors<N, K, HALF>(g, pair, cs, sn, -1.0f);
+          for (int k = 0; k < K; ++k) V::unpack(gr[h][k], g[k]);
+          turn_vectors<N, K, HALF, true>(g, pair, cs, sn);
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+          for (int k = 0; k < K; ++k)
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            if (h < heads) dw[k][i] = fmaf(g[k][i], x[k][i] * r, dw[k][i]);
-            g[k][i] *= w[k][i];
-            along = fmaf(g[k][i], x[k][i], along);
-          }
-        const float back = group_sum(along, a.lanes) * inv_d * r * r;
+            for (int i = 0; i < N / 2; ++i) {
+              if (there) dw[k][i] = fma2_rn(g[k][i], mul2_rn(x[k][i], r2), dw[k][i]);
+              g[k][i] = mul2_rn(g[k][i], w[k][i]);
+              along = fma2_rn(g[k][i], x[k][i], along);
+            }
+          const float back = -group_sum(along.x + along.y, a.lanes) * inv_d * r * r;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+          for (int k = 0; k < K; ++k)
 #pragma unroll
-          for (int i = 0; i < N; ++i) x[k][i] = r * fmaf(-x[k][i], back, g[k][i]);
-      }
-      if (h < heads) {
+            for (int i = 0; i < N / 2; ++i) x[k][i] = mul2_rn(r2, fma2_rn(x[k][i], make_float2(back, back), g[k][i]));
+        }
+        if (there) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-          if (col[k] >= 0)
-            *reinterpret_cast<uint4*>(static_cast<E*>(s.y) + token * s.yt + (head + h) * s.yh + col[k]) = Vec<E>::pack(x[k]);
+          for (int k = 0; k < K; ++k)
+            if (col[k] >= 0) *reinterpret_cast<Raw*>(y0 + (b * H + h) * s.yh + col[k]) = V::pack(x[k]);
+        }
       }
     }
   }
@@ -243,7 +331,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
         for (int k = 0; k < K; ++k)
           if (col[k] >= 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) sums[col[k] + i] = turn == 0 ? dw[k][i] : sums[col[k] + i] + dw[k][i];
+            for (int i = 0; i < N; ++i) {
+              const float v = i & 1 ? dw[k][i / 2].y : dw[k][i / 2].x;
+              sums[col[k] + i] = turn == 0 ? v : sums[col[k] + i] + v;
+            }
           }
       }
       __syncthreads();
@@ -362,59 +453,69 @@ __global__ void __launch_bounds__(256) norm_weights_kernel(const __grid_constant
 }
 
 // CTAs of the two sides: as many as there is work for, at most `most` together,
-// shared in proportion to their items.
+// shared in proportion to their heads.
 void deal_out(NormArgs& a, int64_t per_block, int64_t most) {
   int64_t want[2];
   for (int k = 0; k < 2; ++k) want[k] = (a.side[k].items + per_block - 1) / per_block;
-  const int64_t all = want[0] + want[1];
+  const bool many = want[0] + want[1] > most;
+  const int64_t heads = a.side[0].heads + a.side[1].heads;
   for (int k = 0; k < 2; ++k) {
-    int64_t b = all > most ? want[k] * most / all : want[k];
+    int64_t b = want[k];
+    const int64_t share = most * a.side[k].heads / heads;
+    if (many && b > share) b = share;
     if (b < 1 && a.side[k].heads > 0) b = 1;  // writes dw even with no tokens
     a.side[k].blocks = (int32_t)b;
   }
 }
 
-template <typename E, int K, bool HALF, bool BWD>
+template <typename E, int K, int H, bool HALF, bool BWD>
 cudaError_t launch_vectors(NormArgs& a, cudaStream_t stream) {
-  constexpr int H = BWD ? 2 : K >= 4 ? 2 : 4;
+  auto* kernel = norm_rope_kernel<E, K, H, HALF, BWD>;
+  const int groups = kThreads / a.lanes, pairs = a.rope / 2;
+  const size_t smem = sizeof(uint64_t) * ((pairs + 1) & ~1) + sizeof(float2) * pairs * groups;  // at most 20 KB
+  const int64_t blocks = (int64_t)152 * occupancy((const void*)kernel, kThreads, smem);
   for (int k = 0; k < 2; ++k) {
-    a.side[k].groups = (a.side[k].heads + H - 1) / H;
-    a.side[k].items = a.tokens * a.side[k].groups;
+    Side& s = a.side[k];
+    // An item's heads share its sines: as many as leave each group of lanes two items.
+    // (32768 tokens of 40 heads of 128, half turned: a batch an item 174 us, all heads 116.)
+    s.span = H;
+    while (s.span < s.heads && a.tokens * ((s.heads + 2 * s.span - 1) / (2 * s.span)) >= 2 * blocks * groups) s.span *= 2;
+    s.groups = (s.heads + s.span - 1) / s.span;
+    s.items = a.tokens * s.groups;
   }
-  auto* kernel = norm_rope_kernel<E, K, HALF, BWD>;
-  deal_out(a, kThreads / a.lanes, (int64_t)152 * occupancy((const void*)kernel, kThreads, 0));
-  return launch_dependent(kernel, dim3((unsigned)(a.side[0].blocks + a.side[1].blocks)), dim3(kThreads), 0, stream, a);
+  deal_out(a, groups, blocks);
+  return launch_dependent(kernel, dim3((unsigned)(a.side[0].blocks + a.side[1].blocks)), dim3(kThreads), smem, stream, a);
+}
+
+// One head a token, or several in flight.
+template <typename E, int K, bool HALF, bool BWD>
+cudaError_t launch_heads(NormArgs& a, cudaStream_t stream) {
+  constexpr int columns = K * kChunk<E, HALF>, most = BWD ? 16 : 32;  // of a lane; in flight
+  constexpr int H = columns < most ? most / columns : 1;
+  if (a.side[0].heads == 1 && a.side[1].heads <= 1) return launch_vectors<E, K, 1, HALF, BWD>(a, stream);
+  return launch_vectors<E, K, H, HALF, BWD>(a, stream);
 }
 
 template <typename E, bool HALF, bool BWD>
 cudaError_t launch_kind(NormArgs& a, bool vectors, cudaStream_t stream) {
-  constexpr int N = Vec<E>::N;
+  constexpr int N = kChunk<E, HALF>;
   if (!vectors) {
     for (int k = 0; k < 2; ++k) a.side[k].items = a.tokens * a.side[k].heads;
     deal_out(a, kThreads / 32, 152 * 8);
     return launch_dependent(norm_rope_any_kernel<E, HALF, BWD>, dim3((unsigned)(a.side[0].blocks + a.side[1].blocks)),
                             dim3(kThreads), 0, stream, a);
   }
-  // units that lanes are dealt: vectors, or pairs of them
+  // units that lanes are dealt: vectors, or pairs of them; at most 128
   const int total = a.d / N, hp = a.rope / (2 * N);
   const int units = HALF ? hp + (total - 2 * hp + 1) / 2 : total;
-  auto lanes_for = [&](int each) {
-    int n = 4;
-    while (n < 32 && n * each < units) n *= 2;
-    return n;
-  };
-  if (HALF) {
-    const int each = units <= 32 ? 1 : 2;
-    a.lanes = lanes_for(each);
-    return each == 1 ? launch_vectors<E, 2, HALF, BWD>(a, stream) : launch_vectors<E, 4, HALF, BWD>(a, stream);
-  }
   const int each = units <= 32 ? 1 : units <= 64 ? 2 : 4;
-  a.lanes = lanes_for(each);
-  if constexpr (!HALF) {
-    if (each == 1) return launch_vectors<E, 1, HALF, BWD>(a, stream);
-    if (each == 2) return launch_vectors<E, 2, HALF, BWD>(a, stream);
-  }
-  return launch_vectors<E, 4, HALF, BWD>(a, stream);
+  a.lanes = 4;
+  while (a.lanes < 32 && a.lanes * each < units) a.lanes *= 2;
+  constexpr int V = HALF ? 2 : 1;  // vectors of a unit
+  if (each == 1) return launch_heads<E, V, HALF, BWD>(a, stream);
+  if (each == 2) return launch_heads<E, 2 * V, HALF, BWD>(a, stream);
+  if constexpr (4 * V * N <= 32) return launch_heads<E, 4 * V, HALF, BWD>(a, stream);
+  return cudaErrorInvalidValue;  // fp32 in halves: heads have at most 64 units
 }
 
 template <typename E>
