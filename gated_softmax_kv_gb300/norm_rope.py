@@ -2,25 +2,16 @@
 queries and keys for each head with the rotary positions in the same pass."""
 from __future__ import annotations
 
-import ctypes
+import struct
 
 from .binding import _check, _check_detail, _raise, load
 from .launch import changed, on_device, output_overlaps
 from .rope import LAYOUTS, _dtype_code
 
-
-class _Side(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "weight", "grad", "y", "dweight")]
-                + [(n, ctypes.c_int64) for n in ("xt", "xh", "gt", "gh", "yt", "yh")]
-                + [("heads", ctypes.c_int32)])
-
-
-class _How(ctypes.Structure):
-    _fields_ = [("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("cu_rows", ctypes.c_void_p),
-                ("tokens", ctypes.c_int64), ("position_bits", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
-                ("ratio", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
-                ("offset", ctypes.c_int32), ("layout", ctypes.c_int32), ("dtype", ctypes.c_int32),
-                ("weight_dtype", ctypes.c_int32), ("amplitude", ctypes.c_float), ("eps", ctypes.c_float)]
+# csa_norm_side_t: x, weight, grad, y, dweight; (token, head) strides of x, grad and y; heads
+_side = struct.Struct("@5P6qi4x").pack
+# csa_norm_rope_t: freqs, positions, cu_rows; tokens; nine numbers; amplitude and eps
+_how = struct.Struct("@3Pq9i2f4x").pack
 
 
 def _strides(t, name):
@@ -33,24 +24,61 @@ def _strides(t, name):
     return (t.shape[1], s[0], s[1]) if len(s) == 3 else (1, s[0], 0)
 
 
-def _how(x, weight, freqs, positions, cu_seqlens_comp, ratio, offset, layout, amplitude, eps):
-    """(the C description, the device) of a call, from its first side."""
+def _describe(q, q_weight, k, k_weight, freqs, positions, cu_seqlens_comp, ratio, offset, layout, amplitude, eps):
+    """(the C description, q's and k's (heads, token stride, head stride), the device) of a
+    call. Reading attributes is most of the host's time: each is read once, and the
+    checks that name a fault run where there is one."""
     import torch
-    if not isinstance(x, torch.Tensor):
+    try:
+        dt, dev, wt = q.dtype, q.get_device(), q_weight.dtype
+        code, wcode, (pairs,) = _dtype_code(dt), _dtype_code(wt), freqs.shape
+        T, D, a, b = q.shape[0], q.shape[-1], _strides(q, "q"), None
+        fine = (dev >= 0 and code is not None and (wt is dt or wcode == 2) and q_weight.shape == (D,) and a[0] > 0 and D > 0
+                and q_weight.get_device() == dev and q_weight.is_contiguous() and freqs.dtype is torch.float64
+                and freqs.get_device() == dev and freqs.is_contiguous() and layout in LAYOUTS)
+        if fine and k is not None:
+            b = _strides(k, "k")
+            fine = (k.dtype is dt and k.get_device() == dev and k.shape[0] == T and k.shape[-1] == D and b[0] > 0
+                    and k_weight.dtype is wt and k_weight.get_device() == dev and k_weight.is_contiguous()
+                    and k_weight.shape == (D,))
+        where = positions if positions is not None else cu_seqlens_comp
+        (length,), kind = where.shape, where.dtype
+        fine = (fine and where.get_device() == dev and where.is_contiguous()
+                and (kind is torch.int32 and length > 1 if positions is None else
+                     cu_seqlens_comp is None and length == T and (kind is torch.int64 or kind is torch.int32)))
+    except (AttributeError, ValueError, TypeError):
+        fine = False
+    if not fine:
+        _refuse(q, q_weight, k, k_weight, freqs, positions, cu_seqlens_comp, layout)
+        a, b = _strides(q, "q"), None if k is None else _strides(k, "k")
+        T, D, dev = q.shape[0], q.shape[-1], q.get_device()
+        code, wcode, pairs = _dtype_code(q.dtype), _dtype_code(q_weight.dtype), freqs.shape[0]
+    if positions is None:
+        pos, bits, cu, nseq = 0, 0, cu_seqlens_comp.data_ptr(), cu_seqlens_comp.shape[0] - 1
+    else:  # an empty tensor has no address, and nothing of it is read
+        pos, bits, cu, nseq = positions.data_ptr() if T else freqs.data_ptr(), 8 * positions.element_size(), 0, 0
+    return _how(freqs.data_ptr(), pos, cu, T, bits, nseq, ratio, D, 2 * pairs, offset, LAYOUTS[layout], code, wcode,
+                amplitude, eps), a, b, dev
+
+
+def _refuse(q, q_weight, k, k_weight, freqs, positions, cu_seqlens_comp, layout):
+    """Names what a call's tensors are not; returns where they are unusual but fine."""
+    import torch
+    if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
-    code = _dtype_code(x.dtype)
-    if code is None:
-        raise TypeError(f"q must be bfloat16, float16 or float32, got {x.dtype}")
-    dev = x.get_device()
+    if _dtype_code(q.dtype) is None:
+        raise TypeError(f"q must be bfloat16, float16 or float32, got {q.dtype}")
+    dev = q.get_device()
     if dev < 0:
-        _check_detail(x, "q", x.dtype, 0, None)
+        _check_detail(q, "q", q.dtype, 0, None)
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
     _check(freqs, "freqs", torch.float64, dev, 1)
-    if not isinstance(weight, torch.Tensor) or weight.dtype not in (x.dtype, torch.float32):
+    if not isinstance(q_weight, torch.Tensor) or q_weight.dtype not in (q.dtype, torch.float32):
         raise TypeError("weights must be tensors of q's type or float32")
-    T = x.shape[0] if x.dim() else 0
-    pos, bits, cu, nseq = None, 0, None, 0
+    if q.dim() not in (2, 3) or 0 in q.shape[1:]:
+        raise ValueError("q must be [tokens, heads, head_dim] or [tokens, head_dim], with heads and columns")
+    T, D = q.shape[0], q.shape[-1]
     if positions is not None:
         if cu_seqlens_comp is not None:
             raise ValueError("positions and cu_seqlens_comp exclude each other")
@@ -59,34 +87,22 @@ def _how(x, weight, freqs, positions, cu_seqlens_comp, ratio, offset, layout, am
         _check(positions, "positions", positions.dtype, dev, 1)
         if positions.shape[0] != T:
             raise ValueError("positions must be [tokens]")
-        # an empty tensor has no address, and nothing of it is read
-        pos, bits = positions.data_ptr() if T else freqs.data_ptr(), 8 * positions.element_size()
     elif cu_seqlens_comp is not None:
         _check(cu_seqlens_comp, "cu_seqlens_comp", torch.int32, dev, 1)
-        nseq = cu_seqlens_comp.shape[0] - 1
-        if nseq < 1:
+        if cu_seqlens_comp.shape[0] < 2:
             raise ValueError("cu_seqlens_comp must be [num_seqs + 1]")
-        cu = cu_seqlens_comp.data_ptr()
     else:
         raise ValueError("positions or cu_seqlens_comp must be given")
-    if x.dim() not in (2, 3) or 0 in x.shape[1:]:
-        raise ValueError("q must be [tokens, heads, head_dim] or [tokens, head_dim], with heads and columns")
-    return _How(freqs.data_ptr(), pos, cu, T, bits, nseq, ratio, x.shape[-1], 2 * freqs.shape[0], offset,
-                LAYOUTS[layout], code, _dtype_code(weight.dtype), amplitude, eps), dev
-
-
-def _fits(x, weight, names, how, dev, like, wlike):
-    """Checks a side against the first one's types and sizes."""
-    import torch
-    if not isinstance(x, torch.Tensor) or x.dtype != like.dtype or x.get_device() != dev:
-        raise TypeError(f"{names[0]} must be a tensor of q's type and device")
-    heads, ts, hs = _strides(x, names[0])
-    if x.shape[0] != how.tokens or x.shape[-1] != how.head_dim or heads < 1:
-        raise ValueError(f"{names[0]} must have q's tokens and head_dim, and heads")
-    _check(weight, names[1], wlike.dtype, dev, 1)
-    if weight.shape[0] != how.head_dim:
-        raise ValueError(f"{names[1]} must be [head_dim]")
-    return _Side(x=x.data_ptr(), weight=weight.data_ptr(), xt=ts, xh=hs, heads=heads)
+    for x, w, names in ((q, q_weight, ("q", "q_weight")), (k, k_weight, ("k", "k_weight"))):
+        if x is None:
+            continue
+        if not isinstance(x, torch.Tensor) or x.dtype != q.dtype or x.get_device() != dev:
+            raise TypeError(f"{names[0]} must be a tensor of q's type and device")
+        if _strides(x, names[0])[0] < 1 or x.shape[0] != T or x.shape[-1] != D:
+            raise ValueError(f"{names[0]} must have q's tokens and head_dim, and heads")
+        _check(w, names[1], q_weight.dtype, dev, 1)
+        if w.shape[0] != D:
+            raise ValueError(f"{names[1]} must be [head_dim]")
 
 
 def _target(out, x, name, others, dev):
@@ -134,30 +150,30 @@ def csa_norm_rope(q, q_weight, freqs, positions=None, *, k=None, k_weight=None, 
     autograd.norm_rope is.
     """
     import torch
-    how, dev = _how(q, q_weight, freqs, positions, cu_seqlens_comp, ratio, offset, layout, amplitude, eps)
-    a = _fits(q, q_weight, ("q", "q_weight"), how, dev, q, q_weight)
-    b = None
-    if k is not None:
-        b = _fits(k, k_weight, ("k", "k_weight"), how, dev, q, q_weight)
-    elif k_weight is not None or k_out is not None:
+    if k is None and (k_weight is not None or k_out is not None):
         raise ValueError("k_weight and k_out go with k")
+    how, (heads, xt, xh), side, dev = _describe(q, q_weight, k, k_weight, freqs, positions, cu_seqlens_comp, ratio, offset,
+                                                layout, amplitude, eps)
     given = [t for t in (out, k_out) if t is not None]
     with on_device(dev, stream) as launch:
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            yt, yh = heads * q.shape[-1], q.shape[-1]
         else:
             _target(out, q, "out", (k,), dev)
+            _, yt, yh = _strides(out, "out")
+        a = _side(q.data_ptr(), q_weight.data_ptr(), 0, out.data_ptr(), 0, xt, xh, 0, 0, yt, yh, heads)
+        b = None
         if k is not None:
+            heads, xt, xh = side
             if k_out is None:
                 k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+                yt, yh = heads * k.shape[-1], k.shape[-1]
             else:
                 _target(k_out, k, "k_out", (q, out), dev)
-            _, b.yt, b.yh = _strides(k_out, "k_out")
-            b.y = k_out.data_ptr()
-        _, a.yt, a.yh = _strides(out, "out")
-        a.y = out.data_ptr()
-        st = load().csa_norm_rope(ctypes.byref(how), ctypes.byref(a), None if b is None else ctypes.byref(b),
-                                  launch.handle)
+                _, yt, yh = _strides(k_out, "k_out")
+            b = _side(k.data_ptr(), k_weight.data_ptr(), 0, k_out.data_ptr(), 0, xt, xh, 0, 0, yt, yh, heads)
+        st = load().csa_norm_rope(how, a, b, launch.handle)
         if st != 0:
             _raise(st)
         launch.used(q, k, q_weight, k_weight, freqs, positions, cu_seqlens_comp, out, k_out)
@@ -173,28 +189,25 @@ def csa_norm_rope_bwd(q, q_weight, freqs, grad, positions=None, *, k=None, k_wei
     those of out and k_out; returns (dq, dq_weight, dk, dk_weight), the last two
     None without k. The gradients are contiguous, the weights' in their type."""
     import torch
-    how, dev = _how(q, q_weight, freqs, positions, cu_seqlens_comp, ratio, offset, layout, amplitude, eps)
-    a = _fits(q, q_weight, ("q", "q_weight"), how, dev, q, q_weight)
-    b = None
-    if k is not None:
-        b = _fits(k, k_weight, ("k", "k_weight"), how, dev, q, q_weight)
-    elif k_weight is not None or k_grad is not None:
+    if k is None and (k_weight is not None or k_grad is not None):
         raise ValueError("k_weight and k_grad go with k")
+    how, q_side, k_side, dev = _describe(q, q_weight, k, k_weight, freqs, positions, cu_seqlens_comp, ratio, offset, layout,
+                                         amplitude, eps)
     with on_device(dev, stream) as launch:
-        made = []
-        for s, x, w, g, name in ((a, q, q_weight, grad, "grad"), (b, k, k_weight, k_grad, "k_grad")):
-            if s is None:
+        made, sides = [], []
+        for s, x, w, g, name in ((q_side, q, q_weight, grad, "grad"), (k_side, k, k_weight, k_grad, "k_grad")):
+            if x is None:
                 made += [None, None]
+                sides.append(None)
                 continue
             if not isinstance(g, torch.Tensor) or g.dtype != x.dtype or g.get_device() != dev or g.shape != x.shape:
                 raise TypeError(f"{name} must be a tensor of its input's shape, type and device")
-            _, s.gt, s.gh = _strides(g, name)
+            (heads, xt, xh), (_, gt, gh), D = s, _strides(g, name), x.shape[-1]
             dx, dw = torch.empty_like(x, memory_format=torch.contiguous_format), torch.empty_like(w)
-            _, s.yt, s.yh = _strides(dx, "dx")
-            s.grad, s.y, s.dweight = g.data_ptr(), dx.data_ptr(), dw.data_ptr()
+            sides.append(_side(x.data_ptr(), w.data_ptr(), g.data_ptr(), dx.data_ptr(), dw.data_ptr(), xt, xh, gt, gh,
+                               heads * D, D, heads))
             made += [dx, dw]
-        st = load().csa_norm_rope_bwd(ctypes.byref(how), ctypes.byref(a), None if b is None else ctypes.byref(b),
-                                      launch.handle)
+        st = load().csa_norm_rope_bwd(how, *sides, launch.handle)
         if st != 0:
             _raise(st)
         launch.used(q, k, q_weight, k_weight, freqs, positions, cu_seqlens_comp, grad, k_grad, *made)

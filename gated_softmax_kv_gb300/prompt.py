@@ -2,30 +2,30 @@
 attention over packed sequences, and its gradient."""
 from __future__ import annotations
 
-import ctypes
+import struct
 
 from .binding import _check, _check_detail, _raise, load
 from .launch import _span, changed, on_device
 
 FILL_OUT, FILL_LSE = 1, 2
 
-
-class _Prompt(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "cu_q", "cu_k")]
-                + [(n, ctypes.c_int64) for n in ("num_q", "num_k", "qt", "qh", "kt", "kh", "vt", "vh")]
-                + [(n, ctypes.c_int32) for n in ("num_seqs", "heads", "kv_heads", "head_dim", "dtype", "window")]
-                + [("sm_scale", ctypes.c_float)])
+# csa_prompt_t: five pointers, two counts and six strides, six numbers, the scale
+_pack = struct.Struct("@5P8q6if4x").pack
 
 
-_codes = {}
+class _Types:
+    """torch's types, looked up once."""
 
-
-def _dtype_code(dtype):
-    """CSA_BF16, CSA_FP16; None for other types."""
-    if not _codes:
+    def __getattr__(self, name):
         import torch
-        _codes.update({torch.bfloat16: 0, torch.float16: 1})
-    return _codes.get(dtype)
+        self.i32, self.f32 = torch.int32, torch.float32
+        self.codes = {torch.bfloat16: 0, torch.float16: 1}  # CSA_BF16, CSA_FP16
+        self.contiguous = {"memory_format": torch.contiguous_format}
+        self.empty, self.empty_like = torch.empty, torch.empty_like
+        return self.__dict__[name]
+
+
+_types = _Types()
 
 
 def _rows(t, name, like, dev):
@@ -44,11 +44,39 @@ def _rows(t, name, like, dev):
 
 
 def _describe(q, k, v, cu_q, cu_k, sm_scale, window):
-    """(the C description, the device) of a call."""
+    """(the C description, the device) of a call. Reading attributes is most of the
+    host's time: each is read once, and the checks that name a fault run where there
+    is one."""
+    try:
+        dt, dev, i32 = q.dtype, q.get_device(), _types.i32
+        code = _types.codes.get(dt)
+        (T, H, D), (qt, qh, q1), ks, (kt, kh, k1), (vt, vh, v1), (n,) = (q.shape, q.stride(), k.shape, k.stride(),
+                                                                         v.stride(), cu_q.shape)
+        N, KV, cols = ks
+        fine = (code is not None and dev >= 0 and k.dtype is dt and v.dtype is dt and k.get_device() == dev
+                and v.get_device() == dev and q1 == k1 == v1 == 1 and cols == D and v.shape == ks and KV > 0 and H > 0
+                and H % KV == 0 and n > 1 and cu_q.dtype is i32 and cu_q.get_device() == dev and cu_q.is_contiguous()
+                and (N == T if cu_k is None else
+                     cu_k.dtype is i32 and cu_k.get_device() == dev and cu_k.is_contiguous() and tuple(cu_k.shape) == (n,))
+                and (window is None or window >= 1))
+    except (AttributeError, ValueError, TypeError):
+        fine = False
+    if not fine:
+        _refuse(q, k, v, cu_q, cu_k, window)
+        (T, H, D), (qt, qh, _), (N, KV, _), (kt, kh, _), (vt, vh, _) = q.shape, q.stride(), k.shape, k.stride(), v.stride()
+        code, dev, n = _types.codes[q.dtype], q.get_device(), cu_q.shape[0]
+    # a window of 2^31 tokens and more is none: a sequence has fewer
+    return _pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), 0 if cu_k is None else cu_k.data_ptr(), T, N, qt,
+                 qh, kt, kh, vt, vh, n - 1, H, KV, D, code, 0 if window is None or window >= 2 ** 31 else window,
+                 sm_scale), dev
+
+
+def _refuse(q, k, v, cu_q, cu_k, window):
+    """Names what a call's tensors are not; returns where they are unusual but fine."""
     import torch
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
-    code = _dtype_code(q.dtype)
+    code = _types.codes.get(q.dtype)
     if code is None:
         raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
     dev = q.get_device()
@@ -56,31 +84,26 @@ def _describe(q, k, v, cu_q, cu_k, sm_scale, window):
         _check_detail(q, "q", q.dtype, 0, 3)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, head_dim]")
-    qt, qh = _rows(q, "q", q, dev)
-    kt, kh = _rows(k, "k", q, dev)
-    vt, vh = _rows(v, "v", q, dev)
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _rows(t, name, q, dev)
     if v.shape != k.shape:
         raise ValueError("k and v must have the same shape")
-    T, H, D = q.shape
+    T, H, _ = q.shape
     N, KV, _ = k.shape
     if KV < 1 or H < 1 or H % KV != 0:
         raise ValueError("q's heads must be a multiple of k's")
     _check(cu_q, "cu_q", torch.int32, dev, 1)
-    n = cu_q.shape[0] - 1
-    if n < 1:
+    n = cu_q.shape[0]
+    if n < 2:
         raise ValueError("cu_q must be [num_seqs + 1]")
     if cu_k is not None:
         _check(cu_k, "cu_k", torch.int32, dev, 1)
-        if cu_k.shape[0] != n + 1:
+        if cu_k.shape[0] != n:
             raise ValueError("cu_k must be as long as cu_q")
     elif N != T:
         raise ValueError("without cu_k, k must have q's tokens")
     if window is not None and window < 1:
         raise ValueError("window must be at least 1, or None for all keys")
-    # a window of 2^31 tokens and more is none: a sequence has fewer
-    return _Prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), None if cu_k is None else cu_k.data_ptr(),
-                   T, N, qt, qh, kt, kh, vt, vh, n, H, KV, D, code,
-                   0 if window is None or window >= 2 ** 31 else window, sm_scale), dev
 
 
 def _apart(t, name, *others):
@@ -110,13 +133,12 @@ def csa_prompt_attend(q, k, v, cu_q, sm_scale: float, *, cu_k=None, window=None,
     out's shape) takes what out's rounding left off, for the gradient. Not recorded
     by autograd: autograd.prompt_attend is.
     """
-    import torch
     p, dev = _describe(q, k, v, cu_q, cu_k, sm_scale, window)
     T, H, _ = q.shape
     fill, given = 0, [t for t in (out, lse, rest) if t is not None]
     with on_device(dev, stream) as launch:
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out = _types.empty_like(q, **_types.contiguous)
             fill |= FILL_OUT
         else:
             _check(out, "out", q.dtype, dev, 3)
@@ -124,10 +146,10 @@ def csa_prompt_attend(q, k, v, cu_q, sm_scale: float, *, cu_k=None, window=None,
                 raise ValueError("out must have q's shape")
             _apart(out, "out", q, k, v)
         if lse is None:
-            lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+            lse = _types.empty((T, H), dtype=_types.f32, device=dev)
             fill |= FILL_LSE
         else:
-            _check(lse, "lse", torch.float32, dev, 2)
+            _check(lse, "lse", _types.f32, dev, 2)
             if tuple(lse.shape) != (T, H):
                 raise ValueError("lse must be [tokens, heads]")
             _apart(lse, "lse", q, k, v, out)
@@ -136,7 +158,7 @@ def csa_prompt_attend(q, k, v, cu_q, sm_scale: float, *, cu_k=None, window=None,
             if rest.shape != q.shape:
                 raise ValueError("rest must have q's shape")
             _apart(rest, "rest", q, k, v, out, lse)
-        st = load().csa_prompt_attend(ctypes.byref(p), out.data_ptr(), None if rest is None else rest.data_ptr(),
+        st = load().csa_prompt_attend(p, out.data_ptr(), None if rest is None else rest.data_ptr(),
                                       lse.data_ptr(), fill, launch.handle)
         if st != 0:
             _raise(st)
@@ -151,14 +173,13 @@ def csa_prompt_attend_bwd(q, k, v, out, lse, grad, cu_q, sm_scale: float, *, cu_
     """The gradient of csa_prompt_attend: out, lse and rest are the forward's, grad
     (and grad_lse) those of out (and of lse); returns contiguous (dq, dk, dv), 0 for
     rows of no sequence."""
-    import torch
     p, dev = _describe(q, k, v, cu_q, cu_k, sm_scale, window)
     T, H, _ = q.shape
     gt, gh = _rows(grad, "grad", q, dev)
     if grad.shape != q.shape:
         raise ValueError("grad must have q's shape")
     _check(out, "out", q.dtype, dev, 3)
-    _check(lse, "lse", torch.float32, dev, 2)
+    _check(lse, "lse", _types.f32, dev, 2)
     if out.shape != q.shape or tuple(lse.shape) != (T, H):
         raise ValueError("out and lse must be the forward's")
     if rest is not None:
@@ -166,13 +187,13 @@ def csa_prompt_attend_bwd(q, k, v, out, lse, grad, cu_q, sm_scale: float, *, cu_
         if rest.shape != q.shape:
             raise ValueError("rest must be the forward's")
     if grad_lse is not None:
-        _check(grad_lse, "grad_lse", torch.float32, dev, 2)
+        _check(grad_lse, "grad_lse", _types.f32, dev, 2)
         if grad_lse.shape != lse.shape:
             raise ValueError("grad_lse must have lse's shape")
     with on_device(dev, stream) as launch:
-        dq, dk, dv = (torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k, v))
+        dq, dk, dv = (_types.empty_like(t, **_types.contiguous) for t in (q, k, v))
         st = load().csa_prompt_attend_bwd(
-            ctypes.byref(p), out.data_ptr(), None if rest is None else rest.data_ptr(), lse.data_ptr(), grad.data_ptr(), gt, gh,
+            p, out.data_ptr(), None if rest is None else rest.data_ptr(), lse.data_ptr(), grad.data_ptr(), gt, gh,
             None if grad_lse is None else grad_lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), launch.handle)
         if st != 0:
             _raise(st)

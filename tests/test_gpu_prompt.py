@@ -323,6 +323,43 @@ def test_same_bits_each_time(gsk):
         assert all(torch.equal(a, b) for a, b in zip(r, runs[0]))
 
 
+@pytest.mark.parametrize("nq,nk,H,KV,D,window", [
+    ([1500, 9, 700], None, 8, 2, 128, None), ([900, 333], None, 6, 2, 64, None), ([1000], None, 8, 1, 64, 100),
+    ([3, 1], [5000, 700], 16, 2, 128, None), ([130, 64], [2000, 64], 4, 2, 128, None)])
+def test_many_launches_one_behind_the_other(gsk, nq, nk, H, KV, D, window):
+    """Forward and gradient without a pause between the launches, whose CTAs take over one
+    another's work: every launch gives the first one's bits."""
+    q, k, v = inputs(nq, nk or nq, H, KV, D, "bf16", 5)
+    g, cu, ck = make(q.shape, "bf16", 6), i32(sums(nq)), None if nk is None else i32(sums(nk))
+    runs = []
+    for _ in range(60):
+        out, lse = gsk.csa_prompt_attend(q, k, v, cu, 0.1, cu_k=ck, window=window)
+        runs.append((out, lse, *gsk.csa_prompt_attend_bwd(q, k, v, out, lse, g, cu, 0.1, cu_k=ck, window=window)))
+    torch.cuda.synchronize()
+    for i, r in enumerate(runs):
+        assert all(torch.equal(a, b) for a, b in zip(r, runs[0])), i
+    assert all(torch.isfinite(t).all() for t in runs[0])
+
+
+def test_many_sequences(gsk):
+    """More sequences than a warp searches at a time, some empty, in both lists."""
+    r = np.random.RandomState(3)
+    nq = [int(x) for x in r.randint(0, 9, 1500)]
+    nk = [a + int(x) * (i % 3 == 0) for i, (a, x) in enumerate(zip(nq, r.randint(0, 40, 1500)))]
+    q, k, v = inputs(nq, nk, 2, 1, 64, "bf16", 1)
+    check(gsk, q, k, v, sums(nq), sums(nk), 0.125)
+
+
+def test_long_and_wide(gsk):
+    """Strides past 2^31 bytes."""
+    n, D = 3, 64
+    hold = torch.empty(2 * (2 ** 30 + 512) + 256, dtype=torch.bfloat16, device="cuda")
+    x = hold.as_strided((n, 3, D), (2 ** 30 + 512, D, 1))
+    x.copy_(make((n, 3, D), "bf16", 1))
+    q, k, v = x[:, :1], x[:, 1:2], x[:, 2:]
+    check(gsk, q, k, v, [0, n], None, 0.125)
+
+
 def test_empty(gsk):
     q, k, v = inputs([4], [4], 2, 1, 64, "bf16")
     out, lse = gsk.csa_prompt_attend(q[:0], k[:0], v[:0], i32([0, 0]), 1.0)
