@@ -80,8 +80,10 @@ __global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant
     for (int o = each >> 1; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
   };
-  auto unpack = [&](const void* base, int64_t at, float (&f)[8]) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at));
+  auto at = [&](const void* base, int64_t i) {
+    return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i));
+  };
+  auto unpack = [&](uint4 u, float (&f)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -89,63 +91,82 @@ __global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant
       f[2 * i + 1] = value16<HALF>((uint16_t)(w[i] >> 16));
     }
   };
+  constexpr int U = 4;  // rounds in flight
 #pragma unroll 1
   for (int64_t t = id; t < a.num_q; t += warps) {
-    // the token's sequence: the last one that begins at or before it
-    int lo = 0, span = a.nseq;
-    while (span > 1) {
-      const int step = (span + 31) / 32, at = lo + lane * step;
-      const bool before = lane * step < span && __ldg(a.cu_q + at) <= t;
-      const unsigned who = __ballot_sync(0xFFFFFFFFu, before);
-      const int k = who ? 31 - __clz(who) : 0;
-      span = min(step, span - k * step);
-      lo += k * step;
-    }
-    const Span w = span_of(a, lo);
-    const bool in = t >= w.q0 && t < (int64_t)w.q0 + w.nq;
-    const int hi = w.nk - w.nq + (int)(t - w.q0) + 1;
-    const bool single = in && (a.window == 1 || hi == 1);
-#pragma unroll 4
-    for (int h0 = 0; h0 < a.heads; h0 += per) {
-      const int h = h0 + sub;
-      const bool there = in && h < a.heads;
-      const int64_t row = t * a.heads + h;
-      float dot = 0.0f, size = 0.0f;
-      if (there && col < a.d) {
-        float g[8], o[8], e[8] = {};
-        unpack(a.g, t * a.gt + h * a.gh + col, g);
-        unpack(a.out, row * a.d + col, o);
-        if (a.rest) unpack(a.rest, row * a.d + col, e);
+    bool in = false, single = false;
+#pragma unroll 1
+    for (int h0 = 0; h0 < a.heads; h0 += U * per) {
+      // the loads first, of rows of no sequence too: finding the sequence takes as long
+      uint4 g[U], o[U], e[U];
+      float lse[U], dl[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * per + sub;
+        const bool there = h < a.heads && col < a.d;
+        const int64_t row = t * a.heads + h;
+        g[u] = there ? at(a.g, t * a.gt + h * a.gh + col) : make_uint4(0, 0, 0, 0);
+        o[u] = there ? at(a.out, row * a.d + col) : make_uint4(0, 0, 0, 0);
+        e[u] = there && a.rest ? at(a.rest, row * a.d + col) : make_uint4(0, 0, 0, 0);
+        lse[u] = there ? __ldg(a.lse + row) : 0.0f;
+        dl[u] = there && a.grad_lse ? __ldg(a.grad_lse + row) : 0.0f;
+      }
+      if (h0 == 0) {
+        // the token's sequence: the last one that begins at or before it
+        int lo = 0, span = a.nseq;
+#pragma unroll 1
+        while (span > 1) {
+          const int step = (span + 31) / 32, first = lo + lane * step;
+          const bool before = lane * step < span && __ldg(a.cu_q + first) <= t;
+          const unsigned who = __ballot_sync(0xFFFFFFFFu, before);
+          const int k = who ? 31 - __clz(who) : 0;
+          span = min(step, span - k * step);
+          lo += k * step;
+        }
+        const Span w = span_of(a, lo);
+        in = t >= w.q0 && t < (int64_t)w.q0 + w.nq;
+        single = in && (a.window == 1 || w.nk - w.nq + (int)(t - w.q0) + 1 == 1);
+        if (!in) break;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * per + sub;
+        float x[8], y[8], z[8], dot = 0.0f, size = 0.0f;
+        unpack(g[u], x);
+        unpack(o[u], y);
+        unpack(e[u], z);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          dot = fmaf(g[i], e[i], fmaf(g[i], o[i], dot));
-          size = fmaf(g[i], g[i], size);
+          dot = fmaf(x[i], z[i], fmaf(x[i], y[i], dot));
+          size = fmaf(x[i], x[i], size);
         }
-      }
-      dot = total(dot);
-      if (HALF) size = total(size);
-      if (there && lane % each == 0) {
-        const float dl = a.grad_lse ? __ldg(a.grad_lse + row) : 0.0f, lse = a.lse[row];
-        b.stats[row] = make_float2(lse == -INFINITY ? -INFINITY : kPLift<HALF> - lse * kLog2e, single ? dl : dl - dot);
-        if (HALF) {
-          // NaN compares above every number as bits, which gradient_exponent takes for no size
-          const float s = sqrtf(size);
-          most_g = s != s || s > most_g ? s : most_g;
-          most_l = dl != dl || fabsf(dl) > most_l ? fabsf(dl) : most_l;
+        dot = total(dot);
+        if (HALF) size = total(size);
+        if (h < a.heads && lane % each == 0) {
+          b.stats[t * a.heads + h] =
+              make_float2(lse[u] == -INFINITY ? -INFINITY : kPLift<HALF> - lse[u] * kLog2e, single ? dl[u] : dl[u] - dot);
+          if (HALF) {
+            // NaN compares above every number as bits, which gradient_exponent takes for no size
+            const float s = sqrtf(size);
+            most_g = s != s || s > most_g ? s : most_g;
+            most_l = dl[u] != dl[u] || fabsf(dl[u]) > most_l ? fabsf(dl[u]) : most_l;
+          }
         }
       }
     }
   }
   if (HALF) {
+    // rows of no sequence may hold anything
+    const int64_t k1 = min(__ldg(a.cu_k + a.nseq), a.num_k);
 #pragma unroll 1
-    for (int64_t t = id; t < a.num_k; t += warps)
+    for (int64_t t = max(__ldg(a.cu_k), 0) + id; t < k1; t += warps)
 #pragma unroll 1
       for (int h0 = 0; h0 < a.kv; h0 += per) {
         const int h = h0 + sub;
         float size = 0.0f;
         if (h < a.kv && col < a.d) {
           float v[8];
-          unpack(a.v, t * a.vt + h * a.vh + col, v);
+          unpack(at(a.v, t * a.vt + h * a.vh + col), v);
 #pragma unroll
           for (int i = 0; i < 8; ++i) size = isfinite(v[i]) ? fmaf(v[i], v[i], size) : size;
         }

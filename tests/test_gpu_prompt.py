@@ -307,6 +307,11 @@ def test_small_gradients_in_fp16(gsk):
         n = a.double().norm()
         # 2^-11 each from g's subnormals (below 2^-5 before the scale), the result's rounding and dS's
         assert ((b.double() * 512 - a.double()).norm() / n) <= 2.0 ** -10
+    # rows of no sequence have no say in how dS is scaled
+    more = [torch.cat([t, torch.full_like(t[:7], 60000.0)]) for t in (q, k, v, out, g)]
+    tail = torch.cat([lse, torch.full_like(lse[:7], -math.inf)])
+    got = gsk.csa_prompt_attend_bwd(*more[:4], tail, more[4], i32([0, 500]), 0.125)
+    assert all(torch.equal(a[:500], b) and (a[500:] == 0).all() for a, b in zip(got, one))
     big = gsk.csa_prompt_attend_bwd(q, k, v, out, lse, (g.float() * 64).half(), i32([0, 500]), 0.125)
     for a, b in zip(one, big):
         assert torch.isfinite(b).all() and ((b.double() / 64 - a.double()).norm() / a.double().norm()) <= 2.0 ** -10
