@@ -177,6 +177,37 @@ def test_views_and_strides(gsk):
     check(gsk, q, k, v, sums(nq), None, 0.125)
 
 
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_results_at_16_bytes(gsk, D):
+    """out, rest and every other tensor 16-byte aligned and no better."""
+    def at16(shape, dtype=torch.bfloat16):
+        n = math.prod(shape)
+        t = torch.zeros(n + 16, dtype=dtype, device="cuda")
+        t = t[8: 8 + n] if dtype is torch.bfloat16 else t[4: 4 + n]
+        assert t.data_ptr() % 32 == 16
+        return t.view(shape)
+
+    q0, k0, v0 = inputs([150], [150], 4, 2, D, "bf16", 1)
+    q, k, v, out, rest = at16(q0.shape), at16(k0.shape), at16(v0.shape), at16(q0.shape), at16(q0.shape)
+    for a, b in ((q, q0), (k, k0), (v, v0)):
+        a.copy_(b)
+    lse = at16((150, 4), torch.float32)
+    gsk.csa_prompt_attend(q, k, v, i32([0, 150]), 0.1, out=out, lse=lse, rest=rest)
+    want = gsk.csa_prompt_attend(q0, k0, v0, i32([0, 150]), 0.1)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    # the C call with gradients of that kind
+    import gated_softmax_kv_gb300.prompt as p
+    from gated_softmax_kv_gb300.binding import load
+    cu = i32([0, 150])
+    how, _ = p._describe(q, k, v, cu, None, 0.1, None)
+    dq, dk, dv, g = at16(q.shape), at16(k.shape), at16(k.shape), at16(q.shape)
+    g.copy_(make(q.shape, "bf16", 5))
+    assert load().csa_prompt_attend_bwd(how, out.data_ptr(), rest.data_ptr(), lse.data_ptr(), g.data_ptr(), 4 * D, D, None,
+                                        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+    back = gsk.csa_prompt_attend_bwd(q0, k0, v0, want[0], want[1], g.clone(), cu, 0.1, rest=rest.clone())
+    assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), back))
+
+
 def test_rows_of_no_sequence(gsk):
     nq, H, KV, D = [100, 30], 4, 2, 64
     q, k, v = inputs(nq, nq, H, KV, D, "bf16", 3, spare=20)
