@@ -377,6 +377,30 @@ def test_many_launches_one_behind_the_other(gsk, nq, nk, H, KV, D, window):
     assert all(torch.isfinite(t).all() for t in runs[0])
 
 
+def test_two_streams_at_once(gsk):
+    """Calls of different sizes on two streams, forward and gradient, with nothing between
+    them: each has its own workspace, and its own results."""
+    sets = []
+    for i, (nq, nk, H, KV, D) in enumerate([([700, 300], None, 8, 2, 128), ([5, 3, 1], [900, 200, 2000], 16, 2, 64)]):
+        q, k, v = inputs(nq, nk or nq, H, KV, D, "bf16", i)
+        sets.append((q, k, v, make(q.shape, "bf16", 9), i32(sums(nq)), None if nk is None else i32(sums(nk))))
+
+    def step(q, k, v, g, cu, ck):
+        out, lse = gsk.csa_prompt_attend(q, k, v, cu, 0.1, cu_k=ck)
+        return (out, lse, *gsk.csa_prompt_attend_bwd(q, k, v, out, lse, g, cu, 0.1, cu_k=ck))
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], [[], []]
+    for _ in range(40):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(*sets[i]))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        assert all(torch.equal(a, b) for r in runs for a, b in zip(r, w))
+
+
 def test_many_sequences(gsk):
     """More sequences than a warp searches at a time, some empty, in both lists."""
     r = np.random.RandomState(3)
