@@ -181,10 +181,11 @@ __global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant
     const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most_g) & 0x7FFFFFFFu);
     const uint32_t v = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most_v));
     const uint32_t l = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most_l) & 0x7FFFFFFFu);
-    if (lane == 0) {
-      atomicMax(b.sizes, g);
-      atomicMax(b.sizes + 1, v);
-      atomicMax(b.sizes + 2, l);
+    if (lane == 0) {  // a look first: few of the warps have the largest so far
+      volatile uint32_t* const sizes = b.sizes;
+      if (g > sizes[0]) atomicMax(b.sizes, g);
+      if (v > sizes[1]) atomicMax(b.sizes + 1, v);
+      if (l > sizes[2]) atomicMax(b.sizes + 2, l);
     }
   }
 }
