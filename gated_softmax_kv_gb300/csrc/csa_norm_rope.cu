@@ -14,8 +14,8 @@
 //
 // Angles are those of csa_rope.cu. Memory bounds the forward, with instructions close: 32768
 // tokens of 40 bf16 heads of 128 columns, half turned, 118 us (5.7 TB/s, 84% of the copy
-// rate). The gradient holds x, the gradient and the weights' sums of a lane's columns, 118
-// registers: 16384 tokens of 40 heads, all turned, 142 us (3.5 TB/s).
+// rate). The gradient holds x, the gradient and the weights' sums of a lane's columns, 96
+// registers: 16384 tokens of 40 heads, all turned, 133 us (3.8 TB/s).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -199,8 +199,9 @@ __device__ __forceinline__ int64_t warp_position_of(const NormArgs& a, int64_t t
 }
 
 // H: heads that a group has in flight; an item is a token and a.span of a side's heads.
+// Five CTAs an SM for the gradient of eight columns a lane (96 registers): 142 us, so 133.
 template <typename E, int K, int H, bool HALF, bool BWD>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kThreads, BWD && K * kChunk<E, HALF> <= 8 ? 5 : 1) norm_rope_kernel(const __grid_constant__ NormArgs a) {
   constexpr int N = kChunk<E, HALF>;
   using V = Chunk<E, N>;
   using Raw = typename V::Raw;
