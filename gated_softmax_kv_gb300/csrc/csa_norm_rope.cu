@@ -200,8 +200,10 @@ __device__ __forceinline__ int64_t warp_position_of(const NormArgs& a, int64_t t
 
 // H: heads that a group has in flight; an item is a token and a.span of a side's heads.
 // Five CTAs an SM for the gradient of eight columns a lane (96 registers): 142 us, so 133.
+// No number for the others: with one, 1 already, the compiler takes 112 registers for the
+// forward instead of 72 to 88 (32768 tokens of 40 heads of 128, half turned: 152 us instead of 118).
 template <typename E, int K, int H, bool HALF, bool BWD>
-__global__ void __launch_bounds__(kThreads, BWD && K * kChunk<E, HALF> <= 8 ? 5 : 1) norm_rope_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kThreads, BWD && K * kChunk<E, HALF> <= 8 ? 5 : 0) norm_rope_kernel(const __grid_constant__ NormArgs a) {
   constexpr int N = kChunk<E, HALF>;
   using V = Chunk<E, N>;
   using Raw = typename V::Raw;
