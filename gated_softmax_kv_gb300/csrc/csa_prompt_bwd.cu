@@ -47,23 +47,23 @@ namespace {
 struct BwdArgs {
   PromptArgs a;
   float2* stats;    // [num_q * heads]: -(lse log2 e - lift), -delta
-  uint32_t* sizes;  // fp16: bits of the largest |grad row|, |v row|, |grad_lse|
+  uint32_t* sizes;  // fp16: bits of the largest finite |grad row|, |v row|, |grad_lse|
 };
 
 template <bool HALF>
 constexpr float kPLift = HALF ? 15.0f : 0.0f;
 
 // fp16: |dP - delta| <= 2 |grad| |v| + |grad_lse| < 2^x, so that times 2^-x and a
-// weight of at most 2^15 it stays below 2^15. bf16: x = 0.
+// weight of at most 2^15 it stays below 2^15, in every row that is finite. bf16: x = 0.
 template <bool HALF>
 __device__ __forceinline__ int gradient_exponent(const BwdArgs& b) {
   if (!HALF) return 0;
   const float g = __uint_as_float(__ldg(b.sizes)), v = __uint_as_float(__ldg(b.sizes + 1)), l = __uint_as_float(__ldg(b.sizes + 2));
-  const float most = fmaf(2.0f * g, v, l);
-  if (!(most > 0.0f) || !isfinite(most)) return 0;
+  const float most = fminf(fmaf(2.0f * g, v, l), 3e38f);
+  if (!(most > 0.0f)) return 0;
   int x;
   frexpf(most * 1.01f, &x);
-  return min(max(x, -100), 100);
+  return min(max(x, -100), 128);
 }
 
 // ---- delta -------------------------------------------------------------------
@@ -150,11 +150,12 @@ __global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant
         if (h < a.heads && lane % each == 0) {
           b.stats[t * a.heads + h] =
               make_float2(lse[u] == -INFINITY ? -INFINITY : kPLift<HALF> - lse[u] * kLog2e, single ? dl[u] : dl[u] - dot);
-          if (HALF) {
-            // NaN compares above every number as bits, which gradient_exponent takes for no size
+          // Rows that are not finite stay so whatever the scale, through delta, and those that see
+          // no key have no weight: a scale for either would be the other rows' loss.
+          if (HALF && lse[u] != -INFINITY) {
             const float s = sqrtf(size);
-            most_g = s != s || s > most_g ? s : most_g;
-            most_l = dl[u] != dl[u] || fabsf(dl[u]) > most_l ? fabsf(dl[u]) : most_l;
+            if (isfinite(s)) most_g = fmaxf(most_g, s);
+            if (isfinite(dl[u])) most_l = fmaxf(most_l, fabsf(dl[u]));
           }
         }
       }
@@ -178,9 +179,9 @@ __global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant
         size = sqrtf(total(size));
         most_v = fmaxf(most_v, size);
       }
-    const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most_g) & 0x7FFFFFFFu);
+    const uint32_t g = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most_g));
     const uint32_t v = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most_v));
-    const uint32_t l = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most_l) & 0x7FFFFFFFu);
+    const uint32_t l = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most_l));
     if (lane == 0) {  // a look first: few of the warps have the largest so far
       volatile uint32_t* const sizes = b.sizes;
       if (g > sizes[0]) atomicMax(b.sizes, g);
