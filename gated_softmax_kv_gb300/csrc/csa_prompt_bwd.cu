@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int i = 0; i < kKeyStages; ++i) {
       mbar_init(clean + 8 * i, 1);
       mbar_init(k_full + 8 * i, 1);
-      mbar_init(k_empty + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, 2);  // the matrix instructions and the cleaning warp
     }
 #pragma unroll 1
     for (int i = 0; i < kValueStages; ++i) {
@@ -927,14 +927,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (x.n0 < 0) break;
 #pragma unroll 1
         for (int j = 0; j < x.n0; ++j) {
-          // every block is waited for: a parity tells only whether the one before it in its
-          // place has come
+          // every block is waited for, and its place held until this warp has seen it: a parity
+          // tells only whether the one before it in its place has come
           mbar_wait(k_full + 8 * at.stage, at.parity, dead);
           if (rows_mixed(a, x, j)) {
             clean_operand<C::HALF>(k_ptr + at.stage * C::TILE, C::TILE, lane, &st.bad);
             __syncwarp();
             if (lane == 0) mbar_arrive(clean + 8 * at.stage);
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(k_empty + 8 * at.stage);
           at.next(1);
         }
       }

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 1);
+      mbar_init(empty + 8 * i, 2);  // the matrix instructions and the cleaning warp
       mbar_init(clean + 8 * i, 1);
     }
     mbar_init(q_full, 1);
@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         return item_of(a, shape, id, ids, part, lane);
       });
     } else if (warp == 11) {  // ---- infinities and NaN of values that not every row sees
-      // Every tile of the ring is waited for, keys too: a parity tells only whether the
-      // tile before it in its place has come.
+      // Every tile of the ring is waited for, keys too, and its place is held until this warp
+      // has seen it: a parity tells only whether the tile before it in its place has come.
       Place<C::NS> at = {0, 0};
 #pragma unroll 1
       for (int k = 0;; ++k) {
@@ -302,6 +302,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(clean + 8 * at.stage);
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty + 8 * at.stage);
           at.next(1);
         }
       }
