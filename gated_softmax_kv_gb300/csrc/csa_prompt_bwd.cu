@@ -145,6 +145,9 @@ __global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant
           dot = fmaf(x[i], z[i], fmaf(x[i], y[i], dot));
           size = fmaf(x[i], x[i], size);
         }
+        // A gradient that is not finite has NaN for its delta: dP is formed of operands that the
+        // keys kernel may be cleaning, and whatever it is then, dS is NaN for all keys that the row sees.
+        if (infinite_bits<HALF>(g[u])) dot = NAN;
         dot = total(dot);
         if (HALF) size = total(size);
         if (h < a.heads && lane % each == 0) {
@@ -547,6 +550,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ++loaded;
       }
     } else if (warp == 10) {  // ---- the rows' numbers, with the tile of q; cleaning
+      // S and dP of a tile may be formed before, while or after it is cleaned: a row that holds
+      // infinities has lse or delta to match (-inf where all its logits are, NaN otherwise), which
+      // makes P and dS the same either way. dV and dK wait for clean operands.
       const float f = C::HALF ? exp2f((float)-gradient_exponent<C::HALF>(b)) : 1.0f;
       uint32_t tiles = 0;
       int token[4], head[4];
@@ -660,9 +666,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint32_t tiles = 0, items = 0;
 #pragma unroll 1
     for (int k = 0;; ++k) {
-      const KeysItem x = take(k);
+      KeysItem x = take(k);
       if (x.n0 < 0) break;
       m.key = x.k0 + (threadIdx.x & 127);
+      const int32_t nq = x.w.nq;
+      // Rows that no head uses, behind the 64th, are 0: a key that holds infinities has NaN for
+      // their logits, and all of its tiles are masked as mixed ones are.
+      if (half && rows < 128 && x.n0 > 0) {
+        mbar_wait(s_full, tiles & 1, dead);
+        tc_after();
+        const float z = tc_load1(m.s_at + 63);
+        if (__any_sync(0xFFFFFFFFu, z != z)) x.w.nq = 0;
+      }
 #pragma unroll 1
       for (int j = 0; j < x.n0; ++j, ++tiles) {
         if (keys_mixed(a, x, j))
@@ -670,6 +685,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         else
           keys_step<C, false>(st, m, tiles);
       }
+      x.w.nq = nq;
       // group 0 stores dV, group 1 dK
       if (x.n0 > 0) mbar_wait(done, items++ & 1, dead);
       tc_after();
@@ -719,7 +735,7 @@ struct alignas(16) RowsItem {
 struct RowsState {
   RowsItem item[2];
   WorkState work;
-  uint64_t q_full, q_empty, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], clean[kKeyStages],
+  uint64_t q_full, q_empty, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], clean[kKeyStages], scored[kKeyStages],
       s_full, s_empty, dp_full[2], ds_full[2][2], done;  // ds_full: the arithmetic may be a block ahead
   int32_t dead, bad;
   uint32_t tmem;
@@ -730,6 +746,12 @@ static_assert(sizeof(RowsState) <= 1024, "in front of the tiles");
 __device__ __forceinline__ bool rows_mixed(const PromptArgs& a, const RowsItem& x, int j) {
   const int first = (x.kb0 + j) * 128;
   return first + 128 > x.off + x.t0 + 1 || (a.window && (int64_t)first < (int64_t)x.off + x.t1 - a.window);
+}
+
+// The blocks [from, to) for which that does not hold.
+__device__ __forceinline__ int2 rows_whole(const PromptArgs& a, const RowsItem& x) {
+  const int64_t from = a.window ? ((int64_t)x.off + x.t1 - a.window + 127) >> 7 : 0;
+  return make_int2((int)max(from - x.kb0, (int64_t)0), max(x.off + x.t0 + 1, 0) / 128 - x.kb0);
 }
 
 // What the arithmetic of a row's blocks needs.
@@ -826,13 +848,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t q_full = smem_at(&st.q_full), q_empty = smem_at(&st.q_empty), k_full = smem_at(st.k_full),
                  k_empty = smem_at(st.k_empty), v_full = smem_at(st.v_full), v_empty = smem_at(st.v_empty),
                  s_full = smem_at(&st.s_full), s_empty = smem_at(&st.s_empty), dp_full = smem_at(st.dp_full),
-                 ds_full = smem_at(st.ds_full), done = smem_at(&st.done), clean = smem_at(st.clean);
+                 ds_full = smem_at(st.ds_full), done = smem_at(&st.done), clean = smem_at(st.clean), scored_at = smem_at(st.scored);
   volatile int32_t* const dead = &st.dead;
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
 #pragma unroll 1
     for (int i = 0; i < kKeyStages; ++i) {
       mbar_init(clean + 8 * i, 1);
+      mbar_init(scored_at + 8 * i, 1);
       mbar_init(k_full + 8 * i, 1);
       mbar_init(k_empty + 8 * i, 2);  // the matrix instructions and the cleaning warp
     }
@@ -920,7 +943,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ++loaded;
       }
     } else if (warp == 10) {  // ---- infinities and NaN of keys that not every row sees
+      // S is formed from them as they are (a key may hold -inf to have no weight), so it comes first.
       Place<kKeyStages> at = {0, 0};
+      uint32_t cleaned = 0;  // a parity a stage
 #pragma unroll 1
       for (int k = 0;; ++k) {
         const RowsItem x = take(k);
@@ -931,6 +956,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           // tells only whether the one before it in its place has come
           mbar_wait(k_full + 8 * at.stage, at.parity, dead);
           if (rows_mixed(a, x, j)) {
+            mbar_wait(scored_at + 8 * at.stage, (cleaned >> at.stage) & 1, dead);
+            cleaned ^= 1u << at.stage;
             clean_operand<C::HALF>(k_ptr + at.stage * C::TILE, C::TILE, lane, &st.bad);
             __syncwarp();
             if (lane == 0) mbar_arrive(clean + 8 * at.stage);
@@ -945,12 +972,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       Place<kKeyStages> key = {0, 0}, used = {0, 0};  // of the next S, of the next dQ
       Place<kValueStages> value = {0, 0};
       uint32_t scored = 0, weighed = 0, added = 0, items = 0, cleaned = 0;  // cleaned: a parity a stage
-      auto scores = [&]() {
+      auto scores = [&](bool mixed) {
         mbar_wait(k_full + 8 * key.stage, key.parity, dead);
         mbar_wait(s_empty, (scored & 1) ^ 1, dead);
         tc_after();
         product<C>(leader, S, q_at, k_at + key.stage * C::TILE);
         tc_commit_by(leader, s_full);
+        if (mixed) tc_commit_by(leader, scored_at + 8 * key.stage);
         ++scored;
         key.next(1);
       };
@@ -971,18 +999,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (n == 0) continue;
         mbar_wait(q_full, items & 1, dead);
         ++items;
-        scores();
+        const int2 whole = rows_whole(a, x);
+        const int from = (int)uniform((uint32_t)whole.x), to = (int)uniform((uint32_t)whole.y);
+        auto mixed = [&](int j) { return j < from || j >= to; };
+        scores(mixed(0));
         weights();
         if (n > 1) {
           weights();
-          scores();
+          scores(mixed(1));
         }
         if (n <= 2) tc_commit_by(leader, q_empty);
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
           if (j == max(0, n - 3)) want_work(st.work, lane);
           const uint32_t ready = ds_full + 16 * (added & 1), parity = (added >> 1) & 1;
-          if (rows_mixed(a, x, j)) {
+          if (mixed(j)) {
             mbar_wait(clean + 8 * used.stage, (cleaned >> used.stage) & 1, dead);
             cleaned ^= 1u << used.stage;
           }
@@ -999,7 +1030,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           used.next(1);
           if (j + 2 < n) {
             weights();
-            scores();
+            scores(mixed(j + 2));
             if (j + 3 == n) tc_commit_by(leader, q_empty);
           }
         }
