@@ -99,12 +99,15 @@ csa_status_t check(const csa_prompt_t* p, PromptArgs& a) {
   a.d = p->head_dim;
   a.window = p->window;
   a.scale = p->sm_scale;
+  a.polls = csa_prompt_polls;
   return CSA_OK;
 }
 
 }  // namespace
 
 }  // namespace csa
+
+extern "C" int32_t csa_prompt_polls = csa::kPolls;
 
 extern "C" csa_status_t csa_prompt_attend(const csa_prompt_t* p, void* out, void* rest, float* lse, int32_t fill,
                                           cudaStream_t stream) {

@@ -285,7 +285,7 @@ struct KeysState {
   KeysItem item[2];
   WorkState work;
   uint64_t kv_full, kv_empty, q_full[2], q_empty[2], g_full[2], g_empty[2], r_full[2], s_full, p_full[2], dp_full, ds_full[2], done, clean[2];
-  int32_t dead, bad;
+  int32_t dead, polls, bad;
   uint32_t tmem;
 };
 static_assert(sizeof(KeysState) <= 8192, "HEAD");
@@ -336,8 +336,8 @@ __device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, uint
   constexpr bool HALF = C::HALF;
   const int stage = j & 1, key = m.key, lane = threadIdx.x & 31;
   const float2 c2 = make_float2(m.c, m.c), f2 = make_float2(m.f, m.f);
-  mbar_wait(m.r_full + 8 * stage, (j >> 1) & 1, m.dead);
-  mbar_wait(m.s_full, j & 1, m.dead);
+  wait_for(m.r_full + 8 * stage, (j >> 1) & 1, m.dead);
+  wait_for(m.s_full, j & 1, m.dead);
   tc_after();
   float p[64], d[64];
   tc_load32_async(m.s_at, p);
@@ -375,7 +375,7 @@ __device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, uint
   __syncwarp();
   if (lane == 0) mbar_arrive(m.p_full);
 
-  mbar_wait(m.dp_full, j & 1, m.dead);
+  wait_for(m.dp_full, j & 1, m.dead);
   tc_after();
   tc_load32_async(m.dp_at, d);
   tc_load_wait();
@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   volatile int32_t* const dead = &st.dead;
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
+    st.polls = a.polls;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(clean + 8 * i, 1);
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (x.n0 < 0) break;
         if (x.n0 == 0) continue;
         if (lane == 0) {
-          mbar_wait(kv_empty, (loaded & 1) ^ 1, dead);
+          wait_for(kv_empty, (loaded & 1) ^ 1, dead);
           mbar_expect(kv_full, 2 * C::TILE);
           load_tile<C>(k_at, &mk, x.kvh, x.w.k0 + x.k0, kv_full);
           load_tile<C>(v_at, &mv, x.kvh, x.w.k0 + x.k0, kv_full);
@@ -533,10 +534,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           for (int j = 0; j < x.n0 && !*dead; ++j, ++tiles) {
             const uint32_t stage = tiles & 1, parity = ((tiles >> 1) & 1) ^ 1;
             const int token = x.w.q0 + x.t0 + j * tp;
-            mbar_wait(q_empty + 8 * stage, parity, dead);
+            wait_for(q_empty + 8 * stage, parity, dead);
             mbar_expect(q_full + 8 * stage, bytes);
             load_tile<C>(q_at + stage * C::TILE, &mq, x.kvh * a.group, token, q_full + 8 * stage);
-            mbar_wait(g_empty + 8 * stage, parity, dead);
+            wait_for(g_empty + 8 * stage, parity, dead);
             mbar_expect(g_full + 8 * stage, bytes);
             load_tile<C>(g_at + stage * C::TILE, &mg, x.kvh * a.group, token, g_full + 8 * stage);
           }
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             hi[i] = there ? x.off + t + 1 : 0;
             v[i] = there ? __ldg(b.stats + (int64_t)(x.w.q0 + t) * a.heads + x.kvh * a.group + head[i]) : make_float2(-INFINITY, 0.0f);
           }
-          mbar_wait(q_empty + 8 * stage, ((tiles >> 1) & 1) ^ 1, dead);
+          wait_for(q_empty + 8 * stage, ((tiles >> 1) & 1) ^ 1, dead);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int r = i * 32 + lane;
@@ -590,9 +591,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (lane == 0) mbar_arrive(r_full + 8 * stage);
           if (keys_mixed(a, x, j)) {  // infinities and NaN of rows that do not see every key
             const uint32_t parity = (tiles >> 1) & 1;
-            mbar_wait(q_full + 8 * stage, parity, dead);
+            wait_for(q_full + 8 * stage, parity, dead);
             clean_operand<C::HALF>(q_ptr + stage * C::TILE, C::TILE, lane, &st.bad);
-            mbar_wait(g_full + 8 * stage, parity, dead);
+            wait_for(g_full + 8 * stage, parity, dead);
             clean_operand<C::HALF>(g_ptr + stage * C::TILE, C::TILE, lane, &st.bad);
             __syncwarp();
             if (lane == 0) mbar_arrive(clean + 8 * stage);
@@ -603,13 +604,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const uint32_t leader = tc_leader(), tm = uniform(tmem), S = tm, DP = tm + 128, DV = tm + 256, DK = tm + 256 + C::DP;
       uint32_t tiles = 0, items = 0, cleaned = 0;  // cleaned: a parity a stage
       auto scores = [&](uint32_t j) {
-        mbar_wait(q_full + 8 * (j & 1), (j >> 1) & 1, dead);
+        wait_for(q_full + 8 * (j & 1), (j >> 1) & 1, dead);
         tc_after();
         product<C>(leader, S, k_at, q_at + (j & 1) * C::TILE);
         tc_commit_by(leader, s_full);
       };
       auto weights = [&](uint32_t j) {  // dP
-        mbar_wait(g_full + 8 * (j & 1), (j >> 1) & 1, dead);
+        wait_for(g_full + 8 * (j & 1), (j >> 1) & 1, dead);
         tc_after();
         product<C>(leader, DP, v_at, g_at + (j & 1) * C::TILE);
         tc_commit_by(leader, dp_full);
@@ -617,10 +618,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       auto add = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t ready, uint32_t j, bool first) {
         // An item's first product writes over the last one's sums: both groups of the
         // arithmetic have read them when both have formed something of this item.
-        if (first) mbar_wait(ready + 8, j & 1, dead);
+        if (first) wait_for(ready + 8, j & 1, dead);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          mbar_wait(ready + 8 * half, j & 1, dead);
+          wait_for(ready + 8 * half, j & 1, dead);
           tc_after();
           product_add<C>(leader, d, x, y, half, !first || half > 0);
         }
@@ -631,15 +632,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int n = (int)uniform((uint32_t)x.n0);
         if (n < 0) break;
         if (n == 0) continue;
-        mbar_wait(kv_full, items & 1, dead);
+        wait_for(kv_full, items & 1, dead);
         ++items;
         scores(tiles);
         weights(tiles);
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++tiles) {
+          tile_done(st.work, lane, tiles);
           if (j == max(0, n - 3)) want_work(st.work, lane);
           if (keys_mixed(a, x, j)) {
-            mbar_wait(clean + 8 * (tiles & 1), (cleaned >> (tiles & 1)) & 1, dead);
+            wait_for(clean + 8 * (tiles & 1), (cleaned >> (tiles & 1)) & 1, dead);
             cleaned ^= 1u << (tiles & 1);
             tc_after();
           }
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // Rows that no head uses, behind the 64th, are 0: a key that holds infinities has NaN for
       // their logits, and all of its tiles are masked as mixed ones are.
       if (half && rows < 128 && x.n0 > 0) {
-        mbar_wait(s_full, tiles & 1, dead);
+        wait_for(s_full, tiles & 1, dead);
         tc_after();
         const float z = tc_load1(m.s_at + 63);
         if (__any_sync(0xFFFFFFFFu, z != z)) x.w.nq = 0;
@@ -687,7 +689,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
       x.w.nq = nq;
       // group 0 stores dV, group 1 dK
-      if (x.n0 > 0) mbar_wait(done, items++ & 1, dead);
+      if (x.n0 > 0) wait_for(done, items++ & 1, dead);
       tc_after();
       const bool there = m.key < x.w.nk;
       const int64_t row = ((int64_t)(x.w.k0 + m.key) * a.kv + x.kvh) * a.d;
@@ -737,7 +739,7 @@ struct RowsState {
   WorkState work;
   uint64_t q_full, q_empty, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], clean[kKeyStages], scored[kKeyStages],
       s_full, s_empty, dp_full[2], ds_full[2][2], done;  // ds_full: the arithmetic may be a block ahead
-  int32_t dead, bad;
+  int32_t dead, polls, bad;
   uint32_t tmem;
 };
 static_assert(sizeof(RowsState) <= 1024, "in front of the tiles");
@@ -771,7 +773,7 @@ __device__ __forceinline__ void rows_step(const RowsMath& m, uint32_t j, int fir
   const float2 c2 = make_float2(m.c, m.c), f2 = make_float2(m.f, m.f), l2 = make_float2(m.lse, m.lse),
                d2 = make_float2(m.delta, m.delta);
   const uint32_t dp_at = m.dp_at + 128 * (j & 1);
-  mbar_wait(m.s_full, j & 1, m.dead);
+  wait_for(m.s_full, j & 1, m.dead);
   tc_after();
   float p[64], d[64];
   tc_load32_async(m.s_at, p);
@@ -788,7 +790,7 @@ __device__ __forceinline__ void rows_step(const RowsMath& m, uint32_t j, int fir
     p[k] = ex2_approx_ftz(z.x);
     p[k + 1] = ex2_approx_ftz(z.y);
   }
-  mbar_wait(m.dp_full + 8 * (j & 1), (j >> 1) & 1, m.dead);
+  wait_for(m.dp_full + 8 * (j & 1), (j >> 1) & 1, m.dead);
   tc_after();
   tc_load32_async(dp_at, d);
   tc_load_wait();
@@ -852,6 +854,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   volatile int32_t* const dead = &st.dead;
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
+    st.polls = a.polls;
 #pragma unroll 1
     for (int i = 0; i < kKeyStages; ++i) {
       mbar_init(clean + 8 * i, 1);
@@ -918,17 +921,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (x.n0 < 0) break;
         if (x.n0 == 0) continue;
         if (lane == 0) {
-          mbar_wait(q_empty, (loaded & 1) ^ 1, dead);
+          wait_for(q_empty, (loaded & 1) ^ 1, dead);
           mbar_expect(q_full, 2 * (C::DP / 64) * 128 * rows);
           load_tile<C>(q_at, &mq, x.kvh * a.group, x.w.q0 + x.t0, q_full);
           load_tile<C>(g_at, &mg, x.kvh * a.group, x.w.q0 + x.t0, q_full);
 #pragma unroll 1
           for (int j = 0; j < x.n0 && !*dead; ++j, ++tiles) {
-            mbar_wait(k_empty + 8 * at.stage, at.parity ^ 1, dead);
+            wait_for(k_empty + 8 * at.stage, at.parity ^ 1, dead);
             mbar_expect(k_full + 8 * at.stage, C::TILE);
             load_tile<C>(k_at + at.stage * C::TILE, &mk, x.kvh, x.w.k0 + (x.kb0 + j) * 128, k_full + 8 * at.stage);
             at.next(1);
-            mbar_wait(v_empty + 8 * value.stage, value.parity ^ 1, dead);
+            wait_for(v_empty + 8 * value.stage, value.parity ^ 1, dead);
             mbar_expect(v_full + 8 * value.stage, C::TILE);
             load_tile<C>(v_at + value.stage * C::TILE, &mv, x.kvh, x.w.k0 + (x.kb0 + j) * 128, v_full + 8 * value.stage);
             value.next(1);
@@ -954,9 +957,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int j = 0; j < x.n0; ++j) {
           // every block is waited for, and its place held until this warp has seen it: a parity
           // tells only whether the one before it in its place has come
-          mbar_wait(k_full + 8 * at.stage, at.parity, dead);
+          wait_for(k_full + 8 * at.stage, at.parity, dead);
           if (rows_mixed(a, x, j)) {
-            mbar_wait(scored_at + 8 * at.stage, (cleaned >> at.stage) & 1, dead);
+            wait_for(scored_at + 8 * at.stage, (cleaned >> at.stage) & 1, dead);
             cleaned ^= 1u << at.stage;
             clean_operand<C::HALF>(k_ptr + at.stage * C::TILE, C::TILE, lane, &st.bad);
             __syncwarp();
@@ -973,8 +976,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       Place<kValueStages> value = {0, 0};
       uint32_t scored = 0, weighed = 0, added = 0, items = 0, cleaned = 0;  // cleaned: a parity a stage
       auto scores = [&](bool mixed) {
-        mbar_wait(k_full + 8 * key.stage, key.parity, dead);
-        mbar_wait(s_empty, (scored & 1) ^ 1, dead);
+        wait_for(k_full + 8 * key.stage, key.parity, dead);
+        wait_for(s_empty, (scored & 1) ^ 1, dead);
         tc_after();
         product<C>(leader, S, q_at, k_at + key.stage * C::TILE);
         tc_commit_by(leader, s_full);
@@ -983,7 +986,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         key.next(1);
       };
       auto weights = [&]() {  // dP
-        mbar_wait(v_full + 8 * value.stage, value.parity, dead);
+        wait_for(v_full + 8 * value.stage, value.parity, dead);
         tc_after();
         product<C>(leader, DP + 128 * (weighed & 1), g_at, v_at + value.stage * C::TILE);
         tc_commit_by(leader, v_empty + 8 * value.stage);
@@ -997,7 +1000,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int n = (int)uniform((uint32_t)x.n0);
         if (n < 0) break;
         if (n == 0) continue;
-        mbar_wait(q_full, items & 1, dead);
+        wait_for(q_full, items & 1, dead);
         ++items;
         const int2 whole = rows_whole(a, x);
         const int from = (int)uniform((uint32_t)whole.x), to = (int)uniform((uint32_t)whole.y);
@@ -1011,17 +1014,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (n <= 2) tc_commit_by(leader, q_empty);
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
+          tile_done(st.work, lane, added);
           if (j == max(0, n - 3)) want_work(st.work, lane);
           const uint32_t ready = ds_full + 16 * (added & 1), parity = (added >> 1) & 1;
           if (mixed(j)) {
-            mbar_wait(clean + 8 * used.stage, (cleaned >> used.stage) & 1, dead);
+            wait_for(clean + 8 * used.stage, (cleaned >> used.stage) & 1, dead);
             cleaned ^= 1u << used.stage;
           }
           // the item's first product writes over sums that both groups have to have read
-          if (j == 0) mbar_wait(ready + 8, parity, dead);
+          if (j == 0) wait_for(ready + 8, parity, dead);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            mbar_wait(ready + 8 * half, parity, dead);
+            wait_for(ready + 8 * half, parity, dead);
             tc_after();
             product_add<C>(leader, DQ, DP + 128 * (added & 1), k_at + used.stage * C::TILE, half, j > 0 || half > 0);
           }
@@ -1066,7 +1070,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         else
           rows_step<C, false>(m, tiles, 0);
       }
-      if (x.n0 > 0) mbar_wait(done, items++ & 1, dead);
+      if (x.n0 > 0) wait_for(done, items++ & 1, dead);
       tc_after();
       float factor = a.scale * (C::HALF ? exp2f((float)(e - 15)) : 1.0f);
       if (*dead) factor = NAN;

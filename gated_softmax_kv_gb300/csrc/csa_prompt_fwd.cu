@@ -35,7 +35,7 @@
 // tokens of 64 heads of 64, 92 us. Single tokens: memory, 32 sequences of 8192 keys, 8 key
 // heads of 128, 158 us (6.8 TB/s).
 //
-// Every wait on an mbarrier is bounded: a wait that runs out marks the CTA, whose
+// Every wait on an mbarrier is bounded (csa_prompt_tile.cuh): a wait that runs out marks the CTA, whose
 // later waits return at once and whose results become NaN.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -87,7 +87,7 @@ struct State {
   Item item[2];
   WorkState work;
   uint64_t full[NS], empty[NS], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], pair_full, pair_empty, clean[NS];
-  int32_t dead, bad;
+  int32_t dead, polls, bad;
   uint32_t tmem;
   float ref[128], sum[128];  // group 1's, for group 0; in a cluster: the CTA's
 };
@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const int part = (int)(blockIdx.x - first_id * shape.split);  // of the item, in a cluster
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
+    st.polls = a.polls;
 #pragma unroll 1
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(full + 8 * i, 1);
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int i = 0; i < 2 * n; ++i) {
           bool value;
           const int b = tile_at(i, n, x.step, value);
-          mbar_wait(full + 8 * at.stage, at.parity, dead);
+          wait_for(full + 8 * at.stage, at.parity, dead);
           if (value && !seen.all(b)) {
             clean_operand<C::HALF>(ring_ptr + at.stage * C::TILE, C::TILE, lane, &st.bad);
             __syncwarp();
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (n == 0) continue;
         if (lane == 0) {
           const int tiles = x.step == 1 && x.n1 > 0 ? 2 : 1;
-          mbar_wait(q_empty, (loaded & 1) ^ 1, dead);
+          wait_for(q_empty, (loaded & 1) ^ 1, dead);
           mbar_expect(q_full, tiles * (C::DP / 64) * 128 * rows);
 #pragma unroll 1
           for (int t = 0; t < tiles; ++t)
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           for (int i = 0; i < 2 * n && !*dead; ++i) {
             bool value;
             const int b = tile_at(i, n, x.step, value);
-            mbar_wait(empty + 8 * at.stage, at.parity ^ 1, dead);
+            wait_for(empty + 8 * at.stage, at.parity ^ 1, dead);
             mbar_expect(full + 8 * at.stage, C::TILE);
 #pragma unroll 1
             for (int p = 0; p < C::DP / 64; ++p)
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (n == 0) continue;
         const Seen seen = seen_by(a, x, x.t0, x.last);
         const int seen_from = (int)uniform((uint32_t)seen.from), seen_to = (int)uniform((uint32_t)seen.to);
-        mbar_wait(q_full, loaded & 1, dead);
+        wait_for(q_full, loaded & 1, dead);
         ++loaded;
         // keys and values of the next block to come, of either tile
         Place<C::NS> key = start, value = start;
@@ -387,13 +388,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           tc_commit_by(leader, s_full + 8 * t);
         };
         auto ready = [&](const Place<C::NS>& p) {
-          mbar_wait(full + 8 * p.stage, p.parity, dead);
+          wait_for(full + 8 * p.stage, p.parity, dead);
           tc_after();
         };
         auto valued = [&](int b) {  // the values of block b are there, and clean
           ready(value);
           if (b < seen_from || b >= seen_to) {
-            mbar_wait(clean + 8 * value.stage, (cleaned >> value.stage) & 1, dead);
+            wait_for(clean + 8 * value.stage, (cleaned >> value.stage) & 1, dead);
             cleaned ^= 1u << value.stage;
             tc_after();
           }
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const uint64_t v = v_op + at * (C::TILE / 16);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            mbar_wait(p_full + 16 * t + 8 * h, rounds[t] & 1, dead);
+            wait_for(p_full + 16 * t + 8 * h, rounds[t] & 1, dead);
             tc_after();
             tc_mma4_ts<128>(leader, tm + C::O0 + C::DP * t, tm + C::S0 + 128 * t + 32 * h, v + 512 * h, C::IDESC_O, !first || h > 0);
           }
@@ -417,6 +418,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           key.next(2);
 #pragma unroll 1
           for (int b = 0; b < n; ++b) {
+            tile_done(st.work, lane, copies + 2 * b);
             if (b == max(0, n - 3)) want_work(st.work, lane);
             valued(b);
             const bool more = b + 1 < n;
@@ -457,6 +459,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           key.next(2);
 #pragma unroll 1
           for (int b = 0; b < n; b += 2) {
+            tile_done(st.work, lane, copies + 2 * b);
             if (b == (max(0, n - 6) & ~1)) want_work(st.work, lane);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -504,7 +507,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       float2 l0 = make_float2(0.0f, 0.0f), l1 = l0;
 #pragma unroll 1
       for (int b = x.step == 1 ? 0 : t; b < mine; b += x.step) {
-        mbar_wait(s_full + 8 * t, rounds & 1, dead);
+        wait_for(s_full + 8 * t, rounds & 1, dead);
         ++rounds;
         tc_after();
         float v[128];
@@ -597,7 +600,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int g = 0; g < 4; ++g) weights(g, !C::WINDOW || (some_see >> g & 1));
       }
       float l = (l0.x + l0.y) + (l1.x + l1.y);
-      if (mine > 0) mbar_wait(o_full + 8 * t, results++ & 1, dead);
+      if (mine > 0) wait_for(o_full + 8 * t, results++ & 1, dead);
       tc_after();
       // O = fa O of tile 0 + fb O of tile 1, where both groups have worked on the same rows
       float fa = 1.0f, fb = 0.0f;
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(pair_full);
         } else {
-          mbar_wait(pair_full, pairs & 1, dead);
+          wait_for(pair_full, pairs & 1, dead);
           tc_after();
           const float other = st.ref[r], top = fmaxf(ref, other), safe = top == -INFINITY ? 0.0f : top;
           fa = ex2_approx_ftz(ref - safe);
@@ -678,7 +681,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(pair_empty);
         } else {
-          mbar_wait(pair_empty, pairs & 1, dead);
+          wait_for(pair_empty, pairs & 1, dead);
         }
         ++pairs;
       }

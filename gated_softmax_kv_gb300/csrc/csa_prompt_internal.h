@@ -28,7 +28,11 @@ struct PromptArgs {
   int32_t nseq, heads, kv, group, d, window;
   int32_t fill;
   float scale;
+  int32_t polls;  // of a wait, before its CTA gives up
 };
+
+// What PromptArgs::polls is: kPolls (csa_tc.cuh), unless a test has set it lower.
+extern "C" int32_t csa_prompt_polls;
 
 // A sequence's rows, checked: an empty one where the lists do not make sense.
 struct Span {

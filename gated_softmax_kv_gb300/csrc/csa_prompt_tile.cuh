@@ -58,6 +58,38 @@ __device__ __forceinline__ void fill_rest(const int32_t* cu, int nseq, int32_t n
     to[i / heads < a ? i : i + (b - a) * heads] = v;
 }
 
+// ---- waits --------------------------------------------------------------------
+//
+// Bounded: dead[1] polls after the first without the phase mark the CTA (dead[0]), and no
+// further wait waits. A poll that fails takes about 2700 cycles (1.4 us), so the usual
+// kPolls of them 1.4 s, for what takes microseconds: a copy, a product, a tile's arithmetic.
+
+__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, volatile int32_t* dead) {
+#pragma unroll 1
+  for (int i = 0; !mbar_try(bar, parity); ++i)  // short: it is inlined a hundred times
+    if (*dead || i >= dead[1]) {
+      *dead = 1;
+      return;
+    }
+}
+
+// For what may take as long as an item, and that is as long as the sequence: as many polls
+// each time that *progress (a count of tiles) has moved since the last.
+__device__ __forceinline__ void wait_through(uint32_t bar, uint32_t parity, volatile int32_t* dead, const volatile uint32_t* progress) {
+  uint32_t seen = *progress;
+#pragma unroll 1
+  for (int i = 0; !mbar_try(bar, parity); ++i)
+    if (*dead || i >= dead[1]) {
+      const uint32_t now = *progress;
+      if (*dead || now == seen) {
+        *dead = 1;
+        return;
+      }
+      seen = now;
+      i = 0;
+    }
+}
+
 // ---- items of work -----------------------------------------------------------
 //
 // A warp of its own finds the items (type Item, n0 < 0: none): first the CTA's own, then
@@ -70,6 +102,7 @@ __device__ __forceinline__ void fill_rest(const int32_t* cu, int nseq, int32_t n
 struct WorkState {
   alignas(16) uint32_t stolen[4];
   uint64_t full[2], empty[2], steal, want;
+  uint32_t progress;  // tiles of the matrix instructions
 };
 
 __device__ __forceinline__ void init_work(WorkState& w, int takers) {
@@ -79,6 +112,7 @@ __device__ __forceinline__ void init_work(WorkState& w, int takers) {
   }
   mbar_init(smem_at(&w.steal), 1);
   mbar_init(smem_at(&w.want), 1);
+  w.progress = 0;
 }
 
 template <class Item, class Find>
@@ -91,7 +125,7 @@ __device__ __forceinline__ void find_work(WorkState& w, Item* slots, uint32_t id
   for (int n = 0;; ++n) {
     const Item x = find(id);
     if (x.n0 >= 0) {
-      mbar_wait(empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
+      wait_for(empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
       if (lane == 0) {
         slots[k & 1] = x;
         mbar_arrive(full + 8 * (k & 1));
@@ -99,7 +133,7 @@ __device__ __forceinline__ void find_work(WorkState& w, Item* slots, uint32_t id
       ++k;
     }
     if (once || *dead) break;
-    if (x.keys()) mbar_wait(smem_at(&w.want), wanted++ & 1, dead);
+    if (x.keys()) wait_through(smem_at(&w.want), wanted++ & 1, dead, &w.progress);
     __syncwarp();
     if (lane == 0) {
       mbar_expect(steal, 16);
@@ -109,7 +143,7 @@ __device__ __forceinline__ void find_work(WorkState& w, Item* slots, uint32_t id
           "r"(steal)
           : "memory");
     }
-    mbar_wait(steal, n & 1, dead);
+    wait_for(steal, n & 1, dead);
     uint32_t got;
     asm volatile(
         "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
@@ -120,11 +154,16 @@ __device__ __forceinline__ void find_work(WorkState& w, Item* slots, uint32_t id
         : "memory");
     if (!got || *dead) break;
   }
-  mbar_wait(empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
+  wait_for(empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
   if (lane == 0) {
     slots[k & 1].n0 = -1;
     mbar_arrive(full + 8 * (k & 1));
   }
+}
+
+// The warp of the matrix instructions, once a tile.
+__device__ __forceinline__ void tile_done(WorkState& w, int lane, uint32_t tiles) {
+  if (lane == 0) *(volatile uint32_t*)&w.progress = tiles;
 }
 
 // Once for each item with work for the matrix instructions (Item::keys).
@@ -135,7 +174,7 @@ __device__ __forceinline__ void want_work(WorkState& w, int lane) {
 // The k-th item, for a whole warp; its slot may be filled again after that.
 template <class Item>
 __device__ __forceinline__ Item take_work(WorkState& w, const Item* slots, int k, int lane, volatile int32_t* dead) {
-  mbar_wait(smem_at(&w.full[k & 1]), (k >> 1) & 1, dead);
+  wait_for(smem_at(&w.full[k & 1]), (k >> 1) & 1, dead);
   Item x = slots[k & 1];
   if (*dead) x.n0 = -1;
   __syncwarp();

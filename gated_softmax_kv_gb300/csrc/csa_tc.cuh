@@ -9,7 +9,7 @@
 
 namespace csa {
 
-constexpr int kPolls = 1 << 20;
+constexpr int kPolls = 1 << 20;  // of a wait: a poll that fails takes about 2700 cycles, all of them 1.4 s
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
