@@ -254,13 +254,6 @@ __device__ __forceinline__ void store_columns(void* to, int64_t at, int d, int c
   }
 }
 
-// Copies under way land before a CTA that gave up ends: the last `stages` of a ring.
-__device__ __forceinline__ void drain(uint32_t full, int stages, uint32_t issued) {
-  for (uint32_t j = issued > (uint32_t)stages ? issued - stages : 0; j < issued; ++j)
-    for (int k = 0; k < kPolls && !mbar_try(full + 8 * (j % stages), (j / stages) & 1); ++k) {
-    }
-}
-
 template <class C>
 __device__ __forceinline__ void load_tile(uint32_t to, const CUtensorMap* map, int head, int token, uint32_t bar) {
 #pragma unroll 1
@@ -289,6 +282,27 @@ struct KeysState {
   uint32_t tmem;
 };
 static_assert(sizeof(KeysState) <= 8192, "HEAD");
+
+// Item `id`, by a warp; n0 < 0 where the slot has none. Earlier slots first: a sequence's
+// first keys are seen by the most rows.
+__device__ __forceinline__ KeysItem keys_item(const PromptArgs& a, uint32_t id, int lane) {
+  KeysItem x;
+  const int64_t slot = id / a.kv;
+  x.kvh = (int)(id - slot * a.kv);
+  const int s = seq_of_slot(a.cu_k, a.nseq, 128, slot, lane);
+  x.w = span_of(a, s);
+  x.n0 = -1;
+  const int64_t local = slot - first_slot(a.cu_k, s, 128);
+  if (local < 0 || local * 128 >= x.w.nk) return x;
+  x.k0 = (int)local * 128;
+  x.off = x.w.nk - x.w.nq;
+  x.tp = 128 / a.group;
+  x.t0 = max(0, x.k0 - x.off);
+  int t1 = x.w.nq;  // behind the last query that sees a key
+  if (a.window) t1 = (int)min((int64_t)t1, (int64_t)min(x.k0 + 128, x.w.nk) - 1 - x.off + a.window);
+  x.n0 = t1 > x.t0 ? (t1 - x.t0 + x.tp - 1) / x.tp : 0;
+  return x;
+}
 
 // Whether some row of tile j does not see some key of the CTA, or is not there.
 __device__ __forceinline__ bool keys_mixed(const PromptArgs& a, const KeysItem& x, int j) {
@@ -499,56 +513,44 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int64_t words = (int64_t)a.kv * a.d / 8, from = id * 32 + lane, step = (int64_t)gridDim.x * 32;
         fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dk), from, step);
         fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dv), from, step);
-        // earlier slots first: a sequence's first keys are seen by the most rows
-        KeysItem x;
-        const int64_t slot = id / a.kv;
-        x.kvh = (int)(id - slot * a.kv);
-        const int s = seq_of_slot(a.cu_k, a.nseq, 128, slot, lane);
-        x.w = span_of(a, s);
-        x.n0 = -1;
-        const int64_t local = slot - first_slot(a.cu_k, s, 128);
-        if (local < 0 || local * 128 >= x.w.nk) return x;
-        x.k0 = (int)local * 128;
-        x.off = x.w.nk - x.w.nq;
-        x.tp = tp;
-        x.t0 = max(0, x.k0 - x.off);
-        int t1 = x.w.nq;  // behind the last query that sees a key
-        if (a.window) t1 = (int)min((int64_t)t1, (int64_t)min(x.k0 + 128, x.w.nk) - 1 - x.off + a.window);
-        x.n0 = t1 > x.t0 ? (t1 - x.t0 + tp - 1) / tp : 0;
-        return x;
+        return keys_item(a, id, lane);
       });
     } else if (warp == 9) {  // ---- copies
-      uint32_t tiles = 0, loaded = 0;
+      uint32_t q_tiles = 0, g_tiles = 0, loaded = 0;
       const int bytes = C::DP / 64 * 128 * rows;
 #pragma unroll 1
       for (int k = 0;; ++k) {
         const KeysItem x = take(k);
         if (x.n0 < 0) break;
         if (x.n0 == 0) continue;
-        if (lane == 0) {
-          wait_for(kv_empty, (loaded & 1) ^ 1, dead);
+        if (lane == 0) wait_for(kv_empty, (loaded & 1) ^ 1, dead);
+        if (lane == 0 && !*dead) {
+          ++loaded;
           mbar_expect(kv_full, 2 * C::TILE);
           load_tile<C>(k_at, &mk, x.kvh, x.w.k0 + x.k0, kv_full);
           load_tile<C>(v_at, &mv, x.kvh, x.w.k0 + x.k0, kv_full);
 #pragma unroll 1
-          for (int j = 0; j < x.n0 && !*dead; ++j, ++tiles) {
-            const uint32_t stage = tiles & 1, parity = ((tiles >> 1) & 1) ^ 1;
+          for (int j = 0; j < x.n0; ++j) {
+            const uint32_t stage = q_tiles & 1, parity = ((q_tiles >> 1) & 1) ^ 1;
             const int token = x.w.q0 + x.t0 + j * tp;
             wait_for(q_empty + 8 * stage, parity, dead);
+            if (*dead) break;
+            ++q_tiles;
             mbar_expect(q_full + 8 * stage, bytes);
             load_tile<C>(q_at + stage * C::TILE, &mq, x.kvh * a.group, token, q_full + 8 * stage);
             wait_for(g_empty + 8 * stage, parity, dead);
+            if (*dead) break;
+            ++g_tiles;
             mbar_expect(g_full + 8 * stage, bytes);
             load_tile<C>(g_at + stage * C::TILE, &mg, x.kvh * a.group, token, g_full + 8 * stage);
           }
-          if (*dead) {
-            drain(kv_full, 1, loaded + 1);
-            drain(q_full, 2, tiles);
-            drain(g_full, 2, tiles);
-          }
         }
         __syncwarp();
-        ++loaded;
+      }
+      if (lane == 0) {
+        land_ring(kv_full, 1, loaded);
+        land_ring(q_full, 2, q_tiles);
+        land_ring(g_full, 2, g_tiles);
       }
     } else if (warp == 10) {  // ---- the rows' numbers, with the tile of q; cleaning
       // S and dP of a tile may be formed before, while or after it is cleaned: a row that holds
@@ -657,6 +659,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         tc_commit_by(leader, done);
       }
+      end_products(st.work, leader);
     }
   } else {  // ---- P and dS: a key a thread, half of a tile's rows
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MATH_REGS));
@@ -720,6 +723,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncthreads();
   tc_after();
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (*dead)
+    for_last_items(st.work, [&](uint32_t id) {
+      const KeysItem x = keys_item(a, id, lane);
+      const int vectors = a.d / 8;
+#pragma unroll 1
+      for (int i = threadIdx.x; i < min(128, x.w.nk - x.k0) * vectors; i += C::THREADS) {
+        const int64_t row = (int64_t)(x.w.k0 + x.k0 + i / vectors) * a.kv + x.kvh;
+        put_nan(a.dk, row, vectors, i % vectors);
+        put_nan(a.dv, row, vectors, i % vectors);
+      }
+    });
 }
 
 // ---- dQ -------------------------------------------------------------------------
@@ -743,6 +757,27 @@ struct RowsState {
   uint32_t tmem;
 };
 static_assert(sizeof(RowsState) <= 1024, "in front of the tiles");
+
+// Item `id`, by a warp; n0 < 0 where the slot has none. Later slots first: a sequence's last
+// tiles see the most keys.
+__device__ __forceinline__ RowsItem rows_item(const PromptArgs& a, uint32_t id, uint32_t ids, int lane) {
+  RowsItem x;
+  const int tp = 128 / a.group;
+  id = ids - 1 - id;
+  const int64_t slot = id / a.kv;
+  x.kvh = (int)(id - slot * a.kv);
+  const int s = seq_of_slot(a.cu_q, a.nseq, tp, slot, lane);
+  x.w = span_of(a, s);
+  x.n0 = -1;
+  const int64_t local = slot - first_slot(a.cu_q, s, tp);
+  if (local < 0 || local * tp >= x.w.nq) return x;
+  x.t0 = (int)local * tp;
+  x.t1 = min(x.t0 + tp, x.w.nq);
+  x.off = x.w.nk - x.w.nq;
+  x.kb0 = (a.window ? (int)max((int64_t)0, (int64_t)x.off + x.t0 + 1 - a.window) : 0) / 128;
+  x.n0 = x.off + x.t1 > 0 ? (x.off + x.t1 + 127) / 128 - x.kb0 : 0;
+  return x;
+}
 
 // Whether some row of the item does not see some key of block j.
 __device__ __forceinline__ bool rows_mixed(const PromptArgs& a, const RowsItem& x, int j) {
@@ -894,56 +929,45 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       find_work(st.work, st.item, blockIdx.x, false, lane, dead, [&](uint32_t id) {
         fill_rest(a.cu_q, a.nseq, a.num_q, (int64_t)a.heads * a.d / 8, static_cast<uint4*>(a.dq), id * 32 + lane,
                   (int64_t)gridDim.x * 32);
-        // later slots first: a sequence's last tiles see the most keys
-        RowsItem x;
-        id = gridDim.x - 1 - id;
-        const int64_t slot = id / a.kv;
-        x.kvh = (int)(id - slot * a.kv);
-        const int s = seq_of_slot(a.cu_q, a.nseq, tp, slot, lane);
-        x.w = span_of(a, s);
-        x.n0 = -1;
-        const int64_t local = slot - first_slot(a.cu_q, s, tp);
-        if (local < 0 || local * tp >= x.w.nq) return x;
-        x.t0 = (int)local * tp;
-        x.t1 = min(x.t0 + tp, x.w.nq);
-        x.off = x.w.nk - x.w.nq;
-        x.kb0 = (a.window ? (int)max((int64_t)0, (int64_t)x.off + x.t0 + 1 - a.window) : 0) / 128;
-        x.n0 = x.off + x.t1 > 0 ? (x.off + x.t1 + 127) / 128 - x.kb0 : 0;
-        return x;
+        return rows_item(a, id, gridDim.x, lane);
       });
     } else if (warp == 9) {  // ---- copies
       Place<kKeyStages> at = {0, 0};
       Place<kValueStages> value = {0, 0};
-      uint32_t loaded = 0, tiles = 0;
+      uint32_t loaded = 0, k_tiles = 0, v_tiles = 0;
 #pragma unroll 1
       for (int k = 0;; ++k) {
         const RowsItem x = take(k);
         if (x.n0 < 0) break;
         if (x.n0 == 0) continue;
-        if (lane == 0) {
-          wait_for(q_empty, (loaded & 1) ^ 1, dead);
+        if (lane == 0) wait_for(q_empty, (loaded & 1) ^ 1, dead);
+        if (lane == 0 && !*dead) {
+          ++loaded;
           mbar_expect(q_full, 2 * (C::DP / 64) * 128 * rows);
           load_tile<C>(q_at, &mq, x.kvh * a.group, x.w.q0 + x.t0, q_full);
           load_tile<C>(g_at, &mg, x.kvh * a.group, x.w.q0 + x.t0, q_full);
 #pragma unroll 1
-          for (int j = 0; j < x.n0 && !*dead; ++j, ++tiles) {
+          for (int j = 0; j < x.n0; ++j) {
             wait_for(k_empty + 8 * at.stage, at.parity ^ 1, dead);
+            if (*dead) break;
+            ++k_tiles;
             mbar_expect(k_full + 8 * at.stage, C::TILE);
             load_tile<C>(k_at + at.stage * C::TILE, &mk, x.kvh, x.w.k0 + (x.kb0 + j) * 128, k_full + 8 * at.stage);
             at.next(1);
             wait_for(v_empty + 8 * value.stage, value.parity ^ 1, dead);
+            if (*dead) break;
+            ++v_tiles;
             mbar_expect(v_full + 8 * value.stage, C::TILE);
             load_tile<C>(v_at + value.stage * C::TILE, &mv, x.kvh, x.w.k0 + (x.kb0 + j) * 128, v_full + 8 * value.stage);
             value.next(1);
           }
-          if (*dead) {
-            drain(q_full, 1, loaded + 1);
-            drain(k_full, kKeyStages, tiles);
-            drain(v_full, kValueStages, tiles);
-          }
         }
         __syncwarp();
-        ++loaded;
+      }
+      if (lane == 0) {
+        land_ring(q_full, 1, loaded);
+        land_ring(k_full, kKeyStages, k_tiles);
+        land_ring(v_full, kValueStages, v_tiles);
       }
     } else if (warp == 10) {  // ---- infinities and NaN of keys that not every row sees
       // S is formed from them as they are (a key may hold -inf to have no weight), so it comes first.
@@ -1040,6 +1064,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         tc_commit_by(leader, done);
       }
+      end_products(st.work, leader);
     }
   } else {  // ---- dS: a row a thread, half of a block's keys
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MATH_REGS));
@@ -1089,6 +1114,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncthreads();
   tc_after();
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (*dead)
+    for_last_items(st.work, [&](uint32_t id) {
+      const RowsItem x = rows_item(a, id, gridDim.x, lane);
+      const int vectors = a.d / 8;
+#pragma unroll 1
+      for (int i = threadIdx.x; i < (x.t1 - x.t0) * a.group * vectors; i += C::THREADS) {
+        const int r = i / vectors;
+        const int64_t row = (int64_t)(x.w.q0 + x.t0 + r / a.group) * a.heads + x.kvh * a.group + r % a.group;
+        put_nan(a.dq, row, vectors, i % vectors);
+      }
+    });
 }
 
 template <class C>

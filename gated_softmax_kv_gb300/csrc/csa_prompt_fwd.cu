@@ -35,8 +35,8 @@
 // tokens of 64 heads of 64, 92 us. Single tokens: memory, 32 sequences of 8192 keys, 8 key
 // heads of 128, 158 us (6.8 TB/s).
 //
-// Every wait on an mbarrier is bounded (csa_prompt_tile.cuh): a wait that runs out marks the CTA, whose
-// later waits return at once and whose results become NaN.
+// Every wait on an mbarrier is bounded (csa_prompt_tile.cuh): a wait that runs out marks the
+// CTA, whose later waits return at once and whose unfinished items' results become NaN.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     } else if (warp == 9) {  // ---- copies
       Place<C::NS> at = {0, 0};
       uint32_t loaded = 0;  // items with keys
-      int copies = 0;
+      uint32_t copies = 0;
       if (lane == 0) {
         tma_prefetch(&mq);
         tma_prefetch(&mk);
@@ -323,9 +323,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (x.n0 < 0) break;
         const int n = max(x.n0, x.n1);
         if (n == 0) continue;
-        if (lane == 0) {
+        if (lane == 0) wait_for(q_empty, (loaded & 1) ^ 1, dead);
+        if (lane == 0 && !*dead) {
           const int tiles = x.step == 1 && x.n1 > 0 ? 2 : 1;
-          wait_for(q_empty, (loaded & 1) ^ 1, dead);
           mbar_expect(q_full, tiles * (C::DP / 64) * 128 * rows);
 #pragma unroll 1
           for (int t = 0; t < tiles; ++t)
@@ -333,10 +333,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int p = 0; p < C::DP / 64; ++p)
               tma_load(q_at + t * C::TILE + p * C::SLAB, &mq, p * 64, x.kvh * a.group, x.q0 + x.t0 + t * tp, q_full);
 #pragma unroll 1
-          for (int i = 0; i < 2 * n && !*dead; ++i) {
+          for (int i = 0; i < 2 * n; ++i) {
             bool value;
             const int b = tile_at(i, n, x.step, value);
             wait_for(empty + 8 * at.stage, at.parity ^ 1, dead);
+            if (*dead) break;
             mbar_expect(full + 8 * at.stage, C::TILE);
 #pragma unroll 1
             for (int p = 0; p < C::DP / 64; ++p)
@@ -345,19 +346,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             ++copies;
             at.next(1);
           }
-          if (*dead) {  // copies under way land before the CTA ends
-#pragma unroll 1
-            for (int j = max(0, copies - C::NS); j < copies; ++j)
-#pragma unroll 1
-              for (int i = 0; i < kPolls && !mbar_try(full + 8 * (j % C::NS), (j / C::NS) & 1); ++i) {
-              }
-#pragma unroll 1
-            for (int i = 0; i < kPolls && !mbar_try(q_full, loaded & 1); ++i) {
-            }
-          }
+          ++loaded;
         }
         __syncwarp();
-        ++loaded;
+      }
+      if (lane == 0) {
+        land_ring(full, C::NS, copies);
+        land_ring(q_full, 1, loaded);
       }
     } else if (warp == 8) {  // ---- matrix instructions
       // Issuing them is a warp's whole work: what it counts stays in registers, with no
@@ -483,6 +478,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         copies += 2 * n;
         start = {(int)(copies % C::NS), (copies / C::NS) & 1};
       }
+      end_products(st.work, leader);
     }
   } else {  // ---- softmax and result: a row a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
@@ -691,6 +687,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncthreads();
   tc_after();
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (*dead) {
+    if (shape.split > 1) {
+      if (threadIdx.x < 128) st.ref[threadIdx.x] = NAN;
+    } else {
+      for_last_items(st.work, [&](uint32_t id) {
+        const Item x = item_of(a, shape, id, ids, 0, lane);
+        const int vectors = a.d / 8;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < (x.last - x.t0 + 1) * a.group * vectors; i += C::THREADS) {
+          const int r = i / vectors;
+          const int64_t row = (int64_t)(x.q0 + x.t0 + r / a.group) * a.heads + x.kvh * a.group + r % a.group;
+          put_nan(a.out, row, vectors, i % vectors);
+          if (a.rest) put_nan(a.rest, row, vectors, i % vectors);
+          if (i % vectors == 0) a.lse[row] = NAN;
+        }
+      });
+    }
+  }
   if (shape.split > 1) {
     // The CTAs of the cluster join the rows that are there, eight columns a thread.
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -735,6 +749,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], f, o[i]);
       }
+      if (top != top) l = NAN;  // a CTA that gave up
       const bool some = !(l == 0.0f);
       const float f = some ? 1.0f / l : 0.0f;
       const int64_t row = (int64_t)(x.q0 + x.t0 + r / a.group) * a.heads + x.kvh * a.group + r % a.group;

@@ -61,7 +61,8 @@ __device__ __forceinline__ void fill_rest(const int32_t* cu, int nseq, int32_t n
 // ---- waits --------------------------------------------------------------------
 //
 // Bounded: dead[1] polls after the first without the phase mark the CTA (dead[0]), and no
-// further wait waits. A poll that fails takes about 2700 cycles (1.4 us), so the usual
+// further wait waits. A CTA that gave up copies and takes over nothing more, waits for what it
+// has under way (`land`), and writes NaN over the results of its last items (ids). A poll that fails takes about 2700 cycles (1.4 us), so the usual
 // kPolls of them 1.4 s, for what takes microseconds: a copy, a product, a tile's arithmetic.
 
 __device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, volatile int32_t* dead) {
@@ -72,6 +73,9 @@ __device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, volatile
       return;
     }
 }
+
+// Whether the CTA has given up, the same for a whole warp.
+__device__ __forceinline__ bool gave_up(const volatile int32_t* dead) { return __any_sync(0xFFFFFFFFu, *dead != 0); }
 
 // For what may take as long as an item, and that is as long as the sequence: as many polls
 // each time that *progress (a count of tiles) has moved since the last.
@@ -90,6 +94,20 @@ __device__ __forceinline__ void wait_through(uint32_t bar, uint32_t parity, vola
     }
 }
 
+// For what the hardware has under way, copies, products or an answer, which ends by itself
+// and before the CTA may.
+__device__ __forceinline__ bool land(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < kPolls; ++i)
+    if (mbar_try(bar, parity)) return true;
+  return false;
+}
+// The last `stages` of a ring's copies.
+__device__ __forceinline__ void land_ring(uint32_t full, uint32_t stages, uint32_t issued) {
+#pragma unroll 1
+  for (uint32_t j = issued > stages ? issued - stages : 0; j < issued; ++j) land(full + 8 * (j % stages), (j / stages) & 1);
+}
+
 // ---- items of work -----------------------------------------------------------
 //
 // A warp of its own finds the items (type Item, n0 < 0: none): first the CTA's own, then
@@ -101,8 +119,12 @@ __device__ __forceinline__ void wait_through(uint32_t bar, uint32_t parity, vola
 
 struct WorkState {
   alignas(16) uint32_t stolen[4];
-  uint64_t full[2], empty[2], steal, want;
+  uint64_t full[2], empty[2], steal, want, ended;  // ended: the products
   uint32_t progress;  // tiles of the matrix instructions
+  // Of the items that were found, by their number: unfinished are at most the one whose
+  // result is formed, two in the slots and one that waits for a slot.
+  uint32_t ids[4];
+  int32_t found;
 };
 
 __device__ __forceinline__ void init_work(WorkState& w, int takers) {
@@ -112,7 +134,9 @@ __device__ __forceinline__ void init_work(WorkState& w, int takers) {
   }
   mbar_init(smem_at(&w.steal), 1);
   mbar_init(smem_at(&w.want), 1);
+  mbar_init(smem_at(&w.ended), 1);
   w.progress = 0;
+  w.found = 0;
 }
 
 template <class Item, class Find>
@@ -125,16 +149,21 @@ __device__ __forceinline__ void find_work(WorkState& w, Item* slots, uint32_t id
   for (int n = 0;; ++n) {
     const Item x = find(id);
     if (x.n0 >= 0) {
+      if (lane == 0) {
+        w.ids[k & 3] = id;
+        w.found = k + 1;
+      }
       wait_for(empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
+      if (gave_up(dead)) return;  // the slot may be in use, and no one takes it any more
       if (lane == 0) {
         slots[k & 1] = x;
         mbar_arrive(full + 8 * (k & 1));
       }
       ++k;
     }
-    if (once || *dead) break;
+    if (once) break;
     if (x.keys()) wait_through(smem_at(&w.want), wanted++ & 1, dead, &w.progress);
-    __syncwarp();
+    if (gave_up(dead)) return;
     if (lane == 0) {
       mbar_expect(steal, 16);
       asm volatile(
@@ -143,7 +172,10 @@ __device__ __forceinline__ void find_work(WorkState& w, Item* slots, uint32_t id
           "r"(steal)
           : "memory");
     }
-    wait_for(steal, n & 1, dead);
+    if (!__any_sync(0xFFFFFFFFu, land(steal, n & 1))) {
+      *dead = 1;
+      return;
+    }
     uint32_t got;
     asm volatile(
         "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
@@ -152,9 +184,10 @@ __device__ __forceinline__ void find_work(WorkState& w, Item* slots, uint32_t id
         : "=r"(got), "=r"(id)
         : "r"(stolen)
         : "memory");
-    if (!got || *dead) break;
+    if (!got) break;
   }
   wait_for(empty + 8 * (k & 1), ((k >> 1) & 1) ^ 1, dead);
+  if (gave_up(dead)) return;
   if (lane == 0) {
     slots[k & 1].n0 = -1;
     mbar_arrive(full + 8 * (k & 1));
@@ -164,6 +197,23 @@ __device__ __forceinline__ void find_work(WorkState& w, Item* slots, uint32_t id
 // The warp of the matrix instructions, once a tile.
 __device__ __forceinline__ void tile_done(WorkState& w, int lane, uint32_t tiles) {
   if (lane == 0) *(volatile uint32_t*)&w.progress = tiles;
+}
+
+// The same warp, when it has issued its last: the products are done.
+__device__ __forceinline__ void end_products(WorkState& w, uint32_t leader) {
+  tc_commit_by(leader, smem_at(&w.ended));
+  land(smem_at(&w.ended), 0);
+}
+
+// For a CTA that gave up, when its warps have met: f(id) for its last items.
+template <class F>
+__device__ __forceinline__ void for_last_items(const WorkState& w, F f) {
+#pragma unroll 1
+  for (int k = max(0, w.found - 4); k < w.found; ++k) f(w.ids[k & 3]);
+}
+// NaN of either type in a row of `vectors` 16-byte vectors.
+__device__ __forceinline__ void put_nan(void* to, int64_t row, int vectors, int at) {
+  static_cast<uint4*>(to)[row * vectors + at] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
 }
 
 // Once for each item with work for the matrix instructions (Item::keys).
@@ -176,8 +226,7 @@ template <class Item>
 __device__ __forceinline__ Item take_work(WorkState& w, const Item* slots, int k, int lane, volatile int32_t* dead) {
   wait_for(smem_at(&w.full[k & 1]), (k >> 1) & 1, dead);
   Item x = slots[k & 1];
-  if (*dead) x.n0 = -1;
-  __syncwarp();
+  if (gave_up(dead)) x.n0 = -1;
   if (lane == 0) mbar_arrive(smem_at(&w.empty[k & 1]));
   return x;
 }
