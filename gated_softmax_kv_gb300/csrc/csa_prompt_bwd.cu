@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(128) prompt_delta_kernel(const __grid_constant
           span = min(step, span - k * step);
           lo += k * step;
         }
-        const Span w = span_of(a, lo);
+        const Span w = span_of<false>(a, lo);
         in = t >= w.q0 && t < (int64_t)w.q0 + w.nq;
         single = in && (a.window == 1 || w.nk - w.nq + (int)(t - w.q0) + 1 == 1);
         if (!in) break;
@@ -290,7 +290,7 @@ __device__ __forceinline__ KeysItem keys_item(const PromptArgs& a, uint32_t id, 
   const int64_t slot = id / a.kv;
   x.kvh = (int)(id - slot * a.kv);
   const int s = seq_of_slot(a.cu_k, a.nseq, 128, slot, lane);
-  x.w = span_of(a, s);
+  x.w = span_of<true>(a, s);
   x.n0 = -1;
   const int64_t local = slot - first_slot(a.cu_k, s, 128);
   if (local < 0 || local * 128 >= x.w.nk) return x;
@@ -767,7 +767,7 @@ __device__ __forceinline__ RowsItem rows_item(const PromptArgs& a, uint32_t id, 
   const int64_t slot = id / a.kv;
   x.kvh = (int)(id - slot * a.kv);
   const int s = seq_of_slot(a.cu_q, a.nseq, tp, slot, lane);
-  x.w = span_of(a, s);
+  x.w = span_of<false>(a, s);
   x.n0 = -1;
   const int64_t local = slot - first_slot(a.cu_q, s, tp);
   if (local < 0 || local * tp >= x.w.nq) return x;

@@ -155,7 +155,7 @@ __device__ __forceinline__ Item item_of(const PromptArgs& a, const FwdShape& sha
   const int64_t slot = id / a.kv;
   x.kvh = (int)(id - slot * a.kv);
   const int s = seq_of_slot(a.cu_q, a.nseq, b, slot, lane);
-  const Span w = span_of(a, s);
+  const Span w = span_of<false>(a, s);
   const int64_t local = slot - first_slot(a.cu_q, s, b);
   x.q0 = w.q0;
   x.nq = w.nq;

@@ -34,18 +34,28 @@ struct PromptArgs {
 // What PromptArgs::polls is: kPolls (csa_tc.cuh), unless a test has set it lower.
 extern "C" int32_t csa_prompt_polls;
 
-// A sequence's rows, checked: an empty one where the lists do not make sense.
+// A sequence's rows. Where its lists pass the tensors, or one of them decreases, its queries see
+// no key: to a kernel of query rows it has those inside q and no keys, to one of keys (KEYS)
+// those inside k and no queries, so that their results are written all the same.
 struct Span {
   int32_t q0, nq, k0, nk;
 };
+template <bool KEYS>
 __device__ __forceinline__ Span span_of(const PromptArgs& a, int s) {
   Span w;
   w.q0 = __ldg(a.cu_q + s);
   w.k0 = __ldg(a.cu_k + s);
   const int32_t q1 = __ldg(a.cu_q + s + 1), k1 = __ldg(a.cu_k + s + 1);
   const bool ok = w.q0 >= 0 && w.q0 <= q1 && q1 <= a.num_q && w.k0 >= 0 && w.k0 <= k1 && k1 <= a.num_k;
-  w.nq = ok ? q1 - w.q0 : 0;
-  w.nk = ok ? k1 - w.k0 : 0;
+  if (ok) {
+    w.nq = q1 - w.q0;
+    w.nk = k1 - w.k0;
+  } else {
+    w.q0 = min(max(w.q0, 0), a.num_q);
+    w.k0 = min(max(w.k0, 0), a.num_k);
+    w.nq = KEYS ? 0 : max(min(q1, a.num_q) - w.q0, 0);
+    w.nk = KEYS ? max(min(k1, a.num_k) - w.k0, 0) : 0;
+  }
   return w;
 }
 

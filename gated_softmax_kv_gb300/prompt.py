@@ -127,6 +127,7 @@ def csa_prompt_attend(q, k, v, cu_q, sm_scale: float, *, cu_k=None, window=None,
     behind what is held. window: how many tokens a query sees, its own included
     (None: all). lse (natural logarithm, fp32 [tokens, heads]) lets the result be
     merged with csa_cache_attend's over compressed rows.
+    Lists that pass the tensors leave the queries of those sequences without keys.
 
     Rows of no sequence (a static capacity's) are 0, and -inf in lse, in tensors
     that the call makes, and left as they were in those that it is given. rest (of

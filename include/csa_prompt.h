@@ -46,8 +46,10 @@
  * Rows of no sequence (before cu_q[0], at or behind cu_q[num_seqs]) are left as
  * they were, or with CSA_FILL_OUT become 0 in out and rest, with CSA_FILL_LSE
  * -inf in lse; their dq, and dk and dv of such keys, are 0. cu_q and cu_k do not
- * decrease and end within the tensors; a sequence for which that does not hold
- * is treated as empty. Kernels stay inside the buffers whatever they hold.
+ * decrease and end within the tensors. The queries of a sequence that passes a
+ * tensor's end see no key: out 0, lse -inf, and gradients of 0 for its rows. With
+ * lists that decrease it is not specified what rows hold. Kernels stay inside the
+ * buffers whatever the lists hold.
  *
  * Asynchronous on `stream`, no host synchronisation; lengths are read on the
  * device. Workspaces come from the library's stream-ordered pool. Results are the
