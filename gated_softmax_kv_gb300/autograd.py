@@ -167,5 +167,9 @@ def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch
     """Differentiable csa_prompt_attend (same arguments, no outputs of the caller's):
     (out, lse), both with gradients to q, k and v. A gradient that arrives broadcast
     or unaligned is copied first. The gradient is not itself differentiable.
-    Captured into a CUDA graph under the condition that `rope` states."""
+    For the gradient it keeps q, k, v, out, lse and what out's rounding left off, a tensor
+    of out's size; where none is wanted that is not made. Captured into a CUDA graph
+    under the condition that `rope` states."""
+    if not (torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v))):
+        return csa_prompt_attend(q, k, v, cu_q, sm_scale, cu_k=cu_k, window=window)
     return PromptAttendFunction.apply(q, k, v, cu_q, cu_k, sm_scale, window)
