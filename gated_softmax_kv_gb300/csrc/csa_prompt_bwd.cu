@@ -36,6 +36,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "csa_cache_internal.h"
 #include "csa_internal.h"
 #include "csa_prompt_tile.cuh"
@@ -48,7 +50,18 @@ struct BwdArgs {
   PromptArgs a;
   float2* stats;    // [num_q * heads]: -(lse log2 e - lift), -delta
   uint32_t* sizes;  // fp16: bits of the largest finite |grad row|, |v row|, |grad_lse|
+  // Where items may have more than kSumTiles tiles: a place of two [DP][128] fp32 for each CTA
+  // that can run, and which are taken.
+  float* sums;
+  uint32_t* taken;
+  int32_t places;
 };
+
+// The tensor core truncates as it accumulates: sums of 16 terms more lose about 2^-25 of what
+// is there, always towards 0 (dK of 6.4 million rows, 100003 tokens of 64 heads over one, 1.4%).
+// So dK and dV leave it after this many tiles and are added up in fp32, rounded to nearest:
+// what is lost stays near 2^-13. A power of two.
+constexpr int kSumTiles = 512;
 
 template <bool HALF>
 constexpr float kPLift = HALF ? 15.0f : 0.0f;
@@ -280,6 +293,7 @@ struct KeysState {
   uint64_t kv_full, kv_empty, q_full[2], q_empty[2], g_full[2], g_empty[2], r_full[2], s_full, p_full[2], dp_full, ds_full[2], done, clean[2];
   int32_t dead, polls, bad;
   uint32_t tmem;
+  int32_t place;  // of BwdArgs::sums
 };
 static_assert(sizeof(KeysState) <= 8192, "HEAD");
 
@@ -444,6 +458,22 @@ __device__ __noinline__ void keys_step_some(KeysState& st, const KeysMath& m, ui
   keys_step<C, true>(st, m, j);
 }
 
+// The sums of a stretch of tiles, added to what the stretches before left: a key a thread.
+template <class C>
+__device__ __noinline__ void set_aside(float* sums, uint32_t at, bool first) {
+#pragma unroll 1
+  for (int i = 0; i < C::DP; i += 32) {
+    float o[32];
+    tc_load32(at + i, o);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      float* const to = sums + (i + c) * 128;
+      *to = first ? o[c] : *to + o[c];
+    }
+  }
+  tc_before();
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     prompt_keys_kernel(const __grid_constant__ BwdArgs b, const __grid_constant__ CUtensorMap mq,
@@ -485,6 +515,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     mbar_init(dp_full, 1);
     mbar_init(done, 1);
     init_work(st.work, 11);  // eight warps of the arithmetic, copies, the rows' numbers, matrix instructions
+    if (b.sums) {  // as many places as CTAs reside, so that one is free
+      uint32_t sm;
+      asm("mov.u32 %0, %smid;" : "=r"(sm));
+      int place = (int)(sm % (uint32_t)b.places);
+#pragma unroll 1
+      for (int i = 0; atomicExch(b.taken + place, 1u); ++i) {
+        place = place + 1 < b.places ? place + 1 : 0;
+        if (i == kPolls) {
+          st.dead = 1;
+          break;
+        }
+      }
+      st.place = place;
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // rows of a tile that no head uses are never copied to, and must not hold NaN
@@ -618,8 +662,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         tc_commit_by(leader, dp_full);
       };
       auto add = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t ready, uint32_t j, bool first) {
-        // An item's first product writes over the last one's sums: both groups of the
-        // arithmetic have read them when both have formed something of this item.
+        // The first product of an item, or of a stretch, writes over the last one's sums: both
+        // groups of the arithmetic have read them when both have formed something of this one.
         if (first) wait_for(ready + 8, j & 1, dead);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -647,11 +691,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             cleaned ^= 1u << (tiles & 1);
             tc_after();
           }
-          add(DV, S, g_at + (tiles & 1) * C::TILE, p_full, tiles, j == 0);
+          const bool first = (j & (kSumTiles - 1)) == 0;
+          add(DV, S, g_at + (tiles & 1) * C::TILE, p_full, tiles, first);
           tc_commit_by(leader, g_empty + 8 * (tiles & 1));
           if (j + 1 < n) scores(tiles + 1);
-          add(DK, DP, q_at + (tiles & 1) * C::TILE, ds_full, tiles, j == 0);
+          add(DK, DP, q_at + (tiles & 1) * C::TILE, ds_full, tiles, first);
           tc_commit_by(leader, q_empty + 8 * (tiles & 1));
+          if (((j + 1) & (kSumTiles - 1)) == 0 && j + 1 < n) tc_commit_by(leader, done);
           if (j + 1 < n)
             weights(tiles + 1);
           else
@@ -668,7 +714,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int e = gradient_exponent<C::HALF>(b);
     KeysMath m = {dead, tmem + lanes + col, tmem + 128 + lanes + col, r_full, s_full, p_full + 8 * half, dp_full,
                   ds_full + 8 * half, col, 0, a.scale * kLog2e, C::HALF ? exp2f((float)-e) : 1.0f};
-    uint32_t tiles = 0, items = 0;
+    uint32_t tiles = 0, stretches = 0;
+    // this thread's of the CTA's place
+    float* const sums = b.sums + ((int64_t)(b.sums ? st.place : 0) * 2 + half) * C::DP * 128 + (threadIdx.x & 127);
 #pragma unroll 1
     for (int k = 0;; ++k) {
       KeysItem x = take(k);
@@ -689,10 +737,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           keys_step_some<C>(st, m, tiles);
         else
           keys_step<C, false>(st, m, tiles);
+        if (((j + 1) & (kSumTiles - 1)) == 0 && j + 1 < x.n0) {
+          wait_for(done, stretches++ & 1, dead);
+          tc_after();
+          set_aside<C>(sums, tmem + 256 + half * C::DP + lanes, j < kSumTiles);
+        }
       }
       x.w.nq = nq;
       // group 0 stores dV, group 1 dK
-      if (x.n0 > 0) wait_for(done, items++ & 1, dead);
+      if (x.n0 > 0) wait_for(done, stretches++ & 1, dead);
       tc_after();
       const bool there = m.key < x.w.nk;
       const int64_t row = ((int64_t)(x.w.k0 + m.key) * a.kv + x.kvh) * a.d;
@@ -704,6 +757,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (int i = 0; i < C::DP; i += 32) {
         float o[32];
         if (x.n0 > 0) tc_load32(tmem + 256 + half * C::DP + lanes + i, o);
+        if (x.n0 > kSumTiles) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] += sums[(i + c) * 128];
+        }
 #pragma unroll
         for (int c = 0; c < 32; ++c) o[c] = x.n0 > 0 ? o[c] * factor : 0.0f;
         if (bad && there && i < a.d) {
@@ -723,6 +780,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   __syncthreads();
   tc_after();
   if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (b.sums && threadIdx.x == 0) {
+    __threadfence();
+    atomicExch(b.taken + st.place, 0u);
+  }
   if (*dead)
     for_last_items(st.work, [&](uint32_t id) {
       const KeysItem x = keys_item(a, id, lane);
@@ -1154,15 +1215,22 @@ cudaError_t launch_passes(const BwdArgs& b, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_prompt_bwd(const PromptArgs& a, bool half, cudaStream_t stream) {
-  BwdArgs b;
+  BwdArgs b = {};
   b.a = a;
-  const size_t stats = sizeof(float2) * (size_t)a.num_q * a.heads;
+  const int tp = 128 / a.group;
+  // one CTA an SM resides, by its registers
+  const bool many = (a.window ? std::min((int64_t)a.num_q, (int64_t)a.window + 128) : a.num_q) / tp + 1 > kSumTiles;
+  b.places = many ? sm_count() : 0;
+  const size_t stats = sizeof(float2) * (size_t)a.num_q * a.heads, place = sizeof(float) * 2 * 128 * (a.d <= 64 ? 64 : 128),
+               flags = 16 + sizeof(uint32_t) * (size_t)b.places;
   void* ws = nullptr;
-  cudaError_t e = workspace_take(&ws, stats + 16, stream);
+  cudaError_t e = workspace_take(&ws, place * b.places + stats + flags, stream);
   if (e != cudaSuccess) return e;
-  b.stats = static_cast<float2*>(ws);
-  b.sizes = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + stats);
-  if (half) e = cudaMemsetAsync(b.sizes, 0, 16, stream);
+  if (many) b.sums = static_cast<float*>(ws);
+  b.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + place * b.places);
+  b.sizes = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(b.stats) + stats);
+  b.taken = b.sizes + 4;
+  if (half || many) e = cudaMemsetAsync(b.sizes, 0, flags, stream);
   if (e == cudaSuccess) {
     const int64_t most = half && a.num_k > a.num_q ? a.num_k : a.num_q;
     int64_t blocks = (most + 3) / 4;

@@ -38,10 +38,14 @@
  * dk, dv ([tokens, heads, head_dim]) and lse, grad_lse ([tokens, heads], fp32) are
  * contiguous. Outputs overlap no input.
  *
- * Logits, softmax statistics and sums are fp32; the weights P and dS enter the
- * second products in the inputs' type. rest (may be null) is what the rounding of
- * out left off, out + rest being exact to twice the bits: with it the gradient's
- * delta loses nothing to that rounding.
+ * Logits, softmax statistics and sums are fp32. The tensor core's sums truncate: a
+ * row's over n keys lose up to n 2^-29 of their size, 2^-12 for 131072 keys; dk and
+ * dv, sums over all queries of up to 128 heads, are taken in parts that lose no more
+ * than 2^-13. The weights P and dS enter the second products in the inputs' type;
+ * fp16 lifts dS by one power of two for the whole call, which the largest finite rows
+ * of grad, grad_lse and v allow. rest (may be null) is what the rounding of out left
+ * off, out + rest being exact to twice the bits: with it the gradient's delta loses
+ * nothing to that rounding.
  *
  * Rows of no sequence (before cu_q[0], at or behind cu_q[num_seqs]) are left as
  * they were, or with CSA_FILL_OUT become 0 in out and rest, with CSA_FILL_LSE
