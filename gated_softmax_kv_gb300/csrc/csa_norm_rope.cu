@@ -521,8 +521,9 @@ cudaError_t launch_kind(NormArgs& a, bool vectors, cudaStream_t stream) {
   constexpr int V = HALF ? 2 : 1;  // vectors of a unit
   if (each == 1) return launch_heads<E, V, HALF, BWD>(a, stream);
   if (each == 2) return launch_heads<E, 2 * V, HALF, BWD>(a, stream);
-  if constexpr (4 * V * N <= 32) return launch_heads<E, 4 * V, HALF, BWD>(a, stream);
-  return cudaErrorInvalidValue;  // fp32 in halves: heads have at most 64 units
+  // fp32 in halves has at most 64 units: 128 vectors of 4 columns, two of them each
+  if constexpr (!HALF || sizeof(E) == 2) return launch_heads<E, 4 * V, HALF, BWD>(a, stream);
+  return cudaErrorInvalidValue;
 }
 
 template <typename E>
