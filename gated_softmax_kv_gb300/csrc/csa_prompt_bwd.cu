@@ -57,10 +57,10 @@ struct BwdArgs {
   int32_t places;
 };
 
-// The tensor core truncates as it accumulates: sums of 16 terms more lose about 2^-25 of what
-// is there, always towards 0 (dK of 6.4 million rows, 100003 tokens of 64 heads over one, 1.4%).
-// So dK and dV leave it after this many tiles and are added up in fp32, rounded to nearest:
-// what is lost stays near 2^-13. A power of two.
+// The tensor core truncates as it accumulates: 16 terms more cost up to 2^-24 of what is there,
+// always towards 0 (dK of 6.4 million rows, 100003 tokens of 64 heads over one: 1.4%). So dK
+// and dV leave it after this many tiles, 65536 terms, and are added up in fp32, rounded to
+// nearest: less than 2^-12 is lost. A power of two.
 constexpr int kSumTiles = 512;
 
 template <bool HALF>
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == 11) {  // ---- work
       find_work(st.work, st.item, blockIdx.x, false, lane, dead, [&](uint32_t id) {
-        const int64_t words = (int64_t)a.kv * a.d / 8, from = id * 32 + lane, step = (int64_t)gridDim.x * 32;
+        const int64_t words = (int64_t)a.kv * a.d / 8, from = (int64_t)id * 32 + lane, step = (int64_t)gridDim.x * 32;
         fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dk), from, step);
         fill_rest(a.cu_k, a.nseq, a.num_k, words, static_cast<uint4*>(a.dv), from, step);
         return keys_item(a, id, lane);
@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == 11) {  // ---- work
       find_work(st.work, st.item, blockIdx.x, false, lane, dead, [&](uint32_t id) {
-        fill_rest(a.cu_q, a.nseq, a.num_q, (int64_t)a.heads * a.d / 8, static_cast<uint4*>(a.dq), id * 32 + lane,
+        fill_rest(a.cu_q, a.nseq, a.num_q, (int64_t)a.heads * a.d / 8, static_cast<uint4*>(a.dq), (int64_t)id * 32 + lane,
                   (int64_t)gridDim.x * 32);
         return rows_item(a, id, gridDim.x, lane);
       });

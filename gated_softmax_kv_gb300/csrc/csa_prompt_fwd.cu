@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (warp == 10) {  // ---- work
       find_work(st.work, st.item, first_id, shape.split > 1, lane, dead, [&](uint32_t id) {
         if (part == 0) {  // this item's share of the rows of no sequence
-          const int64_t from = id * 32 + lane, step = (int64_t)ids * 32;
+          const int64_t from = (int64_t)id * 32 + lane, step = (int64_t)ids * 32;
           if (a.fill & CSA_FILL_OUT) {
             const int64_t words = (int64_t)a.heads * a.d / 8;
             fill_rest(a.cu_q, a.nseq, a.num_q, words, static_cast<uint4*>(a.out), from, step);

@@ -39,9 +39,9 @@
  * contiguous. Outputs overlap no input.
  *
  * Logits, softmax statistics and sums are fp32. The tensor core's sums truncate: a
- * row's over n keys lose up to n 2^-29 of their size, 2^-12 for 131072 keys; dk and
+ * row's over n keys lose up to n 2^-28 of their size, 2^-11 for 131072 keys; dk and
  * dv, sums over all queries of up to 128 heads, are taken in parts that lose no more
- * than 2^-13. The weights P and dS enter the second products in the inputs' type;
+ * than 2^-12. The weights P and dS enter the second products in the inputs' type;
  * fp16 lifts dS by one power of two for the whole call, which the largest finite rows
  * of grad, grad_lse and v allow. rest (may be null) is what the rounding of out left
  * off, out + rest being exact to twice the bits: with it the gradient's delta loses
@@ -57,7 +57,8 @@
  *
  * Asynchronous on `stream`, no host synchronisation; lengths are read on the
  * device. Workspaces come from the library's stream-ordered pool. Results are the
- * same from call to call.
+ * same from call to call. Waits inside the kernels are bounded: rows whose work did
+ * not go on for more than a second become NaN.
  */
 #ifndef CSA_PROMPT_H
 #define CSA_PROMPT_H
