@@ -28,9 +28,10 @@
 // as in the forward (csa_prompt_fwd.cu). Waits are bounded as there.
 //
 // What bounds it: on long sequences the tensor core under the power limit (8192 tokens of 32
-// heads over 8 of 128 columns: keys kernel 700 us, 1570 TFLOP/s of its four products, rows
-// kernel 600, 1370); heads of 64 columns the arithmetic, whose products take half as long
-// (8 ragged sequences of up to 1500 tokens, 24 heads over 8: 138 and 90 us).
+// heads over 8 of 128 columns: keys kernel 700 to 735 us by the box, up to 1570 TFLOP/s of its
+// four products, rows kernel 605 to 640, 1360); heads of 64 columns the arithmetic, whose
+// products take half as long (8 ragged sequences of up to 1500 tokens, 24 heads over 8: 140
+// and 96 us).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -74,3 +74,32 @@ def test_the_largest_gradient_of_lse(gsk):  # noqa: F811
     dq, dk, dv = gsk.csa_prompt_attend_bwd(q, k, v, out, lse, torch.zeros_like(q), cu, 0.125, grad_lse=gl)
     assert not torch.isnan(dq).any() and not torch.isnan(dk).any() and (dv == 0).all()
     assert torch.isinf(dq[50, 0]).any() and (dq[:50] == 0).all() and (dq[51:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_a_join_of_two_calls_where_a_query_sees_nothing_in_either(gsk, dtype):  # noqa: F811
+    """As README joins a window with other rows, with gradients: such a row is 0 and has no gradient, and
+    leaves the others' alone."""
+    from gated_softmax_kv_gb300 import autograd
+    nq, D = [6, 50], 64
+    q, k, v = (t.requires_grad_() for t in inputs(nq, [4, 50], 2, 1, D, dtype, 1))
+    k2, v2 = (t.requires_grad_() for t in inputs(nq, [3, 70], 2, 1, D, dtype, 5)[1:])
+    cu = i32(sums(nq))
+
+    def join(q, k, v, k2, v2, cu, ck, ck2):
+        o, lse = autograd.prompt_attend(q, k, v, cu, 0.125, cu_k=i32(ck), window=8)
+        o2, lse2 = autograd.prompt_attend(q, k2, v2, cu, 0.125, cu_k=i32(ck2))
+        both = torch.logaddexp(lse, lse2).clamp_min(-1e30)
+        return (lse - both).exp()[..., None] * o + (lse2 - both).exp()[..., None] * o2
+
+    out = join(q, k, v, k2, v2, cu, [0, 4, 54], [0, 3, 73])
+    assert (out[:2] == 0).all() and (out[2:].abs().sum(-1) > 0).all()
+    g = torch.randn(out.shape, generator=torch.Generator().manual_seed(2)).cuda()
+    got = torch.autograd.grad(out, [q, k, v, k2, v2], g)
+    assert all(torch.isfinite(t).all() for t in got) and (got[0][:2] == 0).all()
+    # the second sequence alone
+    alone = [t.detach()[n:].requires_grad_() for t, n in ((q, 6), (k, 4), (v, 4), (k2, 3), (v2, 3))]
+    one = join(*alone, i32([0, 50]), [0, 50], [0, 70])
+    assert torch.equal(one, out[6:])
+    for a, b, n in zip(got, torch.autograd.grad(one, alone, g[6:]), (6, 4, 4, 3, 3)):
+        near(a[n:], b)
