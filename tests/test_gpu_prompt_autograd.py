@@ -20,7 +20,10 @@ def test_nothing_is_kept_where_no_gradient_is_wanted(gsk, how):  # noqa: F811
     with torch.no_grad() if how == "no_grad" else torch.inference_mode(how == "inference_mode"):
         out, lse = autograd.prompt_attend(q, k, v, cu, 0.1, window=300)
     made = out.numel() * 2 + lse.numel() * 4
-    assert torch.cuda.max_memory_allocated() - before < made + 4096
+    # torch's allocator counts whole blocks: it leaves a cached block unsplit when less than 2^20 bytes would remain (out, of
+    # 4096000 bytes, comes from its pool of large blocks), and rounds lse's 64000 up to 512. A further tensor of out's
+    # size would add 4096000.
+    assert torch.cuda.max_memory_allocated() - before < made + 2 ** 20 + 512
     assert not out.requires_grad and not lse.requires_grad
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
