@@ -170,6 +170,6 @@ def prompt_attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch
     For the gradient it keeps q, k, v, out, lse and what out's rounding left off, a tensor
     of out's size; where none is wanted that is not made. Captured into a CUDA graph
     under the condition that `rope` states."""
-    if not (torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v))):
+    if not (torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (q, k, v))):
         return csa_prompt_attend(q, k, v, cu_q, sm_scale, cu_k=cu_k, window=window)
     return PromptAttendFunction.apply(q, k, v, cu_q, cu_k, sm_scale, window)
