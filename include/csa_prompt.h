@@ -19,8 +19,9 @@
  * and lse -inf. lse lets the result be merged with attention over other rows
  * (csa_cache_attend over compressed ones, say). Keys that a query does not see
  * take no part in its sums, whatever they hold (NaN and infinities included).
- * A key that it sees with a logit of -inf has weight 0, in the gradient too (only
- * that key's infinite columns of dq may be NaN: 0 times infinity). Where grad is not
+ * A key that it sees with a logit of -inf has weight 0, in the gradient too (but in
+ * infinite columns of such a key dq may be NaN, in those of such a query dk: 0 times
+ * infinity). Where grad is not
  * finite, the gradients of the keys that its query sees are not either.
  *
  * The gradient, for grad with respect to out and grad_lse to lse:

@@ -78,8 +78,8 @@ def test_the_largest_gradient_of_lse(gsk):  # noqa: F811
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_a_join_of_two_calls_where_a_query_sees_nothing_in_either(gsk, dtype):  # noqa: F811
-    """As README joins a window with other rows, with gradients: such a row is 0 and has no gradient, and
-    leaves the others' alone."""
+    """A window joined with other rows through lse, with gradients: such a row is 0 and has no gradient,
+    and leaves the others' alone."""
     from gated_softmax_kv_gb300 import autograd
     nq, D = [6, 50], 64
     q, k, v = (t.requires_grad_() for t in inputs(nq, [4, 50], 2, 1, D, dtype, 1))

@@ -71,6 +71,35 @@ def test_items_of_several_stretches(gsk, dtype, D, window):  # noqa: F811
         assert all(torch.equal(a, b) for a, b in zip(r, want))
 
 
+def test_stretches_in_graphs(gsk):  # noqa: F811
+    """Two captured calls, replayed one behind the other and again, on inputs that change between."""
+    q, k, v = inputs([900, 700], [900, 700], 128, 1, 64, "bf16", 1)
+    g, cu = make(q.shape, "bf16", 2), i32([0, 900, 1600])
+
+    def step():
+        out, lse = gsk.csa_prompt_attend(q, k, v, cu, 0.125)
+        return (out, lse, *gsk.csa_prompt_attend_bwd(q, k, v, out, lse, g, cu, 0.125))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            outs.append(step())
+    for seed in (5, 9):
+        for i, t in enumerate((q, k, v, g)):
+            t.copy_(make(t.shape, "bf16", seed + i))
+        for graph in graphs * 2:
+            graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        for o in outs:
+            assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
 def test_sums_of_like_terms_are_not_biased(gsk):  # noqa: F811
     """dV of a key that every query weighs the same, of gradients that are all 1: 128 heads by 4000 tokens over
     one key each, 512000 terms of 1. What is truncated on the way would be missing from the sum."""
