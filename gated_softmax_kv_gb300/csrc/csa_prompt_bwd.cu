@@ -292,7 +292,7 @@ struct KeysState {
   KeysItem item[2];
   WorkState work;
   uint64_t kv_full, kv_empty, q_full[2], q_empty[2], g_full[2], g_empty[2], r_full[2], s_full, p_full[2], dp_full, ds_full[2], done, clean[2];
-  int32_t dead, polls, bad;
+  int32_t dead, bad;
   uint32_t tmem;
   int32_t place;  // of BwdArgs::sums
 };
@@ -352,16 +352,16 @@ __device__ __noinline__ void give_back_grad(const PromptArgs& a, const KeysItem&
 
 // What the arithmetic of the keys kernel's tiles needs.
 struct KeysMath {
-  volatile int32_t* dead;
+  Dead dead;
   uint32_t s_at, dp_at, r_full, s_full, p_full, dp_full, ds_full;
   int col, key;
   float c, f;
 };
 
-// P and dS of the CTA's j-th tile for a key and 64 rows; SOME: some row does not see some key. In
-// two parts of 32 rows: the second's logits arrive while the first's are used.
+// P and dS of the CTA's j-th tile for a key and 64 rows; SOME: some row does not see some key;
+// says whether some key of the warp has NaN for the last row's logit. In two parts of 32 rows: the second's logits arrive while the first's are used.
 template <class C, bool SOME>
-__device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, uint32_t j) {
+__device__ __forceinline__ bool keys_step(KeysState& st, const KeysMath& m, uint32_t j) {
   constexpr bool HALF = C::HALF;
   const int stage = j & 1, key = m.key, lane = threadIdx.x & 31;
   const float2 c2 = make_float2(m.c, m.c), f2 = make_float2(m.f, m.f);
@@ -369,6 +369,7 @@ __device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, uint
   wait_for(m.s_full, j & 1, m.dead);
   tc_after();
   float p[64], d[64];
+  bool nan = false;
   tc_load32_async(m.s_at, p);
   tc_load_wait();
   tc_loaded(p);
@@ -378,6 +379,7 @@ __device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, uint
     if (part) {
       tc_load_wait();
       tc_loaded(p + 32);
+      if constexpr (SOME) nan = p[63] != p[63];
     }
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
@@ -451,12 +453,13 @@ __device__ __forceinline__ void keys_step(KeysState& st, const KeysMath& m, uint
   tc_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(m.ds_full);
+  return SOME && __any_sync(0xFFFFFFFFu, nan);
 }
 // Kept out of the loop: with both forms in it the instruction cache held neither
 // (8192 tokens of 32 heads of 128: 875 us).
 template <class C>
-__device__ __noinline__ void keys_step_some(KeysState& st, const KeysMath& m, uint32_t j) {
-  keys_step<C, true>(st, m, j);
+__device__ __noinline__ bool keys_step_some(KeysState& st, const KeysMath& m, uint32_t j) {
+  return keys_step<C, true>(st, m, j);
 }
 
 // The sums of a stretch of tiles, added to what the stretches before left: a key a thread.
@@ -495,10 +498,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                  r_full = smem_at(st.r_full), s_full = smem_at(&st.s_full), p_full = smem_at(st.p_full),
                  dp_full = smem_at(&st.dp_full), ds_full = smem_at(st.ds_full), done = smem_at(&st.done),
                  clean = smem_at(st.clean);
-  volatile int32_t* const dead = &st.dead;
+  const Dead dead = {&st.dead, a.polls};
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
-    st.polls = a.polls;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(clean + 8 * i, 1);
@@ -636,6 +638,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(r_full + 8 * stage);
+          tile_seen(st.work, lane);
           if (keys_mixed(a, x, j)) {  // infinities and NaN of rows that do not see every key
             const uint32_t parity = (tiles >> 1) & 1;
             wait_for(q_full + 8 * stage, parity, dead);
@@ -685,7 +688,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         weights(tiles);
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++tiles) {
-          tile_done(st.work, lane, tiles);
           if (j == max(0, n - 3)) want_work(st.work, lane);
           if (keys_mixed(a, x, j)) {
             wait_for(clean + 8 * (tiles & 1), (cleaned >> (tiles & 1)) & 1, dead);
@@ -725,23 +727,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       m.key = x.k0 + (threadIdx.x & 127);
       const int32_t nq = x.w.nq;
       // Rows that no head uses, behind the 64th, are 0: a key that holds infinities has NaN for
-      // their logits, and all of its tiles are masked as mixed ones are.
-      if (half && rows < 128 && x.n0 > 0) {
-        wait_for(s_full, tiles & 1, dead);
-        tc_after();
-        const float z = tc_load1(m.s_at + 63);
-        if (__any_sync(0xFFFFFFFFu, z != z)) x.w.nq = 0;
-      }
+      // their logits. The first tile, masked as mixed ones are (nq 0), says so, and all are then.
+      if (half && rows < 128) x.w.nq = 0;
 #pragma unroll 1
-      for (int j = 0; j < x.n0; ++j, ++tiles) {
-        if (keys_mixed(a, x, j))
-          keys_step_some<C>(st, m, tiles);
-        else
-          keys_step<C, false>(st, m, tiles);
-        if (((j + 1) & (kSumTiles - 1)) == 0 && j + 1 < x.n0) {
+      for (int j = 0; j < x.n0;) {  // stretches
+        const int end = min(x.n0, j + kSumTiles);
+#pragma unroll 1
+        for (; j < end; ++j, ++tiles) {
+          if (keys_mixed(a, x, j)) {
+            const bool nan = keys_step_some<C>(st, m, tiles);
+            if (j == 0 && !nan) x.w.nq = nq;
+          } else {
+            keys_step<C, false>(st, m, tiles);
+          }
+        }
+        if (j < x.n0) {
           wait_for(done, stretches++ & 1, dead);
           tc_after();
-          set_aside<C>(sums, tmem + 256 + half * C::DP + lanes, j < kSumTiles);
+          set_aside<C>(sums, tmem + 256 + half * C::DP + lanes, j <= kSumTiles);
         }
       }
       x.w.nq = nq;
@@ -815,7 +818,7 @@ struct RowsState {
   WorkState work;
   uint64_t q_full, q_empty, k_full[kKeyStages], k_empty[kKeyStages], v_full[kValueStages], v_empty[kValueStages], clean[kKeyStages], scored[kKeyStages],
       s_full, s_empty, dp_full[2], ds_full[2][2], done;  // ds_full: the arithmetic may be a block ahead
-  int32_t dead, polls, bad;
+  int32_t dead, bad;
   uint32_t tmem;
 };
 static_assert(sizeof(RowsState) <= 1024, "in front of the tiles");
@@ -855,7 +858,7 @@ __device__ __forceinline__ int2 rows_whole(const PromptArgs& a, const RowsItem& 
 
 // What the arithmetic of a row's blocks needs.
 struct RowsMath {
-  volatile int32_t* dead;
+  Dead dead;
   uint32_t s_at, dp_at, s_full, s_empty, dp_full, ds_full;
   int lo, hi;  // keys that the row sees, from this thread's half of block 0 on
   bool single;
@@ -948,10 +951,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                  k_empty = smem_at(st.k_empty), v_full = smem_at(st.v_full), v_empty = smem_at(st.v_empty),
                  s_full = smem_at(&st.s_full), s_empty = smem_at(&st.s_empty), dp_full = smem_at(st.dp_full),
                  ds_full = smem_at(st.ds_full), done = smem_at(&st.done), clean = smem_at(st.clean), scored_at = smem_at(st.scored);
-  volatile int32_t* const dead = &st.dead;
+  const Dead dead = {&st.dead, a.polls};
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
-    st.polls = a.polls;
 #pragma unroll 1
     for (int i = 0; i < kKeyStages; ++i) {
       mbar_init(clean + 8 * i, 1);
@@ -1053,6 +1055,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(k_empty + 8 * at.stage);
+          tile_seen(st.work, lane);
           at.next(1);
         }
       }
@@ -1100,7 +1103,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (n <= 2) tc_commit_by(leader, q_empty);
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-          tile_done(st.work, lane, added);
           if (j == max(0, n - 3)) want_work(st.work, lane);
           const uint32_t ready = ds_full + 16 * (added & 1), parity = (added >> 1) & 1;
           if (mixed(j)) {

@@ -87,7 +87,7 @@ struct State {
   Item item[2];
   WorkState work;
   uint64_t full[NS], empty[NS], q_full, q_empty, s_full[2], p_full[2][2], o_full[2], pair_full, pair_empty, clean[NS];
-  int32_t dead, polls, bad;
+  int32_t dead, bad;
   uint32_t tmem;
   float ref[128], sum[128];  // group 1's, for group 0; in a cluster: the CTA's
 };
@@ -231,13 +231,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                  q_empty = smem_at(&st.q_empty), s_full = smem_at(st.s_full), p_full = smem_at(st.p_full),
                  o_full = smem_at(st.o_full), pair_full = smem_at(&st.pair_full), pair_empty = smem_at(&st.pair_empty),
                  clean = smem_at(st.clean);
-  volatile int32_t* const dead = &st.dead;
+  const Dead dead = {&st.dead, a.polls};
   const int tp = 128 / a.group, rows = tp * a.group;
   const uint32_t ids = gridDim.x / shape.split, first_id = blockIdx.x / shape.split;
   const int part = (int)(blockIdx.x - first_id * shape.split);  // of the item, in a cluster
   if (threadIdx.x == 0) {
     st.dead = st.bad = 0;
-    st.polls = a.polls;
 #pragma unroll 1
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(full + 8 * i, 1);
@@ -305,6 +304,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(empty + 8 * at.stage);
+          tile_seen(st.work, lane);
           at.next(1);
         }
       }
@@ -413,7 +413,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           key.next(2);
 #pragma unroll 1
           for (int b = 0; b < n; ++b) {
-            tile_done(st.work, lane, copies + 2 * b);
             if (b == max(0, n - 3)) want_work(st.work, lane);
             valued(b);
             const bool more = b + 1 < n;
@@ -454,7 +453,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           key.next(2);
 #pragma unroll 1
           for (int b = 0; b < n; b += 2) {
-            tile_done(st.work, lane, copies + 2 * b);
             if (b == (max(0, n - 6) & ~1)) want_work(st.work, lane);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {

@@ -31,7 +31,7 @@ struct PromptArgs {
   int32_t polls;  // of a wait, before its CTA gives up
 };
 
-// What PromptArgs::polls is: kPolls (csa_tc.cuh), unless a test has set it lower.
+// PromptArgs::polls: kPolls (csa_tc.cuh), unless a test has set it lower.
 extern "C" int32_t csa_prompt_polls;
 
 // A sequence's rows. Where its lists pass the tensors, or one of them decreases, its queries see

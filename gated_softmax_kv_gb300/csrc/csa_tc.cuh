@@ -184,13 +184,6 @@ __device__ __forceinline__ void tc_loaded(float* v) {
                  "+f"(v[29]));
   asm volatile("" : "+f"(v[30]), "+f"(v[31]));
 }
-__device__ __forceinline__ float tc_load1(uint32_t at) {
-  float v;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(v) : "r"(at));
-  tc_load_wait();
-  asm volatile("" : "+f"(v));
-  return v;
-}
 // 16 words a lane, without waiting (tc_store_wait).
 __device__ __forceinline__ void tc_store16_async(uint32_t at, const uint32_t* r) {
   asm volatile(
