@@ -30,8 +30,8 @@
 // What bounds it: on long sequences the tensor core under the power limit (8192 tokens of 32
 // heads over 8 of 128 columns: keys kernel 700 to 735 us by the box, up to 1570 TFLOP/s of its
 // four products, rows kernel 605 to 640, 1360); heads of 64 columns the arithmetic, whose
-// products take half as long (8 ragged sequences of up to 1500 tokens, 24 heads over 8: 140
-// and 96 us).
+// products take half as long (8 ragged sequences of up to 1500 tokens, 24 heads over 8: 141
+// and 95 us).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>

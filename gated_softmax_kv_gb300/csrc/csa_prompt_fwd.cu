@@ -31,7 +31,7 @@
 // What bounds it: on long keys the tensor core under the power limit, 16384 tokens of 16
 // heads over 2 of 128 columns 642 to 737 us by the box (1710 to 1490 TFLOP/s; 2048 cycles of
 // products in 2400 of a round of both tiles). An item costs about 4 us beside its blocks: 12
-// ragged sequences of up to 2047 tokens, 32 heads over 8, 160 us (948 TFLOP/s); a window of
+// ragged sequences of up to 2047 tokens, 32 heads over 8, 159 us (954 TFLOP/s); a window of
 // 128 over 5003 tokens of 64 heads of 64, 92 us. Single tokens: memory, 32 sequences of 8192
 // keys, 8 key heads of 128, 158 us (6.8 TB/s).
 //
